@@ -15,6 +15,17 @@
  *   pkv_combine_partials       log-sum-exp merge of (o, m, l) partials: the manifest's
  *                              AttendSplitKMerge pass and the merge of sparse partials.
  *
+ * Step operators of a decoder with image, video or audio inputs (the pages have no
+ * counterpart; their formulas stand at each call):
+ *
+ *   pkv_paged_schedule         block tables, slot maps and cumulative lengths built on the
+ *                              GPU from request lengths.
+ *   pkv_paged_append_rotary_axes
+ *                              K / V of new tokens into the paged cache, K and Q rotated
+ *                              with one position per axis (time, height, width, ...).
+ *   pkv_cross_attention        attention of ragged queries over an encoder's states in a
+ *                              paged cache (no causal mask, another length).
+ *
  * Conventions for every call:
  *   - Tensor pointers are DEVICE pointers owned by the caller; the library never frees
  *     or retains them. Scratch memory is a caller-provided device workspace whose size
@@ -77,6 +88,8 @@ typedef enum pkv_status {
                                     block-sparse partials) are not written; it waited
                                     (bounded) for what it had issued, freed its tensor
                                     memory and returned */
+#define PKV_DEV_NO_BLOCKS 64u    /* pkv_paged_schedule: the pool has too few free blocks:
+                                    the row gets no tokens this time */
 
 typedef enum pkv_dtype { PKV_F16 = 1, PKV_BF16 = 2, PKV_F32 = 3, PKV_I32 = 4 } pkv_dtype;
 
@@ -408,6 +421,155 @@ typedef struct pkv_combine_args {
 int pkv_combine_partials(const pkv_combine_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * Schedule: block tables and slot maps from request lengths
+ * ------------------------------------------------------------------------------- */
+typedef struct pkv_schedule_args {
+  const int32_t* past_seqlens;   /* [batch] tokens of each row already in the cache */
+  const int32_t* new_seqlens;    /* [batch] tokens the row takes in now (0: idle row) */
+  /* [batch, max_blocks], updated in place. Row b holds its first
+     ceil(past_seqlens[b] / block_size) entries: these are read (an entry of -1 is a hole,
+     skipped; rows may share blocks). The entries behind them, up to
+     ceil((past + new) / block_size), are written; later ones stay as they are. */
+  int32_t* block_table;
+  /* outputs; all but the first may be NULL */
+  int32_t* cumulative_sequence_length;  /* [batch + 1] granted tokens before each row */
+  int32_t* slot_mapping;         /* [num_tokens] block * block_size + offset of each token;
+                                    -1 past the last granted token */
+  int32_t* positions;            /* [num_tokens] past + t of each token, -1 past the last */
+  int32_t* total_seqlens;        /* [batch] past + granted tokens (the next past) */
+  int32_t* free_blocks;          /* [1] blocks of the pool that no row holds afterwards */
+  int32_t* device_status;        /* optional */
+  int64_t batch;
+  int64_t max_blocks;
+  int64_t num_blocks;            /* blocks of the pool */
+  int64_t block_size;
+  int64_t num_tokens;            /* length of slot_mapping and positions */
+} pkv_schedule_args;
+
+/* A block is in use when some row holds it; every other block of the pool is free, so a
+ * finished request gives its blocks back by a past of 0. Row b needs
+ * ceil((past + new) / block_size) - ceil(past / block_size) blocks; counted over the rows
+ * in order, the r-th block asked for is the r-th free block by number. A row is granted all
+ * of its new tokens or none:
+ *   - rows are granted in order while the blocks asked for up to and including the row fit
+ *     the free ones; a row behind that is granted only if it needs no block
+ *     (PKV_DEV_NO_BLOCKS when one is not);
+ *   - and while the granted tokens fit num_tokens (PKV_DEV_BAD_SEQUENCE);
+ *   - a negative length (PKV_DEV_BAD_SEQUENCE), a past + new beyond max_blocks *
+ *     block_size (PKV_DEV_BAD_BLOCK) are granted nothing; a negative past holds nothing.
+ * A row that is granted nothing keeps its table row; total_seqlens gives its past back.
+ * A held entry outside the pool counts as a hole and sets PKV_DEV_BAD_BLOCK; a token
+ * whose held block is a hole gets slot -1 and sets PKV_DEV_BAD_BLOCK.
+ * The result depends on the inputs alone; a second call with the same inputs gives the same.
+ * past_seqlens and new_seqlens must not overlap the outputs. No workspace. Supported:
+ * batch <= 8192, num_blocks <= 2^20, num_blocks * block_size, batch * max_blocks,
+ * max_blocks * block_size and num_tokens below 2^31; otherwise PKV_ERR_UNSUPPORTED. */
+int pkv_paged_schedule(const pkv_schedule_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Paged append with rotary positions of several axes
+ * ------------------------------------------------------------------------------- */
+#define PKV_MAX_ROTARY_AXES 8
+#define PKV_MAX_ROTARY_PAIRS 128
+
+typedef struct pkv_append_axes_args {
+  /* rows of num_tokens tokens, `dtype`: separate mode query [num_tokens, num_heads *
+     head_size] (NULL with query_out NULL: no queries), key and value [num_tokens,
+     kv_num_heads * head_size]; packed mode (key == value == NULL) query holds
+     [Q | K | V] rows of (num_heads + 2 * kv_num_heads) * head_size. */
+  const void* query;
+  const void* key;
+  const void* value;
+  void* query_out;               /* [num_tokens, num_heads * head_size] or NULL: queries
+                                    are not rotated */
+  void* key_cache;               /* [num_blocks, block_size, kv_num_heads, head_size] */
+  void* value_cache;
+  const int32_t* slot_mapping;   /* [num_tokens] flat pool row; negative = padding */
+  const int32_t* positions;      /* [num_axes, num_tokens] (may be NULL without rotary) */
+  const void* cos_cache;         /* [rotary_positions, rotary_dim / 2], `table_dtype` */
+  const void* sin_cache;
+  int32_t* device_status;        /* optional */
+  int64_t num_tokens;
+  int64_t num_heads;
+  int64_t kv_num_heads;
+  int64_t head_size;
+  int64_t block_size;
+  int64_t num_blocks;
+  int64_t rotary_dim;            /* 0 = plain copy; else even, <= head_size */
+  int64_t rotary_positions;
+  int32_t num_axes;              /* 1 .. PKV_MAX_ROTARY_AXES when rotary_dim > 0 */
+  int32_t rotary_interleaved;    /* 0: element i pairs with i + rotary_dim / 2, 1: 2i with
+                                    2i + 1 */
+  int32_t dtype;                 /* PKV_F16 or PKV_BF16 */
+  int32_t table_dtype;           /* `dtype` or PKV_F32 */
+  uint8_t pair_axis[PKV_MAX_ROTARY_PAIRS];  /* axis of pair i < rotary_dim / 2 */
+} pkv_append_axes_args;
+
+/* For token i with slot s = slot_mapping[i] >= 0: pair j of every key (and, with query_out,
+ * query) head turns by the angle whose cos and sin stand in table row
+ * positions[pair_axis[j]][i], column j:
+ *   leading member own*cos - partner*sin, trailing member own*cos + partner*sin,
+ * in 32-bit arithmetic, rounded once to `dtype`; elements from rotary_dim on are copied.
+ * The key row goes to pool row s of key_cache, the value row to value_cache, the query row
+ * to row i of query_out. A negative slot is padding: nothing of the token is read beyond
+ * it, nothing is written. A slot past the pool (PKV_DEV_BAD_SLOT): K and V are not
+ * written, the query is. A position outside [0, rotary_positions) on an axis that some pair
+ * uses (PKV_DEV_BAD_POSITION): K and V are not written, the query row is copied unrotated.
+ * Two tokens of one slot leave either's row. query_out and the caches must not overlap the
+ * inputs or one another. head_size a multiple of 8, <= 256; otherwise
+ * PKV_ERR_UNSUPPORTED. */
+int pkv_paged_append_rotary_axes(const pkv_append_axes_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Cross attention over a paged cache of encoder states
+ * ------------------------------------------------------------------------------- */
+typedef struct pkv_cross_attention_args {
+  const void* query;             /* [num_tokens, num_heads * head_size], `dtype` */
+  const void* key_cache;         /* [num_blocks, block_size, kv_num_heads, head_size] */
+  const void* value_cache;
+  const int32_t* cumulative_sequence_length;  /* [batch + 1] query rows of each sequence */
+  const int32_t* key_seqlens;    /* [batch] encoder states of each sequence (may be 0) */
+  const int32_t* block_table;    /* [batch, max_blocks], -1 (or any id outside the pool) =
+                                    unmapped */
+  void* output;                  /* [num_tokens, num_heads * head_size], `dtype` */
+  float* lse;                    /* optional [num_tokens, num_heads] */
+  int32_t* device_status;        /* optional */
+  int64_t num_tokens;
+  int64_t batch;
+  int64_t num_heads;
+  int64_t kv_num_heads;
+  int64_t head_size;
+  int64_t block_size;
+  int64_t num_blocks;
+  int64_t max_blocks;
+  /* upper bound on the query rows of a sequence, 0 = num_tokens. A step of single tokens
+     that says so (1) leaves out the kernel for many rows. */
+  int64_t max_query_len;
+  int32_t dtype;                 /* PKV_F16 or PKV_BF16 */
+  float scale;                   /* softmax scale; 0 means 1/sqrt(head_size) */
+} pkv_cross_attention_args;
+
+/* Host only: workspace bytes pkv_cross_attention needs on the current device. */
+int pkv_cross_attention_workspace_size(const pkv_cross_attention_args* args, size_t* bytes);
+
+/* Query row i of sequence b, head hq with kv head h = hq / (num_heads / kv_num_heads), over
+ * the n = key_seqlens[b] states of its table row:
+ *   s_j = scale * <q, k_j>, lse = ln sum_j e^{s_j}, output = sum_j e^{s_j - lse} v_j,
+ * summed in 32 bits; the weights e^{s_j - m} are rounded once to `dtype` for the product
+ * with the values, their sum is not. A state whose block is unmapped takes no part and sets
+ * PKV_DEV_BAD_BLOCK (so does an n past max_blocks * block_size, which is cut there). A row
+ * that sees no state gets output 0 and lse -inf. Cache rows behind a sequence's states may
+ * hold anything (NaN too). Sequences whose cumulative lengths are inconsistent or exceed
+ * max_query_len, or whose key_seqlens entry is negative, get zero rows (lse -inf) and set
+ * PKV_DEV_BAD_SEQUENCE; so do rows that no sequence covers, without the flag.
+ * The order of summation depends on the sizes and the device's SM count alone: equal calls
+ * give equal bits. workspace: as in pkv_paged_attention (256-byte aligned, contents need
+ * not be initialised, one per call in flight). Supported: head_size in {64, 128},
+ * num_heads / kv_num_heads <= 16; otherwise PKV_ERR_UNSUPPORTED. */
+int pkv_cross_attention(const pkv_cross_attention_args* args, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
  * Runtime utilities
  * ------------------------------------------------------------------------------- */
 int pkv_abi_version(void);
@@ -419,7 +581,8 @@ int64_t pkv_launch_count(void);
 /* Per-kernel timing: when enabled, every launch is bracketed by CUDA events on its own
  * stream; pkv_profiler_query synchronises those events and returns the summed device
  * time (ms) and launch count of `kernel` ("scatter", "append", "plan", "decode",
- * "prefill", "combine", "sparse_group", "sparse_partials"). Not thread-safe. */
+ * "prefill", "combine", "sparse_group", "sparse_partials", "schedule", "append_axes",
+ * "cross_decode", "cross_tiles", "cross_combine"). Not thread-safe. */
 void pkv_profiler_enable(int on);
 
 /* Testing hook for the give-up path of the tensor-core kernels' bounded waits (the

@@ -22,6 +22,8 @@ STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_NULL", 2: "PKV_ERR_SHAPE", 3: "PKV_ERR_
 PKV_F16, PKV_BF16, PKV_F32, PKV_I32 = 1, 2, 3, 4
 PKV_SPLIT_AUTO, PKV_SPLIT_PAGES, PKV_SPLIT_FIXED = 0, 1, 2
 DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_BAD_POSITION, DEV_BAD_SEQUENCE, DEV_BAD_EDGE = 1, 2, 4, 8, 16
+DEV_TIMEOUT, DEV_NO_BLOCKS = 32, 64
+MAX_ROTARY_PAIRS = 128
 PRED_BITS = {"cacheShapeOk": 1, "headLayoutOk": 2, "scheduleShapeOk": 4, "ioShapeOk": 8,
              "separateKv": 16, "packedKv": 32, "slotShapeOk": 64}
 
@@ -102,10 +104,41 @@ class CombineArgs(ctypes.Structure):
                 ("reserved", c_i32)]
 
 
+class ScheduleArgs(ctypes.Structure):
+    _fields_ = [("past_seqlens", c_vp), ("new_seqlens", c_vp), ("block_table", c_vp),
+                ("cumulative_sequence_length", c_vp), ("slot_mapping", c_vp),
+                ("positions", c_vp), ("total_seqlens", c_vp), ("free_blocks", c_vp),
+                ("device_status", c_vp), ("batch", c_i64), ("max_blocks", c_i64),
+                ("num_blocks", c_i64), ("block_size", c_i64), ("num_tokens", c_i64)]
+
+
+class AppendAxesArgs(ctypes.Structure):
+    _fields_ = [("query", c_vp), ("key", c_vp), ("value", c_vp), ("query_out", c_vp),
+                ("key_cache", c_vp), ("value_cache", c_vp), ("slot_mapping", c_vp),
+                ("positions", c_vp), ("cos_cache", c_vp), ("sin_cache", c_vp),
+                ("device_status", c_vp), ("num_tokens", c_i64), ("num_heads", c_i64),
+                ("kv_num_heads", c_i64), ("head_size", c_i64), ("block_size", c_i64),
+                ("num_blocks", c_i64), ("rotary_dim", c_i64), ("rotary_positions", c_i64),
+                ("num_axes", c_i32), ("rotary_interleaved", c_i32), ("dtype", c_i32),
+                ("table_dtype", c_i32), ("pair_axis", ctypes.c_uint8 * MAX_ROTARY_PAIRS)]
+
+
+class CrossAttentionArgs(ctypes.Structure):
+    _fields_ = [("query", c_vp), ("key_cache", c_vp), ("value_cache", c_vp),
+                ("cumulative_sequence_length", c_vp), ("key_seqlens", c_vp),
+                ("block_table", c_vp), ("output", c_vp), ("lse", c_vp),
+                ("device_status", c_vp), ("num_tokens", c_i64), ("batch", c_i64),
+                ("num_heads", c_i64), ("kv_num_heads", c_i64), ("head_size", c_i64),
+                ("block_size", c_i64), ("num_blocks", c_i64), ("max_blocks", c_i64),
+                ("max_query_len", c_i64), ("dtype", c_i32), ("scale", c_f32)]
+
+
 STRUCTS = {"pkv_paged_attention_args": PagedAttentionArgs, "pkv_paged_plan": PagedPlan,
            "pkv_tensor_desc": TensorDesc, "pkv_paged_shapes": PagedShapes,
            "pkv_kv_append_args": KVAppendArgs, "pkv_sparse_args": SparseArgs,
-           "pkv_combine_args": CombineArgs}
+           "pkv_combine_args": CombineArgs, "pkv_schedule_args": ScheduleArgs,
+           "pkv_append_axes_args": AppendAxesArgs,
+           "pkv_cross_attention_args": CrossAttentionArgs}
 
 _LIB = None
 
@@ -146,6 +179,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             ("pkv_sparse_attention_partials", [ctypes.POINTER(SparseArgs), c_vp,
                                                ctypes.c_size_t, c_vp]),
             ("pkv_combine_partials", [ctypes.POINTER(CombineArgs), c_vp]),
+            ("pkv_paged_schedule", [ctypes.POINTER(ScheduleArgs), c_vp]),
+            ("pkv_paged_append_rotary_axes", [ctypes.POINTER(AppendAxesArgs), c_vp]),
+            ("pkv_cross_attention_workspace_size", [ctypes.POINTER(CrossAttentionArgs),
+                                                    ctypes.POINTER(ctypes.c_size_t)]),
+            ("pkv_cross_attention", [ctypes.POINTER(CrossAttentionArgs), c_vp,
+                                     ctypes.c_size_t, c_vp]),
             ("pkv_testing_wait_limit", [ctypes.c_uint32, c_i32])):
         fn = getattr(lib, name)
         fn.restype = c_i32
@@ -516,6 +555,244 @@ def pkv_combine_partials(o, m, l, segment_offsets=None, *, num_segments: int, la
     _check("pkv_combine_partials",
            load_library().pkv_combine_partials(ctypes.byref(a), _stream(stream)))
     return out, lse
+
+
+# ----------------------------------------------------------------------------- steps
+def _check_tensors(stream, **named):
+    """Each given as name=(tensor or None, dtype, shape): contiguous tensors of that dtype
+    and shape (None = any size) on the current CUDA device, which is the stream's too."""
+    on = {}
+    for name, (t, dtype, shape) in named.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        got = t.shape
+        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(got)}")
+        on[t.get_device()] = name
+    if -1 in on:
+        raise ValueError(f"{on[-1]}: must be a CUDA tensor")
+    here = _torch().cuda.current_device()
+    for device, name in on.items():
+        if device != here:
+            raise ValueError(f"{name}: on device {device}, the current one is {here}")
+    if stream is not None and stream.device_index != here:
+        raise ValueError(f"stream: of device {stream.device_index}, the current one is {here}")
+
+
+def _step_stream(stream, *made):
+    """The raw stream of a call; memory made here for a stream other than the current one
+    is not given away again before that stream has used it."""
+    s = stream if stream is not None else _torch().cuda.current_stream()
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    return s.cuda_stream
+
+
+def _need(**named):
+    for name, t in named.items():
+        if t is None:
+            raise ValueError(f"{name}: required")
+
+
+def pkv_paged_schedule(past_seqlens, new_seqlens, block_table, *, num_blocks: int,
+                       block_size: int, num_tokens: int, cumulative_sequence_length=None,
+                       slot_mapping=None, positions=None, total_seqlens=None,
+                       free_blocks=None, device_status=None, stream=None):
+    """Block tables, slot maps and cumulative lengths from request lengths, on the GPU.
+
+    ``block_table`` [batch, max_blocks] is updated in place: row b holds its first
+    ceil(past / block_size) entries and gets the lowest free blocks for its new tokens.
+    Returns (cumulative_sequence_length [batch + 1], slot_mapping [num_tokens], positions
+    [num_tokens], total_seqlens [batch], free_blocks [1]), all int32; those not passed in
+    are made here. Rows that the pool or ``num_tokens`` cannot take get no tokens."""
+    torch = _torch()
+    i32 = torch.int32
+    _need(past_seqlens=past_seqlens, new_seqlens=new_seqlens, block_table=block_table)
+    num_tokens = int(num_tokens)
+    B = past_seqlens.shape[0] if past_seqlens.dim() == 1 else -1
+    _check_tensors(stream, past_seqlens=(past_seqlens, i32, (B,)),
+                   new_seqlens=(new_seqlens, i32, (B,)),
+                   block_table=(block_table, i32, (B, None)),
+                   cumulative_sequence_length=(cumulative_sequence_length, i32, (B + 1,)),
+                   slot_mapping=(slot_mapping, i32, (num_tokens,)),
+                   positions=(positions, i32, (num_tokens,)),
+                   total_seqlens=(total_seqlens, i32, (B,)),
+                   free_blocks=(free_blocks, i32, (1,)),
+                   device_status=(device_status, i32, (1,)))
+    dev, made = block_table.device, []
+
+    def out(t, n):
+        if t is None:
+            t = torch.empty(n, dtype=i32, device=dev)
+            made.append(t)
+        return t
+
+    cu, slots = out(cumulative_sequence_length, B + 1), out(slot_mapping, num_tokens)
+    pos, total, free = out(positions, num_tokens), out(total_seqlens, B), out(free_blocks, 1)
+    a = ScheduleArgs(past_seqlens.data_ptr(), new_seqlens.data_ptr(), block_table.data_ptr(),
+                     cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), total.data_ptr(),
+                     free.data_ptr(), _ptr(device_status), B, block_table.shape[1],
+                     num_blocks, block_size, num_tokens)
+    _check("pkv_paged_schedule",
+           load_library().pkv_paged_schedule(ctypes.byref(a), _step_stream(stream, *made)))
+    return cu, slots, pos, total, free
+
+
+def rotary_pair_axis(sections, by_turns: bool = False):
+    """Axis of each rotary pair, for ``sections`` pairs per axis: one section after the
+    other (0 0 0 1 1 2), or the axes by turns while they have pairs left (0 1 2 0 1 0)."""
+    left = [int(n) for n in sections]
+    if not left or any(n < 0 for n in left):
+        raise ValueError(f"sections: numbers of pairs, got {sections!r}")
+    if not by_turns:
+        return [a for a, n in enumerate(left) for _ in range(n)]
+    axis = []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                axis.append(a)
+                left[a] = n - 1
+    return axis
+
+
+def pkv_paged_append_rotary_axes(query, key, value, key_cache, value_cache, slot_mapping,
+                                 positions, *, num_heads: int, kv_num_heads: int,
+                                 cos_cache=None, sin_cache=None, rotary_dim: int = 0,
+                                 pair_axis=None, rotary_interleaved: bool = False,
+                                 query_out=None, rotate_query: bool = True,
+                                 device_status=None, stream=None):
+    """K and V rows into the paged cache (pool row slot_mapping[i], negative = padding), K
+    and Q rotated with ``positions`` [axes, num_tokens]; ``pair_axis`` names the axis of each
+    rotary pair (all axis 0 when None). float16 or bfloat16; the tables in that type or
+    float32. Packed rows when key and value are None. Returns the rotated queries
+    [num_tokens, num_heads * head_size] (made here unless ``query_out`` is given; rows of
+    padding are not written), or None without them (``rotate_query`` false, or no query)."""
+    torch = _torch()
+    _need(key_cache=key_cache, value_cache=value_cache, slot_mapping=slot_mapping)
+    dt = key_cache.dtype
+    if dt not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"key_cache: expected float16 or bfloat16, got {dt}")
+    if key_cache.dim() != 4:
+        raise ValueError("key_cache: [num_blocks, block_size, kv_num_heads, head_size]")
+    NB, BS, Hkv, D = key_cache.shape
+    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+    packed = key is None and value is None
+    qh, kvh = num_heads * D, kv_num_heads * D
+    half, axes, tdt = rotary_dim // 2, 0, torch.float32
+    if rotary_dim > 0:
+        _need(positions=positions, cos_cache=cos_cache, sin_cache=sin_cache)
+        axes = positions.shape[0] if positions.dim() == 2 else -1
+        if cos_cache.dtype == dt:
+            tdt = dt
+    table, pairs = None, b""
+    if rotary_dim > 0:
+        table = (cos_cache.shape[0] if cos_cache.dim() else 0, half)
+        pairs = bytes(half) if pair_axis is None else bytes(pair_axis)
+        if len(pairs) != half or half > MAX_ROTARY_PAIRS:
+            raise ValueError(f"pair_axis: one axis for each of {half} pairs (at most "
+                             f"{MAX_ROTARY_PAIRS}), got {len(pairs)}")
+    else:
+        positions = cos_cache = sin_cache = None
+    _check_tensors(stream, query=(query, dt, (T, qh + 2 * kvh if packed else qh)),
+                   key=(key, dt, (T, kvh)), value=(value, dt, (T, kvh)),
+                   query_out=(query_out, dt, (T, qh)),
+                   key_cache=(key_cache, dt, (NB, BS, kv_num_heads, D)),
+                   value_cache=(value_cache, dt, (NB, BS, kv_num_heads, D)),
+                   slot_mapping=(slot_mapping, torch.int32, (T,)),
+                   positions=(positions, torch.int32, (axes, T)),
+                   cos_cache=(cos_cache, tdt, table), sin_cache=(sin_cache, tdt, table),
+                   device_status=(device_status, torch.int32, (1,)))
+    made = None
+    if rotate_query and query is not None and query_out is None:
+        query_out = made = torch.empty((T, qh), dtype=dt, device=key_cache.device)
+    a = AppendAxesArgs(_ptr(query), _ptr(key), _ptr(value), _ptr(query_out),
+                       key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(),
+                       _ptr(positions), _ptr(cos_cache), _ptr(sin_cache),
+                       _ptr(device_status), T, num_heads, kv_num_heads, D, BS, NB,
+                       rotary_dim, cos_cache.shape[0] if rotary_dim > 0 else 0, axes,
+                       1 if rotary_interleaved else 0, _dtype_code(key_cache),
+                       PKV_F32 if tdt == torch.float32 else _dtype_code(key_cache))
+    ctypes.memmove(ctypes.addressof(a) + AppendAxesArgs.pair_axis.offset, pairs, len(pairs))
+    _check("pkv_paged_append_rotary_axes",
+           load_library().pkv_paged_append_rotary_axes(ctypes.byref(a),
+                                                       _step_stream(stream, made)))
+    return query_out
+
+
+def make_cross_args(query, key_cache, value_cache, cumulative_sequence_length, key_seqlens,
+                    block_table, output, lse=None, *, num_heads: int, kv_num_heads: int,
+                    max_query_len: int = 0, scale: float = 0.0,
+                    device_status=None) -> CrossAttentionArgs:
+    """Fill the C argument block of pkv_cross_attention from tensors."""
+    return CrossAttentionArgs(
+        query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+        cumulative_sequence_length.data_ptr(), key_seqlens.data_ptr(), block_table.data_ptr(),
+        output.data_ptr(), _ptr(lse), _ptr(device_status), query.shape[0],
+        key_seqlens.shape[0], num_heads, kv_num_heads, key_cache.shape[3],
+        key_cache.shape[1], key_cache.shape[0], block_table.shape[1], max_query_len,
+        _dtype_code(query), scale)
+
+
+def pkv_cross_attention_workspace_size(args: CrossAttentionArgs) -> int:
+    n = ctypes.c_size_t(0)
+    _check("pkv_cross_attention_workspace_size",
+           load_library().pkv_cross_attention_workspace_size(ctypes.byref(args),
+                                                             ctypes.byref(n)))
+    return n.value
+
+
+def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_length,
+                        key_seqlens, block_table, *, num_heads: int, kv_num_heads: int,
+                        max_query_len: int = 0, scale: float = 0.0, output=None, lse=None,
+                        workspace=None, device_status=None, stream=None):
+    """Attention of ragged query rows over encoder states in a paged cache: row i of
+    sequence b sees the key_seqlens[b] states of table row b. float16 or bfloat16. Returns
+    the output [num_tokens, num_heads * head_size]; with ``lse`` (float32 [num_tokens,
+    num_heads]) the log-sum-exp of each row's scores is written there."""
+    torch = _torch()
+    _need(query=query, key_cache=key_cache, value_cache=value_cache,
+          cumulative_sequence_length=cumulative_sequence_length, key_seqlens=key_seqlens,
+          block_table=block_table)
+    dt = query.dtype
+    if dt not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"query: expected float16 or bfloat16, got {dt}")
+    if key_cache.dim() != 4:
+        raise ValueError("key_cache: [num_blocks, block_size, kv_num_heads, head_size]")
+    NB, BS, Hkv, D = key_cache.shape
+    T = query.shape[0] if query.dim() == 2 else -1
+    B = key_seqlens.shape[0] if key_seqlens.dim() == 1 else -1
+    hidden = (T, num_heads * D)
+    _check_tensors(stream, query=(query, dt, hidden), output=(output, dt, hidden),
+                   key_cache=(key_cache, dt, (NB, BS, kv_num_heads, D)),
+                   value_cache=(value_cache, dt, (NB, BS, kv_num_heads, D)),
+                   key_seqlens=(key_seqlens, torch.int32, (B,)),
+                   cumulative_sequence_length=(cumulative_sequence_length, torch.int32,
+                                               (B + 1,)),
+                   block_table=(block_table, torch.int32, (B, None)),
+                   lse=(lse, torch.float32, (T, num_heads)),
+                   workspace=(workspace, torch.uint8, (None,)),
+                   device_status=(device_status, torch.int32, (1,)))
+    made = None
+    if output is None:
+        output = made = torch.empty(hidden, dtype=dt, device=query.device)
+    a = make_cross_args(query, key_cache, value_cache, cumulative_sequence_length, key_seqlens,
+                        block_table, output, lse, num_heads=num_heads,
+                        kv_num_heads=kv_num_heads, max_query_len=max_query_len, scale=scale,
+                        device_status=device_status)
+    need = pkv_cross_attention_workspace_size(a)
+    scratch = None
+    if workspace is None or workspace.numel() < need:
+        workspace = scratch = torch.empty(need, dtype=torch.uint8, device=query.device)
+    _check("pkv_cross_attention",
+           load_library().pkv_cross_attention(ctypes.byref(a), workspace.data_ptr(), need,
+                                              _step_stream(stream, made, scratch)))
+    return output
 
 
 # ----------------------------------------------------------------------------- runtime

@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["runtime.cpp", "attention.cu", "scatter.cu", "combine.cu", "sparse.cu",
-           "sparse16.cu", "static_workspace.cu"]
+           "sparse16.cu", "static_workspace.cu", "step_runtime.cpp", "schedule.cu",
+           "append_axes.cu", "cross.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

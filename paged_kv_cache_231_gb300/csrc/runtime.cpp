@@ -328,6 +328,9 @@ size_t pkv_sizeof_struct(const char* name) {
   if (n == "pkv_kv_append_args") return sizeof(pkv_kv_append_args);
   if (n == "pkv_sparse_args") return sizeof(pkv_sparse_args);
   if (n == "pkv_combine_args") return sizeof(pkv_combine_args);
+  if (n == "pkv_schedule_args") return sizeof(pkv_schedule_args);
+  if (n == "pkv_append_axes_args") return sizeof(pkv_append_axes_args);
+  if (n == "pkv_cross_attention_args") return sizeof(pkv_cross_attention_args);
   return 0;
 }
 
