@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["runtime.cpp", "attention.cu", "scatter.cu", "combine.cu", "sparse.cu",
            "sparse16.cu", "static_workspace.cu", "step_runtime.cpp", "schedule.cu",
-           "append_axes.cu", "cross.cu"]
+           "append_axes.cu", "cross.cu", "cross_tiles.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -2,144 +2,481 @@
 // (pkv_cross_attention): out = softmax(scale q k^T) v over the n_b states of the row's
 // sequence, lse = ln sum e^{scale q k}. Scores are held in log2 units (scale * log2 e).
 //
-// First form: one warp per (token, query head), lanes across the head; the running maximum
-// and sum of the softmax in registers.
-#include <cuda_bf16.h>
-#include <math.h>
-
-#include "device_common.cuh"
-#include "internal.h"
-#include "step_ops.h"
+// This file: the kernel for few query rows (sequences with at most 16 rows of a kv head:
+// single tokens, drafts), the join of pieces and the launches. cross_tiles.cu: many rows.
+//
+// Few rows: bound by HBM, every key and value row is read once, 4 * D bytes a state and kv
+// head. Each warp of a persistent grid runs through its steps of 16 keys: rows go through the
+// warp's own ring in shared memory by 16-byte asynchronous copies (two steps ahead; the block
+// table a third), scores and products on mma.sync m16n8k16, whose 16 rows are the
+// sequence's query rows x the heads that share the kv head.
+#include "cross_dev.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128;
+using namespace cross;
 
-template <typename T>
-struct Num;
-template <>
-struct Num<__half> {
-  static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
-  static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
-};
-template <>
-struct Num<__nv_bfloat16> {
-  static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
-  static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
-};
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCtasPerSm = 2;
+constexpr int kLeastFew = 8;    // steps of a run, at least
+constexpr int kLeastTile = 4;
 
-// sequence of token i: the last b with cu[b] <= i, or -1
-__device__ __forceinline__ int sequence_of(const CrossParams& p, int i) {
-  int lo = 0, hi = p.B - 1, b = -1;
-  while (lo <= hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu + mid) <= i) {
-      b = mid;
-      lo = mid + 1;
-    } else {
-      hi = mid - 1;
-    }
+template <int D>
+__device__ __forceinline__ int chunk_at(int r, int c) {   // 16-byte chunk c of row r, swizzled
+  return (r * (D / 8) + (c ^ (r & 7))) * 8;
+}
+
+// Lane r < 16: element offset of key k0 + r of (sequence b, kv head h), -1 past the keys or
+// where the block is unmapped.
+__device__ __forceinline__ int64_t key_offset(const CrossParams& p, int b, int h, int k0,
+                                              int keys, int lane, int& flags) {
+  const int j = k0 + lane;
+  if (lane >= kStepKeys || j >= keys) return -1;
+  const int col = p.bs_shift >= 0 ? j >> p.bs_shift : j / p.BS;
+  const int blk = __ldg(p.table + (int64_t)b * p.MB + col);
+  if (blk < 0 || blk >= p.NB) {
+    flags |= PKV_DEV_BAD_BLOCK;
+    return -1;
   }
-  return b;
+  return (((int64_t)blk * p.BS + (j - col * p.BS)) * p.Hkv + h) * p.D;
+}
+
+// Copies the 16 key and value rows whose offsets lanes 0..15 hold; others are zeroed.
+template <typename T, int D>
+__device__ __forceinline__ void copy_step(const CrossParams& p, int64_t off, T* sk, T* sv,
+                                          int lane) {
+  constexpr int CPR = D / 8, RPI = 32 / CPR;
+  const int c = lane % CPR;
+#pragma unroll
+  for (int i = 0; i < kStepKeys / RPI; ++i) {
+    const int r = i * RPI + lane / CPR;
+    const long long o = __shfl_sync(0xffffffffu, (long long)off, r);
+    const int64_t at = o >= 0 ? o + c * 8 : 0;
+    cp_async_16(sk + chunk_at<D>(r, c), static_cast<const T*>(p.kc) + at, o >= 0 ? 16 : 0);
+    cp_async_16(sv + chunk_at<D>(r, c), static_cast<const T*>(p.vc) + at, o >= 0 ? 16 : 0);
+  }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) cross_rows_kernel(CrossParams p) {
+__device__ __forceinline__ void load_queries(const CrossParams& p, const Cursor& c, int lane,
+                                             uint32_t (&qa)[D / 16][4]) {
+  const int R = c.q.rows * p.G;
+  const T* row[2];
+  bool ok[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int r = (lane >> 2) + 8 * x;
+    ok[x] = r < R;
+    const int pos = ok[x] ? r / p.G : 0, g = ok[x] ? r % p.G : 0;
+    row[x] = static_cast<const T*>(p.q) + ((int64_t)(c.q.cu0 + pos) * p.Hq + c.r * p.G + g) * D;
+  }
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const int e = ks * 16 + 2 * (lane & 3);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      qa[ks][x] = ok[x & 1] ? __ldg(reinterpret_cast<const unsigned*>(row[x & 1] + e + (x >> 1) * 8))
+                            : 0u;
+  }
+}
+
+// End of the unit's part of a range: the output if the range lies in the run, else a piece.
+template <typename T, int D>
+__device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int64_t unit,
+                                      bool whole, int slot, float (&m)[2], float (&l)[2],
+                                      float (&o)[D / 8][4], int lane) {
+  const int R = c.q.rows * p.G, t4 = lane & 3;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    const int r = (lane >> 2) + 8 * x;
+    if (r >= R) continue;
+    if (whole) {
+      const float inv = inverse_of(l[x]);
+      const int64_t row = (int64_t)(c.q.cu0 + r / p.G) * p.Hq + c.r * p.G + r % p.G;
+      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D) + t4;
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+        out[d * 4] = Num<T>::pack(o[d][2 * x] * inv, o[d][2 * x + 1] * inv);
+      if (p.lse && t4 == 0) p.lse[row] = lse_of(m[x], l[x]);
+    } else {
+      const int64_t row = (2 * unit + slot) * p.few_rows + r;
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+        *reinterpret_cast<float2*>(p.few_o + row * D + d * 8 + 2 * t4) =
+            make_float2(o[d][2 * x], o[d][2 * x + 1]);
+      if (t4 == 0) {
+        p.few_m[row] = m[x];
+        p.few_l[row] = l[x];
+      }
+    }
+  }
+}
+
+// Rows that no key is seen from, or that no sequence covers: output 0, lse -inf.
+template <typename T, int D>
+__device__ void zero_rows(const CrossParams& p, int unit, int units, int lane) {
+  for (int64_t i0 = (int64_t)unit * 32; i0 < p.T; i0 += (int64_t)units * 32) {
+    const int i = (int)min(i0 + lane, (int64_t)p.T - 1);
+    int lo = 0, hi = p.B - 1, b = -1;
+    while (lo <= hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.cu + mid) <= i) {
+        b = mid;
+        lo = mid + 1;
+      } else {
+        hi = mid - 1;
+      }
+    }
+    bool empty = true;
+    if (b >= 0) {
+      int f = 0;
+      bool z = false;
+      const Seq few = read_seq<false>(p, b, &f, &z), many = read_seq<true>(p, b, &f, &z);
+      empty = few.ranges + many.ranges == 0 || i >= few.cu0 + few.rows;
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, empty && i0 + lane < p.T);
+    for (; todo; todo &= todo - 1) {
+      const int64_t row = i0 + __ffs(todo) - 1;
+      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.Hq * D);
+      for (int c = lane; c < p.Hq * D / 8; c += 32) out[c] = make_uint4(0, 0, 0, 0);
+      if (p.lse)
+        for (int h = lane; h < p.Hq; h += 32) p.lse[row * p.Hq + h] = -INFINITY;
+    }
+  }
+}
+
+template <int D>
+struct Ring {
+  static constexpr int kSteps = D == 64 ? 6 : 3;
+  static constexpr size_t kWarpBytes = (size_t)kSteps * kStepKeys * D * 2 * 2;
+  static constexpr size_t kBytes = kWarps * kWarpBytes;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossParams p) {
+  constexpr int NS = Ring<D>::kSteps;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_pref[kEntries];
+  __shared__ int64_t s_scratch[kWarps + 2];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int flags = 0;
+  const Plan pl = make_plan<false, kThreads>(p, p.few_units, kLeastFew, s_pref, s_scratch, &flags);
+  if (blockIdx.x > 0) flags = 0;   // every block saw them
+  const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
+  if (lane == 0) write_record<false>(p, pl, s_pref, unit, p.few_rec);
+  const int64_t g0 = unit * pl.W;
+  const int nst = g0 < pl.total ? (int)(min(pl.total, g0 + pl.W) - g0) : 0;
+  if (nst > 0) {
+    T* rk = reinterpret_cast<T*>(smem + warp * Ring<D>::kWarpBytes);
+    T* rv = rk + NS * kStepKeys * D;
+    Cursor pc = locate<false>(p, pl, s_pref, g0);   // next step to copy
+    Cursor cc = pc;                                  // step computed
+    uint32_t live[NS];                               // keys of the step that take part
+    int64_t ahead = key_offset(p, pc.b, pc.r, pc.s * kStepKeys, pc.q.keys, lane, flags);
+    const auto issue = [&](int k, int buf) {
+      if (k < nst) {
+        copy_step<T, D>(p, ahead, rk + buf * kStepKeys * D, rv + buf * kStepKeys * D, lane);
+        if (k + 1 < nst) {
+          if (++pc.s == pc.q.steps) next_range<false>(p, pc);
+        }
+      }
+      const uint32_t w = __ballot_sync(0xffffffffu, ahead >= 0);
+      if (k + 1 < nst)
+        ahead = key_offset(p, pc.b, pc.r, pc.s * kStepKeys, pc.q.keys, lane, flags);
+      cp_async_commit();
+      return w;
+    };
+#pragma unroll
+    for (int k = 0; k < NS - 1; ++k) live[k] = issue(k, k);
+    uint32_t qa[D / 16][4];
+    load_queries<T, D>(p, cc, lane, qa);
+    const int t4 = lane & 3;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+    bool from_start = cc.s == 0, first = true;
+
+    for (int k0 = 0; k0 < nst; k0 += NS) {
+#pragma unroll
+      for (int kk = 0; kk < NS; ++kk) {
+        const int k = k0 + kk;
+        if (k >= nst) break;
+        cp_async_wait<NS - 2>();
+        __syncwarp();
+        live[(kk + NS - 1) % NS] = issue(k + NS - 1, (kk + NS - 1) % NS);
+        const T* sk = rk + kk * kStepKeys * D;
+        const T* sv = rv + kk * kStepKeys * D;
+        float s[2][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
+        {
+          const int key = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(b0, b1, b2, b3, sk + chunk_at<D>(key, 2 * ks + half));
+            Num<T>::mma(s[0], qa[ks], b0, b1);
+            Num<T>::mma(s[1], qa[ks], b2, b3);
+          }
+        }
+        const uint32_t w = live[kk];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[n][e] = (w >> (n * 8 + 2 * t4 + (e & 1))) & 1u ? s[n][e] * p.scale_log2 : -INFINITY;
+        // online softmax of rows lane / 4 and lane / 4 + 8
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[x], mx);
+          const float base = mn == -INFINITY ? 0.f : mn;   // scores of -inf weigh nothing
+          const float alpha = ex2(m[x] - base);
+          m[x] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              s[n][2 * x + e] = ex2(s[n][2 * x + e] - base);
+              sum += s[n][2 * x + e];
+            }
+          l[x] = l[x] * alpha + sum;
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            o[d][2 * x] *= alpha;
+            o[d][2 * x + 1] *= alpha;
+          }
+        }
+        // the weights, rounded once to T, times the value rows (l keeps them unrounded)
+        const uint32_t pa[4] = {Num<T>::pack(s[0][0], s[0][1]), Num<T>::pack(s[0][2], s[0][3]),
+                                Num<T>::pack(s[1][0], s[1][1]), Num<T>::pack(s[1][2], s[1][3])};
+        {
+          const int key = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_t(b0, b1, b2, b3, sv + chunk_at<D>(key, 2 * j + half));
+            Num<T>::mma(o[2 * j], pa, b0, b1);
+            Num<T>::mma(o[2 * j + 1], pa, b2, b3);
+          }
+        }
+        const bool last = cc.s == cc.q.steps - 1;
+        if (last || k == nst - 1) {
+          flush<T, D>(p, cc, unit, from_start && last, first ? 0 : 1, m, l, o, lane);
+          m[0] = m[1] = -INFINITY;
+          l[0] = l[1] = 0.f;
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+          first = false;
+          from_start = true;
+        }
+        if (k < nst - 1) {
+          if (last) {
+            next_range<false>(p, cc);
+            load_queries<T, D>(p, cc, lane, qa);
+          } else {
+            ++cc.s;
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+  }
+  if (pl.zero) zero_rows<T, D>(p, (int)unit, p.few_units, lane);
+  if (flags) flag_status(p.status, flags);
+}
+
+// ---------------------------------------------------------------------------- join
+// Over the pieces of a row: M = max m, out = sum 2^{m - M} o / sum 2^{m - M} l. A block takes
+// the record of one unit of the kernel for few rows (8 warps share its rows, several warps a
+// row when there are fewer), or 32 of the up to 256 rows of a record of the other kernel.
+constexpr int kJoinWarps = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams p) {
   constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  if (blockIdx.x == 0) {   // sequences that take no part or are cut
-    int seen = 0;
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-      const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1), n = __ldg(p.klen + b);
-      if (lo < 0 || hi < lo || hi > p.T || hi - lo > p.max_q || n < 0)
-        seen |= PKV_DEV_BAD_SEQUENCE;
-      else if (hi > lo && n > p.MB * p.BS)
-        seen |= PKV_DEV_BAD_BLOCK;
+  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool tile = (int)blockIdx.x >= p.few_units;
+  const int64_t unit = tile ? (blockIdx.x - p.few_units) / 8 : blockIdx.x;
+  const int4* rec = (tile ? p.tile_rec : p.few_rec) + 2 * unit;
+  const int4 a = __ldcg(rec);
+  if (a.x <= 0) return;
+  const int tokens = __ldcg(rec + 1).x;
+  const int rows_at = tile ? 256 : p.few_rows;       // rows of a stored piece
+  const float* po = tile ? p.tile_o : p.few_o;
+  const float* pm = tile ? p.tile_m : p.few_m;
+  const float* pl = tile ? p.tile_l : p.few_l;
+  const int row0 = tile ? ((blockIdx.x - p.few_units) % 8) * 32 : 0;
+  const int rows = tile ? 32 : tokens * p.G;
+  int share = 1;                                     // warps of a row
+  while (share < kJoinWarps && rows * share * 2 <= kJoinWarps) share *= 2;
+  const int PT = p.tile_pos / 2;
+  for (int r0 = 0; r0 < rows; r0 += kJoinWarps / share) {
+    const int r = row0 + r0 + warp / share, part = warp % share;
+    const int pos = tile ? (r >> 7) * PT + (r & 127) / p.G : r / p.G;
+    const bool live = (tile ? (r & 127) < PT * p.G : r < rows) && pos < tokens;
+    float acc[V], M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    if (live) {
+      for (int q = part; q < a.x; q += share)        // the row's maximum over this share
+      {
+        const int64_t at = (2 * (unit + q) + (q == 0 ? a.y : 0)) * rows_at + r;
+        if (__ldcg(pl + at) != 0.f) M = fmaxf(M, __ldcg(pm + at));
+      }
+      const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+      for (int q = part; q < a.x; q += share) {
+        const int64_t at = (2 * (unit + q) + (q == 0 ? a.y : 0)) * rows_at + r;
+        const float l = __ldcg(pl + at);
+        if (l == 0.f) continue;
+        const float w = ex2(__ldcg(pm + at) - base);
+        L += w * l;
+        const float* src = po + at * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          acc[0] += w * x.x;
+          acc[1] += w * x.y;
+          acc[2] += w * x.z;
+          acc[3] += w * x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          acc[0] += w * x.x;
+          acc[1] += w * x.y;
+        }
+      }
     }
-    if (seen) flag_status(p.status, seen);
-  }
-  if (w >= (int64_t)p.T * p.Hq) return;
-  const int i = (int)(w / p.Hq), hq = (int)(w % p.Hq), h = hq / p.G;
-  const int b = sequence_of(p, i);
-  int n = 0, flags = 0;
-  if (b >= 0) {
-    const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
-    n = __ldg(p.klen + b);
-    if (lo < 0 || hi < lo || hi > p.T || hi - lo > p.max_q || n < 0) {
-      flags = PKV_DEV_BAD_SEQUENCE;
-      n = 0;
-    } else if (i >= hi) {
-      n = 0;
-    } else if (n > p.MB * p.BS) {
-      flags = PKV_DEV_BAD_BLOCK;
-      n = p.MB * p.BS;
+    if (share > 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
+      if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = L;
+      }
+      __syncthreads();
+      if (part == 0 && live) {
+        float top = M;
+        for (int k = 1; k < share; ++k) top = fmaxf(top, s_l[warp + k] == 0.f ? -INFINITY : s_m[warp + k]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float w = L == 0.f ? 0.f : ex2(M - base);
+        L *= w;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= w;
+        for (int k = 1; k < share; ++k) {
+          if (s_l[warp + k] == 0.f) continue;
+          w = ex2(s_m[warp + k] - base);
+          L += w * s_l[warp + k];
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] += w * s_o[warp + k][lane * V + v];
+        }
+        M = top;
+      }
+      __syncthreads();
+    }
+    if (live && part == 0) {
+      const int64_t row = (int64_t)(a.z + pos) * p.Hq + a.w * p.G + (tile ? r & 127 : r) % p.G;
+      const float inv = inverse_of(L);
+      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * V);
+#pragma unroll
+      for (int v = 0; v < V; v += 2) out[v / 2] = Num<T>::pack(acc[v] * inv, acc[v + 1] * inv);
+      if (p.lse && lane == 0) p.lse[row] = lse_of(M, L);
     }
   }
-  const T* q = static_cast<const T*>(p.q) + ((int64_t)i * p.Hq + hq) * D;
-  float qv[V], o[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    qv[k] = Num<T>::to(q[lane * V + k]);
-    o[k] = 0.f;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
+  static std::atomic<uint64_t> configured{0};
+  int dev = -1;
+  if (needs_configure(configured, &dev)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        cross_few_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    mark_configured(configured, dev);
   }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < n; ++j) {
-    const int col = p.bs_shift >= 0 ? j >> p.bs_shift : j / p.BS;
-    const int blk = __ldg(p.table + (int64_t)b * p.MB + col);
-    if (blk < 0 || blk >= p.NB) {
-      flags |= PKV_DEV_BAD_BLOCK;
-      continue;
-    }
-    const int64_t row = (((int64_t)blk * p.BS + (j - col * p.BS)) * p.Hkv + h) * D + lane * V;
-    const T* k_ = static_cast<const T*>(p.kc) + row;
-    const T* v_ = static_cast<const T*>(p.vc) + row;
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < V; ++k) s += qv[k] * Num<T>::to(k_[k]);
-    s = warp_sum(s) * p.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float base = mn == -INFINITY ? 0.f : mn;   // scores of -inf weigh nothing
-    const float a = ex2(m - base), e = ex2(s - base);
-    m = mn;
-    l = l * a + e;
-#pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = o[k] * a + e * Num<T>::to(v_[k]);
+  {
+    ProfScope ps("cross_decode", s);
+    cross_few_kernel<T, D><<<p.few_units / kWarps, kThreads, Ring<D>::kBytes, s>>>(p);
   }
-  T* out = static_cast<T*>(p.out) + ((int64_t)i * p.Hq + hq) * D + lane * V;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int k = 0; k < V; ++k) out[k] = Num<T>::from(o[k] * inv);
-  if (lane == 0) {
-    if (p.lse) p.lse[(int64_t)i * p.Hq + hq] = l > 0.f ? m * kLn2 + logf(l) : -INFINITY;
-    if (flags) flag_status(p.status, flags);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (p.tile_units > 0) {
+    e = launch_cross_tiles(p, s);
+    if (e != cudaSuccess) return e;
   }
+  ProfScope ps("cross_combine", s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.few_units + 8 * p.tile_units));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cross_join_kernel<T, D>, p);
 }
 
 }  // namespace
 
-size_t cross_workspace_bytes(const CrossParams& p) {
-  (void)p;
-  return 256;
+size_t cross_layout(CrossParams* p, char* base) {
+  const int sms = device_sms();
+  p->few = 16 / p->G;
+  p->tile_pos = 2 * (128 / p->G);
+  // no more units than the longest possible work has runs of the least length
+  const int64_t keys = (int64_t)p->MB * p->BS;
+  const int64_t seqs = p->T < p->B ? p->T : p->B;
+  const int64_t steps = seqs * p->Hkv * ((keys + kStepKeys - 1) / kStepKeys);
+  const int64_t runs = (steps + kLeastFew - 1) / kLeastFew;
+  int64_t ctas = (runs + kWarps - 1) / kWarps;
+  ctas = ctas < 1 ? 1 : ctas > sms * kCtasPerSm ? sms * kCtasPerSm : ctas;
+  p->few_units = (int)ctas * kWarps;
+  p->few_rows = (p->max_q < p->few ? p->max_q : p->few) * p->G;
+  p->tile_units = 0;
+  if (p->max_q > p->few) {
+    const int64_t tiles = (p->T + p->tile_pos - 1) / p->tile_pos + seqs;
+    const int64_t blocks = tiles * p->Hkv * ((keys + kTileKeys - 1) / kTileKeys);
+    const int64_t t = (blocks + kLeastTile - 1) / kLeastTile;
+    p->tile_units = (int)(t < 1 ? 1 : t > sms ? sms : t);
+  }
+  p->box_keys = 0;
+  if (p->BS % 8 == 0 && p->NB * p->BS <= INT32_MAX) {
+    p->box_keys = 8;
+    while (p->box_keys < 128 && p->BS % (2 * p->box_keys) == 0) p->box_keys *= 2;
+  }
+  size_t off = 0;
+  const auto take = [&](size_t bytes) {
+    char* at = base ? base + off : nullptr;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t fu = (size_t)p->few_units, tu = (size_t)p->tile_units;
+  p->few_rec = reinterpret_cast<int4*>(take(fu * 32));
+  p->few_o = reinterpret_cast<float*>(take(2 * fu * p->few_rows * p->D * 4));
+  p->few_m = reinterpret_cast<float*>(take(2 * fu * p->few_rows * 4));
+  p->few_l = reinterpret_cast<float*>(take(2 * fu * p->few_rows * 4));
+  p->tile_rec = reinterpret_cast<int4*>(take(tu * 32));
+  p->tile_o = reinterpret_cast<float*>(take(2 * tu * 256 * p->D * 4));
+  p->tile_m = reinterpret_cast<float*>(take(2 * tu * 256 * 4));
+  p->tile_l = reinterpret_cast<float*>(take(2 * tu * 256 * 4));
+  return off;
 }
 
-cudaError_t launch_cross(const CrossParams& p, void* workspace, cudaStream_t s) {
-  (void)workspace;
-  ProfScope ps("cross_decode", s);
-  const unsigned grid = (unsigned)(((int64_t)p.T * p.Hq * 32 + kThreads - 1) / kThreads);
-  if (p.bf16) {
-    if (p.D == 64)
-      cross_rows_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, s>>>(p);
-    else
-      cross_rows_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (p.D == 64)
-      cross_rows_kernel<__half, 64><<<grid, kThreads, 0, s>>>(p);
-    else
-      cross_rows_kernel<__half, 128><<<grid, kThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+cudaError_t launch_cross(const CrossParams& p, cudaStream_t s) {
+  if (p.bf16)
+    return p.D == 64 ? launch_typed<__nv_bfloat16, 64>(p, s) : launch_typed<__nv_bfloat16, 128>(p, s);
+  return p.D == 64 ? launch_typed<__half, 64>(p, s) : launch_typed<__half, 128>(p, s);
 }
 
 }  // namespace pkv

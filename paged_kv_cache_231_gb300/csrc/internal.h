@@ -258,6 +258,9 @@ bool sparse_tc_shape(int D, int block_size, int qhead, int page_size, int ppb,
 uint32_t testing_wait_tries();
 int testing_withhold_copy();
 
+// SM count of the current device (runtime.cpp)
+int device_sms();
+
 // profiler hooks (runtime.cpp)
 void prof_begin(const char* name, cudaStream_t s);
 void prof_end(const char* name, cudaStream_t s);

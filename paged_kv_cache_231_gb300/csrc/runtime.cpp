@@ -293,6 +293,9 @@ int log2i(int64_t x) {
 }
 
 }  // namespace
+
+int device_sms() { return num_sms_current(); }
+
 }  // namespace pkv
 
 using namespace pkv;

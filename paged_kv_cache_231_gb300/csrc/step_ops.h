@@ -68,8 +68,30 @@ struct CrossParams {
   int max_q;                 // longest sequence the call admits
   int bf16;
   float scale_log2;          // softmax scale * log2(e)
+  // plan (cross_dev.cuh)
+  int few;                   // query rows of a sequence that the kernel for few rows takes
+  int tile_pos;              // query positions of a tile of the kernel for many rows
+  int few_units;             // warps of the first, blocks of the second (0: not launched)
+  int tile_units;
+  int few_rows;              // rows of a piece of the first: at most 16
+  int box_keys;              // keys of a TMA box (0: rows are copied one by one)
+  uint32_t wait_tries;       // testing hook (pkv_testing_wait_limit), as in AttnParams
+  int withhold_copy;
+  // workspace: records, and pieces of unit u at slots 2u and 2u + 1
+  int4* few_rec;
+  float* few_o;              // [2 * few_units][few_rows][D]
+  float* few_m;              // [2 * few_units][few_rows], log2 units
+  float* few_l;
+  int4* tile_rec;
+  float* tile_o;             // [2 * tile_units][256][D]
+  float* tile_m;
+  float* tile_l;
 };
-size_t cross_workspace_bytes(const CrossParams& p);
-cudaError_t launch_cross(const CrossParams& p, void* workspace, cudaStream_t s);
+// fills the plan fields and the workspace pointers (from base, which may be NULL); returns
+// the workspace bytes
+size_t cross_layout(CrossParams* p, char* base);
+cudaError_t launch_cross(const CrossParams& p, cudaStream_t s);
+// kernel for many rows (cross_tiles.cu)
+cudaError_t launch_cross_tiles(const CrossParams& p, cudaStream_t s);
 
 }  // namespace pkv

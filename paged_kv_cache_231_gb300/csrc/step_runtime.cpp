@@ -68,6 +68,8 @@ int check_cross(const pkv_cross_attention_args* a, CrossParams* p) {
   p->status = a->device_status;
   const double scale = a->scale != 0.f ? (double)a->scale : 1.0 / std::sqrt((double)p->D);
   p->scale_log2 = (float)(scale * 1.4426950408889634);
+  p->wait_tries = testing_wait_tries();
+  p->withhold_copy = testing_withhold_copy();
   return PKV_OK;
 }
 
@@ -191,7 +193,7 @@ int pkv_cross_attention_workspace_size(const pkv_cross_attention_args* args, siz
   CrossParams p{};
   const int st = check_cross(args, &p);
   if (st != PKV_OK) return st;
-  *bytes = cross_workspace_bytes(p);
+  *bytes = cross_layout(&p, nullptr);
   return PKV_OK;
 }
 
@@ -201,9 +203,10 @@ int pkv_cross_attention(const pkv_cross_attention_args* args, void* workspace,
   const int st = check_cross(args, &p);
   if (st != PKV_OK) return st;
   if (args->num_tokens == 0) return PKV_OK;
-  if (!workspace || workspace_bytes < cross_workspace_bytes(p) || !aligned(workspace, 256))
+  if (!workspace || workspace_bytes < cross_layout(&p, static_cast<char*>(workspace)) ||
+      !aligned(workspace, 256))
     return PKV_ERR_WORKSPACE;
-  return status_of(launch_cross(p, workspace, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_cross(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
