@@ -448,7 +448,8 @@ size_t cross_layout(CrossParams* p, char* base) {
     const int64_t tiles = (p->T + p->tile_pos - 1) / p->tile_pos + seqs;
     const int64_t blocks = tiles * p->Hkv * ((keys + kTileKeys - 1) / kTileKeys);
     const int64_t t = (blocks + kLeastTile - 1) / kLeastTile;
-    p->tile_units = (int)(t < 1 ? 1 : t > sms ? sms : t);
+    const int64_t most = sms < kMaxTileUnits ? sms : kMaxTileUnits;
+    p->tile_units = (int)(t < 1 ? 1 : t > most ? most : t);
   }
   p->box_keys = 0;
   if (p->BS % 8 == 0 && p->NB * p->BS <= INT32_MAX) {

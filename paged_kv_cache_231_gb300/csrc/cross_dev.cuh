@@ -3,11 +3,12 @@
 // Plan. A "range" is one (sequence, kv head) with all its query rows (few rows: at most 16)
 // or one tile of up to 256 query rows of it (many rows); its length is counted in "steps"
 // of 16 keys (few rows) or 128 keys (many rows). The ranges of a call are laid end to end and
-// cut into equal runs of W steps, one for each unit of a persistent grid (a warp, or a block):
-// every unit reads the same amount whatever the lengths are. A range that lies inside one run
-// is finished there; of the others each unit keeps an unnormalised (o, m, l) piece in fp32,
-// at most two (where its run begins and where it ends), and the join kernel merges the pieces
-// in order. The unit in whose run such a range begins writes the record that the join reads.
+// cut into runs of equally many steps, one for each unit of a persistent grid (a warp, or a
+// block): every unit does the same amount whatever the lengths are. A range that lies inside
+// one run is finished there; of the others each unit keeps an unnormalised (o, m, l) piece in
+// fp32, at most two (where its run begins and where it ends), and the join kernel merges the
+// pieces in order. The unit in whose run such a range begins writes the record that the join
+// reads. Tiles that are many are dealt out whole first (cross_tiles.cu); the rest is cut.
 // Lengths live on the device, so every block makes the plan for itself from cu and klen.
 #pragma once
 
@@ -26,6 +27,7 @@ constexpr int kStepKeys = 16;      // keys of a step, few rows
 constexpr int kTileKeys = 128;     // keys of a step, many rows
 constexpr int kEntries = 1024;     // prefix entries of a plan
 constexpr int kMaxPieces = 128;    // pieces of a range (bounds the join)
+constexpr int kMaxTileUnits = 256; // blocks of the kernel for many rows
 
 template <typename T>
 struct Num;

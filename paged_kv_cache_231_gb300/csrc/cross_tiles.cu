@@ -8,13 +8,17 @@
 //                   scores, raises its running maximum only when they exceed it by 2^8 (then O
 //                   and l are rescaled), writes the weights, rounded once to T, over the scores
 //                   in TMEM, and at the end writes its output row, or its piece.
-//   warp 8          one thread issues every tcgen05.mma, in the order
-//                   PV_0(j) S_0(j+1) PV_1(j) S_1(j+1): products of one issuing thread run in
-//                   order, so S may overwrite the weights that the PV before it reads, and a
-//                   full S tells that the O of that half is complete.
+//   warps 8, 10     one elected lane each issues the tcgen05.mma of half 0, 1 in the order
+//                   S(0) PV(0) S(1) PV(1) ...: products of one issuing thread run in order, so S
+//                   may overwrite the weights that the PV before it reads, and a full S tells
+//                   that the O of that half is complete and the K and V tiles so far are read.
+//                   The whole warp runs the loop and a lane is elected for the instructions: from
+//                   a lane that runs alone a tcgen05.mma took 85 to 110 cycles, so 56 to 71.
 //   warp 9          loads by TMA into 128-byte-swizzled shared memory: Q of the halves, and one
 //                   ring of K and V tiles in the order of their use (K0 V0 K1 V1 ...). A box is
-//                   up to 128 keys of one cache block. Value rows past the sequence's keys or in
+//                   up to 128 keys of one cache block; a tile lies in groups of 8 keys, the
+//                   64-column halves of a group one after the other, so one copy brings whole
+//                   rows. Value rows past the sequence's keys or in
 //                   unmapped blocks are zero-filled (a weight of zero times what stands there
 //                   must be zero); block sizes that are no multiple of 8 go row by row.
 // TMEM columns: S_0 0..127 (weights over 0..63), S_1 128..255, O_0 256.., O_1 384...
@@ -29,42 +33,57 @@ namespace {
 
 using namespace cross;
 
-constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kLeast = 4;              // steps of a run, at least
 constexpr uint32_t kTries = 1u << 22;  // default bound of a wait (polls)
 constexpr float kRaise = 8.f;          // log2 of the largest weight under an old maximum
-// registers a thread: launch, softmax warpgroups, the third warpgroup. 256 * 208 + 128 * 88 =
-// 384 * 168: the two that grow take what the third gives back
+// registers a thread: launch, softmax warps, the other four; the first take what the last give
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + 4 * kOtherRegs) <= kThreads * kLaunchRegs,
+              "register split");
+
+// What a block does: `whole` tiles, the first at `first`, every further one `units` tiles on;
+// then `steps` steps from `at`.
+struct Run {
+  Cursor first, at;
+  uint32_t tmem;
+  int whole;
+  int64_t steps;
+};
+static_assert(sizeof(Run) <= 96, "run area");
 
 template <int D>
 struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr uint32_t kTile = 128u * D * 2;       // 128 rows of Q, K or V
-  static constexpr uint32_t kSub = 128u * 128;          // 64 columns of them
+  static constexpr uint32_t kSub = 128u * 128;          // Q: 64 columns
+  static constexpr uint32_t kGroup = 8u * D * 2;        // K, V: 8 keys, [D / 64][8][64]
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kBars = kRing + kStages * kTile;
-  static constexpr uint32_t kEnd = kBars + 256;
+  static constexpr uint32_t kSeen = kBars + 256;        // keys of the last 8 steps that take part
+  static constexpr uint32_t kRun = kSeen + 128;          // Run
+  static constexpr uint32_t kEnd = kRun + 96;
   static constexpr size_t kBytes = kEnd + 1024;
 };
 static_assert(Lay<128>::kBytes <= 232448, "shared memory over the limit");
-static_assert((kEntries + 16) * 8 <= Lay<64>::kStages * Lay<64>::kTile, "plan fits the ring");
+static_assert((2 * kEntries + kThreads + 48) * 8 <= Lay<64>::kStages * Lay<64>::kTile, "plan fits the ring");
 
 // mbarriers
 enum {
-  kFull = 0,     // + stage: K or V tile landed (32 lanes' copies + 1 with the TMA bytes)
-  kEmpty = 8,    // + stage: the products that read it completed
+  kFull = 0,     // + stage: K or V tile landed
+  kEmpty = 8,    // + stage: the products that read it completed (2: one for each half)
   kQFull = 16,   // + half
   kQEmpty = 18,  // + half: every S of the range completed
   kSFull = 20,   // + half: S in TMEM (and the O before it complete)
   kPFull = 22,   // + half: the 4 warps wrote their weights
   kOFull = 24,   // + half: the last PV of the range completed
-  kDrain = 26,   // products in flight when a wait gave up
-  kBarriers = 27
+  kDrain = 26,   // + half: products in flight when a wait gave up
+  kTurn = 28,    // + half: the other half issued its products
+  kBarriers = 30
 };
-constexpr uint32_t kTmemWord = 27 * 8, kAbortWord = 27 * 8 + 4;   // behind the barriers
+constexpr uint32_t kAbortWord = kBarriers * 8;   // behind the barriers
 static_assert(kAbortWord + 4 <= 256, "barrier area");
 
 struct Maps {
@@ -96,15 +115,10 @@ struct Wait {   // bounded waits that give up together
   }
 };
 
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-// arrive when every cp.async that this thread issued has landed
-__device__ __forceinline__ void arrive_copies(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar))
+__device__ __forceinline__ void arrive(uint64_t* bar, uint32_t count = 1) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(count)
                : "memory");
 }
-
 // D (+)= A B with A in TMEM
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -116,6 +130,71 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, u
       "}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// true in one lane of a converged warp, always the same one
+__device__ __forceinline__ bool elect() {
+  uint32_t yes;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(yes));
+  return yes != 0;
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// two floats in a register pair, and arithmetic on both at once (each rounded as alone)
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float low_of(uint64_t x) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+  return a;
+}
+__device__ __forceinline__ float high_of(uint64_t x) {
+  float a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+  return b;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -142,28 +221,196 @@ __device__ __forceinline__ Part part_of(const CrossParams& p, const Cursor& c, i
   return t;
 }
 
-// Walks the parts of a run; every role walks for itself.
+// n ranges on from the start of a range; the whole warp (32 sequences at a time)
+__device__ __forceinline__ void skip_ranges(const CrossParams& p, Cursor& c, int n) {
+  const int lane = threadIdx.x & 31;
+  c.s = 0;
+  c.r += n;
+  while (c.r >= c.q.ranges) {
+    int left = c.r - c.q.ranges, f = 0;
+    bool z = false;
+    const int b0 = c.b + 1;
+    Seq q{};
+    if (b0 + lane < p.B) q = read_seq<true>(p, b0 + lane, &f, &z);
+    int upto = q.ranges;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, upto > left);
+    const int at = past ? __ffs(past) - 1 : 31;
+    c.r = left - (__shfl_sync(0xffffffffu, upto, at) - __shfl_sync(0xffffffffu, q.ranges, at));
+    c.q.cu0 = __shfl_sync(0xffffffffu, q.cu0, at);
+    c.q.rows = __shfl_sync(0xffffffffu, q.rows, at);
+    c.q.keys = __shfl_sync(0xffffffffu, q.keys, at);
+    c.q.steps = __shfl_sync(0xffffffffu, q.steps, at);
+    c.q.ranges = __shfl_sync(0xffffffffu, q.ranges, at);
+    c.b = b0 + at;
+    if (c.b >= p.B) return;   // never: the tiles asked for exist
+  }
+}
+
+// Walks the parts of a run; every role walks for itself. f gets the part, its cursor and its
+// number among the cut parts (-1: a whole tile).
 template <typename F>
-__device__ __forceinline__ void each_part(const CrossParams& p, Cursor c, int64_t steps, F f) {
+__device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, F f) {
+  Cursor c = run.first;
+  for (int i = run.whole; i > 0; --i) {
+    if (!f(part_of(p, c, c.q.steps), c, -1)) return;
+    if (i > 1) skip_ranges(p, c, p.tile_units);
+  }
+  c = run.at;
+  int64_t steps = run.steps;
   for (int i = 0; steps > 0; ++i) {
     const Part t = part_of(p, c, steps);
     if (!f(t, c, i)) return;
     steps -= t.n;
-    if (steps > 0) next_range<true>(p, c);
+    if (steps > 0) skip_ranges(p, c, 1);
+  }
+}
+
+// The plan, block-wide: tiles 0 .. whole * units - 1 go to the blocks by turns (tile i to block
+// i % units), so that the blocks read the same keys at about the same time and the cache holds
+// them; of the others (between one and two for each block, if there are as many) each block
+// gets a run of steps that evens out what it had before.
+// mem: [kEntries + 1] steps and tiles before an entry each, [kThreads + 1] cuts, scratch.
+__device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
+  int64_t *steps_at = mem, *tiles_at = steps_at + kEntries + 1, *cut = tiles_at + kEntries + 1,
+          *scratch = cut + kThreads + 1;
+  const int tid = threadIdx.x, units = p.tile_units;
+  const int group = (p.B + kEntries - 1) / kEntries, entries = (p.B + group - 1) / group;
+  int f = 0;
+  bool z = false;
+  int64_t total = 0, tiles = 0;
+  for (int e0 = 0; e0 < entries; e0 += kThreads) {
+    const int e = e0 + tid;
+    int64_t s = 0, n = 0;
+    if (e < entries) {
+      const int b1 = min(p.B, (e + 1) * group);
+      for (int b = e * group; b < b1; ++b) {
+        const Seq q = read_seq<true>(p, b, &f, &z);
+        s += (int64_t)q.steps * q.ranges;
+        n += q.ranges;
+      }
+    }
+    int64_t all_s, all_n;
+    const int64_t upto_s = block_sum<kThreads>(s, &all_s, scratch);
+    const int64_t upto_n = block_sum<kThreads>(n, &all_n, scratch);
+    if (e < entries) {
+      steps_at[e] = total + upto_s - s;
+      tiles_at[e] = tiles + upto_n - n;
+    }
+    total += all_s;
+    tiles += all_n;
+  }
+  if (tid == 0) {
+    steps_at[entries] = total;
+    tiles_at[entries] = tiles;
+  }
+  __syncthreads();
+  const auto entry = [&](const int64_t* at, int64_t k) {   // the last with at[e] <= k
+    int lo = 0, hi = entries - 1, e = 0;
+    while (lo <= hi) {
+      const int mid = (lo + hi) >> 1;
+      if (at[mid] <= k) {
+        e = mid;
+        lo = mid + 1;
+      } else {
+        hi = mid - 1;
+      }
+    }
+    return e;
+  };
+  // cursor at tile k, or (by_step) at step k; *before: steps before it
+  const auto find = [&](int64_t k, bool by_step, int64_t* before) {
+    const int64_t* at = by_step ? steps_at : tiles_at;
+    const int e = entry(at, k);
+    int64_t left = k - at[e], s = steps_at[e];
+    Cursor c{};
+    for (c.b = e * group; c.b < p.B; ++c.b) {
+      c.q = read_seq<true>(p, c.b, &f, &z);
+      const int64_t n = by_step ? (int64_t)c.q.steps * c.q.ranges : c.q.ranges;
+      if (left < n) break;
+      left -= n;
+      s += (int64_t)c.q.steps * c.q.ranges;
+    }
+    const int64_t per = by_step ? max(c.q.steps, 1) : 1;
+    c.r = (int)(left / per);
+    c.s = (int)(left % per);
+    *before = s + (int64_t)c.r * c.q.steps + c.s;
+    return c;
+  };
+  const int64_t whole = max(tiles / units - 1, (int64_t)0);
+  int64_t x, from = 0;
+  if (whole > 0) find(whole * units, false, &from);
+  const int64_t rest = total - from, share = (total + units - 1) / units;
+  // what the whole tiles left of a block's share; of very many tiles the last 64 tell
+  int64_t weight = 0;
+  if (tid < units) {
+    const int64_t i0 = max(whole - 64, (int64_t)0);
+    float had = (float)i0 * (float)total / (float)max(tiles, (int64_t)1);
+    for (int64_t i = i0; i < whole; ++i) {   // a tile's steps, or the mean of its entry's
+      const int e = entry(tiles_at, tid + i * units);
+      had += (float)(steps_at[e + 1] - steps_at[e]) / (float)(tiles_at[e + 1] - tiles_at[e]);
+    }
+    weight = whole > 0 ? max(share - (int64_t)had, (int64_t)1)
+                       : tid < max((rest + kLeast - 1) / kLeast, (int64_t)1);
+  }
+  int64_t all;
+  const int64_t upto = block_sum<kThreads>(weight, &all, scratch);
+  if (tid == 0) cut[0] = from;
+  if (tid < units) cut[tid + 1] = from + rest * upto / max(all, (int64_t)1);
+  __syncthreads();
+  const int u = blockIdx.x;
+  const int64_t c0 = cut[u], c1 = cut[u + 1];
+  if (tid == 0) {
+    run->whole = (int)whole;
+    run->steps = c1 - c0;
+  }
+  if (tid == 32 && whole > 0) run->first = find(u, false, &x);
+  if (tid == 64 && c1 > c0) run->at = find(c0, true, &x);
+  if (tid == 96) {   // the record: the range that begins in the run and ends behind it
+    int4 a = make_int4(0, 0, 0, 0), b = make_int4(0, 0, 0, 0);
+    if (c1 > c0) {
+      const Cursor c = find(c1 - 1, true, &x);
+      const int64_t start = c1 - 1 - c.s, end = start + c.q.steps;
+      if (start >= c0 && end > c1) {
+        int v = u;
+        while (v + 1 < units && cut[v + 1] < end) ++v;
+        const Part t = part_of(p, c, 1);
+        a = make_int4(v - u + 1, start == c0 ? 0 : 1, t.row0, t.h);
+        b.x = t.pos;
+      }
+    }
+    p.tile_rec[2 * u] = a;
+    p.tile_rec[2 * u + 1] = b;
   }
 }
 
 // ---------------------------------------------------------------------------- loader
+// R keys from group of 8 `group` of the pool on, kv head h
+__device__ __forceinline__ void load_box(void* dst, const void* map, int group, int h,
+                                         uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %2, %2, %3, %4}], [%5];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(h), "r"(smem_u32(bar))
+      : "memory");
+}
+
 template <typename T, int D>
 __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char* sm,
-                          const Cursor& c0, int64_t steps, const Wait& wait, int& flags) {
+                          const Run& run, const Wait& wait) {
   using L = Lay<D>;
   uint64_t* bars = wait.bars;
   const int lane = threadIdx.x & 31, R = p.box_keys;
+  int flags = 0;
   uint32_t use = 0;   // ring tiles issued
+  uint32_t* seen_words = reinterpret_cast<uint32_t*>(sm + L::kSeen);
   uint32_t q_use[2] = {0, 0};
   const bool withhold = p.withhold_copy != 0;   // testing hook: the first K tile never comes
-  each_part(p, c0, steps, [&](const Part& t, const Cursor& c, int) {
+  each_part(p, run, [&](const Part& t, const Cursor& c, int) {
     const int PT = p.tile_pos / 2;
     for (int h = 0; h < t.halves; ++h) {
       if (q_use[h] > 0 &&
@@ -178,42 +425,63 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
                           t.row0 + h * PT, bars + kQFull + h);
       }
     }
+    // R consecutive keys of a block to a lane (none when rows are copied one by one); the block
+    // of the step ahead is on its way while a step is loaded
+    const auto column = [&](int key) { return p.bs_shift >= 0 ? key >> p.bs_shift : key / p.BS; };
+    const auto lookup = [&](int key) {
+      int blk;
+      asm volatile("ld.global.nc.b32 %0, [%1];\n"
+                   : "=r"(blk)
+                   : "l"(p.table + (int64_t)t.b * p.MB + column(min(key, c.q.keys - 1))));
+      return blk;
+    };
+    int ahead = lookup(c.s * kTileKeys + lane * R);
     for (int j = c.s; j < c.s + t.n; ++j) {
-      // R consecutive keys of a block to a lane (none when rows are copied one by one)
-      const int key0 = j * kTileKeys + lane * max(R, 1);
-      int row = 0;
-      bool mapped = false;
-      if (R > 0 && lane * R < kTileKeys && key0 < c.q.keys) {
-        const int col = p.bs_shift >= 0 ? key0 >> p.bs_shift : key0 / p.BS;
-        const int blk = __ldg(p.table + (int64_t)t.b * p.MB + col);
-        mapped = blk >= 0 && blk < p.NB;
-        if (mapped)
-          row = blk * p.BS + (key0 - col * p.BS);
-        else
-          flags |= PKV_DEV_BAD_BLOCK;
-      }
+      const int key0 = j * kTileKeys + lane * R;
+      const bool there = R > 0 && lane * R < kTileKeys && key0 < c.q.keys;
+      const bool mapped = there && ahead >= 0 && ahead < p.NB;
+      if (there && !mapped) flags |= PKV_DEV_BAD_BLOCK;
+      uint32_t seen = 0;   // lane x < 4: word x of the step's keys that take part
+      const int row = mapped ? ahead * p.BS + (key0 - column(key0) * p.BS) : 0;
       const bool whole = mapped && key0 + R <= c.q.keys;
+      ahead = lookup(key0 + kTileKeys);
+      // which keys take part: key 4 i + x of the step is bit i of word x. An entry of the 8 is
+      // written again when the K tile 8 steps on has room, so when a score tile 4 steps on was
+      // full and every softmax warp was done with the steps before it.
+      {
+        const int k0 = j * kTileKeys + 4 * lane;   // 4 keys of one block, if boxes are used
+        uint32_t words[4];
+        if (R > 0) {
+          const bool in = __shfl_sync(0xffffffffu, mapped ? 1 : 0, 4 * lane / R) != 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) words[x] = __ballot_sync(0xffffffffu, in && k0 + x < c.q.keys);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int blk = lookup(k0 + x);
+            words[x] = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.NB && k0 + x < c.q.keys);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (lane == x) seen = words[x];
+      }
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++use) {
         const uint32_t st = use % L::kStages, round = use / L::kStages;
         const bool ok = round == 0 || wait(kEmpty + (int)st, (round - 1) & 1u);
         if (!__all_sync(0xffffffffu, ok)) return false;
+        if (kv == 0 && lane < 4) seen_words[(use / 2 % 8) * 4 + lane] = seen;
         unsigned char* dst = sm + L::kRing + st * L::kTile;
         uint64_t* full = bars + kFull + st;
         // keys behind the last one may stay what they are: their scores are masked
         const bool box = kv == 0 ? mapped : whole;
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
-        if (lane == 0) tc::mbar_arrive_expect_tx(full, boxes * R * (D * 2));
-        __syncwarp();
-        if (box && !(withhold && use == 0)) {
-#pragma unroll
-          for (int x = 0; x < D / 64; ++x)
-            tc::tma_load_3d(dst + x * L::kSub + lane * R * 128, kv == 0 ? &maps.k : &maps.v, x * 64,
-                            t.h, row, full);
-        }
+        uint32_t boxes = __ballot_sync(0xffffffffu, box);
         const T* src = static_cast<const T*>(kv == 0 ? p.kc : p.vc);
+        bool rows = false;   // rows copied one by one
         if (R == 0) {
-          for (int r = 0; r < kTileKeys; ++r) {   // 2 or 4 rows would fit an instruction: rare path
+          rows = true;
+          for (int r = 0; r < kTileKeys; ++r) {
             const int key = j * kTileKeys + r;
             int64_t at = -1;
             if (key < c.q.keys) {
@@ -225,11 +493,12 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
                 flags |= PKV_DEV_BAD_BLOCK;
             }
             if (lane < D / 8)
-              cp_async_16(dst + (lane >> 3) * L::kSub + tc::sw128(r, lane & 7),
+              cp_async_16(dst + (r >> 3) * L::kGroup + (lane >> 3) * 1024 + tc::sw128(r & 7, lane & 7),
                           at >= 0 ? src + at + lane * 8 : src, at >= 0 ? 16 : 0);
           }
         } else if (kv == 1) {
           uint32_t rest = __ballot_sync(0xffffffffu, lane * R < kTileKeys && !whole);
+          rows = rest != 0;
           for (; rest; rest &= rest - 1) {
             const int i = __ffs(rest) - 1;
             const int row_i = __shfl_sync(0xffffffffu, row, i);
@@ -238,16 +507,40 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
               const int r = x / (D / 8), ch = x % (D / 8);
               const bool live = mapped_i && j * kTileKeys + i * R + r < c.q.keys;
               const int64_t at = live ? ((int64_t)(row_i + r) * p.Hkv + t.h) * D + ch * 8 : 0;
-              cp_async_16(dst + (ch >> 3) * L::kSub + tc::sw128(i * R + r, ch & 7), src + at,
-                          live ? 16 : 0);
+              const int k = i * R + r;
+              cp_async_16(dst + (k >> 3) * L::kGroup + (ch >> 3) * 1024 + tc::sw128(k & 7, ch & 7),
+                          src + at, live ? 16 : 0);
             }
           }
         }
-        arrive_copies(full);
+        if (rows) {   // these were written by threads: hand them to the tensor core's proxy
+          cp_async_commit();
+          cp_async_wait<0>();
+          tc::fence_async_shared();
+          __syncwarp();
+        }
+        if (elect()) tc::mbar_arrive_expect_tx(full, (uint32_t)__popc(boxes) * R * (D * 2));
+        __syncwarp();
+        if (withhold && use == 0) boxes = 0;
+        for (int i0 = 0; boxes >> i0; i0 += 4) {   // the whole warp: see the products
+          int at[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, row / 8, (i0 + i) & 31);
+          if (elect()) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((boxes >> (i0 + i)) & 1u)
+                load_box(dst + (i0 + i) * (R / 8) * L::kGroup, kv == 0 ? &maps.k : &maps.v, at[i],
+                         t.h, full);
+          }
+          __syncwarp();
+          if (i0 == 28) break;
+        }
       }
     }
     return true;
   });
+  if (flags) flag_status(p.status, flags);
   if (*wait.abort) {   // let what was issued land before the block ends
     const uint32_t n = use < (uint32_t)L::kStages ? use : (uint32_t)L::kStages;
     for (uint32_t k = 0; k < n; ++k) {
@@ -261,112 +554,104 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
 
 // ---------------------------------------------------------------------------- products
 template <typename T, int D>
-__device__ void mma_role(const CrossParams& p, unsigned char* sm, uint32_t tmem,
-                         const Cursor& c0, int64_t steps, const Wait& wait) {
+__device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, const Run& run,
+                         const Wait& wait) {
   using L = Lay<D>;
   uint64_t* bars = wait.bars;
   constexpr uint32_t fmt = Num<T>::kBf16 ? (1u << 7) | (1u << 10) : 0u;   // types of A and B
   constexpr uint32_t id_s = tc::idesc_f16(128, 128, false, false) | fmt;
   constexpr uint32_t id_o = tc::idesc_f16(128, D, false, true) | fmt;
-  const uint32_t q_at = smem_u32(sm + L::kQ), ring = smem_u32(sm + L::kRing);
-  uint32_t use = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
-  const auto scores = [&](int h, uint32_t st) {
-    const uint32_t qa = q_at + h * L::kTile, ka = ring + st * L::kTile;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const uint32_t off = (uint32_t)(ks >> 2) * L::kSub + (uint32_t)(ks & 3) * 32u;
-      tc::mma_f16(tmem + h * 128, tc::smem_desc(qa + off, 16, 1024),
-                  tc::smem_desc(ka + off, 16, 1024), id_s, ks > 0 ? 1u : 0u);
-    }
-    tc::commit(bars + kSFull + h);
-  };
-  const auto products = [&](int h, uint32_t st, bool first) {
-    const uint32_t va = ring + st * L::kTile;
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-      mma_tmem_a(tmem + 256 + h * 128, tmem + h * 128 + (uint32_t)ks * 8u,
-                 tc::smem_desc(va + (uint32_t)ks * 2048u, L::kSub, 1024), id_o,
-                 first && ks == 0 ? 0u : 1u);
+  const uint32_t q_at = smem_u32(sm + L::kQ) + half * L::kTile, ring = smem_u32(sm + L::kRing);
+  const uint32_t s_at = run.tmem + half * 128, o_at = run.tmem + 256 + half * 128;
+  uint32_t use = 0, q_use = 0, p_use = 0, turn = 0;
+  const auto ready = [&](int bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
   };
   const auto full = [&](uint32_t u) {
-    if (!wait(kFull + (int)(u % L::kStages), (u / L::kStages) & 1u)) return false;
-    tc::fence_async_shared();   // rows written by cp.async
-    return true;
+    return ready(kFull + (int)(u % L::kStages), (u / L::kStages) & 1u);
   };
-  each_part(p, c0, steps, [&](const Part& t, const Cursor&, int) {
-    if (!full(use)) return false;                        // K of the first step
-    for (int h = 0; h < t.halves; ++h) {
-      if (!wait(kQFull + h, q_use[h]++ & 1u)) return false;
+  // The halves issue by turns, half 0 first: without it the tensor core shares itself out
+  // between both, they end together, and then both softmaxes run while it idles.
+  const auto my_turn = [&](int halves) {
+    if (halves == 1) return true;
+    const uint32_t n = turn++;
+    if (half == 0) return n == 0 || ready(kTurn, (n - 1) & 1u);
+    return ready(kTurn + 1, n & 1u);
+  };
+  each_part(p, run, [&](const Part& t, const Cursor&, int) {
+    if (half >= t.halves) {
+      use += 2 * t.n;
+      return true;
+    }
+    // round j: PV of step j - 1 (V is tile use - 1), S of step j (K is tile use)
+    for (int j = 0; j <= t.n; ++j, use += 2) {
+      const bool pv = j > 0, s = j < t.n;
+      if (j == 0 && !ready(kQFull + half, q_use++ & 1u)) return false;
+      if (pv && !full(use - 1)) return false;
+      if (s && !full(use)) return false;
+      if (pv && !ready(kPFull + half, p_use++ & 1u)) return false;
+      if (!my_turn(t.halves)) return false;
       tc::fence_after_sync();
-      scores(h, use % L::kStages);
-      if (t.n == 1) tc::commit(bars + kQEmpty + h);
-    }
-    tc::commit(bars + kEmpty + use % L::kStages);
-    for (int j = 0; j < t.n; ++j) {
-      const uint32_t v = use + 1, k = use + 2;           // V of step j, K of step j + 1
-      const bool more = j + 1 < t.n;
-      for (int h = 0; h < t.halves; ++h) {
-        if (!wait(kPFull + h, p_use[h]++ & 1u)) return false;
-        if (h == 0 && !full(v)) return false;
-        tc::fence_after_sync();
-        products(h, v % L::kStages, j == 0);
-        if (h == t.halves - 1) tc::commit(bars + kEmpty + v % L::kStages);
-        if (!more) {
-          tc::commit(bars + kOFull + h);
-          continue;
+      const uint32_t va = ring + ((use - 1) % L::kStages) * L::kTile;
+      const uint32_t ka = ring + (use % L::kStages) * L::kTile;
+      if (elect()) {
+        if (pv) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_tmem_a(o_at, s_at + (uint32_t)ks * 8u,
+                       tc::smem_desc(va + (uint32_t)ks * 2 * L::kGroup, 1024, L::kGroup), id_o,
+                       j == 1 && ks == 0 ? 0u : 1u);
         }
-        if (h == 0 && !full(k)) return false;
-        scores(h, k % L::kStages);
-        if (j + 2 == t.n) tc::commit(bars + kQEmpty + h);
-        if (h == t.halves - 1) tc::commit(bars + kEmpty + k % L::kStages);
+        if (s) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t x = (uint32_t)(ks & 3) * 32u, sub = (uint32_t)(ks >> 2);
+            tc::mma_f16(s_at, tc::smem_desc(q_at + sub * L::kSub + x, 16, 1024),
+                        tc::smem_desc(ka + sub * 1024u + x, 16, L::kGroup), id_s, ks > 0 ? 1u : 0u);
+          }
+          tc::commit(bars + kSFull + half);
+          if (j + 1 == t.n) tc::commit(bars + kQEmpty + half);
+        } else {
+          tc::commit(bars + kOFull + half);
+        }
+        if (t.halves == 2) arrive(bars + kTurn + 1 - half);
       }
-      use += 2;
+      __syncwarp();
     }
+    use -= 2;
     return true;
   });
   if (*wait.abort) {
-    tc::commit(bars + kDrain);
-    tc::mbar_wait(bars + kDrain, 0, wait.tries);
+    if (elect()) tc::commit(bars + kDrain + half);
+    __syncwarp();
+    tc::mbar_wait(bars + kDrain + half, 0, wait.tries);
   }
 }
 
 // ---------------------------------------------------------------------------- softmax
 template <typename T, int D>
-__device__ void softmax_role(const CrossParams& p, uint32_t tmem, int half, int64_t unit,
-                             const Cursor& c0, int64_t steps, const Wait& wait) {
+__device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run& run,
+                             const Wait& wait) {
+  using L = Lay<D>;
   uint64_t* bars = wait.bars;
-  const int r = threadIdx.x & 127, lane = r & 31;
-  const uint32_t lane_at = tmem + ((uint32_t)(r & ~31) << 16);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = warp >> 2, r = threadIdx.x & 127;
+  const uint32_t lane_at = run.tmem + ((uint32_t)(r & ~31) << 16);
   const uint32_t s_at = lane_at + half * 128, o_at = lane_at + 256 + half * 128;
-  const float sl2 = p.scale_log2;
-  const bool up = sl2 >= 0.f;   // a negative scale turns the maximum into a minimum
-  const float hide = up ? -INFINITY : INFINITY;
-  uint32_t s_use = 0, o_use = 0;
-  each_part(p, c0, steps, [&](const Part& t, const Cursor& c, int index) {
-    if (half >= t.halves) return true;
-    const int pos = half * (p.tile_pos / 2) + r / p.G;
-    const bool mine = r < (p.tile_pos / 2) * p.G && pos < t.pos;
-    // lane covers keys [128 j + 4 lane, + 4): one block when its size is a multiple of 4
-    const auto lookup = [&](int key) -> bool {
-      if (key >= c.q.keys) return false;
-      const int col = p.bs_shift >= 0 ? key >> p.bs_shift : key / p.BS;
-      const int blk = __ldg(p.table + (int64_t)t.b * p.MB + col);
-      return blk >= 0 && blk < p.NB;
-    };
-    bool page = lookup(c.s * kTileKeys + 4 * lane);
+  const float sl2 = fabsf(p.scale_log2);   // a negative scale turns the scores around
+  const uint64_t scale2 = pair_of(sl2, sl2);
+  uint32_t s_use = 0, o_use = 0, use = 0;
+  // the products that read ring tile u for this half (or for both, if it is alone) are done
+  const auto release = [&](uint32_t u, int halves) {
+    arrive(bars + kEmpty + u % L::kStages, halves == 2 ? 1 : 2);
+  };
+  each_part(p, run, [&](const Part& t, const Cursor&, int index) {
+    if (half >= t.halves) {
+      use += 2 * t.n;
+      return true;
+    }
     float m = -INFINITY, l = 0.f;
-    for (int j = c.s; j < c.s + t.n; ++j) {
-      const int key0 = j * kTileKeys + 4 * lane;
-      uint32_t words[4];   // key 4 i + x of the step is bit i of words[x]
-      if (p.box_keys > 0) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          words[x] = __ballot_sync(0xffffffffu, page && key0 + x < c.q.keys);
-        if (j + 1 < c.s + t.n) page = lookup(key0 + kTileKeys);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) words[x] = __ballot_sync(0xffffffffu, lookup(key0 + x));
-      }
+    for (int j = 0; j < t.n; ++j, use += 2) {
       // the loads and stores of TMEM below are the whole warp's
       if (!__all_sync(0xffffffffu, wait(kSFull + half, s_use & 1u))) return false;
       ++s_use;
@@ -376,61 +661,71 @@ __device__ void softmax_role(const CrossParams& p, uint32_t tmem, int half, int6
         float (*v32)[32] = reinterpret_cast<float (*)[32]>(v);
 #pragma unroll
         for (int x = 0; x < 4; ++x) tc::tmem_ld32(s_at + x * 32, v32[x]);
-        tc::tmem_wait_ld();
       }
-      if ((words[0] & words[1] & words[2] & words[3]) != 0xffffffffu) {
-#pragma unroll
-        for (int x = 0; x < 128; ++x)
-          v[x] = (words[x & 3] >> (x >> 2)) & 1u ? v[x] : hide;
+      const uint4 seen = *reinterpret_cast<const uint4*>(sm + L::kSeen + (use / 2 % 8) * 16);
+      tc::tmem_wait_ld();
+      if (r == 0) {
+        release(use, t.halves);                      // K of this step
+        if (j > 0) release(use - 1, t.halves);       // V of the one before
       }
-      float top;
-      if (up) {
-        float e[4];
+      if (p.scale_log2 < 0.f) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) e[x] = fmaxf(v[2 * x], v[2 * x + 1]);
-#pragma unroll
-        for (int x = 8; x < 128; x += 8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) e[y] = max3(e[y], v[x + 2 * y], v[x + 2 * y + 1]);
-        top = max3(e[0], e[1], fmaxf(e[2], e[3]));
-      } else {
-        top = v[0];
-#pragma unroll
-        for (int x = 1; x < 128; ++x) top = fminf(top, v[x]);
+        for (int x = 0; x < 128; ++x) v[x] = -v[x];
       }
-      top *= sl2;   // -inf when nothing of the step is seen
-      const bool first = m == -INFINITY;
-      const bool raise = first ? top != -INFINITY : top > m + kRaise;
-      const float alpha = raise && !first ? ex2(m - top) : 1.f;
-      if (raise) m = top;
-      const float base = m == -INFINITY ? 0.f : -m;
-      if (__any_sync(0xffffffffu, alpha != 1.f) && j > c.s) {   // O is complete: see the order
+      if ((seen.x & seen.y & seen.z & seen.w) != 0xffffffffu) {
+        constexpr float hide = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          float o[32];
-          tc::tmem_ld32(o_at + x * 32, o);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] *= alpha;
-          tc::tmem_st32(o_at + x * 32, o);
+        for (int x = 0; x < 32; ++x) {
+          v[4 * x] = (seen.x >> x) & 1u ? v[4 * x] : hide;
+          v[4 * x + 1] = (seen.y >> x) & 1u ? v[4 * x + 1] : hide;
+          v[4 * x + 2] = (seen.z >> x) & 1u ? v[4 * x + 2] : hide;
+          v[4 * x + 3] = (seen.w >> x) & 1u ? v[4 * x + 3] : hide;
         }
       }
-      float la[4] = {0.f, 0.f, 0.f, 0.f}, lb[4] = {0.f, 0.f, 0.f, 0.f};
+      float e[8];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float w[32];   // 64 weights as pairs
+      for (int x = 0; x < 8; ++x) e[x] = fmaxf(v[2 * x], v[2 * x + 1]);
 #pragma unroll
-        for (int x = 0; x < 64; x += 2) {
-          float e0, e1;
-          fma2(e0, e1, v[q * 64 + x], v[q * 64 + x + 1], sl2, base);
-          e0 = ex2(e0);
-          e1 = ex2(e1);
-          add2(la[(x >> 1) & 3], lb[(x >> 1) & 3], e0, e1);
+      for (int x = 16; x < 128; x += 16)
+#pragma unroll
+        for (int y = 0; y < 8; ++y) e[y] = max3(e[y], v[x + 2 * y], v[x + 2 * y + 1]);
+      float top = fmaxf(max3(e[0], e[1], max3(e[2], e[3], e[4])), max3(e[5], e[6], e[7]));
+      top *= sl2;   // -inf when nothing of the step is seen
+      if (__any_sync(0xffffffffu, m == -INFINITY ? top != -INFINITY : top > m + kRaise)) {
+        const bool first = m == -INFINITY;
+        const bool raise = first ? top != -INFINITY : top > m + kRaise;
+        const float alpha = raise && !first ? ex2(m - top) : 1.f;
+        if (raise) m = top;
+        l *= alpha;
+        if (j > 0) {   // O is complete: see the order of the products
+#pragma unroll 1
+          for (int x = 0; x < D / 16; ++x) {
+            float o[16];
+            tmem_ld16(o_at + x * 16, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] *= alpha;
+            tmem_st16(o_at + x * 16, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : -m;
+      const uint64_t base2 = pair_of(base, base);
+      uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float w[16];   // 32 weights as pairs
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const uint64_t e2 = fma_pair(pair_of(v[q * 32 + x], v[q * 32 + x + 1]), scale2, base2);
+          const float e0 = ex2(low_of(e2)), e1 = ex2(high_of(e2));
+          sum[(x >> 1) & 3] = add_pair(sum[(x >> 1) & 3], pair_of(e0, e1));
           w[x / 2] = __uint_as_float(Num<T>::pack(e0, e1));
         }
-        tc::tmem_st32(s_at + q * 32, w);
+        tmem_st16(s_at + q * 16, w);
       }
-      l = l * alpha + (((la[0] + lb[0]) + (la[1] + lb[1])) + ((la[2] + lb[2]) + (la[3] + lb[3])));
+      sum[0] = add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3]));
+      l += low_of(sum[0]) + high_of(sum[0]);
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
@@ -439,6 +734,9 @@ __device__ void softmax_role(const CrossParams& p, uint32_t tmem, int half, int6
     if (!__all_sync(0xffffffffu, wait(kOFull + half, o_use & 1u))) return false;
     ++o_use;
     tc::fence_after_sync();
+    if (r == 0) release(use - 1, t.halves);
+    const int pos = half * (p.tile_pos / 2) + r / p.G;
+    const bool mine = r < (p.tile_pos / 2) * p.G && pos < t.pos;
     if (t.whole) {
       const float inv = inverse_of(l);
       const int64_t row = (int64_t)(t.row0 + pos) * p.Hq + t.h * p.G + r % p.G;
@@ -459,7 +757,7 @@ __device__ void softmax_role(const CrossParams& p, uint32_t tmem, int half, int6
       }
       if (mine && p.lse) p.lse[row] = lse_of(m, l);
     } else {
-      const int64_t row = (2 * unit + (index == 0 ? 0 : 1)) * 256 + half * 128 + r;
+      const int64_t row = (2 * (int64_t)blockIdx.x + (index == 0 ? 0 : 1)) * 256 + half * 128 + r;
       float4* out = reinterpret_cast<float4*>(p.tile_o + row * D);
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
@@ -495,11 +793,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   wait.bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
   wait.abort = reinterpret_cast<volatile int*>(sm + L::kBars + kAbortWord);
   wait.tries = p.wait_tries ? p.wait_tries : kTries;
-  uint32_t* tmem_word = reinterpret_cast<uint32_t*>(sm + L::kBars + kTmemWord);
+  Run* run = reinterpret_cast<Run*>(sm + L::kRun);
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
-      tc::mbar_init(wait.bars + kFull + i, 33);
-      tc::mbar_init(wait.bars + kEmpty + i, 1);
+      tc::mbar_init(wait.bars + kFull + i, 1);
+      tc::mbar_init(wait.bars + kEmpty + i, 2);
     }
     for (int h = 0; h < 2; ++h) {
       tc::mbar_init(wait.bars + kQFull + h, 1);
@@ -507,55 +805,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(wait.bars + kSFull + h, 1);
       tc::mbar_init(wait.bars + kPFull + h, 4);
       tc::mbar_init(wait.bars + kOFull + h, 1);
+      tc::mbar_init(wait.bars + kDrain + h, 1);
+      tc::mbar_init(wait.bars + kTurn + h, 1);
     }
-    tc::mbar_init(wait.bars + kDrain, 1);
     tc::mbar_init_fence();
     *wait.abort = 0;
   }
-  if (warp == 9 && lane == 0 && p.box_keys > 0) {
+  if (warp == kSoftmaxWarps + 1 && lane == 0 && p.box_keys > 0) {
     tc::tma_prefetch_desc(&maps.q);
     tc::tma_prefetch_desc(&maps.k);
     tc::tma_prefetch_desc(&maps.v);
   }
   if (warp == 0) {
-    tc::tmem_alloc(tmem_word, 512);
+    tc::tmem_alloc(&run->tmem, 512);
     tc::tmem_relinquish();
   }
-  // the plan, in the ring's memory before the ring is used
-  int64_t* pref = reinterpret_cast<int64_t*>(sm + L::kRing);
-  int flags = 0;
-  const Plan pl = make_plan<true, kThreads>(p, p.tile_units, kLeast, pref, pref + kEntries, &flags);
-  flags = 0;   // the other kernel reports the sequences
-  const int64_t unit = blockIdx.x, g0 = unit * pl.W;
-  const int64_t steps = g0 < pl.total ? min(pl.total, g0 + pl.W) - g0 : 0;
-  if (tid == 0) write_record<true>(p, pl, pref, unit, p.tile_rec);
-  Cursor c{};
-  if (steps > 0) c = locate<true>(p, pl, pref, g0);
+  // in the ring's memory before the ring is used; the other kernel reports bad sequences
+  plan_tiles(p, reinterpret_cast<int64_t*>(sm + L::kRing), run);
   tc::fence_async_shared();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_word;
-  if (steps > 0) {
-    if (warp < 8) {
+  if (run->steps == 0 && tid < 256)   // a piece of nothing, if a join counts this block in
+    p.tile_l[(int64_t)blockIdx.x * 512 + tid] = 0.f;
+  if (run->whole > 0 || run->steps > 0) {
+    if (warp < kSoftmaxWarps) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
-      softmax_role<T, D>(p, tmem, warp >> 2, unit, c, steps, wait);
+      softmax_role<T, D>(p, sm, *run, wait);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-      if (tid == 256)
-        mma_role<T, D>(p, sm, tmem, c, steps, wait);
-      else if (warp == 9)
-        load_role<T, D>(p, maps, sm, c, steps, wait, flags);
+      if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 2)
+        mma_role<T, D>(p, sm, (warp - kSoftmaxWarps) / 2, *run, wait);
+      else if (warp == kSoftmaxWarps + 1)
+        load_role<T, D>(p, maps, sm, *run, wait);
     }
   }
-  if (tid == 0 && *wait.abort) flags |= PKV_DEV_TIMEOUT;
-  if (flags) flag_status(p.status, flags);
   cp_async_wait<0>();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   if (tid == 0 && *wait.abort) flag_status(p.status, PKV_DEV_TIMEOUT);
-  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+  if (warp == 0) tc::tmem_dealloc(run->tmem, 512);
   // the join behind this kernel waits for it alone: it must not end before the one in front
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
@@ -573,19 +863,32 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// rows of heads of D elements, boxes of 64 elements x b1 x b2 in the 128-byte swizzle
-bool encode(CUtensorMap* m, bool bf16, const void* base, int D, int64_t heads, int64_t rows,
-            int b1, int b2) {
+bool encode(CUtensorMap* m, bool bf16, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2};
-  const cuuint32_t unit[3] = {1, 1, 1};
-  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-            const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, unit,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Q [tokens][Hq][D]: boxes of 64 elements x G heads x 128 / G positions
+bool encode_queries(CUtensorMap* m, const CrossParams& p) {
+  const cuuint64_t D = p.D, dims[3] = {D, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+  const cuuint64_t strides[2] = {D * 2, p.Hq * D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)(p.tile_pos / 2)};
+  return encode(m, p.bf16, p.q, 3, dims, strides, box);
+}
+
+// a pool [rows][Hkv][D] as [Hkv][rows / 8][D / 64][8][64]: boxes of box_keys rows of one head
+bool encode_pool(CUtensorMap* m, const CrossParams& p, const void* base) {
+  const cuuint64_t D = p.D, row = p.Hkv * D * 2;
+  const cuuint64_t dims[5] = {64, 8, D / 64, (cuuint64_t)p.NB * p.BS / 8, (cuuint64_t)p.Hkv};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, D * 2};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)p.D / 64, (cuuint32_t)p.box_keys / 8, 1};
+  return encode(m, p.bf16, base, 5, dims, strides, box);
 }
 
 template <typename T, int D>
@@ -603,11 +906,9 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
     mark_configured(configured, dev);
   }
   Maps maps;
-  const int64_t rows = p.NB * p.BS;
-  if (!encode(&maps.q, p.bf16, p.q, D, p.Hq, p.T, p.G, p.tile_pos / 2)) return cudaErrorInvalidValue;
+  if (!encode_queries(&maps.q, p)) return cudaErrorInvalidValue;
   maps.k = maps.v = maps.q;   // not used without boxes
-  if (p.box_keys > 0 && (!encode(&maps.k, p.bf16, p.kc, D, p.Hkv, rows, 1, p.box_keys) ||
-                         !encode(&maps.v, p.bf16, p.vc, D, p.Hkv, rows, 1, p.box_keys)))
+  if (p.box_keys > 0 && (!encode_pool(&maps.k, p, p.kc) || !encode_pool(&maps.v, p, p.vc)))
     return cudaErrorInvalidValue;
   // may start as blocks of the kernel in front end: it reads inputs and writes other rows
   ProfScope ps("cross_tiles", s);
