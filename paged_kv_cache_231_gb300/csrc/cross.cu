@@ -314,9 +314,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
   if (a.x <= 0) return;
   const int tokens = __ldcg(rec + 1).x;
   const int rows_at = tile ? 256 : p.few_rows;       // rows of a stored piece
-  const float* po = tile ? p.tile_o : p.few_o;
-  const float* pm = tile ? p.tile_m : p.few_m;
-  const float* pl = tile ? p.tile_l : p.few_l;
+  const int64_t first = 2 * unit * rows_at;          // rows of the unit's first piece
+  const float* po = (tile ? p.tile_o : p.few_o) + first * D;
+  const float* pm = (tile ? p.tile_m : p.few_m) + first;
+  const float* pl = (tile ? p.tile_l : p.few_l) + first;
+  const unsigned over_g = 65536u / p.G + 1;          // x / G = x * over_g >> 16 for x < 256
   const int row0 = tile ? ((blockIdx.x - p.few_units) % 8) * 32 : 0;
   const int rows = tile ? 32 : tokens * p.G;
   int share = 1;                                     // warps of a row
@@ -324,37 +326,49 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
   const int PT = p.tile_pos / 2;
   for (int r0 = 0; r0 < rows; r0 += kJoinWarps / share) {
     const int r = row0 + r0 + warp / share, part = warp % share;
-    const int pos = tile ? (r >> 7) * PT + (r & 127) / p.G : r / p.G;
-    const bool live = (tile ? (r & 127) < PT * p.G : r < rows) && pos < tokens;
+    const int x128 = tile ? r & 127 : r, by_g = (int)(x128 * over_g >> 16);
+    const int pos = tile ? (r >> 7) * PT + by_g : by_g;
+    const bool live = (tile ? x128 < PT * p.G : r < rows) && pos < tokens;
+    // four pieces at a time, all loads at once; a piece of no weight may hold anything
     float acc[V], M = -INFINITY, L = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    if (live) {
-      for (int q = part; q < a.x; q += share)        // the row's maximum over this share
-      {
-        const int64_t at = (2 * (unit + q) + (q == 0 ? a.y : 0)) * rows_at + r;
-        if (__ldcg(pl + at) != 0.f) M = fmaxf(M, __ldcg(pm + at));
-      }
-      const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll 4
-      for (int q = part; q < a.x; q += share) {
-        const int64_t at = (2 * (unit + q) + (q == 0 ? a.y : 0)) * rows_at + r;
-        const float l = __ldcg(pl + at);
-        if (l == 0.f) continue;
-        const float w = ex2(__ldcg(pm + at) - base);
-        L += w * l;
-        const float* src = po + at * D + lane * V;
+    for (int q0 = part; live && q0 < a.x; q0 += 4 * share) {
+      float m[4], l[4], x[4][V];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int q = min(q0 + k * share, a.x - 1);
+        const int at = q * 2 * rows_at + (q == 0 ? a.y * rows_at : 0) + r;
+        m[k] = __ldcg(pm + at);
+        l[k] = q0 + k * share < a.x ? __ldcg(pl + at) : 0.f;
+        const float* src = po + (int64_t)at * D + lane * V;
         if constexpr (V == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
-          acc[0] += w * x.x;
-          acc[1] += w * x.y;
-          acc[2] += w * x.z;
-          acc[3] += w * x.w;
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+          x[k][0] = y.x;
+          x[k][1] = y.y;
+          x[k][2] = y.z;
+          x[k][3] = y.w;
         } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-          acc[0] += w * x.x;
-          acc[1] += w * x.y;
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+          x[k][0] = y.x;
+          x[k][1] = y.y;
         }
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = l[k] == 0.f ? top : fmaxf(top, m[k]);
+      const float base = top == -INFINITY ? 0.f : top, old = ex2(M - base);
+      M = top;
+      L *= old;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= old;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (l[k] == 0.f) continue;
+        const float w = ex2(m[k] - base);
+        L += w * l[k];
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += w * x[k][v];
       }
     }
     if (share > 1) {
@@ -385,7 +399,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
       __syncthreads();
     }
     if (live && part == 0) {
-      const int64_t row = (int64_t)(a.z + pos) * p.Hq + a.w * p.G + (tile ? r & 127 : r) % p.G;
+      const int64_t row = (int64_t)(a.z + pos) * p.Hq + a.w * p.G + x128 - by_g * p.G;
       const float inv = inverse_of(L);
       uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * V);
 #pragma unroll
