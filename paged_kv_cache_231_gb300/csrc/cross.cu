@@ -6,10 +6,10 @@
 // single tokens, drafts), the join of pieces and the launches. cross_tiles.cu: many rows.
 //
 // Few rows: bound by HBM, every key and value row is read once, 4 * D bytes a state and kv
-// head. Each warp of a persistent grid runs through its steps of 16 keys: rows go through the
-// warp's own ring in shared memory by 16-byte asynchronous copies (two steps ahead; the block
-// table a third), scores and products on mma.sync m16n8k16, whose 16 rows are the
-// sequence's query rows x the heads that share the kv head.
+// head. Each warp of a persistent grid runs through its steps of 4 KB of keys (16 or 32): rows
+// go through the warp's own ring in shared memory by 16-byte asynchronous copies (two steps
+// ahead; the block table a third), scores and products on mma.sync m16n8k16, whose 16 rows are
+// the sequence's query rows x the heads that share the kv head.
 #include "cross_dev.cuh"
 
 namespace pkv {
@@ -28,12 +28,14 @@ __device__ __forceinline__ int chunk_at(int r, int c) {   // 16-byte chunk c of 
   return (r * (D / 8) + (c ^ (r & 7))) * 8;
 }
 
-// Lane r < 16: element offset of key k0 + r of (sequence b, kv head h), -1 past the keys or
-// where the block is unmapped.
-__device__ __forceinline__ int64_t key_offset(const CrossParams& p, int b, int h, int k0,
-                                              int keys, int lane, int& flags) {
-  const int j = k0 + lane;
-  if (lane >= kStepKeys || j >= keys) return -1;
+// Lane r < few_keys(D): element offset of key r of step s of (sequence b, kv head h), -1 past
+// the keys or where the block is unmapped.
+template <int D>
+__device__ __forceinline__ int64_t key_offset(const CrossParams& p, int b, int h, int s, int keys,
+                                              int lane, int& flags) {
+  constexpr int K = few_keys(D);
+  const int j = s * K + lane;
+  if (lane >= K || j >= keys) return -1;
   const int col = p.bs_shift >= 0 ? j >> p.bs_shift : j / p.BS;
   const int blk = __ldg(p.table + (int64_t)b * p.MB + col);
   if (blk < 0 || blk >= p.NB) {
@@ -43,14 +45,14 @@ __device__ __forceinline__ int64_t key_offset(const CrossParams& p, int b, int h
   return (((int64_t)blk * p.BS + (j - col * p.BS)) * p.Hkv + h) * p.D;
 }
 
-// Copies the 16 key and value rows whose offsets lanes 0..15 hold; others are zeroed.
+// Copies the key and value rows whose offsets the lanes hold; others are zeroed.
 template <typename T, int D>
 __device__ __forceinline__ void copy_step(const CrossParams& p, int64_t off, T* sk, T* sv,
                                           int lane) {
   constexpr int CPR = D / 8, RPI = 32 / CPR;
   const int c = lane % CPR;
 #pragma unroll
-  for (int i = 0; i < kStepKeys / RPI; ++i) {
+  for (int i = 0; i < few_keys(D) / RPI; ++i) {
     const int r = i * RPI + lane / CPR;
     const long long o = __shfl_sync(0xffffffffu, (long long)off, r);
     const int64_t at = o >= 0 ? o + c * 8 : 0;
@@ -151,17 +153,18 @@ __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane) {
 
 template <int D>
 struct Ring {
-  static constexpr int kSteps = D == 64 ? 6 : 3;
-  static constexpr size_t kWarpBytes = (size_t)kSteps * kStepKeys * D * 2 * 2;
+  static constexpr int kSteps = 3;
+  static constexpr size_t kWarpBytes = (size_t)kSteps * few_keys(D) * D * 2 * 2;
   static constexpr size_t kBytes = kWarps * kWarpBytes;
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossParams p) {
-  constexpr int NS = Ring<D>::kSteps;
+  constexpr int NS = Ring<D>::kSteps, K = few_keys(D);
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_pref[kEntries];
   __shared__ int64_t s_scratch[kWarps + 2];
+  __shared__ uint32_t s_live[kWarps][NS];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int flags = 0;
@@ -173,26 +176,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossPa
   const int nst = g0 < pl.total ? (int)(min(pl.total, g0 + pl.W) - g0) : 0;
   if (nst > 0) {
     T* rk = reinterpret_cast<T*>(smem + warp * Ring<D>::kWarpBytes);
-    T* rv = rk + NS * kStepKeys * D;
+    T* rv = rk + NS * K * D;
     Cursor pc = locate<false>(p, pl, s_pref, g0);   // next step to copy
     Cursor cc = pc;                                  // step computed
-    uint32_t live[NS];                               // keys of the step that take part
-    int64_t ahead = key_offset(p, pc.b, pc.r, pc.s * kStepKeys, pc.q.keys, lane, flags);
+    uint32_t* live = s_live[warp];                   // keys of a step that take part
+    int64_t ahead = key_offset<D>(p, pc.b, pc.r, pc.s, pc.q.keys, lane, flags);
     const auto issue = [&](int k, int buf) {
       if (k < nst) {
-        copy_step<T, D>(p, ahead, rk + buf * kStepKeys * D, rv + buf * kStepKeys * D, lane);
+        copy_step<T, D>(p, ahead, rk + buf * K * D, rv + buf * K * D, lane);
         if (k + 1 < nst) {
           if (++pc.s == pc.q.steps) next_range<false>(p, pc);
         }
       }
       const uint32_t w = __ballot_sync(0xffffffffu, ahead >= 0);
+      if (lane == 0) live[buf] = w;
       if (k + 1 < nst)
-        ahead = key_offset(p, pc.b, pc.r, pc.s * kStepKeys, pc.q.keys, lane, flags);
+        ahead = key_offset<D>(p, pc.b, pc.r, pc.s, pc.q.keys, lane, flags);
       cp_async_commit();
-      return w;
     };
-#pragma unroll
-    for (int k = 0; k < NS - 1; ++k) live[k] = issue(k, k);
+    // one copy of the step's code: unrolled over the ring it did not fit the instruction cache
+#pragma unroll 1
+    for (int k = 0; k < NS - 1; ++k) issue(k, k);
     uint32_t qa[D / 16][4];
     load_queries<T, D>(p, cc, lane, qa);
     const int t4 = lane & 3;
@@ -201,92 +205,113 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossPa
     for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
     bool from_start = cc.s == 0, first = true;
 
-    for (int k0 = 0; k0 < nst; k0 += NS) {
+    int in = 0, out = NS - 1;   // ring slots: the step computed, the step copied
+#pragma unroll 1
+    for (int k = 0; k < nst; ++k) {
+      cp_async_wait<NS - 2>();
+      __syncwarp();
+      issue(k + NS - 1, out);
+      const T* sk = rk + in * K * D;
+      const T* sv = rv + in * K * D;
+      float s[K / 8][4];   // scores of rows lane / 4 and lane / 4 + 8
 #pragma unroll
-      for (int kk = 0; kk < NS; ++kk) {
-        const int k = k0 + kk;
-        if (k >= nst) break;
-        cp_async_wait<NS - 2>();
-        __syncwarp();
-        live[(kk + NS - 1) % NS] = issue(k + NS - 1, (kk + NS - 1) % NS);
-        const T* sk = rk + kk * kStepKeys * D;
-        const T* sv = rv + kk * kStepKeys * D;
-        float s[2][4];
+      for (int n = 0; n < K / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      {
+        const int key = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = 0.f;
-        {
-          const int key = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+        for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
+          for (int n = 0; n < K / 16; ++n) {
             uint32_t b0, b1, b2, b3;
-            ldsm_x4(b0, b1, b2, b3, sk + chunk_at<D>(key, 2 * ks + half));
-            Num<T>::mma(s[0], qa[ks], b0, b1);
-            Num<T>::mma(s[1], qa[ks], b2, b3);
+            ldsm_x4(b0, b1, b2, b3, sk + chunk_at<D>(n * 16 + key, 2 * ks + half));
+            Num<T>::mma(s[2 * n], qa[ks], b0, b1);
+            Num<T>::mma(s[2 * n + 1], qa[ks], b2, b3);
           }
+      }
+      const uint32_t w = live[in];
+      const bool all = w == (K == 32 ? 0xffffffffu : 0xffffu);
+#pragma unroll
+      for (int n = 0; n < K / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] *= p.scale_log2;
+          if (!all && !((w >> (n * 8 + 2 * t4 + (e & 1))) & 1u)) s[n][e] = -INFINITY;
         }
-        const uint32_t w = live[kk];
+      // online softmax; a row's maximum is raised when a score exceeds it by kRaise
+      float top[2];
+      bool raise = false;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+      for (int x = 0; x < 2; ++x) {
+        top[x] = fmaxf(s[0][2 * x], s[0][2 * x + 1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[n][e] = (w >> (n * 8 + 2 * t4 + (e & 1))) & 1u ? s[n][e] * p.scale_log2 : -INFINITY;
-        // online softmax of rows lane / 4 and lane / 4 + 8
+        for (int n = 1; n < K / 8; ++n) top[x] = fmaxf(top[x], fmaxf(s[n][2 * x], s[n][2 * x + 1]));
+        raise = raise || (m[x] == -INFINITY ? top[x] != -INFINITY : top[x] > m[x] + kRaise);
+      }
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float mx = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[x], mx);
-          const float base = mn == -INFINITY ? 0.f : mn;   // scores of -inf weigh nothing
-          const float alpha = ex2(m[x] - base);
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+          top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+          const float mn = fmaxf(m[x], top[x]);
+          const float alpha = ex2(m[x] - (mn == -INFINITY ? 0.f : mn));
           m[x] = mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              s[n][2 * x + e] = ex2(s[n][2 * x + e] - base);
-              sum += s[n][2 * x + e];
-            }
-          l[x] = l[x] * alpha + sum;
+          l[x] *= alpha;
 #pragma unroll
           for (int d = 0; d < D / 8; ++d) {
             o[d][2 * x] *= alpha;
             o[d][2 * x + 1] *= alpha;
           }
         }
-        // the weights, rounded once to T, times the value rows (l keeps them unrounded)
-        const uint32_t pa[4] = {Num<T>::pack(s[0][0], s[0][1]), Num<T>::pack(s[0][2], s[0][3]),
-                                Num<T>::pack(s[1][0], s[1][1]), Num<T>::pack(s[1][2], s[1][3])};
-        {
-          const int key = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float base = m[x] == -INFINITY ? 0.f : m[x];   // scores of -inf weigh nothing
+#pragma unroll
+        for (int n = 0; n < K / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[n][2 * x + e] = ex2(s[n][2 * x + e] - base);
+            l[x] += s[n][2 * x + e];
+          }
+      }
+      // the weights, rounded once to T, times the value rows (l keeps them unrounded)
+      {
+        const int key = (lane & 7) + (((lane >> 3) & 1) << 3), half = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < K / 16; ++n) {
+          const uint32_t pa[4] = {
+              Num<T>::pack(s[2 * n][0], s[2 * n][1]), Num<T>::pack(s[2 * n][2], s[2 * n][3]),
+              Num<T>::pack(s[2 * n + 1][0], s[2 * n + 1][1]),
+              Num<T>::pack(s[2 * n + 1][2], s[2 * n + 1][3])};
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(b0, b1, b2, b3, sv + chunk_at<D>(key, 2 * j + half));
+            ldsm_x4_t(b0, b1, b2, b3, sv + chunk_at<D>(n * 16 + key, 2 * j + half));
             Num<T>::mma(o[2 * j], pa, b0, b1);
             Num<T>::mma(o[2 * j + 1], pa, b2, b3);
           }
         }
-        const bool last = cc.s == cc.q.steps - 1;
-        if (last || k == nst - 1) {
-          flush<T, D>(p, cc, unit, from_start && last, first ? 0 : 1, m, l, o, lane);
-          m[0] = m[1] = -INFINITY;
-          l[0] = l[1] = 0.f;
+      }
+      const bool last = cc.s == cc.q.steps - 1;
+      if (last || k == nst - 1) {
+        flush<T, D>(p, cc, unit, from_start && last, first ? 0 : 1, m, l, o, lane);
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
-          first = false;
-          from_start = true;
-        }
-        if (k < nst - 1) {
-          if (last) {
-            next_range<false>(p, cc);
-            load_queries<T, D>(p, cc, lane, qa);
-          } else {
-            ++cc.s;
-          }
+        for (int d = 0; d < D / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+        first = false;
+        from_start = true;
+      }
+      if (k < nst - 1) {
+        if (last) {
+          next_range<false>(p, cc);
+          load_queries<T, D>(p, cc, lane, qa);
+        } else {
+          ++cc.s;
         }
       }
+      in = in + 1 == NS ? 0 : in + 1;
+      out = out + 1 == NS ? 0 : out + 1;
     }
     cp_async_wait<0>();
   }
@@ -451,7 +476,7 @@ size_t cross_layout(CrossParams* p, char* base) {
   // no more units than the longest possible work has runs of the least length
   const int64_t keys = (int64_t)p->MB * p->BS;
   const int64_t seqs = p->T < p->B ? p->T : p->B;
-  const int64_t steps = seqs * p->Hkv * ((keys + kStepKeys - 1) / kStepKeys);
+  const int64_t steps = seqs * p->Hkv * ((keys + few_keys(p->D) - 1) / few_keys(p->D));
   const int64_t runs = (steps + kLeastFew - 1) / kLeastFew;
   int64_t ctas = (runs + kWarps - 1) / kWarps;
   ctas = ctas < 1 ? 1 : ctas > sms * kCtasPerSm ? sms * kCtasPerSm : ctas;

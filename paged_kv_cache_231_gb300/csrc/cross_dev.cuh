@@ -2,7 +2,7 @@
 //
 // Plan. A "range" is one (sequence, kv head) with all its query rows (few rows: at most 16)
 // or one tile of up to 256 query rows of it (many rows); its length is counted in "steps"
-// of 16 keys (few rows) or 128 keys (many rows). The ranges of a call are laid end to end and
+// of 16 or 32 keys (few rows) or 128 keys (many rows). The ranges of a call are laid end to end and
 // cut into runs of equally many steps, one for each unit of a persistent grid (a warp, or a
 // block): every unit does the same amount whatever the lengths are. A range that lies inside
 // one run is finished there; of the others each unit keeps an unnormalised (o, m, l) piece in
@@ -23,9 +23,11 @@
 namespace pkv {
 namespace cross {
 
-constexpr int kStepKeys = 16;      // keys of a step, few rows
+// keys of a step, few rows: 4 KB of keys
+__host__ __device__ constexpr int few_keys(int head_size) { return 2048 / head_size; }
 constexpr int kTileKeys = 128;     // keys of a step, many rows
 constexpr int kEntries = 1024;     // prefix entries of a plan
+constexpr float kRaise = 8.f;      // log2 of the largest weight under an old maximum
 constexpr int kMaxPieces = 128;    // pieces of a range (bounds the join)
 constexpr int kMaxTileUnits = 256; // blocks of the kernel for many rows
 
@@ -89,7 +91,8 @@ __device__ __forceinline__ Seq read_seq(const CrossParams& p, int b, int* flags,
     s.steps = (s.keys + kTileKeys - 1) / kTileKeys;
     s.ranges = p.Hkv * ((s.rows + p.tile_pos - 1) / p.tile_pos);
   } else {
-    s.steps = (s.keys + kStepKeys - 1) / kStepKeys;
+    const int n = few_keys(p.D);
+    s.steps = (s.keys + n - 1) / n;
     s.ranges = p.Hkv;
   }
   return s;

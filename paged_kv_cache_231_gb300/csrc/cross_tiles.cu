@@ -37,7 +37,6 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kLeast = 4;              // steps of a run, at least
 constexpr uint32_t kTries = 1u << 22;  // default bound of a wait (polls)
-constexpr float kRaise = 8.f;          // log2 of the largest weight under an old maximum
 // registers a thread: launch, softmax warps, the other four; the first take what the last give
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + 4 * kOtherRegs) <= kThreads * kLaunchRegs,
