@@ -17,9 +17,8 @@ namespace {
 
 using namespace cross;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 2;
 constexpr int kLeastFew = 8;    // steps of a run, at least
 constexpr int kLeastTile = 4;
 
@@ -62,8 +61,8 @@ __device__ __forceinline__ void copy_step(const CrossParams& p, int64_t off, T* 
 }
 
 template <typename T, int D>
-__device__ __forceinline__ void load_queries(const CrossParams& p, const Cursor& c, int lane,
-                                             uint32_t (&qa)[D / 16][4]) {
+__device__ __forceinline__ void load_queries(const CrossParams& p, const Cursor& c, int h,
+                                             int lane, uint32_t (&qa)[D / 16][4]) {
   const int R = c.q.rows * p.G;
   const T* row[2];
   bool ok[2];
@@ -72,7 +71,7 @@ __device__ __forceinline__ void load_queries(const CrossParams& p, const Cursor&
     const int r = (lane >> 2) + 8 * x;
     ok[x] = r < R;
     const int pos = ok[x] ? r / p.G : 0, g = ok[x] ? r % p.G : 0;
-    row[x] = static_cast<const T*>(p.q) + ((int64_t)(c.q.cu0 + pos) * p.Hq + c.r * p.G + g) * D;
+    row[x] = static_cast<const T*>(p.q) + ((int64_t)(c.q.cu0 + pos) * p.Hq + h * p.G + g) * D;
   }
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
@@ -86,7 +85,7 @@ __device__ __forceinline__ void load_queries(const CrossParams& p, const Cursor&
 
 // End of the unit's part of a range: the output if the range lies in the run, else a piece.
 template <typename T, int D>
-__device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int64_t unit,
+__device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int h, int gw,
                                       bool whole, int slot, float (&m)[2], float (&l)[2],
                                       float (&o)[D / 8][4], int lane) {
   const int R = c.q.rows * p.G, t4 = lane & 3;
@@ -98,14 +97,14 @@ __device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int
     if (r >= R) continue;
     if (whole) {
       const float inv = inverse_of(l[x]);
-      const int64_t row = (int64_t)(c.q.cu0 + r / p.G) * p.Hq + c.r * p.G + r % p.G;
+      const int64_t row = (int64_t)(c.q.cu0 + r / p.G) * p.Hq + h * p.G + r % p.G;
       uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D) + t4;
 #pragma unroll
       for (int d = 0; d < D / 8; ++d)
         out[d * 4] = Num<T>::pack(o[d][2 * x] * inv, o[d][2 * x + 1] * inv);
       if (p.lse && t4 == 0) p.lse[row] = lse_of(m[x], l[x]);
     } else {
-      const int64_t row = (2 * unit + slot) * p.few_rows + r;
+      const int64_t row = (int64_t)(2 * gw + slot) * p.few_rows + r;
 #pragma unroll
       for (int d = 0; d < D / 8; ++d)
         *reinterpret_cast<float2*>(p.few_o + row * D + d * 8 + 2 * t4) =
@@ -159,7 +158,7 @@ struct Ring {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossParams p) {
+__global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   constexpr int NS = Ring<D>::kSteps, K = few_keys(D);
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_pref[kEntries];
@@ -168,37 +167,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossPa
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int flags = 0;
-  const Plan pl = make_plan<false, kThreads>(p, p.few_units, kLeastFew, s_pref, s_scratch, &flags);
+  const Plan pl = make_plan<kThreads>(p, p.few_units / p.few_heads, kLeastFew, s_pref, s_scratch,
+                                      &flags);
   if (blockIdx.x > 0) flags = 0;   // every block saw them
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-  if (lane == 0) write_record<false>(p, pl, s_pref, unit, p.few_rec);
-  const int64_t g0 = unit * pl.W;
+  const int gw = blockIdx.x * kWarps + warp;
+  const int unit = gw / p.few_heads, sub = gw % p.few_heads;
+  if (lane == 0) write_record(p, pl, s_pref, unit, sub, p.few_rec + 2 * gw);
+  const int64_t g0 = (int64_t)unit * pl.W;
   const int nst = g0 < pl.total ? (int)(min(pl.total, g0 + pl.W) - g0) : 0;
   if (nst > 0) {
     T* rk = reinterpret_cast<T*>(smem + warp * Ring<D>::kWarpBytes);
     T* rv = rk + NS * K * D;
-    Cursor pc = locate<false>(p, pl, s_pref, g0);   // next step to copy
+    Cursor pc = locate(p, pl, s_pref, g0);   // next step to copy
     Cursor cc = pc;                                  // step computed
     uint32_t* live = s_live[warp];                   // keys of a step that take part
-    int64_t ahead = key_offset<D>(p, pc.b, pc.r, pc.s, pc.q.keys, lane, flags);
+    int64_t ahead = key_offset<D>(p, pc.b, pc.r * p.few_heads + sub, pc.s, pc.q.keys, lane, flags);
     const auto issue = [&](int k, int buf) {
       if (k < nst) {
         copy_step<T, D>(p, ahead, rk + buf * K * D, rv + buf * K * D, lane);
         if (k + 1 < nst) {
-          if (++pc.s == pc.q.steps) next_range<false>(p, pc);
+          if (++pc.s == pc.q.steps) next_range(p, pc);
         }
       }
       const uint32_t w = __ballot_sync(0xffffffffu, ahead >= 0);
       if (lane == 0) live[buf] = w;
       if (k + 1 < nst)
-        ahead = key_offset<D>(p, pc.b, pc.r, pc.s, pc.q.keys, lane, flags);
+        ahead = key_offset<D>(p, pc.b, pc.r * p.few_heads + sub, pc.s, pc.q.keys, lane, flags);
       cp_async_commit();
     };
     // one copy of the step's code: unrolled over the ring it did not fit the instruction cache
 #pragma unroll 1
     for (int k = 0; k < NS - 1; ++k) issue(k, k);
     uint32_t qa[D / 16][4];
-    load_queries<T, D>(p, cc, lane, qa);
+    load_queries<T, D>(p, cc, cc.r * p.few_heads + sub, lane, qa);
     const int t4 = lane & 3;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
 #pragma unroll
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossPa
       }
       const bool last = cc.s == cc.q.steps - 1;
       if (last || k == nst - 1) {
-        flush<T, D>(p, cc, unit, from_start && last, first ? 0 : 1, m, l, o, lane);
+        flush<T, D>(p, cc, cc.r * p.few_heads + sub, gw, from_start && last, first ? 0 : 1, m, l, o, lane);
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
 #pragma unroll
@@ -304,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossPa
       }
       if (k < nst - 1) {
         if (last) {
-          next_range<false>(p, cc);
-          load_queries<T, D>(p, cc, lane, qa);
+          next_range(p, cc);
+          load_queries<T, D>(p, cc, cc.r * p.few_heads + sub, lane, qa);
         } else {
           ++cc.s;
         }
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cross_few_kernel(CrossPa
     }
     cp_async_wait<0>();
   }
-  if (pl.zero) zero_rows<T, D>(p, (int)unit, p.few_units, lane);
+  if (pl.zero) zero_rows<T, D>(p, gw, p.few_units, lane);
   if (flags) flag_status(p.status, flags);
 }
 
@@ -339,7 +340,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
   if (a.x <= 0) return;
   const int tokens = __ldcg(rec + 1).x;
   const int rows_at = tile ? 256 : p.few_rows;       // rows of a stored piece
-  const int64_t first = 2 * unit * rows_at;          // rows of the unit's first piece
+  const int64_t first = 2 * unit * rows_at;          // rows of the first piece
+  const int apart = 2 * rows_at * (tile ? 1 : p.few_heads);   // rows from a piece to the next
   const float* po = (tile ? p.tile_o : p.few_o) + first * D;
   const float* pm = (tile ? p.tile_m : p.few_m) + first;
   const float* pl = (tile ? p.tile_l : p.few_l) + first;
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int q = min(q0 + k * share, a.x - 1);
-        const int at = q * 2 * rows_at + (q == 0 ? a.y * rows_at : 0) + r;
+        const int at = q * apart + (q == 0 ? a.y * rows_at : 0) + r;
         m[k] = __ldcg(pm + at);
         l[k] = q0 + k * share < a.x ? __ldcg(pl + at) : 0.f;
         const float* src = po + (int64_t)at * D + lane * V;
@@ -479,8 +481,10 @@ size_t cross_layout(CrossParams* p, char* base) {
   const int64_t steps = seqs * p->Hkv * ((keys + few_keys(p->D) - 1) / few_keys(p->D));
   const int64_t runs = (steps + kLeastFew - 1) / kLeastFew;
   int64_t ctas = (runs + kWarps - 1) / kWarps;
-  ctas = ctas < 1 ? 1 : ctas > sms * kCtasPerSm ? sms * kCtasPerSm : ctas;
+  ctas = ctas < 1 ? 1 : ctas > sms ? sms : ctas;
   p->few_units = (int)ctas * kWarps;
+  p->few_heads = kWarps;
+  while (p->Hkv % p->few_heads != 0) p->few_heads /= 2;
   p->few_rows = (p->max_q < p->few ? p->max_q : p->few) * p->G;
   p->tile_units = 0;
   if (p->max_q > p->few) {

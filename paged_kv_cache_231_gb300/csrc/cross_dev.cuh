@@ -93,7 +93,7 @@ __device__ __forceinline__ Seq read_seq(const CrossParams& p, int b, int* flags,
   } else {
     const int n = few_keys(p.D);
     s.steps = (s.keys + n - 1) / n;
-    s.ranges = p.Hkv;
+    s.ranges = p.Hkv / p.few_heads;
   }
   return s;
 }
@@ -122,6 +122,8 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* total, int64_t*
   return before + v;
 }
 
+// The plan of the kernel for few rows. A unit is p.few_heads neighbouring warps, one kv head
+// each: what lies together in a cache row is read at about the same time.
 struct Plan {
   int64_t total;   // steps of all ranges
   int64_t W;       // steps of a run
@@ -131,7 +133,7 @@ struct Plan {
 };
 
 // Block-wide. pref: [kEntries] steps before entry e (shared memory); scratch: [NT / 32 + 2].
-template <bool kTiles, int NT>
+template <int NT>
 __device__ Plan make_plan(const CrossParams& p, int units, int least, int64_t* pref,
                           int64_t* scratch, int* flags) {
   Plan pl;
@@ -146,7 +148,7 @@ __device__ Plan make_plan(const CrossParams& p, int units, int least, int64_t* p
     if (e < pl.entries) {
       const int b1 = min(p.B, (e + 1) * pl.group);
       for (int b = e * pl.group; b < b1; ++b) {
-        const Seq s = read_seq<kTiles>(p, b, flags, &zero);
+        const Seq s = read_seq<false>(p, b, flags, &zero);
         mine += (int64_t)s.steps * s.ranges;
         longest = max(longest, s.steps);
       }
@@ -174,7 +176,6 @@ struct Cursor {
 };
 
 // cursor at step g < total
-template <bool kTiles>
 __device__ __forceinline__ Cursor locate(const CrossParams& p, const Plan& pl,
                                          const int64_t* pref, int64_t g) {
   int lo = 0, hi = pl.entries - 1, e = 0;
@@ -192,7 +193,7 @@ __device__ __forceinline__ Cursor locate(const CrossParams& p, const Plan& pl,
   int f = 0;
   bool z = false;
   for (c.b = e * pl.group; c.b < p.B; ++c.b) {
-    c.q = read_seq<kTiles>(p, c.b, &f, &z);
+    c.q = read_seq<false>(p, c.b, &f, &z);
     const int64_t n = (int64_t)c.q.steps * c.q.ranges;
     if (at < n) break;
     at -= n;
@@ -203,7 +204,6 @@ __device__ __forceinline__ Cursor locate(const CrossParams& p, const Plan& pl,
 }
 
 // first step of the next range
-template <bool kTiles>
 __device__ __forceinline__ void next_range(const CrossParams& p, Cursor& c) {
   c.s = 0;
   if (++c.r < c.q.ranges) return;
@@ -211,38 +211,29 @@ __device__ __forceinline__ void next_range(const CrossParams& p, Cursor& c) {
   int f = 0;
   bool z = false;
   while (++c.b < p.B) {
-    c.q = read_seq<kTiles>(p, c.b, &f, &z);
+    c.q = read_seq<false>(p, c.b, &f, &z);
     if (c.q.ranges > 0) return;
   }
 }
 
-// Record of unit u: the range that begins in its run and ends behind it, if there is one.
-// rec[2u] = {pieces, first piece's slot, first query row, kv head}, rec[2u + 1] = {query rows}
-template <bool kTiles>
+// Record of warp w, which works on head `sub` of unit u: the range that begins in the unit's run
+// and ends behind it, if there is one.
+// rec[2w] = {pieces, first piece's slot, first query row, kv head}, rec[2w + 1] = {query rows}
 __device__ __forceinline__ void write_record(const CrossParams& p, const Plan& pl,
-                                             const int64_t* pref, int64_t u, int4* rec) {
+                                             const int64_t* pref, int64_t u, int sub, int4* rec) {
   const int64_t g0 = u * pl.W, g1 = min(pl.total, g0 + pl.W);
   int4 a = make_int4(0, 0, 0, 0), b = make_int4(0, 0, 0, 0);
   if (g0 < pl.total) {
-    const Cursor c = locate<kTiles>(p, pl, pref, g1 - 1);
+    const Cursor c = locate(p, pl, pref, g1 - 1);
     const int64_t start = g1 - 1 - c.s, end = start + c.q.steps;
     if (start >= g0 && end > g1) {
-      a.x = (int)((end - 1) / pl.W - u) + 1;
-      a.y = start == g0 ? 0 : 1;
-      if (kTiles) {
-        const int tiles = c.q.ranges / p.Hkv, q0 = (c.r % tiles) * p.tile_pos;
-        a.z = c.q.cu0 + q0;
-        a.w = c.r / tiles;
-        b.x = min(p.tile_pos, c.q.rows - q0);
-      } else {
-        a.z = c.q.cu0;
-        a.w = c.r;
-        b.x = c.q.rows;
-      }
+      a = make_int4((int)((end - 1) / pl.W - u) + 1, start == g0 ? 0 : 1, c.q.cu0,
+                    c.r * p.few_heads + sub);
+      b.x = c.q.rows;
     }
   }
-  rec[2 * u] = a;
-  rec[2 * u + 1] = b;
+  rec[0] = a;
+  rec[1] = b;
 }
 
 // natural-log lse of a row with maximum m (log2 units) and sum l; empty: -inf

@@ -71,15 +71,16 @@ struct CrossParams {
   // plan (cross_dev.cuh)
   int few;                   // query rows of a sequence that the kernel for few rows takes
   int tile_pos;              // query positions of a tile of the kernel for many rows
+  int few_heads;             // kv heads that as many neighbouring warps of the first take together
   int few_units;             // warps of the first, blocks of the second (0: not launched)
   int tile_units;
   int few_rows;              // rows of a piece of the first: at most 16
   int box_keys;              // keys of a TMA box (0: rows are copied one by one)
   uint32_t wait_tries;       // testing hook (pkv_testing_wait_limit), as in AttnParams
   int withhold_copy;
-  // workspace: records, and pieces of unit u at slots 2u and 2u + 1
+  // workspace: records, and pieces of warp or block u at slots 2u and 2u + 1
   int4* few_rec;
-  float* few_o;              // [2 * few_units][few_rows][D]
+  float* few_o;              // [2 * few_units][few_rows][D], a piece for each warp and slot
   float* few_m;              // [2 * few_units][few_rows], log2 units
   float* few_l;
   int4* tile_rec;
