@@ -14,7 +14,7 @@
 //                   that the O of that half is complete and the K and V tiles so far are read.
 //                   The whole warp runs the loop and a lane is elected for the instructions: from
 //                   a lane that runs alone a tcgen05.mma took 85 to 110 cycles, so 56 to 71.
-//   warp 9          loads by TMA into 128-byte-swizzled shared memory: Q of the halves, and one
+//   warps 9, 11     load by TMA into 128-byte-swizzled shared memory: Q of the halves, and one
 //                   ring of K and V tiles in the order of their use (K0 V0 K1 V1 ...). A box is
 //                   up to 128 keys of one cache block; a tile lies in groups of 8 keys, the
 //                   64-column halves of a group one after the other, so one copy brings whole
@@ -61,7 +61,7 @@ struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kBars = kRing + kStages * kTile;
-  static constexpr uint32_t kSeen = kBars + 256;        // keys of the last 8 steps that take part
+  static constexpr uint32_t kSeen = kBars + 320;        // keys of the last 8 steps that take part
   static constexpr uint32_t kRun = kSeen + 128;          // Run
   static constexpr uint32_t kEnd = kRun + 96;
   static constexpr size_t kBytes = kEnd + 1024;
@@ -76,14 +76,15 @@ enum {
   kQFull = 16,   // + half
   kQEmpty = 18,  // + half: every S of the range completed
   kSFull = 20,   // + half: S in TMEM (and the O before it complete)
-  kPFull = 22,   // + half: the 4 warps wrote their weights
+  kPFull = 22,   // + half: the 4 warps wrote their weights of the first 64 keys
   kOFull = 24,   // + half: the last PV of the range completed
   kDrain = 26,   // + half: products in flight when a wait gave up
   kTurn = 28,    // + half: the other half issued its products
-  kBarriers = 30
+  kPRest = 30,   // + half: and of the others
+  kBarriers = 32
 };
 constexpr uint32_t kAbortWord = kBarriers * 8;   // behind the barriers
-static_assert(kAbortWord + 4 <= 256, "barrier area");
+static_assert(kAbortWord + 4 <= 320, "barrier area");
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -388,6 +389,8 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
 }
 
 // ---------------------------------------------------------------------------- loader
+// Two warps, one for the key tiles (and Q, and the masks), one for the value tiles: a box costs
+// its issuing warp some 210 cycles.
 // R keys from group of 8 `group` of the pool on, kv head h
 __device__ __forceinline__ void load_box(void* dst, const void* map, int group, int h,
                                          uint64_t* bar) {
@@ -400,18 +403,18 @@ __device__ __forceinline__ void load_box(void* dst, const void* map, int group, 
 
 template <typename T, int D>
 __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char* sm,
-                          const Run& run, const Wait& wait) {
+                          int kv, const Run& run, const Wait& wait) {
   using L = Lay<D>;
   uint64_t* bars = wait.bars;
   const int lane = threadIdx.x & 31, R = p.box_keys;
   int flags = 0;
-  uint32_t use = 0;   // ring tiles issued
+  uint32_t use = (uint32_t)kv, issued = 0;   // ring tile, tiles issued
   uint32_t* seen_words = reinterpret_cast<uint32_t*>(sm + L::kSeen);
   uint32_t q_use[2] = {0, 0};
   const bool withhold = p.withhold_copy != 0;   // testing hook: the first K tile never comes
   each_part(p, run, [&](const Part& t, const Cursor& c, int) {
     const int PT = p.tile_pos / 2;
-    for (int h = 0; h < t.halves; ++h) {
+    for (int h = 0; kv == 0 && h < t.halves; ++h) {
       if (q_use[h] > 0 &&
           !__all_sync(0xffffffffu, wait(kQEmpty + h, (q_use[h] - 1) & 1u)))
         return false;
@@ -447,7 +450,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       // which keys take part: key 4 i + x of the step is bit i of word x. An entry of the 8 is
       // written again when the K tile 8 steps on has room, so when a score tile 4 steps on was
       // full and every softmax warp was done with the steps before it.
-      {
+      if (kv == 0) {
         const int k0 = j * kTileKeys + 4 * lane;   // 4 keys of one block, if boxes are used
         uint32_t words[4];
         if (R > 0) {
@@ -465,8 +468,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
         for (int x = 0; x < 4; ++x)
           if (lane == x) seen = words[x];
       }
-#pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, ++use) {
+      {
         const uint32_t st = use % L::kStages, round = use / L::kStages;
         const bool ok = round == 0 || wait(kEmpty + (int)st, (round - 1) & 1u);
         if (!__all_sync(0xffffffffu, ok)) return false;
@@ -535,15 +537,16 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
           __syncwarp();
           if (i0 == 28) break;
         }
+        use += 2;
+        ++issued;
       }
     }
     return true;
   });
   if (flags) flag_status(p.status, flags);
   if (*wait.abort) {   // let what was issued land before the block ends
-    const uint32_t n = use < (uint32_t)L::kStages ? use : (uint32_t)L::kStages;
-    for (uint32_t k = 0; k < n; ++k) {
-      const uint32_t u = use - 1 - k;
+    for (uint32_t k = 1; k <= min(issued, (uint32_t)L::kStages); ++k) {
+      const uint32_t u = use - 2 * k;
       tc::mbar_wait(bars + kFull + u % L::kStages, (u / L::kStages) & 1u, wait.tries);
     }
     for (int h = 0; h < 2; ++h)
@@ -588,19 +591,31 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
       if (j == 0 && !ready(kQFull + half, q_use++ & 1u)) return false;
       if (pv && !full(use - 1)) return false;
       if (s && !full(use)) return false;
-      if (pv && !ready(kPFull + half, p_use++ & 1u)) return false;
       if (!my_turn(t.halves)) return false;
+      if (pv && !ready(kPFull + half, p_use & 1u)) return false;
       tc::fence_after_sync();
       const uint32_t va = ring + ((use - 1) % L::kStages) * L::kTile;
       const uint32_t ka = ring + (use % L::kStages) * L::kTile;
-      if (elect()) {
-        if (pv) {
+      if (pv) {
+        const auto products = [&](int ks) {
+          mma_tmem_a(o_at, s_at + (uint32_t)ks * 8u,
+                     tc::smem_desc(va + (uint32_t)ks * 2 * L::kGroup, 1024, L::kGroup), id_o,
+                     j == 1 && ks == 0 ? 0u : 1u);
+        };
+        if (elect()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_tmem_a(o_at, s_at + (uint32_t)ks * 8u,
-                       tc::smem_desc(va + (uint32_t)ks * 2 * L::kGroup, 1024, L::kGroup), id_o,
-                       j == 1 && ks == 0 ? 0u : 1u);
+          for (int ks = 0; ks < 4; ++ks) products(ks);
         }
+        __syncwarp();
+        if (!ready(kPRest + half, p_use++ & 1u)) return false;
+        tc::fence_after_sync();
+        if (elect()) {
+#pragma unroll
+          for (int ks = 4; ks < 8; ++ks) products(ks);
+        }
+        __syncwarp();
+      }
+      if (elect()) {
         if (s) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -643,6 +658,12 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
   // the products that read ring tile u for this half (or for both, if it is alone) are done
   const auto release = [&](uint32_t u, int halves) {
     arrive(bars + kEmpty + u % L::kStages, halves == 2 ? 1 : 2);
+  };
+  const auto hand_over = [&](int bar) {   // the warp's weights so far, to the products
+    tc::tmem_wait_st();
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) arrive(bars + bar + half);
   };
   each_part(p, run, [&](const Part& t, const Cursor&, int index) {
     if (half >= t.halves) {
@@ -722,13 +743,11 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
           w[x / 2] = __uint_as_float(Num<T>::pack(e0, e1));
         }
         tmem_st16(s_at + q * 16, w);
+        if (q == 1) hand_over(kPFull);
       }
       sum[0] = add_pair(add_pair(sum[0], sum[1]), add_pair(sum[2], sum[3]));
       l += low_of(sum[0]) + high_of(sum[0]);
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) arrive(bars + kPFull + half);
+      hand_over(kPRest);
     }
     if (!__all_sync(0xffffffffu, wait(kOFull + half, o_use & 1u))) return false;
     ++o_use;
@@ -803,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(wait.bars + kQEmpty + h, 1);
       tc::mbar_init(wait.bars + kSFull + h, 1);
       tc::mbar_init(wait.bars + kPFull + h, 4);
+      tc::mbar_init(wait.bars + kPRest + h, 4);
       tc::mbar_init(wait.bars + kOFull + h, 1);
       tc::mbar_init(wait.bars + kDrain + h, 1);
       tc::mbar_init(wait.bars + kTurn + h, 1);
@@ -835,8 +855,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
       if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 2)
         mma_role<T, D>(p, sm, (warp - kSoftmaxWarps) / 2, *run, wait);
-      else if (warp == kSoftmaxWarps + 1)
-        load_role<T, D>(p, maps, sm, *run, wait);
+      else
+        load_role<T, D>(p, maps, sm, warp == kSoftmaxWarps + 1 ? 0 : 1, *run, wait);
     }
   }
   cp_async_wait<0>();
