@@ -21,6 +21,8 @@
 //                   rows. Value rows past the sequence's keys or in
 //                   unmapped blocks are zero-filled (a weight of zero times what stands there
 //                   must be zero); block sizes that are no multiple of 8 go row by row.
+// A tile of at most 128 rows is worked on by both halves: half 0 takes the even steps, half 1 the
+// odd ones, and half 0 joins the two (m, l, O) at the end.
 // TMEM columns: S_0 0..127 (weights over 0..63), S_1 128..255, O_0 256.., O_1 384...
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -63,7 +65,8 @@ struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr uint32_t kBars = kRing + kStages * kTile;
   static constexpr uint32_t kSeen = kBars + 320;        // keys of the last 8 steps that take part
   static constexpr uint32_t kRun = kSeen + 128;          // Run
-  static constexpr uint32_t kEnd = kRun + 96;
+  static constexpr uint32_t kPairMl = kRun + 96;        // [128] (m, l) of half 1
+  static constexpr uint32_t kEnd = kPairMl + 1024;
   static constexpr size_t kBytes = kEnd + 1024;
 };
 static_assert(Lay<128>::kBytes <= 232448, "shared memory over the limit");
@@ -81,7 +84,9 @@ enum {
   kDrain = 26,   // + half: products in flight when a wait gave up
   kTurn = 28,    // + half: the other half issued its products
   kPRest = 30,   // + half: and of the others
-  kBarriers = 32
+  kPair = 32,    // half 1's (m, l, O) of a shared part are there
+  kPairRead = 33,   // half 0 has read them
+  kBarriers = 34
 };
 constexpr uint32_t kAbortWord = kBarriers * 8;   // behind the barriers
 static_assert(kAbortWord + 4 <= 320, "barrier area");
@@ -206,7 +211,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // This unit's part of a range: the tile under the cursor, steps [c.s, c.s + n).
 struct Part {
   int b, h, row0, pos, n, halves;   // first query row of the tile, its positions, steps, halves
-  bool whole;
+  bool whole, shared;               // shared: one half of rows, both halves at work on it
+  // half h works on steps first(h) + stride() * i, i < count(h)
+  __device__ __forceinline__ bool active(int half) const { return shared || half < halves; }
+  __device__ __forceinline__ int first(int half) const { return shared ? half : 0; }
+  __device__ __forceinline__ int stride() const { return shared ? 2 : 1; }
+  __device__ __forceinline__ int count(int half) const { return shared ? (n + 1 - half) / 2 : n; }
+  // arrivals of a half that release a ring tile (2 in all)
+  __device__ __forceinline__ uint32_t weight() const { return halves == 2 ? 1 : 2; }
 };
 __device__ __forceinline__ Part part_of(const CrossParams& p, const Cursor& c, int64_t left) {
   Part t;
@@ -218,6 +230,7 @@ __device__ __forceinline__ Part part_of(const CrossParams& p, const Cursor& c, i
   t.n = (int)min((int64_t)(c.q.steps - c.s), left);
   t.halves = t.pos > p.tile_pos / 2 ? 2 : 1;
   t.whole = c.s == 0 && t.n == c.q.steps;
+  t.shared = t.halves == 1 && t.n > 1;
   return t;
 }
 
@@ -414,7 +427,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
   const bool withhold = p.withhold_copy != 0;   // testing hook: the first K tile never comes
   each_part(p, run, [&](const Part& t, const Cursor& c, int) {
     const int PT = p.tile_pos / 2;
-    for (int h = 0; kv == 0 && h < t.halves; ++h) {
+    for (int h = 0; kv == 0 && h < (t.shared ? 2 : t.halves); ++h) {
       if (q_use[h] > 0 &&
           !__all_sync(0xffffffffu, wait(kQEmpty + h, (q_use[h] - 1) & 1u)))
         return false;
@@ -424,7 +437,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
 #pragma unroll
         for (int x = 0; x < D / 64; ++x)
           tc::tma_load_3d(sm + L::kQ + h * L::kTile + x * L::kSub, &maps.q, x * 64, t.h * p.G,
-                          t.row0 + h * PT, bars + kQFull + h);
+                          t.row0 + (t.shared ? 0 : h * PT), bars + kQFull + h);
       }
     }
     // R consecutive keys of a block to a lane (none when rows are copied one by one); the block
@@ -545,7 +558,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
   });
   if (flags) flag_status(p.status, flags);
   if (*wait.abort) {   // let what was issued land before the block ends
-    for (uint32_t k = 1; k <= min(issued, (uint32_t)L::kStages); ++k) {
+    for (uint32_t k = 1; k <= min(issued, (uint32_t)(L::kStages + 1) / 2); ++k) {
       const uint32_t u = use - 2 * k;
       tc::mbar_wait(bars + kFull + u % L::kStages, (u / L::kStages) & 1u, wait.tries);
     }
@@ -574,33 +587,35 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
   };
   // The halves issue by turns, half 0 first: without it the tensor core shares itself out
   // between both, they end together, and then both softmaxes run while it idles.
-  const auto my_turn = [&](int halves) {
-    if (halves == 1) return true;
+  const auto my_turn = [&](bool both) {
+    if (!both) return true;
     const uint32_t n = turn++;
     if (half == 0) return n == 0 || ready(kTurn, (n - 1) & 1u);
     return ready(kTurn + 1, n & 1u);
   };
   each_part(p, run, [&](const Part& t, const Cursor&, int) {
-    if (half >= t.halves) {
-      use += 2 * t.n;
-      return true;
-    }
-    // round j: PV of step j - 1 (V is tile use - 1), S of step j (K is tile use)
-    for (int j = 0; j <= t.n; ++j, use += 2) {
-      const bool pv = j > 0, s = j < t.n;
-      if (j == 0 && !ready(kQFull + half, q_use++ & 1u)) return false;
-      if (pv && !full(use - 1)) return false;
-      if (s && !full(use)) return false;
-      if (!my_turn(t.halves)) return false;
+    const uint32_t base = use;   // ring tile of K of step 0; V of step j is base + 2 j + 1
+    use += 2 * t.n;
+    if (!t.active(half)) return true;
+    const bool both = t.shared || t.halves == 2;
+    const int n = t.count(half);
+    // round i: PV of this half's step i - 1, S of step i
+    for (int i = 0; i <= n; ++i) {
+      const bool pv = i > 0, s = i < n;
+      const uint32_t k = base + 2 * (t.first(half) + t.stride() * i), v = k - 2 * t.stride() + 1;
+      if (i == 0 && !ready(kQFull + half, q_use++ & 1u)) return false;
+      if (pv && !full(v)) return false;
+      if (s && !full(k)) return false;
+      if (!my_turn(both)) return false;
       if (pv && !ready(kPFull + half, p_use & 1u)) return false;
       tc::fence_after_sync();
-      const uint32_t va = ring + ((use - 1) % L::kStages) * L::kTile;
-      const uint32_t ka = ring + (use % L::kStages) * L::kTile;
+      const uint32_t va = ring + (v % L::kStages) * L::kTile;
+      const uint32_t ka = ring + (k % L::kStages) * L::kTile;
       if (pv) {
         const auto products = [&](int ks) {
           mma_tmem_a(o_at, s_at + (uint32_t)ks * 8u,
                      tc::smem_desc(va + (uint32_t)ks * 2 * L::kGroup, 1024, L::kGroup), id_o,
-                     j == 1 && ks == 0 ? 0u : 1u);
+                     i == 1 && ks == 0 ? 0u : 1u);
         };
         if (elect()) {
 #pragma unroll
@@ -624,15 +639,19 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
                         tc::smem_desc(ka + sub * 1024u + x, 16, L::kGroup), id_s, ks > 0 ? 1u : 0u);
           }
           tc::commit(bars + kSFull + half);
-          if (j + 1 == t.n) tc::commit(bars + kQEmpty + half);
+          if (i + 1 == n) tc::commit(bars + kQEmpty + half);
         } else {
           tc::commit(bars + kOFull + half);
         }
-        if (t.halves == 2) arrive(bars + kTurn + 1 - half);
+        if (both) arrive(bars + kTurn + 1 - half);
       }
       __syncwarp();
     }
-    use -= 2;
+    if (both && n < t.count(0)) {   // as many turns as the other half
+      if (!my_turn(true)) return false;
+      if (elect()) arrive(bars + kTurn + 1 - half);
+      __syncwarp();
+    }
     return true;
   });
   if (*wait.abort) {
@@ -654,10 +673,11 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
   const uint32_t s_at = lane_at + half * 128, o_at = lane_at + 256 + half * 128;
   const float sl2 = fabsf(p.scale_log2);   // a negative scale turns the scores around
   const uint64_t scale2 = pair_of(sl2, sl2);
-  uint32_t s_use = 0, o_use = 0, use = 0;
-  // the products that read ring tile u for this half (or for both, if it is alone) are done
-  const auto release = [&](uint32_t u, int halves) {
-    arrive(bars + kEmpty + u % L::kStages, halves == 2 ? 1 : 2);
+  uint32_t s_use = 0, o_use = 0, use = 0, pair_use = 0;
+  float2* pair_ml = reinterpret_cast<float2*>(sm + L::kPairMl) + r;
+  // the products that read ring tile u for this half (or for both, if no other reads it) are done
+  const auto release = [&](uint32_t u, uint32_t weight) {
+    arrive(bars + kEmpty + u % L::kStages, weight);
   };
   const auto hand_over = [&](int bar) {   // the warp's weights so far, to the products
     tc::tmem_wait_st();
@@ -666,12 +686,13 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     if (lane == 0) arrive(bars + bar + half);
   };
   each_part(p, run, [&](const Part& t, const Cursor&, int index) {
-    if (half >= t.halves) {
-      use += 2 * t.n;
-      return true;
-    }
+    uint32_t k = use + 2 * t.first(half);   // ring tile of this half's K; V is k + 1
+    use += 2 * t.n;
+    if (!t.active(half)) return true;
+    const uint32_t apart = 2 * t.stride();
     float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < t.n; ++j, use += 2) {
+    const int n = t.count(half);
+    for (int j = 0; j < n; ++j, k += apart) {
       // the loads and stores of TMEM below are the whole warp's
       if (!__all_sync(0xffffffffu, wait(kSFull + half, s_use & 1u))) return false;
       ++s_use;
@@ -682,11 +703,11 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
 #pragma unroll
         for (int x = 0; x < 4; ++x) tc::tmem_ld32(s_at + x * 32, v32[x]);
       }
-      const uint4 seen = *reinterpret_cast<const uint4*>(sm + L::kSeen + (use / 2 % 8) * 16);
+      const uint4 seen = *reinterpret_cast<const uint4*>(sm + L::kSeen + (k / 2 % 8) * 16);
       tc::tmem_wait_ld();
       if (r == 0) {
-        release(use, t.halves);                      // K of this step
-        if (j > 0) release(use - 1, t.halves);       // V of the one before
+        release(k, t.weight());                              // K of this step
+        if (j > 0) release(k - apart + 1, t.weight());       // V of the one before
       }
       if (p.scale_log2 < 0.f) {
 #pragma unroll
@@ -752,7 +773,42 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     if (!__all_sync(0xffffffffu, wait(kOFull + half, o_use & 1u))) return false;
     ++o_use;
     tc::fence_after_sync();
-    if (r == 0) release(use - 1, t.halves);
+    if (r == 0) release(k - apart + 1, t.weight());
+    float mine_by = 1.f, other_by = 0.f;   // what this half's O counts for, and the other's
+    if (t.shared) {
+      if (half == 1) {
+        *pair_ml = make_float2(m, l);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(bars + kPair);
+        if (!__all_sync(0xffffffffu, wait(kPairRead, pair_use++ & 1u))) return false;
+        tc::fence_after_sync();
+        return true;
+      }
+      if (!__all_sync(0xffffffffu, wait(kPair, pair_use++ & 1u))) return false;
+      tc::fence_after_sync();
+      const float2 other = *pair_ml;
+      const float top = fmaxf(l == 0.f ? -INFINITY : m, other.y == 0.f ? -INFINITY : other.x);
+      const float base = top == -INFINITY ? 0.f : top;
+      mine_by = l == 0.f ? 0.f : ex2(m - base);
+      other_by = other.y == 0.f ? 0.f : ex2(other.x - base);
+      m = top;
+      l = l * mine_by + other.y * other_by;
+    }
+    const auto result = [&](int x, float (&o)[32]) {   // 32 columns of O
+      tc::tmem_ld32(o_at + x * 32, o);
+      tc::tmem_wait_ld();
+      if (t.shared) {
+        float y[32];
+        tc::tmem_ld32(o_at + 128 + x * 32, y);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          o[i] = mine_by == 0.f ? 0.f : o[i] * mine_by;   // no weight: anything may stand there
+          o[i] += other_by == 0.f ? 0.f : y[i] * other_by;
+        }
+      }
+    };
     const int pos = half * (p.tile_pos / 2) + r / p.G;
     const bool mine = r < (p.tile_pos / 2) * p.G && pos < t.pos;
     if (t.whole) {
@@ -762,8 +818,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         float o[32];
-        tc::tmem_ld32(o_at + x * 32, o);
-        tc::tmem_wait_ld();
+        result(x, o);
         if (mine) {
 #pragma unroll
           for (int y = 0; y < 4; ++y)
@@ -780,8 +835,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         float o[32];
-        tc::tmem_ld32(o_at + x * 32, o);
-        tc::tmem_wait_ld();
+        result(x, o);
         if (mine) {
 #pragma unroll
           for (int y = 0; y < 8; ++y)
@@ -794,6 +848,10 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
       }
     }
     tc::fence_before_sync();
+    if (t.shared) {
+      __syncwarp();
+      if (lane == 0) arrive(bars + kPairRead);
+    }
     return true;
   });
 }
@@ -827,6 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(wait.bars + kDrain + h, 1);
       tc::mbar_init(wait.bars + kTurn + h, 1);
     }
+    tc::mbar_init(wait.bars + kPair, 4);
+    tc::mbar_init(wait.bars + kPairRead, 4);
     tc::mbar_init_fence();
     *wait.abort = 0;
   }
