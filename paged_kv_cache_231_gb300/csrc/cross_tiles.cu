@@ -56,14 +56,14 @@ static_assert(sizeof(Run) <= 96, "run area");
 
 template <int D>
 struct Lay {   // byte offsets from a 1024-byte-aligned base
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 5 : 12;   // at most 12
   static constexpr uint32_t kTile = 128u * D * 2;       // 128 rows of Q, K or V
   static constexpr uint32_t kSub = 128u * 128;          // Q: 64 columns
   static constexpr uint32_t kGroup = 8u * D * 2;        // K, V: 8 keys, [D / 64][8][64]
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kBars = kRing + kStages * kTile;
-  static constexpr uint32_t kSeen = kBars + 320;        // keys of the last 8 steps that take part
+  static constexpr uint32_t kSeen = kBars + 384;        // keys of the last 8 steps that take part
   static constexpr uint32_t kRun = kSeen + 128;          // Run
   static constexpr uint32_t kPairMl = kRun + 96;        // [128] (m, l) of half 1
   static constexpr uint32_t kEnd = kPairMl + 1024;
@@ -75,21 +75,21 @@ static_assert((2 * kEntries + kThreads + 48) * 8 <= Lay<64>::kStages * Lay<64>::
 // mbarriers
 enum {
   kFull = 0,     // + stage: K or V tile landed
-  kEmpty = 8,    // + stage: the products that read it completed (2: one for each half)
-  kQFull = 16,   // + half
-  kQEmpty = 18,  // + half: every S of the range completed
-  kSFull = 20,   // + half: S in TMEM (and the O before it complete)
-  kPFull = 22,   // + half: the 4 warps wrote their weights of the first 64 keys
-  kOFull = 24,   // + half: the last PV of the range completed
-  kDrain = 26,   // + half: products in flight when a wait gave up
-  kTurn = 28,    // + half: the other half issued its products
-  kPRest = 30,   // + half: and of the others
-  kPair = 32,    // half 1's (m, l, O) of a shared part are there
-  kPairRead = 33,   // half 0 has read them
-  kBarriers = 34
+  kEmpty = 12,   // + stage: the products that read it completed (2: one for each half)
+  kQFull = 24,   // + half
+  kQEmpty = 26,  // + half: every S of the range completed
+  kSFull = 28,   // + half: S in TMEM (and the O before it complete)
+  kPFull = 30,   // + half: the 4 warps wrote their weights of the first 64 keys
+  kPRest = 32,   // + half: and of the others
+  kOFull = 34,   // + half: the last PV of the range completed
+  kTurn = 36,    // + half: the other half issued its products
+  kDrain = 38,   // + half: products in flight when a wait gave up
+  kPair = 40,    // half 1's (m, l, O) of a shared part are there
+  kPairRead = 41,   // half 0 has read them
+  kBarriers = 42
 };
 constexpr uint32_t kAbortWord = kBarriers * 8;   // behind the barriers
-static_assert(kAbortWord + 4 <= 320, "barrier area");
+static_assert(kAbortWord + 4 <= 384, "barrier area");
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -348,16 +348,15 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
       left -= n;
       s += (int64_t)c.q.steps * c.q.ranges;
     }
-    const int64_t per = by_step ? max(c.q.steps, 1) : 1;
-    c.r = (int)(left / per);
-    c.s = (int)(left % per);
+    c.r = by_step ? (int)quotient(left, max(c.q.steps, 1)) : (int)left;
+    c.s = by_step ? (int)(left - (int64_t)c.r * c.q.steps) : 0;
     *before = s + (int64_t)c.r * c.q.steps + c.s;
     return c;
   };
-  const int64_t whole = max(tiles / units - 1, (int64_t)0);
+  const int64_t whole = max(quotient(tiles, units) - 1, (int64_t)0);
   int64_t x, from = 0;
   if (whole > 0) find(whole * units, false, &from);
-  const int64_t rest = total - from, share = (total + units - 1) / units;
+  const int64_t rest = total - from, share = quotient(total + units - 1, units);
   // what the whole tiles left of a block's share; of very many tiles the last 64 tell
   int64_t weight = 0;
   if (tid < units) {
@@ -368,13 +367,65 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
       had += (float)(steps_at[e + 1] - steps_at[e]) / (float)(tiles_at[e + 1] - tiles_at[e]);
     }
     weight = whole > 0 ? max(share - (int64_t)had, (int64_t)1)
-                       : tid < max((rest + kLeast - 1) / kLeast, (int64_t)1);
+                       : tid < max(quotient(rest + kLeast - 1, kLeast), (int64_t)1);
   }
   int64_t all;
   const int64_t upto = block_sum<kThreads>(weight, &all, scratch);
   if (tid == 0) cut[0] = from;
-  if (tid < units) cut[tid + 1] = from + rest * upto / max(all, (int64_t)1);
+  if (tid < units) cut[tid + 1] = from + quotient(rest * upto, max(all, (int64_t)1));
   __syncthreads();
+  // Few tiles: if every range can be cut into pieces of its own, at most `units` in all and not
+  // much longer than an even share, the kv heads of a sequence are read in step: neighbouring
+  // heads lie together in a cache row. (16 heads of 64, 20000 to 60000 keys: MEASURED.)
+  if (tiles <= units && group == 1 && p.Hkv > 1) {
+    int* s_need = reinterpret_cast<int*>(scratch);
+    int lo = (int)max(share, (int64_t)kLeast), hi = lo + lo * 2 / 5;   // the least W in [lo, hi]
+    bool found = false;
+    while (true) {
+      // warp w tries W = lo + (hi - lo) * w / 11
+      const int warp = tid >> 5, lane = tid & 31, W = lo + (int)((int64_t)(hi - lo) * warp / 11);
+      int need = 0;
+      for (int e = lane; e < entries; e += 32) {
+        const int n = (int)(tiles_at[e + 1] - tiles_at[e]);
+        if (n > 0) {
+          const int s = (int)quotient(steps_at[e + 1] - steps_at[e], n);
+          need += n * ((s + W - 1) / W);
+        }
+      }
+      need = __reduce_add_sync(0xffffffffu, need);
+      if (lane == 0) s_need[warp] = need;
+      __syncthreads();
+      int w = 0;
+      while (w < 12 && s_need[w] > units) ++w;
+      __syncthreads();
+      if (w == 12) break;
+      found = true;
+      const int at = lo + (int)((int64_t)(hi - lo) * w / 11);
+      const int before = w > 0 ? lo + (int)((int64_t)(hi - lo) * (w - 1) / 11) + 1 : lo;
+      if (w == 0 || before >= at) {
+        hi = at;
+        break;
+      }
+      lo = before;
+      hi = at;
+    }
+    if (found) {   // hi: the longest piece
+      for (int v = tid; v <= units; v += kThreads) cut[v] = total;
+      __syncthreads();
+      // units before an entry, entry by entry (at most `units` of them hold tiles)
+      int first = 0;
+      for (int e = 0; e < entries; ++e) {
+        const int n = (int)(tiles_at[e + 1] - tiles_at[e]);
+        if (n == 0) continue;
+        const int s = (int)quotient(steps_at[e + 1] - steps_at[e], n), k = (s + hi - 1) / hi;
+        const int len = (s + k - 1) / k;
+        for (int v = tid; v < n * k; v += kThreads)
+          cut[first + v] = steps_at[e] + (int64_t)(v / k) * s + min(v % k * len, s);
+        first += n * k;
+      }
+      __syncthreads();
+    }
+  }
   const int u = blockIdx.x;
   const int64_t c0 = cut[u], c1 = cut[u + 1];
   if (tid == 0) {
@@ -424,7 +475,37 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
   uint32_t use = (uint32_t)kv, issued = 0;   // ring tile, tiles issued
   uint32_t* seen_words = reinterpret_cast<uint32_t*>(sm + L::kSeen);
   uint32_t q_use[2] = {0, 0};
+  const uint32_t every = R > 0 ? 0xffffffffu >> (32 - kTileKeys / R) : 0u;   // boxes of a tile
   const bool withhold = p.withhold_copy != 0;   // testing hook: the first K tile never comes
+  // announces `bytes` and copies the boxes whose bits are set, box i from group `group` of lane i;
+  // the whole warp (see the products)
+  const auto issue = [&](unsigned char* dst, uint64_t* full, int group, uint32_t boxes,
+                         uint32_t bytes, int h) {
+    const void* map = kv == 0 ? &maps.k : &maps.v;
+    int at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, group, i);
+    if (withhold && use == 0) boxes = 0;
+    __syncwarp();   // the masks are written before the tile is announced
+    if (elect()) {
+      tc::mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((boxes >> i) & 1u) load_box(dst + i * (R / 8) * L::kGroup, map, at[i], h, full);
+    }
+    __syncwarp();
+    for (int i0 = 4; i0 < 16 && (boxes >> i0) != 0; i0 += 4) {   // boxes of 8 or 16 keys
+#pragma unroll
+      for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, group, i0 + i);
+      if (elect()) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((boxes >> (i0 + i)) & 1u)
+            load_box(dst + (i0 + i) * (R / 8) * L::kGroup, map, at[i], h, full);
+      }
+      __syncwarp();
+    }
+  };
   each_part(p, run, [&](const Part& t, const Cursor& c, int) {
     const int PT = p.tile_pos / 2;
     for (int h = 0; kv == 0 && h < (t.shared ? 2 : t.halves); ++h) {
@@ -451,18 +532,29 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       return blk;
     };
     int ahead = lookup(c.s * kTileKeys + lane * R);
-    for (int j = c.s; j < c.s + t.n; ++j) {
+    for (int j = c.s; j < c.s + t.n; ++j, use += 2, ++issued) {
       const int key0 = j * kTileKeys + lane * R;
       const bool there = R > 0 && lane * R < kTileKeys && key0 < c.q.keys;
       const bool mapped = there && ahead >= 0 && ahead < p.NB;
-      if (there && !mapped) flags |= PKV_DEV_BAD_BLOCK;
-      uint32_t seen = 0;   // lane x < 4: word x of the step's keys that take part
-      const int row = mapped ? ahead * p.BS + (key0 - column(key0) * p.BS) : 0;
-      const bool whole = mapped && key0 + R <= c.q.keys;
+      const int row = ahead * p.BS + (key0 - column(key0) * p.BS);   // where mapped
+      const uint32_t boxes = __ballot_sync(0xffffffffu, mapped);
+      const bool clear = R > 0 && (j + 1) * kTileKeys <= c.q.keys && boxes == every;
       ahead = lookup(key0 + kTileKeys);
-      // which keys take part: key 4 i + x of the step is bit i of word x. An entry of the 8 is
-      // written again when the K tile 8 steps on has room, so when a score tile 4 steps on was
-      // full and every softmax warp was done with the steps before it.
+      const uint32_t st = use % L::kStages, round = use / L::kStages;
+      if (round > 0 && !__all_sync(0xffffffffu, wait(kEmpty + (int)st, (round - 1) & 1u)))
+        return false;
+      unsigned char* dst = sm + L::kRing + st * L::kTile;
+      uint64_t* full = bars + kFull + st;
+      // Which keys take part: key 4 i + x of the step is bit i of word x. An entry of the 8 is
+      // written again when the K tile 8 steps on has room: then a score tile at least 2 steps on
+      // was full, so every softmax warp that reads the entry was done with the steps before it.
+      uint32_t* seen = seen_words + (use / 2 % 8) * 4 + lane;
+      if (clear) {   // every key is there: whole boxes, nothing masked
+        if (kv == 0 && lane < 4) *seen = 0xffffffffu;
+        issue(dst, full, row / 8, boxes, L::kTile, t.h);
+        continue;
+      }
+      if (there && !mapped) flags |= PKV_DEV_BAD_BLOCK;
       if (kv == 0) {
         const int k0 = j * kTileKeys + 4 * lane;   // 4 keys of one block, if boxes are used
         uint32_t words[4];
@@ -479,18 +571,12 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
         }
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          if (lane == x) seen = words[x];
+          if (lane == x) *seen = words[x];
       }
       {
-        const uint32_t st = use % L::kStages, round = use / L::kStages;
-        const bool ok = round == 0 || wait(kEmpty + (int)st, (round - 1) & 1u);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        if (kv == 0 && lane < 4) seen_words[(use / 2 % 8) * 4 + lane] = seen;
-        unsigned char* dst = sm + L::kRing + st * L::kTile;
-        uint64_t* full = bars + kFull + st;
-        // keys behind the last one may stay what they are: their scores are masked
-        const bool box = kv == 0 ? mapped : whole;
-        uint32_t boxes = __ballot_sync(0xffffffffu, box);
+        // key rows behind the last key may stay what they are: their scores are masked
+        const bool whole = mapped && key0 + R <= c.q.keys;
+        const uint32_t copy = __ballot_sync(0xffffffffu, kv == 0 ? mapped : whole);
         const T* src = static_cast<const T*>(kv == 0 ? p.kc : p.vc);
         bool rows = false;   // rows copied one by one
         if (R == 0) {
@@ -533,25 +619,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
           tc::fence_async_shared();
           __syncwarp();
         }
-        if (elect()) tc::mbar_arrive_expect_tx(full, (uint32_t)__popc(boxes) * R * (D * 2));
-        __syncwarp();
-        if (withhold && use == 0) boxes = 0;
-        for (int i0 = 0; boxes >> i0; i0 += 4) {   // the whole warp: see the products
-          int at[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) at[i] = __shfl_sync(0xffffffffu, row / 8, (i0 + i) & 31);
-          if (elect()) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((boxes >> (i0 + i)) & 1u)
-                load_box(dst + (i0 + i) * (R / 8) * L::kGroup, kv == 0 ? &maps.k : &maps.v, at[i],
-                         t.h, full);
-          }
-          __syncwarp();
-          if (i0 == 28) break;
-        }
-        use += 2;
-        ++issued;
+        issue(dst, full, row / 8, copy, (uint32_t)__popc(copy) * R * (D * 2), t.h);
       }
     }
     return true;
