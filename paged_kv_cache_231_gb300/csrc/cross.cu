@@ -19,7 +19,7 @@ using namespace cross;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLeastFew = 8;    // steps of a run, at least
+constexpr int kLeastFew = 2;    // steps of a run, at least
 constexpr int kLeastTile = 4;
 
 template <int D>
@@ -321,53 +321,31 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
 }
 
 // ---------------------------------------------------------------------------- join
-// Over the pieces of a row: M = max m, out = sum 2^{m - M} o / sum 2^{m - M} l. A block takes
-// the record of one unit of the kernel for few rows (8 warps share its rows, several warps a
-// row when there are fewer), or 32 of the up to 256 rows of a record of the other kernel.
+// Over the pieces of a row: M = max m, out = sum 2^{m - M} o / sum 2^{m - M} l. What it waits for
+// is memory, so a warp asks for four pieces of N rows at once, whether they weigh anything or
+// not; a piece of no weight may hold anything.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 16;   // rows of a tile's record that a block takes (of 16, 32, 64)
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams p) {
-  constexpr int V = D / 32;
-  __shared__ float s_o[kJoinWarps][D];
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool tile = (int)blockIdx.x >= p.few_units;
-  const int64_t unit = tile ? (blockIdx.x - p.few_units) / 8 : blockIdx.x;
-  const int4* rec = (tile ? p.tile_rec : p.few_rec) + 2 * unit;
-  const int4 a = __ldcg(rec);
-  if (a.x <= 0) return;
-  const int tokens = __ldcg(rec + 1).x;
-  const int rows_at = tile ? 256 : p.few_rows;       // rows of a stored piece
-  const int64_t first = 2 * unit * rows_at;          // rows of the first piece
-  const int apart = 2 * rows_at * (tile ? 1 : p.few_heads);   // rows from a piece to the next
-  const float* po = (tile ? p.tile_o : p.few_o) + first * D;
-  const float* pm = (tile ? p.tile_m : p.few_m) + first;
-  const float* pl = (tile ? p.tile_l : p.few_l) + first;
-  const unsigned over_g = 65536u / p.G + 1;          // x / G = x * over_g >> 16 for x < 256
-  const int row0 = tile ? ((blockIdx.x - p.few_units) % 8) * 32 : 0;
-  const int rows = tile ? 32 : tokens * p.G;
-  int share = 1;                                     // warps of a row
-  while (share < kJoinWarps && rows * share * 2 <= kJoinWarps) share *= 2;
-  const int PT = p.tile_pos / 2;
-  for (int r0 = 0; r0 < rows; r0 += kJoinWarps / share) {
-    const int r = row0 + r0 + warp / share, part = warp % share;
-    const int x128 = tile ? r & 127 : r, by_g = (int)(x128 * over_g >> 16);
-    const int pos = tile ? (r >> 7) * PT + by_g : by_g;
-    const bool live = (tile ? x128 < PT * p.G : r < rows) && pos < tokens;
-    // four pieces at a time, all loads at once; a piece of no weight may hold anything
-    float acc[V], M = -INFINITY, L = 0.f;
+template <int D>
+struct Joined {
+  static constexpr int V = D / 32;   // columns of a lane
+  float acc[V], M = -INFINITY, L = 0.f;
+  // pieces from, from + share, ... of `pieces`: rows `apart` one from the other, the first one
+  // `late` rows on
+  __device__ __forceinline__ void add(const float* po, const float* pm, const float* pl, int row,
+                                      int late, int apart, int pieces, int from, int share,
+                                      int lane) {
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int q0 = part; live && q0 < a.x; q0 += 4 * share) {
+    for (int q0 = from; q0 < pieces; q0 += 4 * share) {
       float m[4], l[4], x[4][V];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int q = min(q0 + k * share, a.x - 1);
-        const int at = q * apart + (q == 0 ? a.y * rows_at : 0) + r;
+        const int q = min(q0 + k * share, pieces - 1);
+        const int at = q * apart + (q == 0 ? late : 0) + row;
         m[k] = __ldcg(pm + at);
-        l[k] = q0 + k * share < a.x ? __ldcg(pl + at) : 0.f;
+        l[k] = q0 + k * share < pieces ? __ldcg(pl + at) : 0.f;
         const float* src = po + (int64_t)at * D + lane * V;
         if constexpr (V == 4) {
           const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
@@ -398,41 +376,90 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
         for (int v = 0; v < V; ++v) acc[v] += w * x[k][v];
       }
     }
+  }
+  template <typename T>
+  __device__ __forceinline__ void write(const CrossParams& p, int64_t row, int lane) const {
+    const float inv = inverse_of(L);
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * V);
+#pragma unroll
+    for (int v = 0; v < V; v += 2) out[v / 2] = Num<T>::pack(acc[v] * inv, acc[v + 1] * inv);
+    if (p.lse && lane == 0) p.lse[row] = lse_of(M, L);
+  }
+};
+
+// Blocks 0 .. : kJoinRows rows of a tile's record each (256 / kJoinRows blocks a record). Behind
+// them a block for the record of each warp of the kernel for few rows: 8 warps share its rows,
+// several warps a row when there are fewer.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams p) {
+  constexpr int V = D / 32, kBlocks = 256 / kJoinRows;
+  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile_blocks = p.tile_units * kBlocks;
+  const bool tile = (int)blockIdx.x < tile_blocks;
+  const int unit = tile ? blockIdx.x / kBlocks : blockIdx.x - tile_blocks;
+  const int4* rec = (tile ? p.tile_rec : p.few_rec) + 2 * unit;
+  const int4 a = __ldcg(rec);
+  const int tokens = __ldcg(&rec[1].x);
+  if (a.x <= 0) return;
+  const unsigned over_g = 65536u / p.G + 1;          // x / G = x * over_g >> 16 for x < 256
+  if (tile) {
+    const int64_t first = (int64_t)unit * 512;
+    const int PT = p.tile_pos / 2, row0 = blockIdx.x % kBlocks * kJoinRows;
+    for (int i = warp; i < kJoinRows; i += kJoinWarps) {
+      const int row = row0 + i, x = row & 127, by_g = (int)(x * over_g >> 16);
+      const int pos = (row >> 7) * PT + by_g;
+      if (x >= PT * p.G || pos >= tokens) continue;
+      Joined<D> j;
+      j.add(p.tile_o + first * D, p.tile_m + first, p.tile_l + first, row, a.y * 256, 512, a.x, 0,
+            1, lane);
+      j.template write<T>(p, (int64_t)(a.z + pos) * p.Hq + a.w * p.G + x - by_g * p.G, lane);
+    }
+    return;
+  }
+  const int64_t first = (int64_t)2 * unit * p.few_rows;
+  const int rows = tokens * p.G;
+  int share = 1;                                     // warps of a row
+  while (share < kJoinWarps && rows * share * 2 <= kJoinWarps) share *= 2;
+  for (int r0 = 0; r0 < rows; r0 += kJoinWarps / share) {
+    const int r = r0 + warp / share, part = warp % share;
+    const bool live = r < rows;
+    Joined<D> j;
+    j.add(p.few_o + first * D, p.few_m + first, p.few_l + first, live ? r : 0, a.y * p.few_rows,
+          2 * p.few_rows * p.few_heads, live ? a.x : 0, part, share, lane);
     if (share > 1) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
+      for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = j.acc[v];
       if (lane == 0) {
-        s_m[warp] = M;
-        s_l[warp] = L;
+        s_m[warp] = j.M;
+        s_l[warp] = j.L;
       }
       __syncthreads();
       if (part == 0 && live) {
-        float top = M;
-        for (int k = 1; k < share; ++k) top = fmaxf(top, s_l[warp + k] == 0.f ? -INFINITY : s_m[warp + k]);
+        float top = j.M;
+        for (int k = 1; k < share; ++k)
+          top = fmaxf(top, s_l[warp + k] == 0.f ? -INFINITY : s_m[warp + k]);
         const float base = top == -INFINITY ? 0.f : top;
-        float w = L == 0.f ? 0.f : ex2(M - base);
-        L *= w;
+        float w = j.L == 0.f ? 0.f : ex2(j.M - base);
+        j.L *= w;
 #pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] *= w;
+        for (int v = 0; v < V; ++v) j.acc[v] *= w;
         for (int k = 1; k < share; ++k) {
           if (s_l[warp + k] == 0.f) continue;
           w = ex2(s_m[warp + k] - base);
-          L += w * s_l[warp + k];
+          j.L += w * s_l[warp + k];
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[v] += w * s_o[warp + k][lane * V + v];
+          for (int v = 0; v < V; ++v) j.acc[v] += w * s_o[warp + k][lane * V + v];
         }
-        M = top;
+        j.M = top;
       }
       __syncthreads();
     }
-    if (live && part == 0) {
-      const int64_t row = (int64_t)(a.z + pos) * p.Hq + a.w * p.G + x128 - by_g * p.G;
-      const float inv = inverse_of(L);
-      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * V);
-#pragma unroll
-      for (int v = 0; v < V; v += 2) out[v / 2] = Num<T>::pack(acc[v] * inv, acc[v + 1] * inv);
-      if (p.lse && lane == 0) p.lse[row] = lse_of(M, L);
-    }
+    const int by_g = (int)(r * over_g >> 16);
+    if (live && part == 0)
+      j.template write<T>(p, (int64_t)(a.z + by_g) * p.Hq + a.w * p.G + r - by_g * p.G, lane);
   }
 }
 
@@ -458,7 +485,7 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   }
   ProfScope ps("cross_combine", s);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.few_units + 8 * p.tile_units));
+  cfg.gridDim = dim3((unsigned)(p.few_units + 256 / kJoinRows * p.tile_units));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
