@@ -26,6 +26,7 @@
 // TMEM columns: S_0 0..127 (weights over 0..63), S_1 128..255, O_0 256.., O_1 384...
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <limits.h>
 
 #include "cross_dev.cuh"
 #include "tcgen05.cuh"
@@ -70,7 +71,7 @@ struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr size_t kBytes = kEnd + 1024;
 };
 static_assert(Lay<128>::kBytes <= 232448, "shared memory over the limit");
-static_assert((2 * kEntries + kThreads + 48) * 8 <= Lay<64>::kStages * Lay<64>::kTile, "plan fits the ring");
+static_assert((3 * kEntries + kThreads + 48) * 8 <= Lay<64>::kStages * Lay<64>::kTile, "plan fits the ring");
 
 // mbarriers
 enum {
@@ -287,10 +288,12 @@ __device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, 
 // i % units), so that the blocks read the same keys at about the same time and the cache holds
 // them; of the others (between one and two for each block, if there are as many) each block
 // gets a run of steps that evens out what it had before.
-// mem: [kEntries + 1] steps and tiles before an entry each, [kThreads + 1] cuts, scratch.
+// mem: [kEntries + 1] steps and tiles before an entry each, [kThreads + 1] cuts, scratch, [kEntries]
+// steps of an entry's tiles (the mean, where an entry holds several sequences).
 __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   int64_t *steps_at = mem, *tiles_at = steps_at + kEntries + 1, *cut = tiles_at + kEntries + 1,
           *scratch = cut + kThreads + 1;
+  int* per_tile = reinterpret_cast<int*>(scratch + 32);
   const int tid = threadIdx.x, units = p.tile_units;
   const int group = (p.B + kEntries - 1) / kEntries, entries = (p.B + group - 1) / group;
   int f = 0;
@@ -313,6 +316,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     if (e < entries) {
       steps_at[e] = total + upto_s - s;
       tiles_at[e] = tiles + upto_n - n;
+      per_tile[e] = n > 0 ? (int)quotient(s, n) : 0;
     }
     total += all_s;
     tiles += all_n;
@@ -355,18 +359,26 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   };
   const int64_t whole = max(quotient(tiles, units) - 1, (int64_t)0);
   int64_t x, from = 0;
-  if (whole > 0) find(whole * units, false, &from);
+  if (whole > 0) {
+    const int64_t k = whole * units;
+    if (group == 1) {
+      const int e = entry(tiles_at, k);
+      from = steps_at[e] + (k - tiles_at[e]) * per_tile[e];
+    } else {
+      find(k, false, &from);
+    }
+  }
   const int64_t rest = total - from, share = quotient(total + units - 1, units);
   // what the whole tiles left of a block's share; of very many tiles the last 64 tell
   int64_t weight = 0;
   if (tid < units) {
     const int64_t i0 = max(whole - 64, (int64_t)0);
-    float had = (float)i0 * (float)total / (float)max(tiles, (int64_t)1);
-    for (int64_t i = i0; i < whole; ++i) {   // a tile's steps, or the mean of its entry's
-      const int e = entry(tiles_at, tid + i * units);
-      had += (float)(steps_at[e + 1] - steps_at[e]) / (float)(tiles_at[e + 1] - tiles_at[e]);
+    int64_t had = i0 > 0 ? quotient(i0 * total, tiles) : 0, k = tid + i0 * units;
+    for (int e = whole > 0 ? entry(tiles_at, k) : 0; k < whole * units; k += units) {
+      while (tiles_at[e + 1] <= k) ++e;
+      had += per_tile[e];
     }
-    weight = whole > 0 ? max(share - (int64_t)had, (int64_t)1)
+    weight = whole > 0 ? max(share - had, (int64_t)1)
                        : tid < max(quotient(rest + kLeast - 1, kLeast), (int64_t)1);
   }
   int64_t all;
@@ -377,38 +389,22 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   // Few tiles: if every range can be cut into pieces of its own, at most `units` in all and not
   // much longer than an even share, the kv heads of a sequence are read in step: neighbouring
   // heads lie together in a cache row. (16 heads of 64, 20000 to 60000 keys: MEASURED.)
-  if (tiles <= units && group == 1 && p.Hkv > 1) {
-    int* s_need = reinterpret_cast<int*>(scratch);
-    int lo = (int)max(share, (int64_t)kLeast), hi = lo + lo * 2 / 5;   // the least W in [lo, hi]
-    bool found = false;
-    while (true) {
-      // warp w tries W = lo + (hi - lo) * w / 11
-      const int warp = tid >> 5, lane = tid & 31, W = lo + (int)((int64_t)(hi - lo) * warp / 11);
-      int need = 0;
-      for (int e = lane; e < entries; e += 32) {
-        const int n = (int)(tiles_at[e + 1] - tiles_at[e]);
-        if (n > 0) {
-          const int s = (int)quotient(steps_at[e + 1] - steps_at[e], n);
-          need += n * ((s + W - 1) / W);
-        }
-      }
-      need = __reduce_add_sync(0xffffffffu, need);
-      if (lane == 0) s_need[warp] = need;
-      __syncthreads();
-      int w = 0;
-      while (w < 12 && s_need[w] > units) ++w;
-      __syncthreads();
-      if (w == 12) break;
-      found = true;
-      const int at = lo + (int)((int64_t)(hi - lo) * w / 11);
-      const int before = w > 0 ? lo + (int)((int64_t)(hi - lo) * (w - 1) / 11) + 1 : lo;
-      if (w == 0 || before >= at) {
-        hi = at;
-        break;
-      }
-      lo = before;
-      hi = at;
-    }
+  if (tiles <= units && entries <= 64 && p.Hkv > 1) {
+    // thread t tries pieces of at most lo + (hi - lo) * t / (kThreads - 1) steps
+    const int lo = (int)max(share, (int64_t)kLeast), span = lo * 2 / 5;
+    int need = 0;
+    const int W = lo + span * tid / (kThreads - 1);
+    for (int e = 0; e < entries; ++e)
+      need += (int)(tiles_at[e + 1] - tiles_at[e]) * ((per_tile[e] + W - 1) / W);
+    int* least = reinterpret_cast<int*>(scratch);
+    if (tid == 0) *least = INT_MAX;
+    __syncthreads();
+    const uint32_t fit = __ballot_sync(0xffffffffu, need <= units);
+    if (fit && (tid & 31) == __ffs(fit) - 1) atomicMin(least, W);
+    __syncthreads();
+    const int hi = *least;
+    const bool found = hi != INT_MAX;
+    __syncthreads();
     if (found) {   // hi: the longest piece
       for (int v = tid; v <= units; v += kThreads) cut[v] = total;
       __syncthreads();
@@ -417,7 +413,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
       for (int e = 0; e < entries; ++e) {
         const int n = (int)(tiles_at[e + 1] - tiles_at[e]);
         if (n == 0) continue;
-        const int s = (int)quotient(steps_at[e + 1] - steps_at[e], n), k = (s + hi - 1) / hi;
+        const int s = per_tile[e], k = (s + hi - 1) / hi;
         const int len = (s + k - 1) / k;
         for (int v = tid; v < n * k; v += kThreads)
           cut[first + v] = steps_at[e] + (int64_t)(v / k) * s + min(v % k * len, s);
