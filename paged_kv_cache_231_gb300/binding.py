@@ -8,7 +8,9 @@ raises. Function names match the C entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -558,46 +560,92 @@ def pkv_combine_partials(o, m, l, segment_offsets=None, *, num_segments: int, la
 
 
 # ----------------------------------------------------------------------------- steps
-def _check_tensors(stream, **named):
-    """Each given as name=(tensor or None, dtype, shape): contiguous tensors of that dtype
-    and shape (None = any size) on the current CUDA device, which is the stream's too."""
-    on = {}
-    for name, (t, dtype, shape) in named.items():
+# A decode step makes these calls once a layer, on the host thread that feeds the GPU: the
+# argument blocks are packed in one go (fields as in the ctypes structures above) and passed
+# as bytes, and a call's tensors are looked at once.
+_SCHEDULE_PACK = struct.Struct("@9Q5q")
+_AXES_PACK = struct.Struct("@11Q8q4i128s")
+_CROSS_PACK = struct.Struct("@9Q9qif")
+_STEP = {}   # entry points that take packed blocks
+
+
+def _step_call(name: str, *args):
+    fn = _STEP.get(name)
+    if fn is None:
+        lib = load_library()
+        for pack, cls in ((_SCHEDULE_PACK, ScheduleArgs), (_AXES_PACK, AppendAxesArgs),
+                          (_CROSS_PACK, CrossAttentionArgs)):
+            assert pack.size == ctypes.sizeof(cls)
+        for n, more in (("pkv_paged_schedule", [c_vp]), ("pkv_paged_append_rotary_axes", [c_vp]),
+                        ("pkv_cross_attention", [c_vp, ctypes.c_size_t, c_vp])):
+            f = lib[n]   # a function object of its own
+            f.restype, f.argtypes = c_i32, [ctypes.c_char_p] + more
+            _STEP[n] = f
+        fn = _STEP[name]
+    status = fn(*args)
+    if status != PKV_OK:
+        raise PagedKVError(name, status)
+
+
+def _refuse(stream, tensors):
+    """Names what is wrong with a call's tensors (see _check_tensors)."""
+    for name, t, dtype, shape in tensors:
         if t is None:
             continue
         if t.dtype != dtype:
             raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous")
-        got = t.shape
-        if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
-            raise ValueError(f"{name}: expected shape {shape}, got {tuple(got)}")
-        on[t.get_device()] = name
-    if -1 in on:
-        raise ValueError(f"{on[-1]}: must be a CUDA tensor")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    for name, t, _, _ in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name}: must be a CUDA tensor")
     here = _torch().cuda.current_device()
-    for device, name in on.items():
-        if device != here:
-            raise ValueError(f"{name}: on device {device}, the current one is {here}")
-    if stream is not None and stream.device_index != here:
-        raise ValueError(f"stream: of device {stream.device_index}, the current one is {here}")
+    for name, t, _, _ in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{name}: on device {t.get_device()}, the current one is {here}")
+    raise ValueError(f"stream: of device {stream.device_index}, the current one is {here}")
 
 
-def _step_stream(stream, *made):
-    """The raw stream of a call; memory made here for a stream other than the current one
-    is not given away again before that stream has used it."""
-    s = stream if stream is not None else _torch().cuda.current_stream()
+def _check_tensors(stream, tensors) -> int:
+    """tensors: (name, tensor or None, dtype, shape) each. They have to be contiguous, of that
+    dtype and shape, on the current CUDA device, which is the stream's too. Returns the raw
+    stream."""
+    device = None
+    for _, t, dtype, shape in tensors:
+        if t is None:
+            continue
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            _refuse(stream, tensors)
+        at = t.get_device()
+        if at != device:
+            if device is not None or at < 0:
+                _refuse(stream, tensors)
+            device = at
+    cuda = _torch().cuda
+    if device != cuda.current_device() or (stream is not None and stream.device_index != device):
+        _refuse(stream, tensors)
+    return (stream if stream is not None else cuda.current_stream(device)).cuda_stream
+
+
+def _keep(stream, *made):
+    """Memory made here for a stream other than the current one is not given away again
+    before that stream has used it."""
     if stream is not None:
         for t in made:
             if t is not None:
                 t.record_stream(stream)
-    return s.cuda_stream
 
 
 def _need(**named):
     for name, t in named.items():
         if t is None:
             raise ValueError(f"{name}: required")
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def pkv_paged_schedule(past_seqlens, new_seqlens, block_table, *, num_blocks: int,
@@ -613,34 +661,34 @@ def pkv_paged_schedule(past_seqlens, new_seqlens, block_table, *, num_blocks: in
     are made here. Rows that the pool or ``num_tokens`` cannot take get no tokens."""
     torch = _torch()
     i32 = torch.int32
-    _need(past_seqlens=past_seqlens, new_seqlens=new_seqlens, block_table=block_table)
-    num_tokens = int(num_tokens)
+    if past_seqlens is None or new_seqlens is None or block_table is None:
+        _need(past_seqlens=past_seqlens, new_seqlens=new_seqlens, block_table=block_table)
     B = past_seqlens.shape[0] if past_seqlens.dim() == 1 else -1
-    _check_tensors(stream, past_seqlens=(past_seqlens, i32, (B,)),
-                   new_seqlens=(new_seqlens, i32, (B,)),
-                   block_table=(block_table, i32, (B, None)),
-                   cumulative_sequence_length=(cumulative_sequence_length, i32, (B + 1,)),
-                   slot_mapping=(slot_mapping, i32, (num_tokens,)),
-                   positions=(positions, i32, (num_tokens,)),
-                   total_seqlens=(total_seqlens, i32, (B,)),
-                   free_blocks=(free_blocks, i32, (1,)),
-                   device_status=(device_status, i32, (1,)))
-    dev, made = block_table.device, []
+    MB = block_table.shape[1] if block_table.dim() == 2 else -1
+    raw = _check_tensors(stream, (
+        ("past_seqlens", past_seqlens, i32, (B,)), ("new_seqlens", new_seqlens, i32, (B,)),
+        ("block_table", block_table, i32, (B, MB)),
+        ("cumulative_sequence_length", cumulative_sequence_length, i32, (B + 1,)),
+        ("slot_mapping", slot_mapping, i32, (num_tokens,)),
+        ("positions", positions, i32, (num_tokens,)),
+        ("total_seqlens", total_seqlens, i32, (B,)), ("free_blocks", free_blocks, i32, (1,)),
+        ("device_status", device_status, i32, (1,))))
 
-    def out(t, n):
+    def made(t, n):
         if t is None:
-            t = torch.empty(n, dtype=i32, device=dev)
-            made.append(t)
+            t = torch.empty(n, dtype=i32, device=block_table.device)
+            _keep(stream, t)
         return t
 
-    cu, slots = out(cumulative_sequence_length, B + 1), out(slot_mapping, num_tokens)
-    pos, total, free = out(positions, num_tokens), out(total_seqlens, B), out(free_blocks, 1)
-    a = ScheduleArgs(past_seqlens.data_ptr(), new_seqlens.data_ptr(), block_table.data_ptr(),
-                     cu.data_ptr(), slots.data_ptr(), pos.data_ptr(), total.data_ptr(),
-                     free.data_ptr(), _ptr(device_status), B, block_table.shape[1],
-                     num_blocks, block_size, num_tokens)
-    _check("pkv_paged_schedule",
-           load_library().pkv_paged_schedule(ctypes.byref(a), _step_stream(stream, *made)))
+    cu, slots = made(cumulative_sequence_length, B + 1), made(slot_mapping, num_tokens)
+    pos, total = made(positions, num_tokens), made(total_seqlens, B)
+    free = made(free_blocks, 1)
+    _step_call("pkv_paged_schedule",
+               _SCHEDULE_PACK.pack(past_seqlens.data_ptr(), new_seqlens.data_ptr(),
+                                   block_table.data_ptr(), cu.data_ptr(), slots.data_ptr(),
+                                   pos.data_ptr(), total.data_ptr(), free.data_ptr(),
+                                   _at(device_status), B, MB, num_blocks, block_size,
+                                   num_tokens), raw)
     return cu, slots, pos, total, free
 
 
@@ -674,54 +722,53 @@ def pkv_paged_append_rotary_axes(query, key, value, key_cache, value_cache, slot
     [num_tokens, num_heads * head_size] (made here unless ``query_out`` is given; rows of
     padding are not written), or None without them (``rotate_query`` false, or no query)."""
     torch = _torch()
-    _need(key_cache=key_cache, value_cache=value_cache, slot_mapping=slot_mapping)
-    dt = key_cache.dtype
-    if dt not in (torch.float16, torch.bfloat16):
+    if key_cache is None or value_cache is None or slot_mapping is None:
+        _need(key_cache=key_cache, value_cache=value_cache, slot_mapping=slot_mapping)
+    dt, f32, i32 = key_cache.dtype, torch.float32, torch.int32
+    if dt is torch.float16:
+        code = PKV_F16
+    elif dt is torch.bfloat16:
+        code = PKV_BF16
+    else:
         raise TypeError(f"key_cache: expected float16 or bfloat16, got {dt}")
     if key_cache.dim() != 4:
         raise ValueError("key_cache: [num_blocks, block_size, kv_num_heads, head_size]")
-    NB, BS, Hkv, D = key_cache.shape
+    NB, BS, _, D = key_cache.shape
     T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
-    packed = key is None and value is None
     qh, kvh = num_heads * D, kv_num_heads * D
-    half, axes, tdt = rotary_dim // 2, 0, torch.float32
+    pool = (NB, BS, kv_num_heads, D)
+    half, axes, rows, tdt, pairs = rotary_dim // 2, 0, 0, f32, b""
     if rotary_dim > 0:
-        _need(positions=positions, cos_cache=cos_cache, sin_cache=sin_cache)
+        if positions is None or cos_cache is None or sin_cache is None:
+            _need(positions=positions, cos_cache=cos_cache, sin_cache=sin_cache)
         axes = positions.shape[0] if positions.dim() == 2 else -1
-        if cos_cache.dtype == dt:
+        rows = cos_cache.shape[0] if cos_cache.dim() == 2 else -1
+        if cos_cache.dtype is dt:
             tdt = dt
-    table, pairs = None, b""
-    if rotary_dim > 0:
-        table = (cos_cache.shape[0] if cos_cache.dim() else 0, half)
         pairs = bytes(half) if pair_axis is None else bytes(pair_axis)
         if len(pairs) != half or half > MAX_ROTARY_PAIRS:
             raise ValueError(f"pair_axis: one axis for each of {half} pairs (at most "
                              f"{MAX_ROTARY_PAIRS}), got {len(pairs)}")
     else:
         positions = cos_cache = sin_cache = None
-    _check_tensors(stream, query=(query, dt, (T, qh + 2 * kvh if packed else qh)),
-                   key=(key, dt, (T, kvh)), value=(value, dt, (T, kvh)),
-                   query_out=(query_out, dt, (T, qh)),
-                   key_cache=(key_cache, dt, (NB, BS, kv_num_heads, D)),
-                   value_cache=(value_cache, dt, (NB, BS, kv_num_heads, D)),
-                   slot_mapping=(slot_mapping, torch.int32, (T,)),
-                   positions=(positions, torch.int32, (axes, T)),
-                   cos_cache=(cos_cache, tdt, table), sin_cache=(sin_cache, tdt, table),
-                   device_status=(device_status, torch.int32, (1,)))
-    made = None
+    raw = _check_tensors(stream, (
+        ("query", query, dt, (T, qh + 2 * kvh if key is None and value is None else qh)),
+        ("key", key, dt, (T, kvh)), ("value", value, dt, (T, kvh)),
+        ("query_out", query_out, dt, (T, qh)), ("key_cache", key_cache, dt, pool),
+        ("value_cache", value_cache, dt, pool), ("slot_mapping", slot_mapping, i32, (T,)),
+        ("positions", positions, i32, (axes, T)), ("cos_cache", cos_cache, tdt, (rows, half)),
+        ("sin_cache", sin_cache, tdt, (rows, half)), ("device_status", device_status, i32, (1,))))
     if rotate_query and query is not None and query_out is None:
-        query_out = made = torch.empty((T, qh), dtype=dt, device=key_cache.device)
-    a = AppendAxesArgs(_ptr(query), _ptr(key), _ptr(value), _ptr(query_out),
-                       key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(),
-                       _ptr(positions), _ptr(cos_cache), _ptr(sin_cache),
-                       _ptr(device_status), T, num_heads, kv_num_heads, D, BS, NB,
-                       rotary_dim, cos_cache.shape[0] if rotary_dim > 0 else 0, axes,
-                       1 if rotary_interleaved else 0, _dtype_code(key_cache),
-                       PKV_F32 if tdt == torch.float32 else _dtype_code(key_cache))
-    ctypes.memmove(ctypes.addressof(a) + AppendAxesArgs.pair_axis.offset, pairs, len(pairs))
-    _check("pkv_paged_append_rotary_axes",
-           load_library().pkv_paged_append_rotary_axes(ctypes.byref(a),
-                                                       _step_stream(stream, made)))
+        query_out = torch.empty((T, qh), dtype=dt, device=key_cache.device)
+        _keep(stream, query_out)
+    _step_call("pkv_paged_append_rotary_axes",
+               _AXES_PACK.pack(_at(query), _at(key), _at(value), _at(query_out),
+                               key_cache.data_ptr(), value_cache.data_ptr(),
+                               slot_mapping.data_ptr(), _at(positions), _at(cos_cache),
+                               _at(sin_cache), _at(device_status), T, num_heads, kv_num_heads,
+                               D, BS, NB, rotary_dim, rows, axes,
+                               1 if rotary_interleaved else 0, code,
+                               PKV_F32 if tdt is f32 else code, pairs), raw)
     return query_out
 
 
@@ -747,6 +794,13 @@ def pkv_cross_attention_workspace_size(args: CrossAttentionArgs) -> int:
     return n.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _cross_workspace(device: int, *sizes) -> int:
+    """Workspace bytes for these sizes (the fields from num_tokens on) on this device."""
+    a = CrossAttentionArgs(*([256] * 8), None, *sizes, 0.0)
+    return pkv_cross_attention_workspace_size(a)
+
+
 def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_length,
                         key_seqlens, block_table, *, num_heads: int, kv_num_heads: int,
                         max_query_len: int = 0, scale: float = 0.0, output=None, lse=None,
@@ -756,42 +810,48 @@ def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_lengt
     the output [num_tokens, num_heads * head_size]; with ``lse`` (float32 [num_tokens,
     num_heads]) the log-sum-exp of each row's scores is written there."""
     torch = _torch()
-    _need(query=query, key_cache=key_cache, value_cache=value_cache,
-          cumulative_sequence_length=cumulative_sequence_length, key_seqlens=key_seqlens,
-          block_table=block_table)
-    dt = query.dtype
-    if dt not in (torch.float16, torch.bfloat16):
+    if (query is None or key_cache is None or value_cache is None or block_table is None or
+            cumulative_sequence_length is None or key_seqlens is None):
+        _need(query=query, key_cache=key_cache, value_cache=value_cache,
+              cumulative_sequence_length=cumulative_sequence_length, key_seqlens=key_seqlens,
+              block_table=block_table)
+    dt, i32 = query.dtype, torch.int32
+    if dt is torch.float16:
+        code = PKV_F16
+    elif dt is torch.bfloat16:
+        code = PKV_BF16
+    else:
         raise TypeError(f"query: expected float16 or bfloat16, got {dt}")
     if key_cache.dim() != 4:
         raise ValueError("key_cache: [num_blocks, block_size, kv_num_heads, head_size]")
-    NB, BS, Hkv, D = key_cache.shape
+    NB, BS, _, D = key_cache.shape
     T = query.shape[0] if query.dim() == 2 else -1
     B = key_seqlens.shape[0] if key_seqlens.dim() == 1 else -1
-    hidden = (T, num_heads * D)
-    _check_tensors(stream, query=(query, dt, hidden), output=(output, dt, hidden),
-                   key_cache=(key_cache, dt, (NB, BS, kv_num_heads, D)),
-                   value_cache=(value_cache, dt, (NB, BS, kv_num_heads, D)),
-                   key_seqlens=(key_seqlens, torch.int32, (B,)),
-                   cumulative_sequence_length=(cumulative_sequence_length, torch.int32,
-                                               (B + 1,)),
-                   block_table=(block_table, torch.int32, (B, None)),
-                   lse=(lse, torch.float32, (T, num_heads)),
-                   workspace=(workspace, torch.uint8, (None,)),
-                   device_status=(device_status, torch.int32, (1,)))
-    made = None
+    MB = block_table.shape[1] if block_table.dim() == 2 else -1
+    hidden, pool = (T, num_heads * D), (NB, BS, kv_num_heads, D)
+    raw = _check_tensors(stream, (
+        ("query", query, dt, hidden), ("output", output, dt, hidden),
+        ("key_cache", key_cache, dt, pool), ("value_cache", value_cache, dt, pool),
+        ("key_seqlens", key_seqlens, i32, (B,)),
+        ("cumulative_sequence_length", cumulative_sequence_length, i32, (B + 1,)),
+        ("block_table", block_table, i32, (B, MB)),
+        ("lse", lse, torch.float32, (T, num_heads)),
+        ("workspace", workspace, torch.uint8, None if workspace is None else workspace.shape),
+        ("device_status", device_status, i32, (1,))))
     if output is None:
-        output = made = torch.empty(hidden, dtype=dt, device=query.device)
-    a = make_cross_args(query, key_cache, value_cache, cumulative_sequence_length, key_seqlens,
-                        block_table, output, lse, num_heads=num_heads,
-                        kv_num_heads=kv_num_heads, max_query_len=max_query_len, scale=scale,
-                        device_status=device_status)
-    need = pkv_cross_attention_workspace_size(a)
-    scratch = None
+        output = torch.empty(hidden, dtype=dt, device=query.device)
+        _keep(stream, output)
+    sizes = (T, B, num_heads, kv_num_heads, D, BS, NB, MB, max_query_len, code)
+    need = _cross_workspace(query.get_device(), *sizes)
     if workspace is None or workspace.numel() < need:
-        workspace = scratch = torch.empty(need, dtype=torch.uint8, device=query.device)
-    _check("pkv_cross_attention",
-           load_library().pkv_cross_attention(ctypes.byref(a), workspace.data_ptr(), need,
-                                              _step_stream(stream, made, scratch)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+        _keep(stream, workspace)
+    _step_call("pkv_cross_attention",
+               _CROSS_PACK.pack(query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                cumulative_sequence_length.data_ptr(), key_seqlens.data_ptr(),
+                                block_table.data_ptr(), output.data_ptr(), _at(lse),
+                                _at(device_status), *sizes, scale),
+               workspace.data_ptr(), need, raw)
     return output
 
 
