@@ -5,13 +5,13 @@
 // S = Q K^T and O += P V for both halves (4 * 128 * 128 * D multiply-adds); the halves take
 // turns, so one half's softmax runs while the other half's products do:
 //   warps 0-3, 4-7  softmax of half 0, 1: a thread owns a row (one TMEM lane). It reads its 128
-//                   scores, raises its running maximum only when they exceed it by 2^8 (then O
-//                   and l are rescaled), writes the weights, rounded once to T, over the scores
+//                   scores and their maximum (TMEM loads reduce on the way), raises its running
+//                   maximum only when they exceed it by 2^8 (then O and l are rescaled), writes the weights, rounded once to T, over the scores
 //                   in TMEM, and at the end writes its output row, or its piece.
 //   warps 8, 10     one elected lane each issues the tcgen05.mma of half 0, 1 in the order
 //                   S(0) PV(0) S(1) PV(1) ...: products of one issuing thread run in order, so S
 //                   may overwrite the weights that the PV before it reads, and a full S tells
-//                   that the O of that half is complete and the K and V tiles so far are read.
+//                   that the O of that half is complete.
 //                   The whole warp runs the loop and a lane is elected for the instructions: from
 //                   a lane that runs alone a tcgen05.mma took 85 to 110 cycles, so 56 to 71.
 //   warps 9, 11     load by TMA into 128-byte-swizzled shared memory: Q of the halves, and one
@@ -119,12 +119,36 @@ struct Wait {   // bounded waits that give up together
     *abort = 1;
     return false;
   }
+  // the same for a whole warp (every lane asks: with one lane alone and a vote behind it the
+  // kernel took a fifth longer)
+  __device__ __forceinline__ bool warp(int bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(bar, parity)) != 0;
+  }
 };
 
 __device__ __forceinline__ void arrive(uint64_t* bar, uint32_t count = 1) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(count)
                : "memory");
 }
+
+// a place in a ring of N stages and the parity of its round
+template <int N>
+struct Place {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step(int n) {
+    stage += n;
+    if (stage >= N) {   // once for the steps of a loop
+      if (n > N) {
+        phase ^= (uint32_t)(stage / N) & 1u;
+        stage %= N;
+      } else {
+        phase ^= 1u;
+        stage -= N;
+      }
+    }
+  }
+};
 // D (+)= A B with A in TMEM
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -176,6 +200,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const float (&v)[16]) {
       : "memory");
 }
 
+// 32 consecutive fp32 columns of this thread's TMEM lane and the largest of them (NaN passed over)
+__device__ __forceinline__ void tmem_ld32_max(uint32_t at, float (&v)[32], float& top) {
+  uint32_t r[32], m;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(m)
+      : "r"(at));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  top = __uint_as_float(m);
+}
+
 // two floats in a register pair, and arithmetic on both at once (each rounded as alone)
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
   uint64_t r;
@@ -218,8 +260,6 @@ struct Part {
   __device__ __forceinline__ int first(int half) const { return shared ? half : 0; }
   __device__ __forceinline__ int stride() const { return shared ? 2 : 1; }
   __device__ __forceinline__ int count(int half) const { return shared ? (n + 1 - half) / 2 : n; }
-  // arrivals of a half that release a ring tile (2 in all)
-  __device__ __forceinline__ uint32_t weight() const { return halves == 2 ? 1 : 2; }
 };
 __device__ __forceinline__ Part part_of(const CrossParams& p, const Cursor& c, int64_t left) {
   Part t;
@@ -469,6 +509,8 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
   const int lane = threadIdx.x & 31, R = p.box_keys;
   int flags = 0;
   uint32_t use = (uint32_t)kv, issued = 0;   // ring tile, tiles issued
+  Place<L::kStages> to;
+  to.step(kv);
   uint32_t* seen_words = reinterpret_cast<uint32_t*>(sm + L::kSeen);
   uint32_t q_use[2] = {0, 0};
   const uint32_t every = R > 0 ? 0xffffffffu >> (32 - kTileKeys / R) : 0u;   // boxes of a tile
@@ -506,7 +548,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
     const int PT = p.tile_pos / 2;
     for (int h = 0; kv == 0 && h < (t.shared ? 2 : t.halves); ++h) {
       if (q_use[h] > 0 &&
-          !__all_sync(0xffffffffu, wait(kQEmpty + h, (q_use[h] - 1) & 1u)))
+          !wait.warp(kQEmpty + h, (q_use[h] - 1) & 1u))
         return false;
       ++q_use[h];
       if (lane == 0) {
@@ -536,11 +578,12 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       const uint32_t boxes = __ballot_sync(0xffffffffu, mapped);
       const bool clear = R > 0 && (j + 1) * kTileKeys <= c.q.keys && boxes == every;
       ahead = lookup(key0 + kTileKeys);
-      const uint32_t st = use % L::kStages, round = use / L::kStages;
-      if (round > 0 && !__all_sync(0xffffffffu, wait(kEmpty + (int)st, (round - 1) & 1u)))
+      if (use >= (uint32_t)L::kStages &&
+          !wait.warp(kEmpty + to.stage, to.phase ^ 1u))
         return false;
-      unsigned char* dst = sm + L::kRing + st * L::kTile;
-      uint64_t* full = bars + kFull + st;
+      unsigned char* dst = sm + L::kRing + to.stage * L::kTile;
+      uint64_t* full = bars + kFull + to.stage;
+      to.step(2);
       // Which keys take part: key 4 i + x of the step is bit i of word x. An entry of the 8 is
       // written again when the K tile 8 steps on has room: then a score tile at least 2 steps on
       // was full, so every softmax warp that reads the entry was done with the steps before it.
@@ -642,12 +685,10 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
   constexpr uint32_t id_o = tc::idesc_f16(128, D, false, true) | fmt;
   const uint32_t q_at = smem_u32(sm + L::kQ) + half * L::kTile, ring = smem_u32(sm + L::kRing);
   const uint32_t s_at = run.tmem + half * 128, o_at = run.tmem + 256 + half * 128;
-  uint32_t use = 0, q_use = 0, p_use = 0, turn = 0;
+  uint32_t q_use = 0, p_use = 0, turn = 0;
+  Place<L::kStages> next;   // of the part's first K tile
   const auto ready = [&](int bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
-  };
-  const auto full = [&](uint32_t u) {
-    return ready(kFull + (int)(u % L::kStages), (u / L::kStages) & 1u);
+    return wait.warp(bar, parity);
   };
   // The halves issue by turns, half 0 first: without it the tensor core shares itself out
   // between both, they end together, and then both softmaxes run while it idles.
@@ -658,23 +699,23 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
     return ready(kTurn + 1, n & 1u);
   };
   each_part(p, run, [&](const Part& t, const Cursor&, int) {
-    const uint32_t base = use;   // ring tile of K of step 0; V of step j is base + 2 j + 1
-    use += 2 * t.n;
+    Place<L::kStages> k = next, v = next;   // K of step j is 2 j tiles on, V 2 j + 1
+    next.step(2 * t.n);
     if (!t.active(half)) return true;
     const bool both = t.shared || t.halves == 2;
-    const int n = t.count(half);
+    const int n = t.count(half), apart = 2 * t.stride();
+    k.step(2 * t.first(half));
+    v.step(2 * t.first(half) + 1);
     // round i: PV of this half's step i - 1, S of step i
     for (int i = 0; i <= n; ++i) {
       const bool pv = i > 0, s = i < n;
-      const uint32_t k = base + 2 * (t.first(half) + t.stride() * i), v = k - 2 * t.stride() + 1;
       if (i == 0 && !ready(kQFull + half, q_use++ & 1u)) return false;
-      if (pv && !full(v)) return false;
-      if (s && !full(k)) return false;
+      if (pv && !ready(kFull + v.stage, v.phase)) return false;
+      if (s && !ready(kFull + k.stage, k.phase)) return false;
       if (!my_turn(both)) return false;
       if (pv && !ready(kPFull + half, p_use & 1u)) return false;
       tc::fence_after_sync();
-      const uint32_t va = ring + (v % L::kStages) * L::kTile;
-      const uint32_t ka = ring + (k % L::kStages) * L::kTile;
+      const uint32_t va = ring + v.stage * L::kTile, ka = ring + k.stage * L::kTile;
       if (pv) {
         const auto products = [&](int ks) {
           mma_tmem_a(o_at, s_at + (uint32_t)ks * 8u,
@@ -693,6 +734,7 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
           for (int ks = 4; ks < 8; ++ks) products(ks);
         }
         __syncwarp();
+        v.step(apart);
       }
       if (elect()) {
         if (s) {
@@ -710,6 +752,7 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
         if (both) arrive(bars + kTurn + 1 - half);
       }
       __syncwarp();
+      k.step(apart);
     }
     if (both && n < t.count(0)) {   // as many turns as the other half
       if (!my_turn(true)) return false;
@@ -738,11 +781,8 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
   const float sl2 = fabsf(p.scale_log2);   // a negative scale turns the scores around
   const uint64_t scale2 = pair_of(sl2, sl2);
   uint32_t s_use = 0, o_use = 0, use = 0, pair_use = 0;
+  Place<L::kStages> next;   // of the part's first K tile
   float2* pair_ml = reinterpret_cast<float2*>(sm + L::kPairMl) + r;
-  // the products that read ring tile u for this half (or for both, if no other reads it) are done
-  const auto release = [&](uint32_t u, uint32_t weight) {
-    arrive(bars + kEmpty + u % L::kStages, weight);
-  };
   const auto hand_over = [&](int bar) {   // the warp's weights so far, to the products
     tc::tmem_wait_st();
     tc::fence_before_sync();
@@ -751,50 +791,56 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
   };
   each_part(p, run, [&](const Part& t, const Cursor&, int index) {
     uint32_t k = use + 2 * t.first(half);   // ring tile of this half's K; V is k + 1
+    Place<L::kStages> tile = next;          // the next tile to be given back: K, V, K, V ...
     use += 2 * t.n;
+    next.step(2 * t.n);
     if (!t.active(half)) return true;
     const uint32_t apart = 2 * t.stride();
+    tile.step(2 * t.first(half));
+    // Two arrivals free a tile: the halves', or both from the one half that reads it. A full S tells
+    // that the products in front of it are done. (Committed by the issuing lane instead, an arrival
+    // took it some 90 cycles.)
+    const auto give_back = [&](int further) {
+      arrive(bars + kEmpty + tile.stage, t.halves == 2 ? 1 : 2);
+      tile.step(further);
+    };
     float m = -INFINITY, l = 0.f;
     const int n = t.count(half);
     for (int j = 0; j < n; ++j, k += apart) {
       // the loads and stores of TMEM below are the whole warp's
-      if (!__all_sync(0xffffffffu, wait(kSFull + half, s_use & 1u))) return false;
+      if (!wait.warp(kSFull + half, s_use & 1u)) return false;
       ++s_use;
       tc::fence_after_sync();
-      float v[128];
+      if (r == 0) {
+        if (j > 0) give_back((int)apart - 1);   // V of the step before
+        give_back(1);                           // K of this one
+      }
+      float v[128], e[4];
       {
         float (*v32)[32] = reinterpret_cast<float (*)[32]>(v);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) tc::tmem_ld32(s_at + x * 32, v32[x]);
+        for (int x = 0; x < 4; ++x) tmem_ld32_max(s_at + x * 32, v32[x], e[x]);
       }
       const uint4 seen = *reinterpret_cast<const uint4*>(sm + L::kSeen + (k / 2 % 8) * 16);
       tc::tmem_wait_ld();
-      if (r == 0) {
-        release(k, t.weight());                              // K of this step
-        if (j > 0) release(k - apart + 1, t.weight());       // V of the one before
-      }
-      if (p.scale_log2 < 0.f) {
-#pragma unroll
-        for (int x = 0; x < 128; ++x) v[x] = -v[x];
-      }
-      if ((seen.x & seen.y & seen.z & seen.w) != 0xffffffffu) {
-        constexpr float hide = -INFINITY;
+      const bool masked = (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu;
+      if (masked || p.scale_log2 < 0.f) {   // the maximum is another one
+        const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
-          v[4 * x] = (seen.x >> x) & 1u ? v[4 * x] : hide;
-          v[4 * x + 1] = (seen.y >> x) & 1u ? v[4 * x + 1] : hide;
-          v[4 * x + 2] = (seen.z >> x) & 1u ? v[4 * x + 2] : hide;
-          v[4 * x + 3] = (seen.w >> x) & 1u ? v[4 * x + 3] : hide;
+          v[4 * x] = (seen.x >> x) & 1u ? sign * v[4 * x] : -INFINITY;
+          v[4 * x + 1] = (seen.y >> x) & 1u ? sign * v[4 * x + 1] : -INFINITY;
+          v[4 * x + 2] = (seen.z >> x) & 1u ? sign * v[4 * x + 2] : -INFINITY;
+          v[4 * x + 3] = (seen.w >> x) & 1u ? sign * v[4 * x + 3] : -INFINITY;
         }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) e[y] = fmaxf(v[2 * y], v[2 * y + 1]);
+#pragma unroll
+        for (int x = 8; x < 128; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) e[y] = max3(e[y], v[x + 2 * y], v[x + 2 * y + 1]);
       }
-      float e[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) e[x] = fmaxf(v[2 * x], v[2 * x + 1]);
-#pragma unroll
-      for (int x = 16; x < 128; x += 16)
-#pragma unroll
-        for (int y = 0; y < 8; ++y) e[y] = max3(e[y], v[x + 2 * y], v[x + 2 * y + 1]);
-      float top = fmaxf(max3(e[0], e[1], max3(e[2], e[3], e[4])), max3(e[5], e[6], e[7]));
+      float top = max3(e[0], e[1], fmaxf(e[2], e[3]));
       top *= sl2;   // -inf when nothing of the step is seen
       if (__any_sync(0xffffffffu, m == -INFINITY ? top != -INFINITY : top > m + kRaise)) {
         const bool first = m == -INFINITY;
@@ -834,10 +880,10 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
       l += low_of(sum[0]) + high_of(sum[0]);
       hand_over(kPRest);
     }
-    if (!__all_sync(0xffffffffu, wait(kOFull + half, o_use & 1u))) return false;
+    if (!wait.warp(kOFull + half, o_use & 1u)) return false;
     ++o_use;
     tc::fence_after_sync();
-    if (r == 0) release(k - apart + 1, t.weight());
+    if (r == 0) give_back(1);
     float mine_by = 1.f, other_by = 0.f;   // what this half's O counts for, and the other's
     if (t.shared) {
       if (half == 1) {
@@ -845,11 +891,11 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive(bars + kPair);
-        if (!__all_sync(0xffffffffu, wait(kPairRead, pair_use++ & 1u))) return false;
+        if (!wait.warp(kPairRead, pair_use++ & 1u)) return false;
         tc::fence_after_sync();
         return true;
       }
-      if (!__all_sync(0xffffffffu, wait(kPair, pair_use++ & 1u))) return false;
+      if (!wait.warp(kPair, pair_use++ & 1u)) return false;
       tc::fence_after_sync();
       const float2 other = *pair_ml;
       const float top = fmaxf(l == 0.f ? -INFINITY : m, other.y == 0.f ? -INFINITY : other.x);
