@@ -737,6 +737,8 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
         v.step(apart);
       }
       if (elect()) {
+        // the other half's turn; it takes about as long to notice as the S below to be issued
+        if (both) arrive(bars + kTurn + 1 - half);
         if (s) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -749,7 +751,6 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
         } else {
           tc::commit(bars + kOFull + half);
         }
-        if (both) arrive(bars + kTurn + 1 - half);
       }
       __syncwarp();
       k.step(apart);
