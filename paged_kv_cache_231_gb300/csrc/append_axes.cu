@@ -74,31 +74,16 @@ __device__ __forceinline__ void report(const AxesParams& p, const Token& k) {
     flag_status(p.status, (k.known ? 0 : PKV_DEV_BAD_POSITION) | (k.fits ? 0 : PKV_DEV_BAD_SLOT));
 }
 
-// items: items of a token; tokens: tokens that a block holds side by side (1 when a token has
-// more items than threads). A thread does the same item of N tokens, `tokens` apart.
-template <typename T, typename TT, bool kSide, int N>
-__global__ void __launch_bounds__(kMaxThreads)
-    append_axes_items_kernel(const __grid_constant__ AxesParams p, int items, int tokens) {
-  // [N * tokens][4][R / 16] (cos, cos, sin, sin) of pairs 2 y and 2 y + 1 of item c at [y][c], so
-  // that neighbouring threads read neighbouring words; then (slot, flags) of each token
-  extern __shared__ __align__(16) float4 turn[];
-  const int half = p.R / 2, cpr = p.D / 8;
-  const int per_head = p.R / 16, rotated = (p.Hq + p.Hkv) * per_head;
-  const int plain = cpr - 2 * per_head;            // chunks of a rotated head behind rotary_dim
-  const int t0 = blockIdx.x * tokens * N;
-  const int mine = tokens > 1 ? threadIdx.x / items : 0;
-  const bool there = mine < tokens;
-  const int step = tokens > 1 ? items : blockDim.x;
-  int i = tokens > 1 ? threadIdx.x - mine * items : threadIdx.x;
-  int2* about = reinterpret_cast<int2*>(turn + N * tokens * per_head * 4);
-
-  // the two chunks of item i: where they are read and written from token 0 (slot 0) on, and what
-  // they are (0 query, 1 key, 2 value, 3 nothing)
+// The two chunks of item i of a token: where they are read and written from token 0 (slot 0) on.
+template <typename T>
+struct Item {
   const T* src[2];
   T* dst[2];
-  int kind[2];
-  const int q_row = p.Hq * p.D, kv_row = p.Hkv * p.D;
-  const auto place = [&](int i) {
+  int kind[2];   // 0 query, 1 key, 2 value, 3 nothing
+  template <bool kSide>
+  __device__ __forceinline__ void place(const AxesParams& p, int i) {
+    const int cpr = p.D / 8, per_head = p.R / 16, rotated = (p.Hq + p.Hkv) * per_head;
+    const int plain = cpr - 2 * per_head;   // chunks of a rotated head behind rotary_dim
     int h[2], ch[2];
     if (i < rotated) {
       h[0] = h[1] = i / per_head;
@@ -122,22 +107,165 @@ __global__ void __launch_bounds__(kMaxThreads)
       src[x] = static_cast<const T*>(kind[x] == 0 ? p.q : kind[x] == 1 ? p.k : p.v) + e;
       dst[x] = static_cast<T*>(kind[x] == 0 ? p.q_out : kind[x] == 1 ? p.kc : p.vc) + e;
     }
+  }
+  __device__ __forceinline__ void load(const AxesParams& p, int t, uint4 (&x)[2]) const {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      if (kind[y] < 3)
+        x[y] = __ldcs(reinterpret_cast<const uint4*>(
+            src[y] + (int64_t)t * (kind[y] == 0 ? p.q_stride : p.kv_stride)));
+  }
+  // about: the token's slot, and 1 for known | 2 for known and inside the pool
+  __device__ __forceinline__ void store(const AxesParams& p, int t, int2 about,
+                                        const uint4 (&x)[2]) const {
+    const int q_row = p.Hq * p.D, kv_row = p.Hkv * p.D;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      if (kind[y] == 0)
+        *reinterpret_cast<uint4*>(dst[y] + (int64_t)t * q_row) = x[y];
+      else if (kind[y] < 3 && (about.y & 2))
+        *reinterpret_cast<uint4*>(dst[y] + (int64_t)about.x * kv_row) = x[y];
+    }
+  }
+};
+
+// Turns the 8 pairs of an item; cs[y * apart]: (cos, cos, sin, sin) of pairs 2 y and 2 y + 1.
+template <typename T, bool kSide>
+__device__ __forceinline__ void turn_item(uint4 (&x)[2], const float4* cs, int apart) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&x[0]);
+  uint32_t* b = reinterpret_cast<uint32_t*>(&x[1]);
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const float4 c = cs[y * apart];
+    if constexpr (kSide) {        // a pair is one 32-bit word
+      uint32_t* z = y < 2 ? a + 2 * y : b + 2 * (y - 2);
+      const float2 u = Num<T>::to2(z[0]), v = Num<T>::to2(z[1]);
+      z[0] = Num<T>::from2(u.x * c.x - u.y * c.z, u.y * c.x + u.x * c.z);
+      z[1] = Num<T>::from2(v.x * c.y - v.y * c.w, v.y * c.y + v.x * c.w);
+    } else {
+      const float2 u = Num<T>::to2(a[y]), v = Num<T>::to2(b[y]);
+      a[y] = Num<T>::from2(u.x * c.x - v.x * c.z, u.y * c.y - v.y * c.w);
+      b[y] = Num<T>::from2(v.x * c.x + u.x * c.z, v.y * c.y + u.y * c.w);
+    }
+  }
+}
+
+// Many tokens of many items: a block stays and goes through groups of two tokens. While one group
+// is turned and written, the next one's rows and table entries are on their way and the slots and
+// positions of the one behind it, so that loads are under way all the time.
+constexpr int kPair = 2;
+template <typename T, typename TT, bool kSide>
+__global__ void __launch_bounds__(kMaxThreads)
+    append_axes_stream_kernel(const __grid_constant__ AxesParams p, int items) {
+  extern __shared__ __align__(16) float4 turn[];   // [2][kPair][4][R / 16], as below; then about
+  const int half = p.R / 2, per_head = p.R / 16, rotated = (p.Hq + p.Hkv) * per_head;
+  const int words = kPair * per_head * 4;          // of a group
+  int2* about = reinterpret_cast<int2*>(turn + 2 * words);   // [2][kPair]
+  const int i = threadIdx.x, groups = (p.T + kPair - 1) / kPair;
+  const bool mine = i < items;
+  Item<T> it;
+  if (mine) it.template place<kSide>(p, i);
+  // this thread's share of the gathering: pair gj of token gw of a group; the first threads look
+  // after the tokens themselves
+  const bool gathers = i < kPair * half;
+  const int gw = gathers ? i / half : 0, gj = gathers ? i - gw * half : 0;
+  const int* gpos = gathers ? p.pos + (int64_t)p.pair_axis[gj] * p.T : nullptr;
+  float* const put = reinterpret_cast<float*>(turn + (gw * 4 + (gj & 7) / 2) * per_head + gj / 8) + (gj & 1);
+  const int tw = i;                                // token of the group that this thread reports
+
+  const auto row_of = [&](int g) {                 // table row of this thread's pair, -1: none
+    const int t = g * kPair + gw;
+    return gathers && g < groups && t < p.T ? __ldg(gpos + t) : -1;
   };
+  const auto fetch = [&](int r, float& c, float& s) {
+    if (r >= 0 && r < p.P) {
+      const int64_t at = (int64_t)r * half + gj;
+      c = Num<TT>::to(__ldg(static_cast<const TT*>(p.cos) + at));
+      s = Num<TT>::to(__ldg(static_cast<const TT*>(p.sin) + at));
+    }
+  };
+  uint4 x[kPair][2], ahead[kPair][2];
+  const auto load = [&](int g, uint4 (&v)[kPair][2]) {
+#pragma unroll
+    for (int n = 0; n < kPair; ++n)
+      if (mine && g < groups && g * kPair + n < p.T) it.load(p, g * kPair + n, v[n]);
+  };
+  const auto token = [&](int g, int buf) {
+    const int t = g * kPair + tw;
+    if (tw < kPair && g < groups && t < p.T) {
+      const Token k = read_token(p, t);
+      report(p, k);
+      about[buf * kPair + tw] = make_int2(k.slot, (k.known ? 1 : 0) | (k.known && k.fits ? 2 : 0));
+    }
+  };
+
+  int g = blockIdx.x;
+  const int apart = gridDim.x;
+  float c = 0.f, s = 0.f;
+  load(g, x);
+  fetch(row_of(g), c, s);
+  int row = row_of(g + apart);
+  token(g, 0);
+  if (gathers) {
+    put[0] = c;
+    put[2] = s;
+  }
+  __syncthreads();
+  for (int buf = 0; g < groups; g += apart, buf ^= 1) {
+    load(g + apart, ahead);
+    fetch(row, c, s);
+    row = row_of(g + 2 * apart);
+    token(g + apart, buf ^ 1);
+#pragma unroll
+    for (int n = 0; n < kPair; ++n) {
+      const int t = g * kPair + n;
+      if (!mine || t >= p.T) break;
+      const int2 k = about[buf * kPair + n];
+      if (k.x < 0) continue;
+      if (i < rotated && (k.y & 1))
+        turn_item<T, kSide>(x[n], turn + buf * words + n * 4 * per_head + i % per_head, per_head);
+      it.store(p, t, k, x[n]);
+    }
+    if (gathers) {
+      put[(buf ^ 1) * words * 4] = c;
+      put[(buf ^ 1) * words * 4 + 2] = s;
+    }
+#pragma unroll
+    for (int n = 0; n < kPair; ++n)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) x[n][y] = ahead[n][y];
+    __syncthreads();
+  }
+}
+
+// items: items of a token; tokens: tokens that a block holds side by side (1 when a token has
+// more items than threads). A thread does the same item of N tokens, `tokens` apart.
+template <typename T, typename TT, bool kSide, int N>
+__global__ void __launch_bounds__(kMaxThreads)
+    append_axes_items_kernel(const __grid_constant__ AxesParams p, int items, int tokens) {
+  // [N * tokens][4][R / 16] (cos, cos, sin, sin) of pairs 2 y and 2 y + 1 of item c at [y][c], so
+  // that neighbouring threads read neighbouring words; then (slot, flags) of each token
+  extern __shared__ __align__(16) float4 turn[];
+  const int half = p.R / 2, per_head = p.R / 16, rotated = (p.Hq + p.Hkv) * per_head;
+  const int t0 = blockIdx.x * tokens * N;
+  const int mine = tokens > 1 ? threadIdx.x / items : 0;
+  const bool there = mine < tokens;
+  const int step = tokens > 1 ? items : blockDim.x;
+  int i = tokens > 1 ? threadIdx.x - mine * items : threadIdx.x;
+  int2* about = reinterpret_cast<int2*>(turn + N * tokens * per_head * 4);
+
+  Item<T> it;
   uint4 x[N][2];
+  const bool any = there && i < items;
   const auto load = [&]() {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int t = t0 + mine + n * tokens;
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-        if (t < p.T && kind[y] < 3)
-          x[n][y] = __ldcs(reinterpret_cast<const uint4*>(
-              src[y] + (int64_t)t * (kind[y] == 0 ? p.q_stride : p.kv_stride)));
+      if (t < p.T) it.load(p, t, x[n]);
     }
   };
-  const bool any = there && i < items;
   if (any) {
-    place(i);
+    it.template place<kSide>(p, i);
     load();
   }
   if (threadIdx.x < N * tokens && t0 + threadIdx.x < p.T) {
@@ -164,36 +292,13 @@ __global__ void __launch_bounds__(kMaxThreads)
       if (t0 + w >= p.T) break;
       const int2 k = about[w];
       if (k.x < 0) continue;
-      if (i < rotated && (k.y & 1)) {
-        const float4* cs = turn + w * 4 * per_head + i % per_head;
-        uint32_t* a = reinterpret_cast<uint32_t*>(&x[n][0]);
-        uint32_t* b = reinterpret_cast<uint32_t*>(&x[n][1]);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float4 c = cs[y * per_head];
-          if constexpr (kSide) {        // a pair is one 32-bit word
-            uint32_t* z = y < 2 ? a + 2 * y : b + 2 * (y - 2);
-            const float2 u = Num<T>::to2(z[0]), v = Num<T>::to2(z[1]);
-            z[0] = Num<T>::from2(u.x * c.x - u.y * c.z, u.y * c.x + u.x * c.z);
-            z[1] = Num<T>::from2(v.x * c.y - v.y * c.w, v.y * c.y + v.x * c.w);
-          } else {
-            const float2 u = Num<T>::to2(a[y]), v = Num<T>::to2(b[y]);
-            a[y] = Num<T>::from2(u.x * c.x - v.x * c.z, u.y * c.y - v.y * c.w);
-            b[y] = Num<T>::from2(v.x * c.x + u.x * c.z, v.y * c.y + u.y * c.w);
-          }
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        if (kind[y] == 0)
-          *reinterpret_cast<uint4*>(dst[y] + (int64_t)(t0 + w) * q_row) = x[n][y];
-        else if (kind[y] < 3 && (k.y & 2))
-          *reinterpret_cast<uint4*>(dst[y] + (int64_t)k.x * kv_row) = x[n][y];
-      }
+      if (i < rotated && (k.y & 1))
+        turn_item<T, kSide>(x[n], turn + w * 4 * per_head + i % per_head, per_head);
+      it.store(p, t0 + w, k, x[n]);
     }
     i += step;
     if (tokens > 1 || i >= items) break;
-    place(i);
+    it.template place<kSide>(p, i);
     load();
   }
 }
@@ -262,12 +367,25 @@ void launch_typed(const AxesParams& p, cudaStream_t s) {
   const int tokens = items * 2 <= kThreads ? kThreads / items : 1;
   const int threads = tokens > 1 ? (tokens * items + 31) / 32 * 32
                                  : (items < kMaxThreads ? (items + 31) / 32 * 32 : kMaxThreads);
-  // Many tokens: four to a thread, so that enough of their loads are under way at once; few: one,
-  // so that they are spread over the SMs. MEASURED
-  if (p.T >= 4 * tokens * 2 * device_sms())
+  const int sms = device_sms();
+  if (tokens == 1 && items <= kMaxThreads && p.T >= 8 * sms && p.R <= kMaxThreads / kPair * 2) {
+    // Many tokens of many items stay with the blocks that fit the SMs (80 registers a thread):
+    // 32768 tokens of 384 items take 133 us (6182 GB/s, 91 % of measured copy bandwidth), 152 us
+    // with a block for four tokens, 272 us with one for each.
+    int block = items > p.R ? items : p.R;   // R: kPair * R / 2 gathering threads
+    block = (block + 31) / 32 * 32;
+    const int per_sm = 65536 / (block * 80) > 1 ? 65536 / (block * 80) : 1;
+    const size_t smem = 2 * (sizeof(float4) * kPair * (p.R / 4) + sizeof(int2) * kPair);
+    if (p.interleaved)
+      append_axes_stream_kernel<T, TT, true><<<per_sm * sms, block, smem, s>>>(p, items);
+    else
+      append_axes_stream_kernel<T, TT, false><<<per_sm * sms, block, smem, s>>>(p, items);
+  } else if (p.T >= 8 * tokens * sms) {
+    // four tokens to a thread, so that enough of their loads are under way at once
     launch_items<T, TT, 4>(p, items, tokens, threads, s);
-  else
+  } else {   // few: spread over the SMs (64 tokens of 384 items: 3.4 us)
     launch_items<T, TT, 1>(p, items, tokens, threads, s);
+  }
 }
 
 }  // namespace

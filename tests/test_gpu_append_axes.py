@@ -168,3 +168,51 @@ def test_captured_and_replayed():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref[0]) and torch.equal(kc, ref[1]) and torch.equal(vc, ref[2])
+
+
+def _slices_give_the_whole(c, step):
+    """One call over all tokens equals calls over `step` of them at a time, bit for bit."""
+    whole = c.gpu()
+    kc, vc = c.kc.to(DEV), c.vc.to(DEV)
+    out = torch.full_like(whole[0], 7.0) if c.query else None
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    cos, sin = c.cos.to(DEV), c.sin.to(DEV)
+    for t in range(0, c.T, step):
+        part = lambda x: None if x is None else x[t:t + step].contiguous().to(DEV)  # noqa: E731
+        B.pkv_paged_append_rotary_axes(
+            part(c.q), part(c.k), part(c.v), kc, vc, i32(c.slots[t:t + step]),
+            i32(c.pos[:, t:t + step]), num_heads=c.hq, kv_num_heads=c.hkv, cos_cache=cos,
+            sin_cache=sin, rotary_dim=c.r, pair_axis=c.axis, rotary_interleaved=c.interleaved,
+            query_out=None if out is None else out[t:t + step], rotate_query=out is not None,
+            device_status=st)
+    torch.cuda.synchronize()
+    if out is not None:
+        assert torch.equal(out, whole[0])
+    assert torch.equal(kc, whole[1]) and torch.equal(vc, whole[2])
+    assert int(st.item()) == whole[3]
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(tokens=2433, num_heads=16, kv_heads=4, head_size=128, rotary_dim=128),
+    dict(tokens=1500, num_heads=16, kv_heads=4, head_size=128, rotary_dim=64, packed=True),
+    dict(tokens=1217, num_heads=9, kv_heads=9, head_size=128, rotary_dim=0, axes=0, query=False),
+    dict(tokens=10001, num_heads=4, kv_heads=2, head_size=64, rotary_dim=64, turns=True),
+    dict(tokens=30007, num_heads=1, kv_heads=1, head_size=64, rotary_dim=32),
+    dict(tokens=1300, num_heads=96, kv_heads=8, head_size=128, rotary_dim=128, axes=2),
+], ids=str)
+def test_many_tokens_equal_few_at_a_time(kw, interleaved):
+    c = Case(9, interleaved=interleaved, pad=(1, 2, 700, kw["tokens"] - 1), **kw)
+    if c.r:
+        c.pos[0, 5], c.pos[-1, 900] = -4, 300
+    c.slots[44] = c.nb * c.bs
+    if c.r == 0:
+        c.pos = np.zeros((1, c.T), np.int32)
+    _slices_give_the_whole(c, 500)
+
+
+def test_many_tokens_match_the_oracle():
+    c = Case(10, 1290, num_heads=16, kv_heads=4, head_size=128, rotary_dim=128, dtype="bf16",
+             packed=True, turns=True, pad=(0, 77, 1289))
+    c.pos[1, 1000] = 300
+    c.check()
