@@ -462,8 +462,9 @@ typedef struct pkv_schedule_args {
  * whose held block is a hole gets slot -1 and sets PKV_DEV_BAD_BLOCK.
  * The result depends on the inputs alone; a second call with the same inputs gives the same.
  * past_seqlens and new_seqlens must not overlap the outputs. No workspace. Supported:
- * batch <= 8192, num_blocks <= 2^20, num_blocks * block_size, batch * max_blocks,
- * max_blocks * block_size and num_tokens below 2^31; otherwise PKV_ERR_UNSUPPORTED. */
+ * batch <= 8192, num_blocks <= 2^20; num_blocks * block_size, batch * max_blocks and
+ * num_tokens below 2^31, max_blocks * block_size below 2^31 - 16; otherwise
+ * PKV_ERR_UNSUPPORTED. */
 int pkv_paged_schedule(const pkv_schedule_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------------
@@ -511,8 +512,8 @@ typedef struct pkv_append_axes_args {
  *   leading member own*cos - partner*sin, trailing member own*cos + partner*sin,
  * in 32-bit arithmetic, rounded once to `dtype`; elements from rotary_dim on are copied.
  * The key row goes to pool row s of key_cache, the value row to value_cache, the query row
- * to row i of query_out. A negative slot is padding: nothing of the token is read beyond
- * it, nothing is written. A slot past the pool (PKV_DEV_BAD_SLOT): K and V are not
+ * to row i of query_out. A negative slot is padding: whatever the token's rows and
+ * positions hold, nothing is written for it. A slot past the pool (PKV_DEV_BAD_SLOT): K and V are not
  * written, the query is. A position outside [0, rotary_positions) on an axis that some pair
  * uses (PKV_DEV_BAD_POSITION): K and V are not written, the query row is copied unrotated.
  * Two tokens of one slot leave either's row. query_out and the caches must not overlap the
@@ -563,8 +564,10 @@ int pkv_cross_attention_workspace_size(const pkv_cross_attention_args* args, siz
  * max_query_len, or whose key_seqlens entry is negative, get zero rows (lse -inf) and set
  * PKV_DEV_BAD_SEQUENCE; so do rows that no sequence covers, without the flag.
  * The order of summation depends on the sizes and the device's SM count alone: equal calls
- * give equal bits. workspace: as in pkv_paged_attention (256-byte aligned, contents need
- * not be initialised, one per call in flight). Supported: head_size in {64, 128},
+ * give equal bits. Output and lse must not overlap the inputs. workspace: as in
+ * pkv_paged_attention (256-byte aligned, contents need not be initialised, one per call in
+ * flight). After PKV_DEV_TIMEOUT the rows of the tiles that gave up, and those joined from
+ * their pieces, are not valid. Supported: head_size in {64, 128},
  * num_heads / kv_num_heads <= 16; otherwise PKV_ERR_UNSUPPORTED. */
 int pkv_cross_attention(const pkv_cross_attention_args* args, void* workspace,
                         size_t workspace_bytes, void* stream);
@@ -586,7 +589,8 @@ int64_t pkv_launch_count(void);
 void pkv_profiler_enable(int on);
 
 /* Testing hook for the give-up path of the tensor-core kernels' bounded waits (the
- * tcgen05 prefill and the two block-sparse partial kernels). The pages have no
+ * tcgen05 prefill, the two block-sparse partial kernels and the cross attention's kernel for
+ * many rows). The pages have no
  * counterpart. max_polls replaces the default poll bound of every such wait (0 restores
  * the default); with withhold_first_copy != 0 (which needs max_polls > 0) every CTA of
  * those kernels announces its first bulk copy (the first K box of its first prefill

@@ -745,7 +745,7 @@ def pkv_paged_append_rotary_axes(query, key, value, key_cache, value_cache, slot
         rows = cos_cache.shape[0] if cos_cache.dim() == 2 else -1
         if cos_cache.dtype is dt:
             tdt = dt
-        pairs = bytes(half) if pair_axis is None else bytes(pair_axis)
+        pairs = bytes(half) if pair_axis is None else bytes(list(pair_axis))
         if len(pairs) != half or half > MAX_ROTARY_PAIRS:
             raise ValueError(f"pair_axis: one axis for each of {half} pairs (at most "
                              f"{MAX_ROTARY_PAIRS}), got {len(pairs)}")

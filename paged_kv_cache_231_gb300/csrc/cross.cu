@@ -502,24 +502,21 @@ size_t cross_layout(CrossParams* p, char* base) {
   const int sms = device_sms();
   p->few = 16 / p->G;
   p->tile_pos = 2 * (128 / p->G);
-  // no more units than the longest possible work has runs of the least length
-  const int64_t keys = (int64_t)p->MB * p->BS;
-  const int64_t seqs = p->T < p->B ? p->T : p->B;
-  const int64_t steps = seqs * p->Hkv * ((keys + few_keys(p->D) - 1) / few_keys(p->D));
-  const int64_t runs = (steps + kLeastFew - 1) / kLeastFew;
-  int64_t ctas = (runs + kWarps - 1) / kWarps;
-  ctas = ctas < 1 ? 1 : ctas > sms ? sms : ctas;
-  p->few_units = (int)ctas * kWarps;
+  // no more units than the longest possible work has runs of the least length (in floating point:
+  // the products may pass 64 bits)
+  const double keys = (double)p->MB * p->BS, seqs = p->T < p->B ? p->T : p->B;
+  const double runs = seqs * p->Hkv * (keys / few_keys(p->D) + 1) / kLeastFew;
+  const int ctas = runs >= (double)sms * kWarps ? sms : (int)(runs / kWarps) + 1;
+  p->few_units = ctas * kWarps;
   p->few_heads = kWarps;
   while (p->Hkv % p->few_heads != 0) p->few_heads /= 2;
   p->few_rows = (p->max_q < p->few ? p->max_q : p->few) * p->G;
   p->tile_units = 0;
   if (p->max_q > p->few) {
-    const int64_t tiles = (p->T + p->tile_pos - 1) / p->tile_pos + seqs;
-    const int64_t blocks = tiles * p->Hkv * ((keys + kTileKeys - 1) / kTileKeys);
-    const int64_t t = (blocks + kLeastTile - 1) / kLeastTile;
-    const int64_t most = sms < kMaxTileUnits ? sms : kMaxTileUnits;
-    p->tile_units = (int)(t < 1 ? 1 : t > most ? most : t);
+    const double tiles = (double)p->T / p->tile_pos + seqs;
+    const double pieces = tiles * p->Hkv * (keys / kTileKeys + 1) / kLeastTile;
+    const int most = sms < kMaxTileUnits ? sms : kMaxTileUnits;
+    p->tile_units = pieces >= (double)most ? most : (int)pieces + 1;
   }
   p->box_keys = 0;
   if (p->BS % 8 == 0 && p->NB * p->BS <= INT32_MAX) {

@@ -421,6 +421,9 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     weight = whole > 0 ? max(share - had, (int64_t)1)
                        : tid < max(quotient(rest + kLeast - 1, kLeast), (int64_t)1);
   }
+  // below 2^20 each, so that the product below stays below 2^63
+  const int down = max(0, 44 - __clzll(share));
+  if (weight > 0) weight = max(weight >> down, (int64_t)1);
   int64_t all;
   const int64_t upto = block_sum<kThreads>(weight, &all, scratch);
   if (tid == 0) cut[0] = from;

@@ -87,7 +87,7 @@ int pkv_paged_schedule(const pkv_schedule_args* a, void* stream) {
     return PKV_ERR_SHAPE;
   if (a->batch > kScheduleMaxBatch || a->num_blocks > kScheduleMaxBlocks ||
       a->block_size > kMax32 || a->max_blocks > kMax32 || a->num_tokens >= kMax32 ||
-      a->num_blocks * a->block_size > kMax32 || a->max_blocks * a->block_size > kMax32 ||
+      a->num_blocks * a->block_size > kMax32 || a->max_blocks * a->block_size > kMax32 - 16 ||
       a->batch * a->max_blocks > kMax32)
     return PKV_ERR_UNSUPPORTED;
   if (!a->past_seqlens || !a->new_seqlens || !a->block_table || !a->cumulative_sequence_length)
@@ -203,6 +203,7 @@ int pkv_cross_attention(const pkv_cross_attention_args* args, void* workspace,
   const int st = check_cross(args, &p);
   if (st != PKV_OK) return st;
   if (args->num_tokens == 0) return PKV_OK;
+  if (args->output == args->query) return PKV_ERR_SHAPE;
   if (!workspace || workspace_bytes < cross_layout(&p, static_cast<char*>(workspace)) ||
       !aligned(workspace, 256))
     return PKV_ERR_WORKSPACE;

@@ -124,6 +124,6 @@ class CrossCase:
         if lse is not None:
             empty = np.isneginf(rlse)
             assert (np.isneginf(lse.numpy()) == empty).all()
-            dl = np.abs(wide(lse) - rlse)[~empty]
+            dl = np.abs(wide(lse)[~empty] - rlse[~empty])
             assert (dl <= tol_lse[~empty]).all(), float(dl.max())
         return out, lse

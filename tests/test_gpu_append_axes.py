@@ -216,3 +216,19 @@ def test_many_tokens_match_the_oracle():
              packed=True, turns=True, pad=(0, 77, 1289))
     c.pos[1, 1000] = 300
     c.check()
+
+
+def test_pool_rows_past_32_bit_offsets():
+    c = Case(11, 40, num_heads=8, kv_heads=8, head_size=128, rotary_dim=128)
+    want = c.gpu()
+    first = 2 ** 31 // (c.bs * 8 * 128) + 3
+    kc = torch.zeros((first + c.nb, c.bs, 8, 128), dtype=c.t, device=DEV)
+    vc = torch.zeros_like(kc)
+    kc[first:], vc[first:] = c.kc.to(DEV), c.vc.to(DEV)
+    out = B.pkv_paged_append_rotary_axes(
+        c.q.to(DEV), c.k.to(DEV), c.v.to(DEV), kc, vc, i32(c.slots + first * c.bs), i32(c.pos),
+        num_heads=8, kv_num_heads=8, cos_cache=c.cos.to(DEV), sin_cache=c.sin.to(DEV),
+        rotary_dim=128, pair_axis=c.axis)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0])
+    assert torch.equal(kc[first:], want[1]) and torch.equal(vc[first:], want[2])

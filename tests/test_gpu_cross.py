@@ -196,3 +196,53 @@ def test_merges_with_the_scores_of_another_cache():
     w = [torch.exp(p[1].double() - lse.double())[..., None] for p in parts]
     both = sum(x * p[0].double().reshape(-1, 4, 128) for x, p in zip(w, parts))
     assert torch.allclose(both, whole.double().reshape(-1, 4, 128), atol=4 * 2.0 ** -11)
+
+
+@pytest.mark.parametrize("nq", [[1, 2], [140, 33]], ids=str)
+def test_cache_past_32_bit_offsets(nq):
+    # the same states at blocks behind 2^31 elements and 2^32 bytes of each cache
+    c = CrossCase(32, nq, [300, 77], num_heads=8, kv_heads=8, head_size=128, block_size=16)
+    want = c.gpu()
+    blocks = c.k.shape[0]
+    first = 2 ** 31 // (16 * 8 * 128) + 5
+    k = torch.empty((first + blocks, 16, 8, 128), dtype=c.t, device=DEV)
+    v = torch.empty_like(k)
+    k[first:], v[first:] = c.k.to(DEV), c.v.to(DEV)
+    out = B.pkv_cross_attention(c.q.to(DEV), k, v, i32(c.cu), i32(c.nk),
+                                i32(np.where(c.table >= 0, c.table + first, -1)),
+                                num_heads=8, kv_num_heads=8)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want[0])
+
+
+@pytest.mark.parametrize("heads,kv", [(3, 3), (5, 5), (6, 6), (12, 12), (7, 1), (11, 1), (9, 3),
+                                      (24, 24), (20, 4)])
+def test_head_counts(heads, kv):
+    # kv heads that neighbouring warps take together: 8, 4, 2 or 1; rows that do not fill a tile
+    for nq in ([1, 1, 2], [50, 3, 200]):
+        CrossCase(33, nq, [130, 0, 700], num_heads=heads, kv_heads=kv, head_size=64,
+                  block_size=16).check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_whole_tiles(d):
+    # more tiles than twice the SMs: dealt out whole, the rest cut; sequences of one tile, of many,
+    # and empty ones between them
+    rng = np.random.default_rng(4)
+    nq = [int(x) for x in rng.integers(0, 90, 60)] + [700, 1, 0, 2]
+    nk = [int(x) for x in rng.integers(0, 400, 60)] + [150, 900, 30, 0]
+    CrossCase(34, nq, nk, num_heads=16, kv_heads=8, head_size=d, block_size=16).check()
+
+
+def test_many_whole_tiles_of_more_sequences_than_one_scan():
+    rng = np.random.default_rng(5)
+    nq = [int(x) for x in rng.integers(0, 40, 1500)]
+    nk = [int(x) for x in rng.integers(0, 60, 1500)]
+    CrossCase(35, nq, nk, num_heads=2, kv_heads=1, head_size=64, block_size=16).check()
+
+
+def test_few_tiles_cut_in_step():
+    # ranges cut into pieces of their own (several kv heads, few tiles), uneven lengths
+    for nk in ([5000, 0, 3000], [130, 9000, 400], [128 * 31, 128 * 33, 1]):
+        CrossCase(36, [100, 30, 129], nk, num_heads=8, kv_heads=4, head_size=64, block_size=64,
+                  dtype="bf16").check()

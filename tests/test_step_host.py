@@ -35,6 +35,7 @@ def schedule_args(**kw):
     (dict(num_blocks=(1 << 20) + 1), 9), (dict(block_size=1 << 40), 9),
     (dict(max_blocks=1 << 40), 9), (dict(num_tokens=2**31 - 1), 9),
     (dict(max_blocks=1 << 27), 9),                      # max_blocks * block_size = 2^31
+    (dict(max_blocks=2**31 - 10, block_size=1, batch=1), 9),
     (dict(num_blocks=1 << 20, block_size=1 << 11), 9),  # slots past 2^31
     (dict(past_seqlens=None), 1), (dict(new_seqlens=None), 1), (dict(block_table=None), 1),
     (dict(cumulative_sequence_length=None), 1), (dict(total_seqlens=P), 2),
@@ -123,6 +124,9 @@ def test_cross_workspace_refusals(lib):
     for ws, size in ((None, n.value), (P, n.value - 1), (P + 128, n.value)):
         assert lib.pkv_cross_attention(ctypes.byref(a), ws, size, None) == 7
     assert lib.pkv_cross_attention(ctypes.byref(cross_args(num_tokens=0)), None, 0, None) == 0
+    assert B.pkv_launch_count() == before
+    # the output in the place of the query: tiles read rows that others have written
+    assert lib.pkv_cross_attention(ctypes.byref(cross_args(output=P)), P, n.value, None) == 2
     assert B.pkv_launch_count() == before
     assert lib.pkv_cross_attention(None, P, n.value, None) == 1
     assert lib.pkv_paged_schedule(None, None) == 1
