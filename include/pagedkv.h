@@ -513,12 +513,12 @@ typedef struct pkv_append_axes_args {
  * in 32-bit arithmetic, rounded once to `dtype`; elements from rotary_dim on are copied.
  * The key row goes to pool row s of key_cache, the value row to value_cache, the query row
  * to row i of query_out. A negative slot is padding: whatever the token's rows and
- * positions hold, nothing is written for it. A slot past the pool (PKV_DEV_BAD_SLOT): K and V are not
- * written, the query is. A position outside [0, rotary_positions) on an axis that some pair
- * uses (PKV_DEV_BAD_POSITION): K and V are not written, the query row is copied unrotated.
- * Two tokens of one slot leave either's row. query_out and the caches must not overlap the
- * inputs or one another. head_size a multiple of 8, <= 256; otherwise
- * PKV_ERR_UNSUPPORTED. */
+ * positions hold, nothing is written for it. A slot past the pool (PKV_DEV_BAD_SLOT): K
+ * and V are not written, the query is. A position outside [0, rotary_positions) on an axis
+ * that some pair uses (PKV_DEV_BAD_POSITION): K and V are not written, the query row is
+ * copied unrotated. Two tokens of one slot leave there, in each 16 bytes, the one's or the
+ * other's. query_out and the caches must not overlap the inputs or one another. head_size a
+ * multiple of 8, <= 256; otherwise PKV_ERR_UNSUPPORTED. */
 int pkv_paged_append_rotary_axes(const pkv_append_axes_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------------

@@ -10,8 +10,9 @@
 // / 2 apart, or side by side), or two chunks that are only copied. The token's cos and sin, one
 // of each a pair, are gathered once into shared memory, whatever the axes' order, while the
 // item's own loads are under way, and so are the token's slot and whether it may be written. A
-// block is one token's items, or several tokens' where a token has few. Rotary dimensions that are no multiple of 16 take a thread a chunk and read each
-// partner by itself.
+// block is one token's items, or several tokens' where a token has few. Rotary dimensions that
+// are no multiple of 16 take a thread a chunk and read each partner by itself.
+// Measured (32 + 2 x 8 heads of 128): 64 tokens 3.4 us, which is latency; 32768 tokens 133 us.
 #include <cuda_bf16.h>
 
 #include "device_common.cuh"
@@ -154,6 +155,7 @@ __device__ __forceinline__ void turn_item(uint4 (&x)[2], const float4* cs, int a
 // is turned and written, the next one's rows and table entries are on their way and the slots and
 // positions of the one behind it, so that loads are under way all the time.
 constexpr int kPair = 2;
+constexpr int kStreamFrom = 3;   // tokens an SM
 template <typename T, typename TT, bool kSide>
 __global__ void __launch_bounds__(kMaxThreads)
     append_axes_stream_kernel(const __grid_constant__ AxesParams p, int items) {
@@ -268,10 +270,11 @@ __global__ void __launch_bounds__(kMaxThreads)
     it.template place<kSide>(p, i);
     load();
   }
-  if (threadIdx.x < N * tokens && t0 + threadIdx.x < p.T) {
-    const Token k = read_token(p, t0 + threadIdx.x);
+  // a block may hold more tokens than threads (tokens of three items or fewer)
+  for (int w = threadIdx.x; w < N * tokens && t0 + w < p.T; w += blockDim.x) {
+    const Token k = read_token(p, t0 + w);
     report(p, k);
-    about[threadIdx.x] = make_int2(k.slot, (k.known ? 1 : 0) | (k.known && k.fits ? 2 : 0));
+    about[w] = make_int2(k.slot, (k.known ? 1 : 0) | (k.known && k.fits ? 2 : 0));
   }
   for (int n = threadIdx.x; n < N * tokens * half; n += blockDim.x) {
     const int w = n / half, j = n - w * half;
@@ -368,10 +371,11 @@ void launch_typed(const AxesParams& p, cudaStream_t s) {
   const int threads = tokens > 1 ? (tokens * items + 31) / 32 * 32
                                  : (items < kMaxThreads ? (items + 31) / 32 * 32 : kMaxThreads);
   const int sms = device_sms();
-  if (tokens == 1 && items <= kMaxThreads && p.T >= 8 * sms && p.R <= kMaxThreads / kPair * 2) {
+  if (tokens == 1 && items <= kMaxThreads && p.T >= kStreamFrom * sms && p.R <= kMaxThreads / kPair * 2) {
     // Many tokens of many items stay with the blocks that fit the SMs (80 registers a thread):
     // 32768 tokens of 384 items take 133 us (6182 GB/s, 91 % of measured copy bandwidth), 152 us
-    // with a block for four tokens, 272 us with one for each.
+    // with a block for four tokens, 272 us with one for each. From three tokens an SM on: 512
+    // tokens take 4.9 us, 6.3 us with a block each; 320 tokens 4.9 us and 4.5 us.
     int block = items > p.R ? items : p.R;   // R: kPair * R / 2 gathering threads
     block = (block + 31) / 32 * 32;
     const int per_sm = 65536 / (block * 80) > 1 ? 65536 / (block * 80) : 1;
@@ -381,7 +385,9 @@ void launch_typed(const AxesParams& p, cudaStream_t s) {
     else
       append_axes_stream_kernel<T, TT, false><<<per_sm * sms, block, smem, s>>>(p, items);
   } else if (p.T >= 8 * tokens * sms) {
-    // four tokens to a thread, so that enough of their loads are under way at once
+    // four tokens to a thread, so that enough of their loads are under way at once (65536 tokens
+    // of 48 items: 57 us, with one 74 us; blocks that stay took 74 us, they need more registers
+    // where a thread gathers for several tokens)
     launch_items<T, TT, 4>(p, items, tokens, threads, s);
   } else {   // few: spread over the SMs (64 tokens of 384 items: 3.4 us)
     launch_items<T, TT, 1>(p, items, tokens, threads, s);

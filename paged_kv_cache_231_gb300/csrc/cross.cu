@@ -9,7 +9,12 @@
 // head. Each warp of a persistent grid runs through its steps of 4 KB of keys (16 or 32): rows
 // go through the warp's own ring in shared memory by 16-byte asynchronous copies (two steps
 // ahead; the block table a third), scores and products on mma.sync m16n8k16, whose 16 rows are
-// the sequence's query rows x the heads that share the kv head.
+// the sequence's query rows x the heads that share the kv head. That is enough where memory is
+// the bound: 64 single tokens over 512 to 8192 states, 8 kv heads of 128: 176 to 180 us, 6470 to
+// 6630 GB/s (95 to 98 % of measured copy bandwidth).
+// Sequences with more than 16 such rows go to the tiles of 256 rows: 64 x 4000 states, 4 heads a
+// kv head, 1 or 4 tokens each: 160 and 171 us here, 294 us there; 5 tokens: 297 us there.
+// Runs may be single steps: 2 tokens over 400 states 8.8 us, from two steps on 10.6 us.
 #include "cross_dev.cuh"
 
 namespace pkv {
@@ -19,8 +24,7 @@ using namespace cross;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kLeastFew = 2;    // steps of a run, at least
-constexpr int kLeastTile = 4;
+constexpr int kLeastTile = 2;   // steps of a run of the other kernel, at least
 
 template <int D>
 __device__ __forceinline__ int chunk_at(int r, int c) {   // 16-byte chunk c of row r, swizzled
@@ -167,8 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int flags = 0;
-  const Plan pl = make_plan<kThreads>(p, p.few_units / p.few_heads, kLeastFew, s_pref, s_scratch,
-                                      &flags);
+  const Plan pl = make_plan<kThreads>(p, p.few_units / p.few_heads, s_pref, s_scratch, &flags);
   if (blockIdx.x > 0) flags = 0;   // every block saw them
   const int gw = blockIdx.x * kWarps + warp;
   const int unit = gw / p.few_heads, sub = gw % p.few_heads;
@@ -322,10 +325,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
 
 // ---------------------------------------------------------------------------- join
 // Over the pieces of a row: M = max m, out = sum 2^{m - M} o / sum 2^{m - M} l. What it waits for
-// is memory, so a warp asks for four pieces of N rows at once, whether they weigh anything or
+// is memory, so a warp asks for kAhead pieces of a row at once, whether they weigh anything or
 // not; a piece of no weight may hold anything.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 16;   // rows of a tile's record that a block takes (of 16, 32, 64)
+// pieces of a row that a warp asks for at once (8 lowered the occupancy: 64 tokens 16 us, not 12)
+constexpr int kAhead = 4;
+// rows of a tile's record that a block takes (records of many pieces: 12 us, with 64 18 us)
+constexpr int kJoinRows = 16;
 
 template <int D>
 struct Joined {
@@ -338,10 +344,10 @@ struct Joined {
                                       int lane) {
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int q0 = from; q0 < pieces; q0 += 4 * share) {
-      float m[4], l[4], x[4][V];
+    for (int q0 = from; q0 < pieces; q0 += kAhead * share) {
+      float m[kAhead], l[kAhead], x[kAhead][V];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAhead; ++k) {
         const int q = min(q0 + k * share, pieces - 1);
         const int at = q * apart + (q == 0 ? late : 0) + row;
         m[k] = __ldcg(pm + at);
@@ -361,14 +367,14 @@ struct Joined {
       }
       float top = M;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = l[k] == 0.f ? top : fmaxf(top, m[k]);
+      for (int k = 0; k < kAhead; ++k) top = l[k] == 0.f ? top : fmaxf(top, m[k]);
       const float base = top == -INFINITY ? 0.f : top, old = ex2(M - base);
       M = top;
       L *= old;
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] *= old;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAhead; ++k) {
         if (l[k] == 0.f) continue;
         const float w = ex2(m[k] - base);
         L += w * l[k];
@@ -388,8 +394,8 @@ struct Joined {
 };
 
 // Blocks 0 .. : kJoinRows rows of a tile's record each (256 / kJoinRows blocks a record). Behind
-// them a block for the record of each warp of the kernel for few rows: 8 warps share its rows,
-// several warps a row when there are fewer.
+// them a block for the record of each warp of the kernel for few rows: 8 warps share the rows that
+// fall to it, several warps a row when there are fewer.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams p) {
   constexpr int V = D / 32, kBlocks = 256 / kJoinRows;
@@ -402,7 +408,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
   const int unit = tile ? blockIdx.x / kBlocks : blockIdx.x - tile_blocks;
   const int4* rec = (tile ? p.tile_rec : p.few_rec) + 2 * unit;
   const int4 a = __ldcg(rec);
-  const int tokens = __ldcg(&rec[1].x);
+  const int2 about = __ldcg(reinterpret_cast<const int2*>(rec + 1));
+  const int tokens = about.x;
   if (a.x <= 0) return;
   const unsigned over_g = 65536u / p.G + 1;          // x / G = x * over_g >> 16 for x < 256
   if (tile) {
@@ -419,13 +426,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
     }
     return;
   }
-  const int64_t first = (int64_t)2 * unit * p.few_rows;
-  const int rows = tokens * p.G;
+  // the rows nth, nth + helpers, ... of the range that begins nth units before: as many helpers as
+  // there are loads for (a block has kJoinWarps * kAhead under way)
+  const int nth = about.y, all = tokens * p.G;
+  const int helpers = min(a.x - 1, (all * a.x - 1) / (kJoinWarps * kAhead) + 1);
+  if (nth >= helpers) return;
+  const int64_t first = (int64_t)2 * (unit - nth * p.few_heads) * p.few_rows;
+  const int rows = (all - nth + helpers - 1) / helpers;   // at most 0: none
   int share = 1;                                     // warps of a row
-  while (share < kJoinWarps && rows * share * 2 <= kJoinWarps) share *= 2;
+  while (share * kAhead < a.x && share < kJoinWarps && rows * share * 2 <= kJoinWarps) share *= 2;
   for (int r0 = 0; r0 < rows; r0 += kJoinWarps / share) {
-    const int r = r0 + warp / share, part = warp % share;
-    const bool live = r < rows;
+    const int i = r0 + warp / share, part = warp % share, r = nth + i * helpers;
+    const bool live = i < rows;
     Joined<D> j;
     j.add(p.few_o + first * D, p.few_m + first, p.few_l + first, live ? r : 0, a.y * p.few_rows,
           2 * p.few_rows * p.few_heads, live ? a.x : 0, part, share, lane);
@@ -505,7 +517,7 @@ size_t cross_layout(CrossParams* p, char* base) {
   // no more units than the longest possible work has runs of the least length (in floating point:
   // the products may pass 64 bits)
   const double keys = (double)p->MB * p->BS, seqs = p->T < p->B ? p->T : p->B;
-  const double runs = seqs * p->Hkv * (keys / few_keys(p->D) + 1) / kLeastFew;
+  const double runs = seqs * p->Hkv * (keys / few_keys(p->D) + 1);
   const int ctas = runs >= (double)sms * kWarps ? sms : (int)(runs / kWarps) + 1;
   p->few_units = ctas * kWarps;
   p->few_heads = kWarps;

@@ -28,7 +28,9 @@ __host__ __device__ constexpr int few_keys(int head_size) { return 2048 / head_s
 constexpr int kTileKeys = 128;     // keys of a step, many rows
 constexpr int kEntries = 1024;     // prefix entries of a plan
 constexpr float kRaise = 8.f;      // log2 of the largest weight under an old maximum
-constexpr int kMaxPieces = 128;    // pieces of a range (bounds the join)
+// pieces of a range (bounds the join): 400000 states of one kv head 76 us, with 128 pieces 228 us,
+// without a bound 77 us
+constexpr int kMaxPieces = 512;
 constexpr int kMaxTileUnits = 256; // blocks of the kernel for many rows
 
 template <typename T>
@@ -140,8 +142,8 @@ struct Plan {
 
 // Block-wide. pref: [kEntries] steps before entry e (shared memory); scratch: [NT / 32 + 2].
 template <int NT>
-__device__ Plan make_plan(const CrossParams& p, int units, int least, int64_t* pref,
-                          int64_t* scratch, int* flags) {
+__device__ Plan make_plan(const CrossParams& p, int units, int64_t* pref, int64_t* scratch,
+                          int* flags) {
   Plan pl;
   pl.group = (p.B + kEntries - 1) / kEntries;
   pl.entries = (p.B + pl.group - 1) / pl.group;
@@ -172,7 +174,7 @@ __device__ Plan make_plan(const CrossParams& p, int units, int least, int64_t* p
   if ((threadIdx.x & 31) == 0) atomicMax(word, longest);
   pl.zero = __syncthreads_or(zero) || __ldg(p.cu) != 0 || __ldg(p.cu + p.B) != p.T;
   pl.W = quotient(carry + units - 1, units);
-  pl.W = max(pl.W, (int64_t)max(least, (word[0] + kMaxPieces - 2) / (kMaxPieces - 1)));
+  pl.W = max(pl.W, (int64_t)max(1, (word[0] + kMaxPieces - 2) / (kMaxPieces - 1)));
   return pl;
 }
 
@@ -222,9 +224,10 @@ __device__ __forceinline__ void next_range(const CrossParams& p, Cursor& c) {
   }
 }
 
-// Record of warp w, which works on head `sub` of unit u: the range that begins in the unit's run
-// and ends behind it, if there is one.
-// rec[2w] = {pieces, first piece's slot, first query row, kv head}, rec[2w + 1] = {query rows}
+// Record of warp w, which works on head `sub` of unit u: the range of its last step, if that ends
+// behind the unit's run. The unit in whose run the range begins joins its pieces, and so do the
+// units that hold nothing else: unit number i of them takes the rows i, i + n, ... of n units.
+// rec[2w] = {pieces, first piece's slot, first query row, kv head}, rec[2w + 1] = {query rows, i}
 __device__ __forceinline__ void write_record(const CrossParams& p, const Plan& pl,
                                              const int64_t* pref, int64_t u, int sub, int4* rec) {
   const int64_t g0 = u * pl.W, g1 = min(pl.total, g0 + pl.W);
@@ -232,10 +235,12 @@ __device__ __forceinline__ void write_record(const CrossParams& p, const Plan& p
   if (g0 < pl.total) {
     const Cursor c = locate(p, pl, pref, g1 - 1);
     const int64_t start = g1 - 1 - c.s, end = start + c.q.steps;
-    if (start >= g0 && end > g1) {
-      a = make_int4((int)(quotient(end - 1, pl.W) - u) + 1, start == g0 ? 0 : 1, c.q.cu0,
+    if (end > g1) {
+      const int64_t own = quotient(start, pl.W);
+      a = make_int4((int)(quotient(end - 1, pl.W) - own) + 1, start == own * pl.W ? 0 : 1, c.q.cu0,
                     c.r * p.few_heads + sub);
       b.x = c.q.rows;
+      b.y = (int)(u - own);
     }
   }
   rec[0] = a;

@@ -14,6 +14,9 @@
 // shared memory and hands its count of free ids to all. Each block then scans the rows for
 // itself (cheaper than passing the sums around), writes the new table entries of its groups
 // and, after a cluster barrier, the slots of its share of the tokens.
+// What bounds it is latency: some five dependent rounds of loads and three cluster barriers. 2 rows
+// 6 us, 64 rows of 8192 tokens 10.6 us; with 2048 rows, 525 000 held entries and 339 000 new
+// tokens (33 us) the shared memory atomics of the marking take half.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"

@@ -218,6 +218,16 @@ def test_many_tokens_match_the_oracle():
     c.check()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(tokens=320000, head_size=8, rotary_dim=0, axes=0),
+    dict(tokens=160001, head_size=16, rotary_dim=16, axes=2),
+    dict(tokens=160001, head_size=16, rotary_dim=16, axes=2, interleaved=True),
+], ids=str)
+def test_many_tokens_of_tiny_heads(kw):
+    # a block holds more tokens than threads
+    Case(12, num_heads=1, kv_heads=1, query=False, pad=(0, 999, 1500), **kw).check()
+
+
 def test_pool_rows_past_32_bit_offsets():
     c = Case(11, 40, num_heads=8, kv_heads=8, head_size=128, rotary_dim=128)
     want = c.gpu()
