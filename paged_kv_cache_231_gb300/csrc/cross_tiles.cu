@@ -95,8 +95,9 @@ enum {
   kPairRead = 41,   // half 0 has read them
   kBarriers = 42
 };
-constexpr uint32_t kAbortWord = kBarriers * 8;   // behind the barriers
-static_assert(kAbortWord + 4 <= 384, "barrier area");
+constexpr uint32_t kAbortWord = kBarriers * 8;      // behind the barriers
+constexpr uint32_t kRoomWord = kAbortWord + 4;      // [2] tiles that a loader found room for
+static_assert(kRoomWord + 8 <= 384, "barrier area");
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -517,6 +518,27 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
   uint32_t q_use[2] = {0, 0};
   const uint32_t every = R > 0 ? 0xffffffffu >> (32 - kTileKeys / R) : 0u;   // boxes of a tile
   const bool withhold = p.withhold_copy != 0;   // testing hook: the first K tile never comes
+  // Room for the tile `use`: the one kStages before it was given back. A wait for a parity tells two
+  // rounds of a stage apart, not three, so the round before must be known to be over. That is the
+  // loader's own doing where its tiles come back to the same stages; with an odd number of stages
+  // they alternate with the other loader's, which has to have found room for that tile before.
+  volatile uint32_t* found = reinterpret_cast<volatile uint32_t*>(sm + L::kBars + kRoomWord);
+  const auto room = [&]() {
+    if (use >= (uint32_t)L::kStages) {
+      if constexpr (L::kStages % 2 != 0) {
+        bool there = false;
+        for (uint32_t i = 0; i < wait.tries && !there; ++i) {
+          there = found[1 - kv] + (uint32_t)L::kStages > use;
+          if ((i & 255u) == 255u && *wait.abort) break;
+        }
+        if (!there) *wait.abort = 1;
+        if (!__all_sync(0xffffffffu, there)) return false;
+      }
+      if (!wait.warp(kEmpty + to.stage, to.phase ^ 1u)) return false;
+    }
+    if (L::kStages % 2 != 0 && lane == 0) found[kv] = use + 1;
+    return true;
+  };
   // announces `bytes` and copies the boxes whose bits are set, box i from group `group` of lane i;
   // the whole warp (see the products)
   const auto issue = [&](unsigned char* dst, uint64_t* full, int group, uint32_t boxes,
@@ -580,9 +602,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       const uint32_t boxes = __ballot_sync(0xffffffffu, mapped);
       const bool clear = R > 0 && (j + 1) * kTileKeys <= c.q.keys && boxes == every;
       ahead = lookup(key0 + kTileKeys);
-      if (use >= (uint32_t)L::kStages &&
-          !wait.warp(kEmpty + to.stage, to.phase ^ 1u))
-        return false;
+      if (!room()) return false;
       unsigned char* dst = sm + L::kRing + to.stage * L::kTile;
       uint64_t* full = bars + kFull + to.stage;
       to.step(2);
@@ -713,8 +733,14 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
       const bool pv = i > 0, s = i < n;
       if (i == 0 && !ready(kQFull + half, q_use++ & 1u)) return false;
       if (pv && !ready(kFull + v.stage, v.phase)) return false;
-      if (s && !ready(kFull + k.stage, k.phase)) return false;
+      // A parity waited for too early is that of two rounds before. What the stage of this K tile
+      // held before may be the other half's: an earlier part's, or (an odd number of stages) a value
+      // tile of this shared part; then its turn tells that it landed. Else there is no need to wait
+      // with the question (a step of many takes 5 % longer).
+      const bool early = i > 0 && (L::kStages % 2 == 0 || !t.shared);
+      if (s && early && !ready(kFull + k.stage, k.phase)) return false;
       if (!my_turn(both)) return false;
+      if (s && !early && !ready(kFull + k.stage, k.phase)) return false;
       if (pv && !ready(kPFull + half, p_use & 1u)) return false;
       tc::fence_after_sync();
       const uint32_t va = ring + v.stage * L::kTile, ka = ring + k.stage * L::kTile;
@@ -1002,6 +1028,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(wait.bars + kPairRead, 4);
     tc::mbar_init_fence();
     *wait.abort = 0;
+    uint32_t* found = reinterpret_cast<uint32_t*>(sm + L::kBars + kRoomWord);
+    found[0] = found[1] = 0;
   }
   if (warp == kSoftmaxWarps + 1 && lane == 0 && p.box_keys > 0) {
     tc::tma_prefetch_desc(&maps.q);

@@ -246,3 +246,24 @@ def test_few_tiles_cut_in_step():
     for nk in ([5000, 0, 3000], [130, 9000, 400], [128 * 31, 128 * 33, 1]):
         CrossCase(36, [100, 30, 129], nk, num_heads=8, kv_heads=4, head_size=64, block_size=64,
                   dtype="bf16").check()
+
+
+@pytest.mark.parametrize("d,bs", [(128, 128), (128, 32), (64, 128)])
+def test_few_rows_of_tiles_under_load(d, bs):
+    # one half of rows, both halves at work on it, tiles arriving in any order: equal bits each time
+    c = CrossCase(37, [5] * 64, [4000] * 64, num_heads=8, kv_heads=2, head_size=d, block_size=bs)
+    first, _ = c.check()
+    for _ in range(10):
+        assert torch.equal(c.gpu()[0], first)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tiles_of_one_step_and_of_many(d):
+    # tiles that one half works on alone, then tiles of both: equal bits each time
+    rng = np.random.default_rng(6)
+    nk = [int(x) for x in rng.choice([1, 90, 128, 129, 300, 1500], 200)]
+    nq = [int(x) for x in rng.choice([20, 33, 70], 200)]
+    c = CrossCase(38, nq, nk, num_heads=4, kv_heads=2, head_size=d, block_size=32)
+    first, _ = c.check()
+    for _ in range(10):
+        assert torch.equal(c.gpu()[0], first)
