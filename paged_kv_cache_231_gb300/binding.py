@@ -623,10 +623,12 @@ def _check_tensors(stream, tensors) -> int:
             if device is not None or at < 0:
                 _refuse(stream, tensors)
             device = at
-    cuda = _torch().cuda
-    if device != cuda.current_device() or (stream is not None and stream.device_index != device):
+    torch = _torch()
+    if device != torch.cuda.current_device() or (stream is not None and
+                                                 stream.device_index != device):
         _refuse(stream, tensors)
-    return (stream if stream is not None else cuda.current_stream(device)).cuda_stream
+    # the current stream's handle without an object for it (a microsecond of the call)
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 def _keep(stream, *made):
