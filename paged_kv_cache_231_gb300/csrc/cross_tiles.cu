@@ -64,6 +64,7 @@ static_assert(sizeof(Run) <= 96, "run area");
 template <int D>
 struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr int kStages = D == 128 ? 5 : 12;   // at most 12
+  static constexpr bool kScarce = D == 128;             // two steps take nearly all of them
   static constexpr uint32_t kTile = 128u * D * 2;       // 128 rows of Q, K or V
   static constexpr uint32_t kSub = 128u * 128;          // Q: 64 columns
   static constexpr uint32_t kGroup = 8u * D * 2;        // K, V: 8 keys, [D / 64][8][64]
@@ -740,7 +741,6 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
       const bool early = i > 0 && (L::kStages % 2 == 0 || !t.shared);
       if (s && early && !ready(kFull + k.stage, k.phase)) return false;
       if (!my_turn(both)) return false;
-      if (s && !early && !ready(kFull + k.stage, k.phase)) return false;
       if (pv && !ready(kPFull + half, p_use & 1u)) return false;
       tc::fence_after_sync();
       const uint32_t va = ring + v.stage * L::kTile, ka = ring + k.stage * L::kTile;
@@ -760,9 +760,17 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
         if (elect()) {
 #pragma unroll
           for (int ks = 4; ks < 8; ++ks) products(ks);
+          if (L::kScarce && t.shared) {   // both arrivals; the S behind may have to wait for its keys
+            tc::commit(bars + kEmpty + v.stage);
+            tc::commit(bars + kEmpty + v.stage);
+          }
         }
         __syncwarp();
         v.step(apart);
+      }
+      if (s && !early) {   // behind the PV: that gives a stage back while this tile is on its way
+        if (!ready(kFull + k.stage, k.phase)) return false;
+        tc::fence_after_sync();
       }
       if (elect()) {
         // the other half's turn; it takes about as long to notice as the S below to be issued
@@ -828,9 +836,10 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     tile.step(2 * t.first(half));
     // Two arrivals free a tile: the halves', or both from the one half that reads it. A full S tells
     // that the products in front of it are done. (Committed by the issuing lane instead, an arrival
-    // took it some 90 cycles.)
-    const auto give_back = [&](int further) {
-      arrive(bars + kEmpty + tile.stage, t.halves == 2 ? 1 : 2);
+    // takes it some 90 cycles; so it is done for the value tiles of shared parts alone, where memory
+    // is the bound.)
+    const auto give_back = [&](int further, bool given) {
+      if (!given) arrive(bars + kEmpty + tile.stage, t.halves == 2 ? 1 : 2);
       tile.step(further);
     };
     float m = -INFINITY, l = 0.f;
@@ -841,8 +850,8 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
       ++s_use;
       tc::fence_after_sync();
       if (r == 0) {
-        if (j > 0) give_back((int)apart - 1);   // V of the step before
-        give_back(1);                           // K of this one
+        if (j > 0) give_back((int)apart - 1, L::kScarce && t.shared);   // V of the step before
+        give_back(1, false);                              // K of this one
       }
       float v[128], e[4];
       {
@@ -912,7 +921,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     if (!wait.warp(kOFull + half, o_use & 1u)) return false;
     ++o_use;
     tc::fence_after_sync();
-    if (r == 0) give_back(1);
+    if (r == 0) give_back(1, L::kScarce && t.shared);
     float mine_by = 1.f, other_by = 0.f;   // what this half's O counts for, and the other's
     if (t.shared) {
       if (half == 1) {
