@@ -321,6 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   }
   if (pl.zero) zero_rows<T, D>(p, gw, p.few_units, lane);
   if (flags) flag_status(p.status, flags);
+  // the join behind this kernel waits for it alone: it must not end before the one in front
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------- join
@@ -485,25 +487,31 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     mark_configured(configured, dev);
   }
-  {
-    ProfScope ps("cross_decode", s);
-    cross_few_kernel<T, D><<<p.few_units / kWarps, kThreads, Ring<D>::kBytes, s>>>(p);
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (p.tile_units > 0) {
-    e = launch_cross_tiles(p, s);
-    if (e != cudaSuccess) return e;
-  }
-  ProfScope ps("cross_combine", s);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.few_units + 256 / kJoinRows * p.tile_units));
-  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  // The tiles first: the other kernel's blocks then fill the SMs as theirs end (a call without few
+  // rows spends 7 us on them otherwise). They read inputs and write rows of their own.
+  if (p.tile_units > 0) {
+    const cudaError_t e = launch_cross_tiles(p, s);
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 1;
+  }
+  {
+    ProfScope ps("cross_decode", s);
+    cfg.gridDim = dim3((unsigned)(p.few_units / kWarps));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<D>::kBytes;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D>, p);
+    if (e != cudaSuccess) return e;
+  }
+  ProfScope ps("cross_combine", s);
+  cfg.gridDim = dim3((unsigned)(p.few_units + 256 / kJoinRows * p.tile_units));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, cross_join_kernel<T, D>, p);
 }

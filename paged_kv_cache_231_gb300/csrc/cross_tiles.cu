@@ -1075,8 +1075,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   if (tid == 0 && *wait.abort) flag_status(p.status, PKV_DEV_TIMEOUT);
   if (warp == 0) tc::tmem_dealloc(run->tmem, 512);
-  // the join behind this kernel waits for it alone: it must not end before the one in front
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -1139,19 +1137,9 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   maps.k = maps.v = maps.q;   // not used without boxes
   if (p.box_keys > 0 && (!encode_pool(&maps.k, p, p.kc) || !encode_pool(&maps.v, p, p.vc)))
     return cudaErrorInvalidValue;
-  // may start as blocks of the kernel in front end: it reads inputs and writes other rows
   ProfScope ps("cross_tiles", s);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.tile_units);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Lay<D>::kBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cross_tiles_kernel<T, D>, p, maps);
+  cross_tiles_kernel<T, D><<<p.tile_units, kThreads, Lay<D>::kBytes, s>>>(p, maps);
+  return cudaGetLastError();
 }
 
 }  // namespace
