@@ -85,7 +85,8 @@ typedef enum pkv_status {
                                     partial */
 #define PKV_DEV_TIMEOUT 32u      /* a bounded wait of a tensor-core kernel gave up: the
                                     outputs that CTA had not yet written (prefill tiles,
-                                    block-sparse partials) are not written; it waited
+                                    block-sparse partials, cross attention tiles) are
+                                    not written or not valid; it waited
                                     (bounded) for what it had issued, freed its tensor
                                     memory and returned */
 #define PKV_DEV_NO_BLOCKS 64u    /* pkv_paged_schedule: the pool has too few free blocks:
@@ -562,9 +563,10 @@ int pkv_cross_attention_workspace_size(const pkv_cross_attention_args* args, siz
  * that sees no state gets output 0 and lse -inf. Cache rows behind a sequence's states may
  * hold anything (NaN too). Sequences whose cumulative lengths are inconsistent or exceed
  * max_query_len, or whose key_seqlens entry is negative, get zero rows (lse -inf) and set
- * PKV_DEV_BAD_SEQUENCE; so do rows that no sequence covers, without the flag.
- * The order of summation depends on the sizes and the device's SM count alone: equal calls
- * give equal bits. Output and lse must not overlap the inputs. workspace: as in
+ * PKV_DEV_BAD_SEQUENCE; so do rows that no sequence covers, without the flag. A row that
+ * two sequences claim is one's or the other's, in parts.
+ * The order of summation depends on the sizes, the lengths and the device's SM count alone:
+ * equal calls give equal bits. Output and lse must not overlap the inputs. workspace: as in
  * pkv_paged_attention (256-byte aligned, contents need not be initialised, one per call in
  * flight). After PKV_DEV_TIMEOUT the rows of the tiles that gave up, and those joined from
  * their pieces, are not valid. Supported: head_size in {64, 128},

@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(kMaxThreads)
   const bool gathers = i < kPair * half;
   const int gw = gathers ? i / half : 0, gj = gathers ? i - gw * half : 0;
   const int* gpos = gathers ? p.pos + (int64_t)p.pair_axis[gj] * p.T : nullptr;
-  float* const put = reinterpret_cast<float*>(turn + (gw * 4 + (gj & 7) / 2) * per_head + gj / 8) + (gj & 1);
+  float* const put =
+      reinterpret_cast<float*>(turn + (gw * 4 + (gj & 7) / 2) * per_head + gj / 8) + (gj & 1);
   const int tw = i;                                // token of the group that this thread reports
 
   const auto row_of = [&](int g) {                 // table row of this thread's pair, -1: none
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(kMaxThreads)
     const int r = __ldg(p.pos + (int64_t)p.pair_axis[j] * p.T + t0 + w);
     if (r >= 0 && r < p.P) {
       const int64_t at = (int64_t)r * half + j;
-      float* z = reinterpret_cast<float*>(turn + (w * 4 + (j & 7) / 2) * per_head + j / 8) + (j & 1);
+      float* z =
+          reinterpret_cast<float*>(turn + (w * 4 + (j & 7) / 2) * per_head + j / 8) + (j & 1);
       z[0] = Num<TT>::to(static_cast<const TT*>(p.cos)[at]);
       z[2] = Num<TT>::to(static_cast<const TT*>(p.sin)[at]);
     }
@@ -325,7 +327,8 @@ __global__ void __launch_bounds__(kThreads)
     if (!isq && !write_kv) continue;
     const int kh = isv ? h - p.Hq - p.Hkv : h - p.Hq;
     const T* src = isq ? static_cast<const T*>(p.q) + (int64_t)t * p.q_stride + (int64_t)h * p.D
-                       : static_cast<const T*>(isv ? p.v : p.k) + (int64_t)t * p.kv_stride + (int64_t)kh * p.D;
+                       : static_cast<const T*>(isv ? p.v : p.k) + (int64_t)t * p.kv_stride +
+                             (int64_t)kh * p.D;
     T* dst = isq ? static_cast<T*>(p.q_out) + ((int64_t)t * p.Hq + h) * p.D
                  : static_cast<T*>(isv ? p.vc : p.kc) + ((int64_t)k.slot * p.Hkv + kh) * p.D;
     __align__(16) T x[8];
@@ -371,7 +374,8 @@ void launch_typed(const AxesParams& p, cudaStream_t s) {
   const int threads = tokens > 1 ? (tokens * items + 31) / 32 * 32
                                  : (items < kMaxThreads ? (items + 31) / 32 * 32 : kMaxThreads);
   const int sms = device_sms();
-  if (tokens == 1 && items <= kMaxThreads && p.T >= kStreamFrom * sms && p.R <= kMaxThreads / kPair * 2) {
+  if (tokens == 1 && items <= kMaxThreads && p.T >= kStreamFrom * sms &&
+      p.R <= kMaxThreads / kPair * 2) {
     // Many tokens of many items stay with the blocks that fit the SMs (80 registers a thread):
     // 32768 tokens of 384 items take 133 us (6182 GB/s, 91 % of measured copy bandwidth), 152 us
     // with a block for four tokens, 272 us with one for each. From three tokens an SM on: 512

@@ -12,8 +12,8 @@
 // the sequence's query rows x the heads that share the kv head. That is enough where memory is
 // the bound: 64 single tokens over 512 to 8192 states, 8 kv heads of 128: 176 to 180 us, 6470 to
 // 6630 GB/s (95 to 98 % of measured copy bandwidth).
-// Sequences with more than 16 such rows go to the tiles of 256 rows: 64 x 4000 states, 4 heads a
-// kv head, 1 or 4 tokens each: 160 and 171 us here, 294 us there; 5 tokens: 297 us there.
+// Sequences with more than 16 such rows go to the tiles of 256 rows: 64 x 4000 states, 4 heads of
+// 128 a kv head, 1 or 4 tokens each: 161 and 169 us here, 203 us there (5 tokens).
 // Runs may be single steps: 2 tokens over 400 states 8.8 us, from two steps on 10.6 us.
 #include "cross_dev.cuh"
 
@@ -82,8 +82,9 @@ __device__ __forceinline__ void load_queries(const CrossParams& p, const Cursor&
     const int e = ks * 16 + 2 * (lane & 3);
 #pragma unroll
     for (int x = 0; x < 4; ++x)
-      qa[ks][x] = ok[x & 1] ? __ldg(reinterpret_cast<const unsigned*>(row[x & 1] + e + (x >> 1) * 8))
-                            : 0u;
+      qa[ks][x] = ok[x & 1]
+                      ? __ldg(reinterpret_cast<const unsigned*>(row[x & 1] + e + (x >> 1) * 8))
+                      : 0u;
   }
 }
 
@@ -298,7 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
       }
       const bool last = cc.s == cc.q.steps - 1;
       if (last || k == nst - 1) {
-        flush<T, D>(p, cc, cc.r * p.few_heads + sub, gw, from_start && last, first ? 0 : 1, m, l, o, lane);
+        flush<T, D>(p, cc, cc.r * p.few_heads + sub, gw, from_start && last, first ? 0 : 1, m, l, o,
+                    lane);
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
 #pragma unroll
@@ -563,7 +565,8 @@ size_t cross_layout(CrossParams* p, char* base) {
 
 cudaError_t launch_cross(const CrossParams& p, cudaStream_t s) {
   if (p.bf16)
-    return p.D == 64 ? launch_typed<__nv_bfloat16, 64>(p, s) : launch_typed<__nv_bfloat16, 128>(p, s);
+    return p.D == 64 ? launch_typed<__nv_bfloat16, 64>(p, s)
+                     : launch_typed<__nv_bfloat16, 128>(p, s);
   return p.D == 64 ? launch_typed<__half, 64>(p, s) : launch_typed<__half, 128>(p, s);
 }
 

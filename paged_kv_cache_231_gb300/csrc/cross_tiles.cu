@@ -25,10 +25,11 @@
 // A tile of at most 128 rows is worked on by both halves: half 0 takes the even steps, half 1 the
 // odd ones, and half 0 joins the two (m, l, O) at the end.
 // TMEM columns: S_0 0..127 (weights over 0..63), S_1 128..255, O_0 256.., O_1 384...
-// Measured: 8 sequences of up to 2048 queries over up to 4096 states, 32 heads of 128 on 8 kv
-// heads: 466 us for 0.571 TFLOP, 1225 TFLOP/s (63 % of the measured dense rate): a step of 256 rows
-// takes the softmax of one half, the hand-offs and the products of the other one after the other.
-// Few rows and long sequences (100 queries, 20000 to 60000 states, 16 heads of 64): 80 us, 4.7 TB/s.
+// Measured: 16 sequences of up to 2048 queries over up to 4096 states, 32 heads of 128 on 8 kv
+// heads: 460 us for 0.571 TFLOP, 1240 TFLOP/s (64 % of the measured dense rate; the tensor pipe is
+// active 56 % of the time): the two halves' softmaxes, each a chain of TMEM loads, exponentials and
+// TMEM stores, and the hand-offs between them and the products set the pace. Few rows and long
+// sequences (100 queries, 20000 to 60000 states, 16 heads of 64): 80 us, 4.7 TB/s.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <limits.h>
@@ -78,7 +79,9 @@ struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr size_t kBytes = kEnd + 1024;
 };
 static_assert(Lay<128>::kBytes <= 232448, "shared memory over the limit");
-static_assert((3 * kEntries + kThreads + 48) * 8 <= Lay<64>::kStages * Lay<64>::kTile, "plan fits the ring");
+static_assert((3 * kEntries + kThreads + 48) * 8 <= Lay<64>::kStages * Lay<64>::kTile &&
+                  (3 * kEntries + kThreads + 48) * 8 <= Lay<128>::kStages * Lay<128>::kTile,
+              "plan fits the ring");
 
 // mbarriers
 enum {
@@ -233,7 +236,9 @@ __device__ __forceinline__ uint64_t pair_of(float a, float b) {
   return r;
 }
 __device__ __forceinline__ float low_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float high_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ float high_of(uint64_t x) {
+  return __uint_as_float((uint32_t)(x >> 32));
+}
 __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -328,8 +333,8 @@ __device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, 
 // i % units), so that the blocks read the same keys at about the same time and the cache holds
 // them; of the others (between one and two for each block, if there are as many) each block
 // gets a run of steps that evens out what it had before.
-// mem: [kEntries + 1] steps and tiles before an entry each, [kThreads + 1] cuts, scratch, [kEntries]
-// steps of an entry's tiles (the mean, where an entry holds several sequences).
+// mem: [kEntries + 1] steps and tiles before an entry each, [kThreads + 1] cuts, scratch,
+// [kEntries] steps of an entry's tiles (the mean, where an entry holds several sequences).
 __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   int64_t *steps_at = mem, *tiles_at = steps_at + kEntries + 1, *cut = tiles_at + kEntries + 1,
           *scratch = cut + kThreads + 1;
@@ -519,10 +524,10 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
   uint32_t q_use[2] = {0, 0};
   const uint32_t every = R > 0 ? 0xffffffffu >> (32 - kTileKeys / R) : 0u;   // boxes of a tile
   const bool withhold = p.withhold_copy != 0;   // testing hook: the first K tile never comes
-  // Room for the tile `use`: the one kStages before it was given back. A wait for a parity tells two
-  // rounds of a stage apart, not three, so the round before must be known to be over. That is the
-  // loader's own doing where its tiles come back to the same stages; with an odd number of stages
-  // they alternate with the other loader's, which has to have found room for that tile before.
+  // Room for the tile `use`: the one kStages before it was given back. A wait for a parity tells
+  // two rounds of a stage apart, not three, so the round before must be known to be over. That is
+  // the loader's own doing where its tiles come back to the same stages; with an odd number of
+  // stages they alternate with the other loader's, which has to have found room for that tile.
   volatile uint32_t* found = reinterpret_cast<volatile uint32_t*>(sm + L::kBars + kRoomWord);
   const auto room = [&]() {
     if (use >= (uint32_t)L::kStages) {
@@ -623,7 +628,8 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
         if (R > 0) {
           const bool in = __shfl_sync(0xffffffffu, mapped ? 1 : 0, 4 * lane / R) != 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) words[x] = __ballot_sync(0xffffffffu, in && k0 + x < c.q.keys);
+          for (int x = 0; x < 4; ++x)
+            words[x] = __ballot_sync(0xffffffffu, in && k0 + x < c.q.keys);
         } else {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -655,7 +661,8 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
                 flags |= PKV_DEV_BAD_BLOCK;
             }
             if (lane < D / 8)
-              cp_async_16(dst + (r >> 3) * L::kGroup + (lane >> 3) * 1024 + tc::sw128(r & 7, lane & 7),
+              cp_async_16(dst + (r >> 3) * L::kGroup + (lane >> 3) * 1024 +
+                              tc::sw128(r & 7, lane & 7),
                           at >= 0 ? src + at + lane * 8 : src, at >= 0 ? 16 : 0);
           }
         } else if (kv == 1) {
@@ -735,9 +742,9 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
       if (i == 0 && !ready(kQFull + half, q_use++ & 1u)) return false;
       if (pv && !ready(kFull + v.stage, v.phase)) return false;
       // A parity waited for too early is that of two rounds before. What the stage of this K tile
-      // held before may be the other half's: an earlier part's, or (an odd number of stages) a value
-      // tile of this shared part; then its turn tells that it landed. Else there is no need to wait
-      // with the question (a step of many takes 5 % longer).
+      // held before may be the other half's: an earlier part's, or (an odd number of stages) a
+      // value tile of this shared part; then its turn tells that it landed. Else there is no need
+      // to wait with the question (head size 64: 80 us, asked behind the turn 84 us).
       const bool early = i > 0 && (L::kStages % 2 == 0 || !t.shared);
       if (s && early && !ready(kFull + k.stage, k.phase)) return false;
       if (!my_turn(both)) return false;
@@ -760,7 +767,7 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
         if (elect()) {
 #pragma unroll
           for (int ks = 4; ks < 8; ++ks) products(ks);
-          if (L::kScarce && t.shared) {   // both arrivals; the S behind may have to wait for its keys
+          if (L::kScarce && t.shared) {   // both arrivals; the S behind may wait for its keys
             tc::commit(bars + kEmpty + v.stage);
             tc::commit(bars + kEmpty + v.stage);
           }
@@ -834,10 +841,11 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     if (!t.active(half)) return true;
     const uint32_t apart = 2 * t.stride();
     tile.step(2 * t.first(half));
-    // Two arrivals free a tile: the halves', or both from the one half that reads it. A full S tells
-    // that the products in front of it are done. (Committed by the issuing lane instead, an arrival
-    // takes it some 90 cycles; so it is done for the value tiles of shared parts alone, where memory
-    // is the bound.)
+    // Two arrivals free a tile: the halves', or both from the one half that reads it. A full S
+    // tells that the products in front of it are done. (Committed by the issuing lane instead, an
+    // arrival takes it some 90 cycles; so it is done where stages are scarce alone: the value tiles
+    // of shared parts of head size 128. 64 x 4000 states, 20 rows of 8 kv heads: 217 us, 260 us
+    // without.)
     const auto give_back = [&](int further, bool given) {
       if (!given) arrive(bars + kEmpty + tile.stage, t.halves == 2 ? 1 : 2);
       tile.step(further);
@@ -1146,7 +1154,8 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
 
 cudaError_t launch_cross_tiles(const CrossParams& p, cudaStream_t s) {
   if (p.bf16)
-    return p.D == 64 ? launch_typed<__nv_bfloat16, 64>(p, s) : launch_typed<__nv_bfloat16, 128>(p, s);
+    return p.D == 64 ? launch_typed<__nv_bfloat16, 64>(p, s)
+                     : launch_typed<__nv_bfloat16, 128>(p, s);
   return p.D == 64 ? launch_typed<__half, 64>(p, s) : launch_typed<__half, 128>(p, s);
 }
 

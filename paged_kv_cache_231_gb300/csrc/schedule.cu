@@ -14,9 +14,10 @@
 // shared memory and hands its count of free ids to all. Each block then scans the rows for
 // itself (cheaper than passing the sums around), writes the new table entries of its groups
 // and, after a cluster barrier, the slots of its share of the tokens.
-// What bounds it is latency: some five dependent rounds of loads and three cluster barriers. 2 rows
-// 6 us, 64 rows of 8192 tokens 10.6 us; with 2048 rows, 525 000 held entries and 339 000 new
-// tokens (33 us) the shared memory atomics of the marking take half.
+// What bounds it is latency: some five dependent rounds of loads and three cluster barriers.
+// 2 rows take 6.0 us, 64 rows of up to 8192 tokens 10.6 us, 16 rows of which half take in up to
+// 2048 tokens 13.8 us; with 2048 rows, 433 000 held entries and 325 000 new tokens (33 us) the
+// shared memory atomics of the marking take half.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -203,7 +204,8 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(ScheduleParams p) {
       given = asked == 0 || upto[b] <= free_ids ? want : 0;
     }
     int64_t total;
-    const int64_t upto_t = tokens + block_sum<int64_t>(given, &total, s_tokens[(c0 / kThreads) & 1]);
+    const int64_t upto_t =
+        tokens + block_sum<int64_t>(given, &total, s_tokens[(c0 / kThreads) & 1]);
     tokens += total;
     const bool fits = upto_t <= p.T;
     if (b < p.B) cu[b + 1] = fits ? (int)upto_t : -1;
@@ -378,9 +380,9 @@ cudaError_t launch_schedule(const ScheduleParams& p, cudaStream_t s) {
       (void)cudaGetLastError();
     mark_configured(configured, dev);
   }
-  // Blocks of the cluster: 16 where many entries or tokens are to be gone through (2048 rows of 600
-  // entries and 339 000 tokens: 52 us with 8, 33 us with 16), else 8 (64 rows of 520 entries: 10.6 us
-  // with 8, 13.9 us with 1; 2 rows: 6.1 us with either).
+  // Blocks of the cluster: 16 where many entries or tokens are to be gone through (2048 rows of
+  // 600 entries and 325 000 tokens: 52 us with 8, 33 us with 16), else 8 (64 rows of 520 entries:
+  // 10.6 us with 8, 13.9 us with 1; 2 rows: 6.1 us with either).
   const int64_t work = (int64_t)p.B * ((p.MB + kChunk - 1) / kChunk) / kWarps +
                        (int64_t)p.T / (kThreads * kTokens) + p.groups / kWarps;
   const bool can = dev >= 0 && dev < 64 && (wide.load() & (1ull << dev));
