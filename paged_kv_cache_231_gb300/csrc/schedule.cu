@@ -8,16 +8,17 @@
 // conditions are prefix sums. Token i of row b (cu_b <= i < cu_{b+1}) has position
 // p_b + i - cu_b and slot table[b][pos / BS] * BS + pos % BS.
 //
-// One launch, one cluster of C blocks, no workspace. Every block marks the held entries that
+// One cluster of C blocks, no workspace. Every block marks the held entries that
 // it reads in a bitmap of the whole pool in its own shared memory (local atomics); group g of
 // 1024 ids belongs to block g % C, which joins the C bitmaps of the group through distributed
 // shared memory and hands its count of free ids to all. Each block then scans the rows for
 // itself (cheaper than passing the sums around), writes the new table entries of its groups
 // and, after a cluster barrier, the slots of its share of the tokens.
+// Very many tokens' slots are left to a second kernel on all SMs.
 // What bounds it is latency: some five dependent rounds of loads and three cluster barriers.
 // 2 rows take 6.0 us, 64 rows of up to 8192 tokens 10.6 us, 16 rows of which half take in up to
-// 2048 tokens 13.8 us; with 2048 rows, 433 000 held entries and 325 000 new tokens (33 us) the
-// shared memory atomics of the marking take half.
+// 2048 tokens 13.8 us; with 2048 rows, 433 000 held entries and 325 000 new tokens (27 us) the
+// marking takes a third.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -35,6 +36,9 @@ constexpr int kChunk = 128;   // table columns of a row that a warp marks as one
 constexpr unsigned kMaxCluster = 16;
 constexpr int kUnits = 4;     // such pieces whose loads are under way at once
 constexpr int kTokens = 8;    // tokens of a thread
+// Tokens from which their slots are a kernel of their own, on all SMs: 487 000 tokens of 2048 rows
+// 23.6 us, with the cluster's blocks 32.9 us; 61 000 tokens 16.1 and 16.4 us, 31 000 16.4 and 15.5.
+constexpr int kApartFrom = 65536;
 static_assert(kScheduleMaxBlocks / 1024 <= kThreads, "a thread a group");
 
 struct Row {
@@ -105,6 +109,75 @@ __device__ __forceinline__ int first_above(const int* a, int n, int x) {
   return lo;
 }
 
+// Slots and positions of many tokens, kTokens to a thread from `from` on and every further
+// `stride`: the first one's row by a search in cu (shared memory), its block and the next one ahead
+// of the rest. Returns what is wrong.
+__device__ __forceinline__ int many_slots(const ScheduleParams& p, const int* cu, int granted,
+                                          int64_t from, int64_t stride) {
+  int flags = 0;
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) |
+                      reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
+  for (int64_t i0 = from; i0 < p.T; i0 += stride) {
+    int slot[kTokens], pos[kTokens];
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) slot[k] = pos[k] = -1;
+    if (i0 < granted) {
+      int b = first_above(cu + 1, p.B, (int)i0);
+      const int pos0 = __ldg(p.past + b) + (int)i0 - cu[b], col0 = column(p, pos0);
+      const int32_t* entry = p.table + (int64_t)b * p.MB + col0;
+      const int id0 = __ldcg(entry), id1 = col0 + 1 < p.MB ? __ldcg(entry + 1) : -1;
+      const int last = column(p, pos0 + kTokens - 1);
+      if (i0 + kTokens <= cu[b + 1] && last <= col0 + 1 && id0 >= 0 && id0 < p.NB &&
+          (last == col0 || (id1 >= 0 && id1 < p.NB))) {   // one row, at most two blocks
+        const int turn = (col0 + 1) * p.BS - pos0;          // tokens of the first block
+        const int base0 = id0 * p.BS + (pos0 - col0 * p.BS), base1 = id1 * p.BS - turn;
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+          pos[k] = pos0 + k;
+          slot[k] = (k < turn ? base0 : base1) + k;
+        }
+      } else {
+        int id[kTokens];   // all the blocks at once: the loads are what takes time
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+          id[k] = 0;
+          if (i0 + k >= granted) continue;
+          while (cu[b + 1] <= i0 + k) ++b;
+          pos[k] = __ldg(p.past + b) + (int)(i0 + k) - cu[b];
+          id[k] = __ldcg(p.table + (int64_t)b * p.MB + column(p, pos[k]));
+        }
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+          if (i0 + k >= granted) continue;
+          if (id[k] >= 0 && id[k] < p.NB)
+            slot[k] = id[k] * p.BS + (pos[k] - column(p, pos[k]) * p.BS);
+          else
+            flags |= PKV_DEV_BAD_BLOCK;
+        }
+      }
+    }
+    if (wide && i0 + kTokens <= p.T) {
+#pragma unroll
+      for (int k = 0; k < kTokens; k += 4) {
+        if (p.slots)
+          *reinterpret_cast<int4*>(p.slots + i0 + k) =
+              make_int4(slot[k], slot[k + 1], slot[k + 2], slot[k + 3]);
+        if (p.positions)
+          *reinterpret_cast<int4*>(p.positions + i0 + k) =
+              make_int4(pos[k], pos[k + 1], pos[k + 2], pos[k + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kTokens; ++k) {
+        if (i0 + k >= p.T) break;
+        if (p.slots) p.slots[i0 + k] = slot[k];
+        if (p.positions) p.positions[i0 + k] = pos[k];
+      }
+    }
+  }
+  return flags;
+}
+
 __global__ void __launch_bounds__(kThreads) schedule_kernel(ScheduleParams p) {
   extern __shared__ __align__(16) int smem[];
   __shared__ int s_asked[2][kWarps], s_groups[kWarps];   // one of two: see block_sum
@@ -115,6 +188,7 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(ScheduleParams p) {
   int* gfree = cu + p.B + 1;         // [groups] free ids of a group, then those before it
   uint32_t* bits = reinterpret_cast<uint32_t*>(gfree + p.groups);   // [groups * 32]
 
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -256,8 +330,6 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(ScheduleParams p) {
   }
 
   const int granted = cu[p.B];
-  const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) |
-                      reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
   if (p.T <= C * kThreads) {   // few tokens: one to a thread
     const int i = tid * C + rank;   // spread over the blocks
     if (i < p.T && (p.slots || p.positions)) {
@@ -277,69 +349,23 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(ScheduleParams p) {
     if (flags) flag_status(p.status, flags);
     return;
   }
-  // many: kTokens to a thread; the first one's row by a search, its block and the next one ahead of
-  // the rest
   const int64_t stride = (int64_t)C * kThreads * kTokens;
   const int at = p.T <= stride ? tid * C + rank : rank * kThreads + tid;   // one round: spread
-  for (int64_t i0 = p.slots || p.positions ? (int64_t)at * kTokens : p.T;
-       i0 < p.T; i0 += stride) {
-    int slot[kTokens], pos[kTokens];
-#pragma unroll
-    for (int k = 0; k < kTokens; ++k) slot[k] = pos[k] = -1;
-    if (i0 < granted) {
-      int b = first_above(cu + 1, p.B, (int)i0);
-      const int pos0 = __ldg(p.past + b) + (int)i0 - cu[b], col0 = column(p, pos0);
-      const int32_t* entry = p.table + (int64_t)b * p.MB + col0;
-      const int id0 = __ldcg(entry), id1 = col0 + 1 < p.MB ? __ldcg(entry + 1) : -1;
-      const int last = column(p, pos0 + kTokens - 1);
-      if (i0 + kTokens <= cu[b + 1] && last <= col0 + 1 && id0 >= 0 && id0 < p.NB &&
-          (last == col0 || (id1 >= 0 && id1 < p.NB))) {   // one row, at most two blocks
-        const int turn = (col0 + 1) * p.BS - pos0;          // tokens of the first block
-        const int base0 = id0 * p.BS + (pos0 - col0 * p.BS), base1 = id1 * p.BS - turn;
-#pragma unroll
-        for (int k = 0; k < kTokens; ++k) {
-          pos[k] = pos0 + k;
-          slot[k] = (k < turn ? base0 : base1) + k;
-        }
-      } else {
-        int id[kTokens];   // all the blocks at once: the loads are what takes time
-#pragma unroll
-        for (int k = 0; k < kTokens; ++k) {
-          id[k] = 0;
-          if (i0 + k >= granted) continue;
-          while (cu[b + 1] <= i0 + k) ++b;
-          pos[k] = __ldg(p.past + b) + (int)(i0 + k) - cu[b];
-          id[k] = __ldcg(p.table + (int64_t)b * p.MB + column(p, pos[k]));
-        }
-#pragma unroll
-        for (int k = 0; k < kTokens; ++k) {
-          if (i0 + k >= granted) continue;
-          if (id[k] >= 0 && id[k] < p.NB)
-            slot[k] = id[k] * p.BS + (pos[k] - column(p, pos[k]) * p.BS);
-          else
-            flags |= PKV_DEV_BAD_BLOCK;
-        }
-      }
-    }
-    if (wide && i0 + kTokens <= p.T) {
-#pragma unroll
-      for (int k = 0; k < kTokens; k += 4) {
-        if (p.slots)
-          *reinterpret_cast<int4*>(p.slots + i0 + k) =
-              make_int4(slot[k], slot[k + 1], slot[k + 2], slot[k + 3]);
-        if (p.positions)
-          *reinterpret_cast<int4*>(p.positions + i0 + k) =
-              make_int4(pos[k], pos[k + 1], pos[k + 2], pos[k + 3]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kTokens; ++k) {
-        if (i0 + k >= p.T) break;
-        if (p.slots) p.slots[i0 + k] = slot[k];
-        if (p.positions) p.positions[i0 + k] = pos[k];
-      }
-    }
-  }
+  if (!p.apart && (p.slots || p.positions))
+    flags |= many_slots(p, cu, granted, (int64_t)at * kTokens, stride);
+  if (flags) flag_status(p.status, flags);
+}
+
+// The slots of very many tokens, on all SMs, behind the kernel above.
+constexpr int kSlotThreads = 512;
+__global__ void __launch_bounds__(kSlotThreads) schedule_slots_kernel(ScheduleParams p) {
+  extern __shared__ __align__(16) int smem[];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  for (int b = threadIdx.x; b <= p.B; b += kSlotThreads) smem[b] = __ldcg(p.cu + b);
+  __syncthreads();
+  const int64_t at = (int64_t)blockIdx.x * kSlotThreads + threadIdx.x;
+  const int flags =
+      many_slots(p, smem, smem[p.B], at * kTokens, (int64_t)gridDim.x * kSlotThreads * kTokens);
   if (flags) flag_status(p.status, flags);
 }
 
@@ -381,17 +407,31 @@ cudaError_t launch_schedule(const ScheduleParams& p, cudaStream_t s) {
     mark_configured(configured, dev);
   }
   // Blocks of the cluster: 16 where many entries or tokens are to be gone through (2048 rows of
-  // 600 entries and 325 000 tokens: 52 us with 8, 33 us with 16), else 8 (64 rows of 520 entries:
-  // 10.6 us with 8, 13.9 us with 1; 2 rows: 6.1 us with either).
+  // 600 entries and 325 000 tokens, their slots included: 52 us with 8, 33 us with 16), else 8 (64
+  // rows of 520 entries: 10.6 us with 8, 13.9 us with 1; 2 rows: 6.1 us with either).
   const int64_t work = (int64_t)p.B * ((p.MB + kChunk - 1) / kChunk) / kWarps +
                        (int64_t)p.T / (kThreads * kTokens) + p.groups / kWarps;
   const bool can = dev >= 0 && dev < 64 && (wide.load() & (1ull << dev));
   const unsigned C = work < 64 || !can ? 8 : kMaxCluster;
+  ScheduleParams q = p;
+  q.apart = (p.slots || p.positions) && p.T >= kApartFrom ? 1 : 0;
+  {
+    ProfScope ps("schedule", s);
+    cfg.gridDim = dim3(C);
+    cfg.dynamicSmemBytes = schedule_smem(p);
+    attr[0].val.clusterDim.x = C;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, schedule_kernel, q);
+    if (e != cudaSuccess || !q.apart) return e;
+  }
   ProfScope ps("schedule", s);
-  cfg.gridDim = dim3(C);
-  cfg.dynamicSmemBytes = schedule_smem(p);
-  attr[0].val.clusterDim.x = C;
-  return cudaLaunchKernelEx(&cfg, schedule_kernel, p);
+  const int64_t blocks = ((int64_t)p.T + kSlotThreads * kTokens - 1) / (kSlotThreads * kTokens);
+  const int fit = 2 * device_sms();
+  cfg.gridDim = dim3((unsigned)(blocks < fit ? blocks : fit));
+  cfg.blockDim = dim3(kSlotThreads);
+  cfg.dynamicSmemBytes = sizeof(int) * ((size_t)p.B + 1);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, schedule_slots_kernel, q);
 }
 
 }  // namespace pkv

@@ -23,6 +23,7 @@ struct ScheduleParams {
   int B, MB, BS, NB, T;
   int bs_shift;              // log2(BS) when BS is a power of two, else -1
   int groups;                // groups of 1024 block ids
+  int apart;                 // the tokens' slots are left to a kernel of their own
 };
 constexpr int kScheduleMaxBatch = 8192;
 constexpr int kScheduleMaxBlocks = 1 << 20;

@@ -149,3 +149,40 @@ def test_captured_and_replayed_on_a_side_stream():
         for name, x, r in zip(NAMES, [*out, t], ref):
             np.testing.assert_array_equal(x.cpu().numpy().reshape(-1),
                                           np.asarray(r).reshape(-1), err_msg=f"{name} {step}")
+
+
+@pytest.mark.parametrize("rows,past,new,bs,cut", [
+    (150, 3000, 1200, 16, -5), (150, 3000, 1200, 24, 900), (40, 500, 5000, 1, 0),
+    (8192, 40, 40, 8, -1), (1, 3, 90000, 32, -30000)])
+def test_very_many_tokens(rows, past, new, bs, cut):
+    # so many that their slots are a kernel of their own; a hole among the held blocks
+    p, n, table, blocks = drawn(rows + bs, rows, past, new, bs, spare=4, idle=0.1)
+    if p[0] % bs:
+        table[0, p[0] // bs] = -1
+    tokens = int(n.sum()) - cut
+    assert tokens >= 65536
+    kw = dict(num_blocks=blocks, block_size=bs, num_tokens=tokens)
+    got = check(p, n, table, **kw)
+    buf = torch.full((2, tokens + 9), 5, dtype=torch.int32, device=DEV)   # not 16-byte aligned
+    slots, pos = buf[0, 1:tokens + 1], buf[1, 3:tokens + 3]
+    more, _ = run(p, n, table, slot_mapping=slots, positions=pos, **kw)
+    for x, y in zip(got, more):
+        np.testing.assert_array_equal(x, y)
+    assert buf[0, 0] == 5 and (buf[0, tokens + 1:] == 5).all()
+    assert (buf[1, :3] == 5).all() and (buf[1, tokens + 3:] == 5).all()
+
+
+def test_very_many_tokens_in_a_graph():
+    p, n, table, blocks = drawn(3, 200, 3000, 900, 16, spare=4, idle=0.1)
+    kw = dict(num_blocks=blocks, block_size=16, num_tokens=int(n.sum()))
+    want, _ = run(p, n, table, **kw)
+    past, new, t = i32(p), i32(n), i32(table)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = B.pkv_paged_schedule(past, new, t, **kw)
+    for _ in range(3):
+        t.copy_(i32(table))
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(list(out) + [t], want):
+            np.testing.assert_array_equal(x.cpu().numpy(), y)
