@@ -388,14 +388,23 @@ void launch_typed(const AxesParams& p, cudaStream_t s) {
       append_axes_stream_kernel<T, TT, true><<<per_sm * sms, block, smem, s>>>(p, items);
     else
       append_axes_stream_kernel<T, TT, false><<<per_sm * sms, block, smem, s>>>(p, items);
-  } else if (p.T >= 8 * tokens * sms) {
-    // four tokens to a thread, so that enough of their loads are under way at once (65536 tokens
-    // of 48 items: 57 us, with one 74 us; blocks that stay took 74 us, they need more registers
-    // where a thread gathers for several tokens)
-    launch_items<T, TT, 4>(p, items, tokens, threads, s);
-  } else {   // few: spread over the SMs (64 tokens of 384 items: 3.4 us)
-    launch_items<T, TT, 1>(p, items, tokens, threads, s);
+    return;
   }
+  // Tokens of a thread (one, two, four: 56, 64, 80 registers): as few as one wave of blocks takes
+  // them all with; else two, so that the last wave is no longer than it has to be, and four where
+  // the waves are many. Tokens of 48 items, with 1, 2, 4: 4096 6.9, 5.9, 7.1 us; 8192 11.1, 10.2,
+  // 8.8 us; 12000 15.0, 12.1, 14.4 us. Of 80 items, with 2, 4: 12000 17.4, 18.5 us; 65536 83, 74 us.
+  // (Blocks that stay took 74 us for 65536 of 48 items, 57 us with four: they need more registers
+  // where a thread gathers for several tokens.)
+  const auto wave = [&](int n, int regs) {
+    return (int64_t)(65536 / (threads * regs)) * n * tokens * sms;
+  };
+  if (p.T <= wave(1, 56))
+    launch_items<T, TT, 1>(p, items, tokens, threads, s);
+  else if (p.T > wave(2, 64) && (p.T <= wave(4, 80) || p.T > 3 * wave(4, 80)))
+    launch_items<T, TT, 4>(p, items, tokens, threads, s);
+  else
+    launch_items<T, TT, 2>(p, items, tokens, threads, s);
 }
 
 }  // namespace
