@@ -220,6 +220,7 @@ def test_many_tokens_match_the_oracle():
 
 @pytest.mark.parametrize("kw", [
     dict(tokens=320000, head_size=8, rotary_dim=0, axes=0),
+    dict(tokens=100001, head_size=16, rotary_dim=16, axes=2),
     dict(tokens=160001, head_size=16, rotary_dim=16, axes=2),
     dict(tokens=160001, head_size=16, rotary_dim=16, axes=2, interleaved=True),
 ], ids=str)
