@@ -14,7 +14,9 @@
 // 6630 GB/s (95 to 98 % of measured copy bandwidth).
 // Sequences with more than 16 such rows go to the tiles of 256 rows: 64 x 4000 states, 4 heads of
 // 128 a kv head, 1 or 4 tokens each: 161 and 169 us here, 203 us there (5 tokens).
-// Runs may be single steps: 2 tokens over 400 states 8.8 us, from two steps on 10.6 us.
+// Few and short sequences take one launch (kSmall): 2 tokens over 400 states 5.2 us.
+#include <cmath>
+
 #include "cross_dev.cuh"
 
 namespace pkv {
@@ -155,6 +157,81 @@ __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane) {
   }
 }
 
+// ---------------------------------------------------------------------------- join
+// Over the pieces of a row: M = max m, out = sum 2^{m - M} o / sum 2^{m - M} l. What it waits for
+// is memory, so a warp asks for kAhead pieces of a row at once, whether they weigh anything or
+// not; a piece of no weight may hold anything.
+constexpr int kJoinWarps = 8;
+// pieces of a row that a warp asks for at once (8 lowered the occupancy: 64 tokens 16 us, not 12)
+constexpr int kAhead = 4;
+// rows of a tile's record that a block takes (records of many pieces: 12 us, with 64 18 us)
+constexpr int kJoinRows = 16;
+
+template <int D>
+struct Joined {
+  static constexpr int V = D / 32;   // columns of a lane
+  float acc[V], M = -INFINITY, L = 0.f;
+  // pieces from, from + share, ... of `pieces`: rows `apart` one from the other, the first one
+  // `late` rows on
+  __device__ __forceinline__ void add(const float* po, const float* pm, const float* pl, int row,
+                                      int late, int apart, int pieces, int from, int share,
+                                      int lane) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int q0 = from; q0 < pieces; q0 += kAhead * share) {
+      float m[kAhead], l[kAhead], x[kAhead][V];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int q = min(q0 + k * share, pieces - 1);
+        const int at = q * apart + (q == 0 ? late : 0) + row;
+        m[k] = __ldcg(pm + at);
+        l[k] = q0 + k * share < pieces ? __ldcg(pl + at) : 0.f;
+        const float* src = po + (int64_t)at * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+          x[k][0] = y.x;
+          x[k][1] = y.y;
+          x[k][2] = y.z;
+          x[k][3] = y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+          x[k][0] = y.x;
+          x[k][1] = y.y;
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) top = l[k] == 0.f ? top : fmaxf(top, m[k]);
+      const float base = top == -INFINITY ? 0.f : top, old = ex2(M - base);
+      M = top;
+      L *= old;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= old;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (l[k] == 0.f) continue;
+        const float w = ex2(m[k] - base);
+        L += w * l[k];
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += w * x[k][v];
+      }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void write(const CrossParams& p, int64_t row, int lane) const {
+    const float inv = inverse_of(L);
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * V);
+#pragma unroll
+    for (int v = 0; v < V; v += 2) out[v / 2] = Num<T>::pack(acc[v] * inv, acc[v + 1] * inv);
+    if (p.lse && lane == 0) p.lse[row] = lse_of(M, L);
+  }
+};
+
+// ---------------------------------------------------------------------------- few rows
+__device__ __forceinline__ void named_barrier() {
+  asm volatile("bar.sync 1, %0;\n" ::"n"(kThreads) : "memory");
+}
+
 template <int D>
 struct Ring {
   static constexpr int kSteps = 3;
@@ -162,7 +239,10 @@ struct Ring {
   static constexpr size_t kBytes = kWarps * kWarpBytes;
 };
 
-template <typename T, int D>
+// kSmall: a block takes one sequence and kv head, its warps an eighth of the steps each, and joins
+// what they have in shared memory (few and short sequences: p.small). Behind these blocks are a few
+// that look for rows to be zeroed.
+template <typename T, int D, bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   constexpr int NS = Ring<D>::kSteps, K = few_keys(D);
   extern __shared__ __align__(128) unsigned char smem[];
@@ -172,17 +252,37 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int flags = 0;
-  const Plan pl = make_plan<kThreads>(p, p.few_units / p.few_heads, s_pref, s_scratch, &flags);
-  if (blockIdx.x > 0) flags = 0;   // every block saw them
   const int gw = blockIdx.x * kWarps + warp;
-  const int unit = gw / p.few_heads, sub = gw % p.few_heads;
-  const int64_t g0 = (int64_t)unit * pl.W;
-  const int nst = g0 < pl.total ? (int)(min(pl.total, g0 + pl.W) - g0) : 0;
+  Plan pl{};
+  Cursor cc{};   // step computed
+  int nst = 0, unit = 0, sub = 0;
+  if constexpr (kSmall) {
+    const int work = p.B * p.Hkv;
+    if ((int)blockIdx.x >= work) {
+      zero_rows<T, D>(p, gw - work * kWarps, ((int)gridDim.x - work) * kWarps, lane);
+      return;
+    }
+    bool zero;
+    cc.b = blockIdx.x / p.Hkv;
+    cc.r = blockIdx.x - cc.b * p.Hkv;
+    cc.q = read_seq<false>(p, cc.b, &flags, &zero);
+    if (cc.r > 0 || warp > 0) flags = 0;   // every block of the sequence saw them
+    const int share = (cc.q.steps + kWarps - 1) / kWarps;
+    cc.s = warp * share;
+    nst = max(0, min(share, cc.q.steps - cc.s));
+  } else {
+    pl = make_plan<kThreads>(p, p.few_units / p.few_heads, s_pref, s_scratch, &flags);
+    if (blockIdx.x > 0) flags = 0;   // every block saw them
+    unit = gw / p.few_heads;
+    sub = gw % p.few_heads;
+    const int64_t g0 = (int64_t)unit * pl.W;
+    nst = g0 < pl.total ? (int)(min(pl.total, g0 + pl.W) - g0) : 0;
+    if (nst > 0) cc = locate(p, pl, s_pref, g0);
+  }
   if (nst > 0) {
     T* rk = reinterpret_cast<T*>(smem + warp * Ring<D>::kWarpBytes);
     T* rv = rk + NS * K * D;
-    Cursor pc = locate(p, pl, s_pref, g0);   // next step to copy
-    Cursor cc = pc;                                  // step computed
+    Cursor pc = cc;                                  // next step to copy
     uint32_t* live = s_live[warp];                   // keys of a step that take part
     int64_t ahead = key_offset<D>(p, pc.b, pc.r * p.few_heads + sub, pc.s, pc.q.keys, lane, flags);
     const auto issue = [&](int k, int buf) {
@@ -204,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
     uint32_t qa[D / 16][4];
     load_queries<T, D>(p, cc, cc.r * p.few_heads + sub, lane, qa);
     // while the first steps are on their way (in front of them it took 1 us of 64 tokens' 178 us)
-    if (lane == 0) write_record(p, pl, s_pref, unit, sub, p.few_rec + 2 * gw);
+    if (!kSmall && lane == 0) write_record(p, pl, s_pref, unit, sub, p.few_rec + 2 * gw);
     __syncwarp();
     const int t4 = lane & 3;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
@@ -300,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
         }
       }
       const bool last = cc.s == cc.q.steps - 1;
-      if (last || k == nst - 1) {
+      if (!kSmall && (last || k == nst - 1)) {
         flush<T, D>(p, cc, cc.r * p.few_heads + sub, gw, from_start && last, first ? 0 : 1, m, l, o,
                     lane);
         m[0] = m[1] = -INFINITY;
@@ -322,84 +422,56 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
       out = out + 1 == NS ? 0 : out + 1;
     }
     cp_async_wait<0>();
+    if constexpr (kSmall) {
+      named_barrier();   // the pieces take the rings' place
+      CrossParams here = p;
+      here.few_o = reinterpret_cast<float*>(smem);
+      here.few_m = here.few_o + 2 * kWarps * 16 * D;
+      here.few_l = here.few_m + 2 * kWarps * 16;
+      here.few_rows = 16;
+      flush<T, D>(here, cc, cc.r, warp, false, 0, m, l, o, lane);
+    }
+  } else if constexpr (kSmall) {
+    named_barrier();
+    float* const l = reinterpret_cast<float*>(smem) + 2 * kWarps * 16 * (D + 1);
+    if (lane < 16) l[2 * warp * 16 + lane] = 0.f;
   } else if (lane == 0) {
     p.few_rec[2 * gw] = make_int4(0, 0, 0, 0);   // nothing to join
   }
-  if (pl.zero) zero_rows<T, D>(p, gw, p.few_units, lane);
+  if constexpr (kSmall) {
+    __syncthreads();
+    const float* const po = reinterpret_cast<const float*>(smem);
+    const float *pm = po + 2 * kWarps * 16 * D, *pl_ = pm + 2 * kWarps * 16;
+    const int rows = cc.q.ranges > 0 ? cc.q.rows * p.G : 0;
+    for (int r = warp; r < rows; r += kWarps) {
+      Joined<D> j;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        top = pl_[2 * w * 16 + r] == 0.f ? top : fmaxf(top, pm[2 * w * 16 + r]);
+      const float base = top == -INFINITY ? 0.f : top;
+      j.M = top;
+#pragma unroll
+      for (int v = 0; v < Joined<D>::V; ++v) j.acc[v] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int at = 2 * w * 16 + r;
+        if (pl_[at] == 0.f) continue;
+        const float by = ex2(pm[at] - base);
+        j.L += by * pl_[at];
+#pragma unroll
+        for (int v = 0; v < Joined<D>::V; ++v)
+          j.acc[v] += by * po[at * D + lane * Joined<D>::V + v];
+      }
+      j.template write<T>(p, (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G, lane);
+    }
+  } else if (pl.zero) {
+    zero_rows<T, D>(p, gw, p.few_units, lane);
+  }
   if (flags) flag_status(p.status, flags);
   // the join behind this kernel waits for it alone: it must not end before the one in front
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
-
-// ---------------------------------------------------------------------------- join
-// Over the pieces of a row: M = max m, out = sum 2^{m - M} o / sum 2^{m - M} l. What it waits for
-// is memory, so a warp asks for kAhead pieces of a row at once, whether they weigh anything or
-// not; a piece of no weight may hold anything.
-constexpr int kJoinWarps = 8;
-// pieces of a row that a warp asks for at once (8 lowered the occupancy: 64 tokens 16 us, not 12)
-constexpr int kAhead = 4;
-// rows of a tile's record that a block takes (records of many pieces: 12 us, with 64 18 us)
-constexpr int kJoinRows = 16;
-
-template <int D>
-struct Joined {
-  static constexpr int V = D / 32;   // columns of a lane
-  float acc[V], M = -INFINITY, L = 0.f;
-  // pieces from, from + share, ... of `pieces`: rows `apart` one from the other, the first one
-  // `late` rows on
-  __device__ __forceinline__ void add(const float* po, const float* pm, const float* pl, int row,
-                                      int late, int apart, int pieces, int from, int share,
-                                      int lane) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int q0 = from; q0 < pieces; q0 += kAhead * share) {
-      float m[kAhead], l[kAhead], x[kAhead][V];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int q = min(q0 + k * share, pieces - 1);
-        const int at = q * apart + (q == 0 ? late : 0) + row;
-        m[k] = __ldcg(pm + at);
-        l[k] = q0 + k * share < pieces ? __ldcg(pl + at) : 0.f;
-        const float* src = po + (int64_t)at * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-          x[k][0] = y.x;
-          x[k][1] = y.y;
-          x[k][2] = y.z;
-          x[k][3] = y.w;
-        } else {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-          x[k][0] = y.x;
-          x[k][1] = y.y;
-        }
-      }
-      float top = M;
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) top = l[k] == 0.f ? top : fmaxf(top, m[k]);
-      const float base = top == -INFINITY ? 0.f : top, old = ex2(M - base);
-      M = top;
-      L *= old;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] *= old;
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (l[k] == 0.f) continue;
-        const float w = ex2(m[k] - base);
-        L += w * l[k];
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += w * x[k][v];
-      }
-    }
-  }
-  template <typename T>
-  __device__ __forceinline__ void write(const CrossParams& p, int64_t row, int lane) const {
-    const float inv = inverse_of(L);
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * V);
-#pragma unroll
-    for (int v = 0; v < V; v += 2) out[v / 2] = Num<T>::pack(acc[v] * inv, acc[v + 1] * inv);
-    if (p.lse && lane == 0) p.lse[row] = lse_of(M, L);
-  }
-};
 
 // Blocks 0 .. : kJoinRows rows of a tile's record each (256 / kJoinRows blocks a record). Behind
 // them a block for the record of each warp of the kernel for few rows: 8 warps share the rows that
@@ -488,10 +560,21 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
   int dev = -1;
   if (needs_configure(configured, &dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        cross_few_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<D>::kBytes);
+    cudaError_t e = cudaFuncSetAttribute(cross_few_kernel<T, D, false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Ring<D>::kBytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(cross_few_kernel<T, D, true>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<D>::kBytes);
     if (e != cudaSuccess) return e;
     mark_configured(configured, dev);
+  }
+  if (p.small) {
+    ProfScope ps("cross_decode", s);
+    const unsigned zero = (unsigned)((p.T + kThreads - 1) / kThreads);
+    cross_few_kernel<T, D, true>
+        <<<(unsigned)(p.B * p.Hkv) + zero, kThreads, Ring<D>::kBytes, s>>>(p);
+    return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
@@ -511,7 +594,7 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
     cfg.gridDim = dim3((unsigned)(p.few_units / kWarps));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Ring<D>::kBytes;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D, false>, p);
     if (e != cudaSuccess) return e;
   }
   ProfScope ps("cross_combine", s);
@@ -555,6 +638,21 @@ size_t cross_layout(CrossParams* p, char* base) {
     off += (bytes + 255) / 256 * 256;
     return at;
   };
+  // A block for each sequence and kv head (one launch, no plan) or an even share for every warp and
+  // the join, in units of a step of 0.85 us: steps of a warp and 3.5 for every further wave, or 5
+  // for plan and join and the even share. 2 tokens over 400 states, 2 kv heads of 64: 5.2 and 8.9 us;
+  // 16 x 500, 8 kv heads of 64: 6.1 and 12.1 us; 19 x 1000, 8 of 128: 16.0 and 23.9 us; 1 x 2000,
+  // 2 of 64: 11.8 and 9.9 us; 64 x 250, 8 of 64: 15.3 and 13.9 us.
+  const double ranges = (double)p->B * p->Hkv, waves = std::ceil(ranges / sms);
+  const double steps = std::ceil(std::ceil(keys / few_keys(p->D)) / kWarps);
+  const double even = ranges * steps / sms;
+  p->small = p->max_q <= p->few && ranges <= 4.0 * sms &&
+             waves * steps + 3.5 * (waves - 1) <= 5 + (even > 1 ? even : 1);
+  if (p->small) {
+    p->few_heads = 1;
+    take(256);   // as much as nothing: no workspace is used
+    return off;
+  }
   const size_t fu = (size_t)p->few_units, tu = (size_t)p->tile_units;
   p->few_rec = reinterpret_cast<int4*>(take(fu * 32));
   p->few_o = reinterpret_cast<float*>(take(2 * fu * p->few_rows * p->D * 4));

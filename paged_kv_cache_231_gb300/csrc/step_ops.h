@@ -75,6 +75,7 @@ struct CrossParams {
   int few_heads;             // kv heads that as many neighbouring warps of the first take together
   int few_units;             // warps of the first, blocks of the second (0: not launched)
   int tile_units;
+  int small;                 // a block for each sequence and kv head, nothing else (few rows)
   int few_rows;              // rows of a piece of the first: at most 16
   int box_keys;              // keys of a TMA box (0: rows are copied one by one)
   uint32_t wait_tries;       // testing hook (pkv_testing_wait_limit), as in AttnParams

@@ -267,3 +267,17 @@ def test_tiles_of_one_step_and_of_many(d):
     first, _ = c.check()
     for _ in range(10):
         assert torch.equal(c.gpu()[0], first)
+
+
+@pytest.mark.parametrize("d,bs,nk", [(64, 16, 500), (128, 8, 120), (64, 24, 2000), (128, 16, 700)])
+@pytest.mark.parametrize("batch,kv,heads", [(1, 1, 1), (3, 5, 15), (37, 2, 8), (70, 4, 4)])
+def test_few_and_short_sequences(batch, kv, heads, d, bs, nk):
+    # one launch for these, an even share of many steps for others: lengths of 0, 1 and all between,
+    # several rows a sequence, rows that no sequence covers
+    rng = np.random.default_rng(batch + d)
+    keys = [int(x) for x in rng.integers(0, nk + 1, batch)]
+    keys[0], keys[-1] = nk, min(1, nk)
+    nq = [int(x) for x in rng.integers(0, 4, batch)]
+    nq[0] = 3
+    c = CrossCase(39, nq, keys, num_heads=heads, kv_heads=kv, head_size=d, block_size=bs, pad=300)
+    c.check(max_query_len=3)
