@@ -640,7 +640,7 @@ size_t cross_layout(CrossParams* p, char* base) {
   };
   // A block for each sequence and kv head (one launch, no plan) or an even share for every warp and
   // the join, in units of a step of 0.85 us: steps of a warp and 3.5 for every further wave, or 5
-  // for plan and join and the even share. 2 tokens over 400 states, 2 kv heads of 64: 5.2 and 8.9 us;
+  // for plan and join and the even share. 2 tokens over 400 states, 2 heads of 64: 5.2 and 8.9 us;
   // 16 x 500, 8 kv heads of 64: 6.1 and 12.1 us; 19 x 1000, 8 of 128: 16.0 and 23.9 us; 1 x 2000,
   // 2 of 64: 11.8 and 9.9 us; 64 x 250, 8 of 64: 15.3 and 13.9 us.
   const double ranges = (double)p->B * p->Hkv, waves = std::ceil(ranges / sms);
