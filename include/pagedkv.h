@@ -551,7 +551,8 @@ typedef struct pkv_cross_attention_args {
   float scale;                   /* softmax scale; 0 means 1/sqrt(head_size) */
 } pkv_cross_attention_args;
 
-/* Host only: workspace bytes pkv_cross_attention needs on the current device. */
+/* Host only: workspace bytes pkv_cross_attention needs on the current device; 0 where few and
+ * short sequences need none (workspace may then be NULL). */
 int pkv_cross_attention_workspace_size(const pkv_cross_attention_args* args, size_t* bytes);
 
 /* Query row i of sequence b, head hq with kv head h = hq / (num_heads / kv_num_heads), over

@@ -845,7 +845,7 @@ def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_lengt
         _keep(stream, output)
     sizes = (T, B, num_heads, kv_num_heads, D, BS, NB, MB, max_query_len, code)
     need = _cross_workspace(query.get_device(), *sizes)
-    if workspace is None or workspace.numel() < need:
+    if need and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
         _keep(stream, workspace)
     _step_call("pkv_cross_attention",
@@ -853,7 +853,7 @@ def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_lengt
                                 cumulative_sequence_length.data_ptr(), key_seqlens.data_ptr(),
                                 block_table.data_ptr(), output.data_ptr(), _at(lse),
                                 _at(device_status), *sizes, scale),
-               workspace.data_ptr(), need, raw)
+               _at(workspace), need, raw)
     return output
 
 

@@ -650,8 +650,7 @@ size_t cross_layout(CrossParams* p, char* base) {
              waves * steps + 3.5 * (waves - 1) <= 5 + (even > 1 ? even : 1);
   if (p->small) {
     p->few_heads = 1;
-    take(256);   // as much as nothing: no workspace is used
-    return off;
+    return 0;
   }
   const size_t fu = (size_t)p->few_units, tu = (size_t)p->tile_units;
   p->few_rec = reinterpret_cast<int4*>(take(fu * 32));

@@ -204,8 +204,8 @@ int pkv_cross_attention(const pkv_cross_attention_args* args, void* workspace,
   if (st != PKV_OK) return st;
   if (args->num_tokens == 0) return PKV_OK;
   if (args->output == args->query) return PKV_ERR_SHAPE;
-  if (!workspace || workspace_bytes < cross_layout(&p, static_cast<char*>(workspace)) ||
-      !aligned(workspace, 256))
+  const size_t need = cross_layout(&p, static_cast<char*>(workspace));
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return PKV_ERR_WORKSPACE;
   return status_of(launch_cross(p, static_cast<cudaStream_t>(stream)));
 }

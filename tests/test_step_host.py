@@ -119,6 +119,9 @@ def test_cross_refusals(lib, change, status):
 def test_cross_workspace_refusals(lib):
     a, n = cross_args(), ctypes.c_size_t(0)
     assert lib.pkv_cross_attention_workspace_size(ctypes.byref(a), ctypes.byref(n)) == 0
+    assert n.value == 0      # few and short sequences need none
+    a = cross_args(max_blocks=4096)
+    assert lib.pkv_cross_attention_workspace_size(ctypes.byref(a), ctypes.byref(n)) == 0
     assert n.value > 0
     before = B.pkv_launch_count()
     for ws, size in ((None, n.value), (P, n.value - 1), (P + 128, n.value)):
