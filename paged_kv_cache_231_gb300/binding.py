@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -803,6 +804,28 @@ def _cross_workspace(device: int, *sizes) -> int:
     return pkv_cross_attention_workspace_size(a)
 
 
+_OWN = threading.local()
+_OWN_BYTES = 128 << 20
+
+
+def _own_workspace(need: int, like, stream, raw: int):
+    """A workspace for a call that brought none. Each thread keeps one for each stream it calls
+    on as the current one (an allocation costs a call 6 us): calls of one thread on one stream
+    run one after the other. A call that is captured gets memory of its graph's, one on another
+    stream than the current one or of a large workspace its own."""
+    torch = _torch()
+    if stream is not None or need > _OWN_BYTES or torch.cuda.is_current_stream_capturing():
+        made = torch.empty(need, dtype=torch.uint8, device=like.device)
+        _keep(stream, made)
+        return made
+    kept = _OWN.__dict__
+    key = (like.get_device(), raw)
+    own = kept.get(key)
+    if own is None or own.numel() < need:
+        own = kept[key] = torch.empty(need, dtype=torch.uint8, device=like.device)
+    return own
+
+
 def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_length,
                         key_seqlens, block_table, *, num_heads: int, kv_num_heads: int,
                         max_query_len: int = 0, scale: float = 0.0, output=None, lse=None,
@@ -810,7 +833,8 @@ def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_lengt
     """Attention of ragged query rows over encoder states in a paged cache: row i of
     sequence b sees the key_seqlens[b] states of table row b. float16 or bfloat16. Returns
     the output [num_tokens, num_heads * head_size]; with ``lse`` (float32 [num_tokens,
-    num_heads]) the log-sum-exp of each row's scores is written there."""
+    num_heads]) the log-sum-exp of each row's scores is written there. Without ``workspace``
+    one is kept for the calling thread and stream (see _own_workspace)."""
     torch = _torch()
     if (query is None or key_cache is None or value_cache is None or block_table is None or
             cumulative_sequence_length is None or key_seqlens is None):
@@ -846,8 +870,7 @@ def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_lengt
     sizes = (T, B, num_heads, kv_num_heads, D, BS, NB, MB, max_query_len, code)
     need = _cross_workspace(query.get_device(), *sizes)
     if need and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
-        _keep(stream, workspace)
+        workspace = _own_workspace(need, query, stream, raw)
     _step_call("pkv_cross_attention",
                _CROSS_PACK.pack(query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                                 cumulative_sequence_length.data_ptr(), key_seqlens.data_ptr(),

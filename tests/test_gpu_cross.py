@@ -1,4 +1,6 @@
 """GPU parity of pkv_cross_attention against its definition in 64 bits."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -281,3 +283,61 @@ def test_few_and_short_sequences(batch, kv, heads, d, bs, nk):
     nq[0] = 3
     c = CrossCase(39, nq, keys, num_heads=heads, kv_heads=kv, head_size=d, block_size=bs, pad=300)
     c.check(max_query_len=3)
+
+
+def _pieces(seed, dtype="f16"):
+    # ranges that are cut, so that the workspace is used; and few and many rows in one call
+    return CrossCase(seed, [1, 70, 2, 1], [9000, 4000, 70, 12000], num_heads=8, kv_heads=2,
+                     head_size=128, block_size=16, dtype=dtype)
+
+
+class _Call:
+    def __init__(self, c):
+        self.k = dict(num_heads=c.hq, kv_num_heads=c.hkv)
+        self.a = [c.q.to(DEV), c.k.to(DEV), c.v.to(DEV), i32(c.cu), i32(c.nk), i32(c.table)]
+
+    def __call__(self, **kw):
+        return B.pkv_cross_attention(*self.a, **self.k, **kw)
+
+
+def test_own_workspaces_of_threads_and_streams():
+    calls = [_Call(_pieces(40)), _Call(_pieces(41))]
+    size = 64 << 20
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    want = [c(workspace=ws) for c in calls]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(c, expected, stream):
+        with torch.cuda.stream(stream):
+            got = [c() for _ in range(40)]
+        torch.cuda.synchronize()
+        bad.extend(i for i, g in enumerate(got) if not torch.equal(g, expected))
+
+    one = torch.cuda.Stream()
+    for streams in ((one, one), (one, torch.cuda.Stream())):   # two threads on one stream too
+        threads = [threading.Thread(target=work, args=(c, w, s))
+                   for c, w, s in zip(calls, want, streams)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not bad
+
+
+def test_captured_call_beside_eager_ones():
+    a, b = _Call(_pieces(42)), _Call(_pieces(43))
+    want_a, want_b = a(), b()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = [a() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            graph.replay()
+        eager = [b() for _ in range(6)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want_a) for x in out)
+        assert all(torch.equal(x, want_b) for x in eager)
