@@ -124,9 +124,20 @@ __device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int
   }
 }
 
-// Rows that no key is seen from, or that no sequence covers: output 0, lse -inf.
+// Whether row i lies in sequence b and sees a key of it.
+__device__ __forceinline__ bool holds_row(const CrossParams& p, int b, int i) {
+  int f = 0;
+  bool z = false;
+  const Seq few = read_seq<false>(p, b, &f, &z), many = read_seq<true>(p, b, &f, &z);
+  return few.ranges + many.ranges > 0 && i >= few.cu0 && i < few.cu0 + few.rows;
+}
+
+// Rows that no key is seen from, or that no sequence covers: output 0, lse -inf. Where the
+// cumulative lengths ascend, only the last sequence that begins at or in front of a row can hold
+// it. Where they do not (`ordered` false: some sequence is bad), a later or an earlier one can: a
+// row that the search does not find held is looked for in all of them.
 template <typename T, int D>
-__device__ void zero_rows(const CrossParams& p, int unit, int units, int lane) {
+__device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, bool ordered) {
   for (int64_t i0 = (int64_t)unit * 32; i0 < p.T; i0 += (int64_t)units * 32) {
     const int i = (int)min(i0 + lane, (int64_t)p.T - 1);
     int lo = 0, hi = p.B - 1, b = -1;
@@ -139,16 +150,14 @@ __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane) {
         hi = mid - 1;
       }
     }
-    bool empty = true;
-    if (b >= 0) {
-      int f = 0;
-      bool z = false;
-      const Seq few = read_seq<false>(p, b, &f, &z), many = read_seq<true>(p, b, &f, &z);
-      empty = few.ranges + many.ranges == 0 || i >= few.cu0 + few.rows;
-    }
+    const bool empty = b < 0 || !holds_row(p, b, i);
     uint32_t todo = __ballot_sync(0xffffffffu, empty && i0 + lane < p.T);
     for (; todo; todo &= todo - 1) {
       const int64_t row = i0 + __ffs(todo) - 1;
+      bool held = false;
+      for (int b0 = 0; !ordered && !held && b0 < p.B; b0 += 32)
+        held = __any_sync(0xffffffffu, b0 + lane < p.B && holds_row(p, b0 + lane, (int)row));
+      if (held) continue;
       uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.Hq * D);
       for (int c = lane; c < p.Hq * D / 8; c += 32) out[c] = make_uint4(0, 0, 0, 0);
       if (p.lse)
@@ -259,7 +268,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   if constexpr (kSmall) {
     const int work = p.B * p.Hkv;
     if ((int)blockIdx.x >= work) {
-      zero_rows<T, D>(p, gw - work * kWarps, ((int)gridDim.x - work) * kWarps, lane);
+      bool descends = false;
+      for (int b = threadIdx.x; b < p.B; b += kThreads)
+        descends |= __ldg(p.cu + b + 1) < __ldg(p.cu + b);
+      const bool ordered = !__syncthreads_or(descends);
+      zero_rows<T, D>(p, gw - work * kWarps, ((int)gridDim.x - work) * kWarps, lane, ordered);
       return;
     }
     bool zero;
@@ -466,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
       j.template write<T>(p, (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G, lane);
     }
   } else if (pl.zero) {
-    zero_rows<T, D>(p, gw, p.few_units, lane);
+    zero_rows<T, D>(p, gw, p.few_units, lane, pl.ordered);
   }
   if (flags) flag_status(p.status, flags);
   // the join behind this kernel waits for it alone: it must not end before the one in front

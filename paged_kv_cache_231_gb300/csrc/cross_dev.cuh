@@ -139,6 +139,7 @@ struct Plan {
   int group;       // sequences of a prefix entry
   int entries;
   bool zero;       // some row sees no key (or belongs to no sequence)
+  bool ordered;    // the cumulative lengths ascend
 };
 
 // Block-wide. pref: [kEntries] steps before entry e (shared memory); scratch: [NT / 32 + 2].
@@ -149,7 +150,7 @@ __device__ Plan make_plan(const CrossParams& p, int units, int64_t* pref, int64_
   pl.group = (p.B + kEntries - 1) / kEntries;
   pl.entries = (p.B + pl.group - 1) / pl.group;
   int longest = 0;
-  bool zero = false;
+  bool zero = false, descends = false;
   int64_t carry = 0;
   for (int e0 = 0; e0 < pl.entries; e0 += NT) {
     const int e = e0 + threadIdx.x;
@@ -158,6 +159,7 @@ __device__ Plan make_plan(const CrossParams& p, int units, int64_t* pref, int64_
       const int b1 = min(p.B, (e + 1) * pl.group);
       for (int b = e * pl.group; b < b1; ++b) {
         const Seq s = read_seq<false>(p, b, flags, &zero);
+        descends |= __ldg(p.cu + b + 1) < s.cu0;
         mine += (int64_t)s.steps * s.ranges;
         longest = max(longest, s.steps);
       }
@@ -169,11 +171,13 @@ __device__ Plan make_plan(const CrossParams& p, int units, int64_t* pref, int64_
   }
   pl.total = carry;
   int* word = reinterpret_cast<int*>(scratch + NT / 32);
-  if (threadIdx.x == 0) word[0] = 0;
+  if (threadIdx.x == 0) word[0] = word[1] = 0;
   __syncthreads();
   longest = __reduce_max_sync(0xffffffffu, longest);
   if ((threadIdx.x & 31) == 0) atomicMax(word, longest);
+  if (descends) word[1] = 1;
   pl.zero = __syncthreads_or(zero) || __ldg(p.cu) != 0 || __ldg(p.cu + p.B) != p.T;
+  pl.ordered = word[1] == 0;
   pl.W = quotient(carry + units - 1, units);
   pl.W = max(pl.W, (int64_t)max(1, (word[0] + kMaxPieces - 2) / (kMaxPieces - 1)));
   return pl;
