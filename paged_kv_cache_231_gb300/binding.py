@@ -632,13 +632,22 @@ def _check_tensors(stream, tensors) -> int:
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
-def _keep(stream, *made):
-    """Memory made here for a stream other than the current one is not given away again
-    before that stream has used it."""
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+def _made(stream, shape, dtype, device, returned=True):
+    """A tensor for a call on ``stream`` (None: the current one). The allocator hands memory
+    out in the order of the stream that it is asked on: a block of the current stream's may
+    still be in use there by kernels that were enqueued before it was freed, and a call on
+    another stream would not wait for them. So it is asked for on the call's stream (in a
+    capture there, of the graph's memory); what is returned to the caller, who works on the
+    current stream, is given away again only after that stream's use too."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and stream != current:
+        t.record_stream(current)
+    return t
 
 
 def _need(**named):
@@ -678,10 +687,7 @@ def pkv_paged_schedule(past_seqlens, new_seqlens, block_table, *, num_blocks: in
         ("device_status", device_status, i32, (1,))))
 
     def made(t, n):
-        if t is None:
-            t = torch.empty(n, dtype=i32, device=block_table.device)
-            _keep(stream, t)
-        return t
+        return _made(stream, n, i32, block_table.device) if t is None else t
 
     cu, slots = made(cumulative_sequence_length, B + 1), made(slot_mapping, num_tokens)
     pos, total = made(positions, num_tokens), made(total_seqlens, B)
@@ -762,8 +768,7 @@ def pkv_paged_append_rotary_axes(query, key, value, key_cache, value_cache, slot
         ("positions", positions, i32, (axes, T)), ("cos_cache", cos_cache, tdt, (rows, half)),
         ("sin_cache", sin_cache, tdt, (rows, half)), ("device_status", device_status, i32, (1,))))
     if rotate_query and query is not None and query_out is None:
-        query_out = torch.empty((T, qh), dtype=dt, device=key_cache.device)
-        _keep(stream, query_out)
+        query_out = _made(stream, (T, qh), dt, key_cache.device)
     _step_call("pkv_paged_append_rotary_axes",
                _AXES_PACK.pack(_at(query), _at(key), _at(value), _at(query_out),
                                key_cache.data_ptr(), value_cache.data_ptr(),
@@ -815,9 +820,7 @@ def _own_workspace(need: int, like, stream, raw: int):
     stream than the current one or of a large workspace its own."""
     torch = _torch()
     if stream is not None or need > _OWN_BYTES or torch.cuda.is_current_stream_capturing():
-        made = torch.empty(need, dtype=torch.uint8, device=like.device)
-        _keep(stream, made)
-        return made
+        return _made(stream, need, torch.uint8, like.device, returned=False)
     kept = _OWN.__dict__
     key = (like.get_device(), raw)
     own = kept.get(key)
@@ -865,8 +868,7 @@ def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_lengt
         ("workspace", workspace, torch.uint8, None if workspace is None else workspace.shape),
         ("device_status", device_status, i32, (1,))))
     if output is None:
-        output = torch.empty(hidden, dtype=dt, device=query.device)
-        _keep(stream, output)
+        output = _made(stream, hidden, dt, query.device)
     sizes = (T, B, num_heads, kv_num_heads, D, BS, NB, MB, max_query_len, code)
     need = _cross_workspace(query.get_device(), *sizes)
     if need and (workspace is None or workspace.numel() < need):
