@@ -232,6 +232,24 @@ def _stream(stream) -> Optional[int]:
     return s.cuda_stream
 
 
+def _made(stream, shape, dtype, device, returned=True):
+    """A tensor for a call on ``stream`` (None: the current one). The allocator hands memory
+    out in the order of the stream that it is asked on: a block of the current stream's may
+    still be in use there by kernels that were enqueued before it was freed, and a call on
+    another stream would not wait for them. So it is asked for on the call's stream (in a
+    capture there, of the graph's memory); what is returned to the caller, who works on the
+    current stream, is given away again only after that stream's use too."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and stream != current:
+        t.record_stream(current)
+    return t
+
+
 def _require(t, dtype, name, device=True):
     torch = _torch()
     if t is None:
@@ -371,8 +389,8 @@ def pkv_paged_attention(query, key, value, key_cache, value_cache,
     attention. Returns the fp16 output [num_tokens, num_heads*head_size]."""
     torch = _torch()
     if output is None:
-        output = torch.empty((query.shape[0], num_heads * key_cache.shape[3]),
-                             dtype=torch.float16, device=query.device)
+        output = _made(stream, (query.shape[0], num_heads * key_cache.shape[3]),
+                       torch.float16, query.device)
     _check_paged_tensors(query, key, value, key_cache, value_cache,
                          cumulative_sequence_length, past_seqlens, block_table,
                          slot_mapping, output, num_heads, kv_num_heads, is_causal)
@@ -389,7 +407,7 @@ def pkv_paged_attention(query, key, value, key_cache, value_cache,
                         split_min_keys=split_min_keys, rotary_query=rotary_query)
     need = pkv_paged_attention_workspace_size(a)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=query.device)
+        workspace = _made(stream, max(need, 1), torch.uint8, query.device, returned=False)
     _check("pkv_paged_attention",
            load_library().pkv_paged_attention(ctypes.byref(a), workspace.data_ptr(), need,
                                               _stream(stream)))
@@ -516,18 +534,18 @@ def pkv_sparse_attention_partials(q, k_pages, v_pages, edge_meta, block_tables, 
     P = int(edge_meta.shape[0]) * qhead
     D = int(q.shape[2])
     if o is None:
-        o = torch.empty((P, D), dtype=torch.float32, device=q.device)
+        o = _made(stream, (P, D), torch.float32, q.device)
     if m is None:
-        m = torch.empty(P, dtype=torch.float32, device=q.device)
+        m = _made(stream, P, torch.float32, q.device)
     if l is None:
-        l = torch.empty(P, dtype=torch.float32, device=q.device)
+        l = _made(stream, P, torch.float32, q.device)
     a = make_sparse_args(q, k_pages, v_pages, edge_meta, block_tables, o, m, l, qhead=qhead,
                          block_size=block_size, page_size=page_size,
                          pages_per_block=pages_per_block, softmax_scale=softmax_scale,
                          device_status=device_status, query_positions=query_positions)
     need = pkv_sparse_attention_partials_workspace_size(a)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, max(need, 1), torch.uint8, q.device, returned=False)
     _check("pkv_sparse_attention_partials",
            load_library().pkv_sparse_attention_partials(ctypes.byref(a), workspace.data_ptr(),
                                                         need, _stream(stream)))
@@ -546,8 +564,7 @@ def pkv_combine_partials(o, m, l, segment_offsets=None, *, num_segments: int, la
     _require(segment_offsets, torch.int32, "segment_offsets")
     D = int(o.shape[-1])
     if out is None:
-        out = torch.empty((num_segments * lanes, D), dtype=out_dtype or torch.float32,
-                          device=o.device)
+        out = _made(stream, (num_segments * lanes, D), out_dtype or torch.float32, o.device)
     a = CombineArgs()
     a.o, a.m, a.l = _ptr(o), _ptr(m), _ptr(l)
     a.segment_offsets = _ptr(segment_offsets)
@@ -630,24 +647,6 @@ def _check_tensors(stream, tensors) -> int:
         _refuse(stream, tensors)
     # the current stream's handle without an object for it (a microsecond of the call)
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
-
-
-def _made(stream, shape, dtype, device, returned=True):
-    """A tensor for a call on ``stream`` (None: the current one). The allocator hands memory
-    out in the order of the stream that it is asked on: a block of the current stream's may
-    still be in use there by kernels that were enqueued before it was freed, and a call on
-    another stream would not wait for them. So it is asked for on the call's stream (in a
-    capture there, of the graph's memory); what is returned to the caller, who works on the
-    current stream, is given away again only after that stream's use too."""
-    torch = _torch()
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    current = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned and stream != current:
-        t.record_stream(current)
-    return t
 
 
 def _need(**named):
