@@ -46,6 +46,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kLeast = 2;              // steps of a run, at least (2 x 100 queries, 200 keys:
                                        // 18.5 us, with 4 20.3 us, with 8 22.3 us)
+constexpr int kMasks = 8;              // steps whose masks are held (a ring)
 constexpr uint32_t kTries = 1u << 22;  // default bound of a wait (polls)
 // registers a thread: launch, softmax warps, the other four; the first take what the last give
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -72,8 +73,8 @@ struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kBars = kRing + kStages * kTile;
-  static constexpr uint32_t kSeen = kBars + 384;        // keys of the last 8 steps that take part
-  static constexpr uint32_t kRun = kSeen + 128;          // Run
+  static constexpr uint32_t kSeen = kBars + 384;        // [kMasks] keys of a step that take part
+  static constexpr uint32_t kRun = kSeen + 16 * kMasks;  // Run
   static constexpr uint32_t kPairMl = kRun + 96;        // [128] (m, l) of half 1
   static constexpr uint32_t kEnd = kPairMl + 1024;
   static constexpr size_t kBytes = kEnd + 1024;
@@ -528,21 +529,36 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
   // two rounds of a stage apart, not three, so the round before must be known to be over. That is
   // the loader's own doing where its tiles come back to the same stages; with an odd number of
   // stages they alternate with the other loader's, which has to have found room for that tile.
+  //
+  // Room for the masks of step J = use / 2, which take the place of step J - kMasks's: those were
+  // read by every warp of the halves at work on that step once its value tile was given back (each
+  // half gives it back behind its product, and that waits for the weights of all four warps; the
+  // key tile is given back in front of that, by one warp). With an odd number of stages the room
+  // for the key tile of step J - kMasks + (kStages + 1) / 2 has told so. With an even one the
+  // other loader tells: it found room for the tile kStages behind that value tile, 2 (J - kMasks) +
+  // 1 + kStages. (That value tile came back before the key tile two steps behind it, whose stage
+  // this one takes.)
   volatile uint32_t* found = reinterpret_cast<volatile uint32_t*>(sm + L::kBars + kRoomWord);
+  constexpr bool kAlternate = L::kStages % 2 != 0;
+  static_assert(kAlternate ? (L::kStages + 1) / 2 <= kMasks : L::kStages < 2 * kMasks, "mask ring");
+  const auto other_found = [&](uint32_t tiles) {   // waits for the other loader's `found`
+    bool there = false;
+    for (uint32_t i = 0; i < wait.tries && !there; ++i) {
+      there = found[1 - kv] >= tiles;
+      if ((i & 255u) == 255u && *wait.abort) break;
+    }
+    if (!there) *wait.abort = 1;
+    return __all_sync(0xffffffffu, there) != 0;
+  };
   const auto room = [&]() {
     if (use >= (uint32_t)L::kStages) {
-      if constexpr (L::kStages % 2 != 0) {
-        bool there = false;
-        for (uint32_t i = 0; i < wait.tries && !there; ++i) {
-          there = found[1 - kv] + (uint32_t)L::kStages > use;
-          if ((i & 255u) == 255u && *wait.abort) break;
-        }
-        if (!there) *wait.abort = 1;
-        if (!__all_sync(0xffffffffu, there)) return false;
-      }
+      if (kAlternate && !other_found(use + 1 - L::kStages)) return false;
       if (!wait.warp(kEmpty + to.stage, to.phase ^ 1u)) return false;
     }
-    if (L::kStages % 2 != 0 && lane == 0) found[kv] = use + 1;
+    if (!kAlternate && kv == 0 && use >= 2u * kMasks &&
+        !other_found(use + 2 + L::kStages - 2 * kMasks))
+      return false;
+    if ((kAlternate || kv == 1) && lane == 0) found[kv] = use + 1;
     return true;
   };
   // announces `bytes` and copies the boxes whose bits are set, box i from group `group` of lane i;
@@ -612,10 +628,8 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       unsigned char* dst = sm + L::kRing + to.stage * L::kTile;
       uint64_t* full = bars + kFull + to.stage;
       to.step(2);
-      // Which keys take part: key 4 i + x of the step is bit i of word x. An entry of the 8 is
-      // written again when the K tile 8 steps on has room: then a score tile at least 2 steps on
-      // was full, so every softmax warp that reads the entry was done with the steps before it.
-      uint32_t* seen = seen_words + (use / 2 % 8) * 4 + lane;
+      // Which keys take part: key 4 i + x of the step is bit i of word x.
+      uint32_t* seen = seen_words + (use / 2 % kMasks) * 4 + lane;
       if (clear) {   // every key is there: whole boxes, nothing masked
         if (kv == 0 && lane < 4) *seen = 0xffffffffu;
         issue(dst, full, row / 8, boxes, L::kTile, t.h);
@@ -867,7 +881,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld32_max(s_at + x * 32, v32[x], e[x]);
       }
-      const uint4 seen = *reinterpret_cast<const uint4*>(sm + L::kSeen + (k / 2 % 8) * 16);
+      const uint4 seen = *reinterpret_cast<const uint4*>(sm + L::kSeen + (k / 2 % kMasks) * 16);
       tc::tmem_wait_ld();
       const bool masked = (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu;
       if (masked || p.scale_log2 < 0.f) {   // the maximum is another one
