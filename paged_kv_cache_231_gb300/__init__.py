@@ -11,4 +11,5 @@ from .binding import (  # noqa: F401
     pkv_paged_attention_plan, pkv_paged_attention_workspace_size, pkv_paged_contract_check,
     pkv_paged_scatter_kv, pkv_paged_schedule, rotary_pair_axis,
     pkv_profiler_enable, pkv_profiler_query, pkv_profiler_reset,
-    pkv_sparse_attention_partials, pkv_sparse_attention_partials_workspace_size)
+    pkv_sparse_attention_partials, pkv_sparse_attention_partials_workspace_size,
+    release_workspaces)

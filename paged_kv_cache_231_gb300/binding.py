@@ -808,24 +808,36 @@ def _cross_workspace(device: int, *sizes) -> int:
     return pkv_cross_attention_workspace_size(a)
 
 
-_OWN = threading.local()
-_OWN_BYTES = 128 << 20
+_OWN = threading.local()   # (device, raw stream) -> workspace, the last used one last
+_OWN_STREAMS = 4
 
 
 def _own_workspace(need: int, like, stream, raw: int):
-    """A workspace for a call that brought none. Each thread keeps one for each stream it calls
-    on as the current one (an allocation costs a call 6 us): calls of one thread on one stream
-    run one after the other. A call that is captured gets memory of its graph's, one on another
-    stream than the current one or of a large workspace its own."""
+    """A workspace for a call that brought none. Each thread keeps one for each of the last
+    ``_OWN_STREAMS`` streams that it called on as the current one (an allocation costs a call
+    6 us): calls of one thread on one stream run one after the other. One takes up to 61 MB on
+    a GPU of 152 SMs, as much as its largest call needed, until the thread ends, has called on
+    as many other streams, or calls release_workspaces. A call that is captured gets memory of
+    its graph's, one on another stream than the current one its own."""
     torch = _torch()
-    if stream is not None or need > _OWN_BYTES or torch.cuda.is_current_stream_capturing():
+    if stream is not None or torch.cuda.is_current_stream_capturing():
         return _made(stream, need, torch.uint8, like.device, returned=False)
     kept = _OWN.__dict__
     key = (like.get_device(), raw)
-    own = kept.get(key)
+    own = kept.pop(key, None)
     if own is None or own.numel() < need:
-        own = kept[key] = torch.empty(need, dtype=torch.uint8, device=like.device)
+        own = None   # its memory may serve the new one
+        own = torch.empty(need, dtype=torch.uint8, device=like.device)
+    kept[key] = own
+    if len(kept) > _OWN_STREAMS:
+        del kept[next(iter(kept))]
     return own
+
+
+def release_workspaces():
+    """Gives back the workspaces that pkv_cross_attention keeps for the calling thread (memory
+    of torch's caching allocator; calls under way finish undisturbed)."""
+    _OWN.__dict__.clear()
 
 
 def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_length,
@@ -835,8 +847,9 @@ def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_lengt
     """Attention of ragged query rows over encoder states in a paged cache: row i of
     sequence b sees the key_seqlens[b] states of table row b. float16 or bfloat16. Returns
     the output [num_tokens, num_heads * head_size]; with ``lse`` (float32 [num_tokens,
-    num_heads]) the log-sum-exp of each row's scores is written there. Without ``workspace``
-    one is kept for the calling thread and stream (see _own_workspace)."""
+    num_heads]) the log-sum-exp of each row's scores is written there. Without a ``workspace``
+    (uint8, 256-byte aligned) of at least pkv_cross_attention_workspace_size bytes one of up to
+    61 MB is kept for the calling thread and stream (see _own_workspace, release_workspaces)."""
     torch = _torch()
     if (query is None or key_cache is None or value_cache is None or block_table is None or
             cumulative_sequence_length is None or key_seqlens is None):
