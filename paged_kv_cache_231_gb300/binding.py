@@ -645,8 +645,12 @@ def _check_tensors(stream, tensors) -> int:
     if device != torch.cuda.current_device() or (stream is not None and
                                                  stream.device_index != device):
         _refuse(stream, tensors)
-    # the current stream's handle without an object for it (a microsecond of the call)
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without an object for it (a microsecond of the call), where
+    # this torch has that
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _need(**named):
