@@ -559,7 +559,8 @@ int pkv_cross_attention_workspace_size(const pkv_cross_attention_args* args, siz
  * the n = key_seqlens[b] states of its table row:
  *   s_j = scale * <q, k_j>, lse = ln sum_j e^{s_j}, output = sum_j e^{s_j - lse} v_j,
  * summed in 32 bits; the weights e^{s_j - m} are rounded once to `dtype` for the product
- * with the values, their sum is not. A state whose block is unmapped takes no part and sets
+ * with the values (in fp16 by at most 2^-11 of each and 2^-32 of the row's largest), their sum
+ * is not. A state whose block is unmapped takes no part and sets
  * PKV_DEV_BAD_BLOCK (so does an n past max_blocks * block_size, which is cut there). A row
  * that sees no state gets output 0 and lse -inf. Cache rows behind a sequence's states may
  * hold anything (NaN too). Sequences whose cumulative lengths are inconsistent or exceed

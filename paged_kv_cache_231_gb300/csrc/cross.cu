@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
           s[n][e] *= p.scale_log2;
           if (!all && !((w >> (n * 8 + 2 * t4 + (e & 1))) & 1u)) s[n][e] = -INFINITY;
         }
-      // online softmax; a row's maximum is raised when a score exceeds it by kRaise
+      // online softmax; m is raised when a score exceeds the maximum that it stands for by kRaise
       float top[2];
       bool raise = false;
 #pragma unroll
@@ -365,14 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
         top[x] = fmaxf(s[0][2 * x], s[0][2 * x + 1]);
 #pragma unroll
         for (int n = 1; n < K / 8; ++n) top[x] = fmaxf(top[x], fmaxf(s[n][2 * x], s[n][2 * x + 1]));
-        raise = raise || (m[x] == -INFINITY ? top[x] != -INFINITY : top[x] > m[x] + kRaise);
+        raise =
+            raise || (m[x] == -INFINITY ? top[x] != -INFINITY : top[x] > m[x] + (kLift + kRaise));
       }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
           top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-          const float mn = fmaxf(m[x], top[x]);
+          const float mn = fmaxf(m[x], top[x] - kLift);
           const float alpha = ex2(m[x] - (mn == -INFINITY ? 0.f : mn));
           m[x] = mn;
           l[x] *= alpha;

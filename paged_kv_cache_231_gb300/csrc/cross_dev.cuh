@@ -27,7 +27,11 @@ namespace cross {
 __host__ __device__ constexpr int few_keys(int head_size) { return 2048 / head_size; }
 constexpr int kTileKeys = 128;     // keys of a step, many rows
 constexpr int kEntries = 1024;     // prefix entries of a plan
-constexpr float kRaise = 8.f;      // log2 of the largest weight under an old maximum
+// A weight is 2^(score - m), where m is the row's maximum less kLift, raised when the maximum
+// passes it by kLift + kRaise: the largest is 2^7 to 2^15. Rounded to fp16 for the product with the
+// values, weights of 2^-32 of the largest and less are lost, and others err by as much; without the
+// lift it was 2^-25, and 60 000 states of such weights 2e-3 of the whole.
+constexpr float kLift = 7.f, kRaise = 8.f;
 // pieces of a range (bounds the join): 400000 states of one kv head 76 us, with 128 pieces 228 us,
 // without a bound 77 us
 constexpr int kMaxPieces = 512;

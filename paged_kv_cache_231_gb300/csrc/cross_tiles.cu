@@ -902,11 +902,11 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
       }
       float top = max3(e[0], e[1], fmaxf(e[2], e[3]));
       top *= sl2;   // -inf when nothing of the step is seen
-      if (__any_sync(0xffffffffu, m == -INFINITY ? top != -INFINITY : top > m + kRaise)) {
+      if (__any_sync(0xffffffffu, m == -INFINITY ? top != -INFINITY : top > m + (kLift + kRaise))) {
         const bool first = m == -INFINITY;
-        const bool raise = first ? top != -INFINITY : top > m + kRaise;
-        const float alpha = raise && !first ? ex2(m - top) : 1.f;
-        if (raise) m = top;
+        const bool raise = first ? top != -INFINITY : top > m + (kLift + kRaise);
+        const float alpha = raise && !first ? ex2(m - (top - kLift)) : 1.f;
+        if (raise) m = top - kLift;
         l *= alpha;
         if (j > 0) {   // O is complete: see the order of the products
 #pragma unroll 1
