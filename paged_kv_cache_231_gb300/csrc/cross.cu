@@ -134,10 +134,11 @@ __device__ __forceinline__ bool holds_row(const CrossParams& p, int b, int i) {
 
 // Rows that no key is seen from, or that no sequence covers: output 0, lse -inf. Where the
 // cumulative lengths ascend, only the last sequence that begins at or in front of a row can hold
-// it. Where they do not (`ordered` false: some sequence is bad), a later or an earlier one can: a
-// row that the search does not find held is looked for in all of them.
+// it. Where they do not (some sequence is bad), a later or an earlier one can: a row that the search
+// does not find held is looked for in all of them.
+// ordered: 1 they ascend, 0 they do not, -1 not known; then a warp looks when it has such a row.
 template <typename T, int D>
-__device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, bool ordered) {
+__device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, int ordered) {
   for (int64_t i0 = (int64_t)unit * 32; i0 < p.T; i0 += (int64_t)units * 32) {
     const int i = (int)min(i0 + lane, (int64_t)p.T - 1);
     int lo = 0, hi = p.B - 1, b = -1;
@@ -152,10 +153,15 @@ __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, b
     }
     const bool empty = b < 0 || !holds_row(p, b, i);
     uint32_t todo = __ballot_sync(0xffffffffu, empty && i0 + lane < p.T);
+    if (todo && ordered < 0) {
+      bool descends = false;
+      for (int c = lane; c < p.B; c += 32) descends |= __ldg(p.cu + c + 1) < __ldg(p.cu + c);
+      ordered = __any_sync(0xffffffffu, descends) ? 0 : 1;
+    }
     for (; todo; todo &= todo - 1) {
       const int64_t row = i0 + __ffs(todo) - 1;
       bool held = false;
-      for (int b0 = 0; !ordered && !held && b0 < p.B; b0 += 32)
+      for (int b0 = 0; ordered == 0 && !held && b0 < p.B; b0 += 32)
         held = __any_sync(0xffffffffu, b0 + lane < p.B && holds_row(p, b0 + lane, (int)row));
       if (held) continue;
       uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.Hq * D);
@@ -268,11 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   if constexpr (kSmall) {
     const int work = p.B * p.Hkv;
     if ((int)blockIdx.x >= work) {
-      bool descends = false;
-      for (int b = threadIdx.x; b < p.B; b += kThreads)
-        descends |= __ldg(p.cu + b + 1) < __ldg(p.cu + b);
-      const bool ordered = !__syncthreads_or(descends);
-      zero_rows<T, D>(p, gw - work * kWarps, ((int)gridDim.x - work) * kWarps, lane, ordered);
+      zero_rows<T, D>(p, gw - work * kWarps, ((int)gridDim.x - work) * kWarps, lane, -1);
       return;
     }
     bool zero;
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
       j.template write<T>(p, (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G, lane);
     }
   } else if (pl.zero) {
-    zero_rows<T, D>(p, gw, p.few_units, lane, pl.ordered);
+    zero_rows<T, D>(p, gw, p.few_units, lane, pl.ordered ? 1 : 0);
   }
   if (flags) flag_status(p.status, flags);
   // the join behind this kernel waits for it alone: it must not end before the one in front
