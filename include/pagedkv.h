@@ -455,7 +455,8 @@ typedef struct pkv_schedule_args {
  *   - rows are granted in order while the blocks asked for up to and including the row fit
  *     the free ones; a row behind that is granted only if it needs no block
  *     (PKV_DEV_NO_BLOCKS when one is not);
- *   - and while the granted tokens fit num_tokens (PKV_DEV_BAD_SEQUENCE);
+ *   - and while the tokens of the rows up to it that the pool takes fit num_tokens: from the first
+ *     one that does not on, no row that brings tokens is granted any (PKV_DEV_BAD_SEQUENCE);
  *   - a negative length (PKV_DEV_BAD_SEQUENCE), a past + new beyond max_blocks *
  *     block_size (PKV_DEV_BAD_BLOCK) are granted nothing; a negative past holds nothing.
  * A row that is granted nothing keeps its table row; total_seqlens gives its past back.
@@ -519,7 +520,10 @@ typedef struct pkv_append_axes_args {
  * that some pair uses (PKV_DEV_BAD_POSITION): K and V are not written, the query row is
  * copied unrotated. Two tokens of one slot leave there, in each 16 bytes, the one's or the
  * other's. query_out and the caches must not overlap the inputs or one another. head_size a
- * multiple of 8, <= 256; otherwise PKV_ERR_UNSUPPORTED. */
+ * multiple of 8, <= 256; otherwise PKV_ERR_UNSUPPORTED.
+ * pkv_paged_attention reads fp16 pools alone. A bf16 pool is read by pkv_cross_attention, which has
+ * no causal mask: single tokens over their past + 1 states and encoder states, not the tokens of a
+ * prompt over one another. */
 int pkv_paged_append_rotary_axes(const pkv_append_axes_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------------
