@@ -15,10 +15,11 @@
 // itself (cheaper than passing the sums around), writes the new table entries of its groups
 // and, after a cluster barrier, the slots of its share of the tokens.
 // Very many tokens' slots are left to a second kernel on all SMs.
-// What bounds it is latency: some five dependent rounds of loads and three cluster barriers.
-// 2 rows take 6.0 us, 64 rows of up to 8192 tokens 10.6 us, 16 rows of which half take in up to
-// 2048 tokens 13.8 us; with 2048 rows, 433 000 held entries and 325 000 new tokens (27 us) the
-// marking takes a third.
+// What bounds it is latency, phase behind phase: 2 rows take 6.0 us (9700 cycles of scans and
+// barriers), 64 rows of up to 8192 tokens 10.7 us (19 100: marking 4000, new entries and the barrier
+// behind them 6000), 16 rows of which half take in up to 2048 tokens 13.9 us (24 900: new entries
+// 13 800, as a lane writes those of its 32 ids one after the other); with 2048 rows, 433 000 held
+// entries and 325 000 new tokens (27.2 us) the marking takes 18 400 of 42 900 cycles.
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
