@@ -25,6 +25,14 @@
  *                              with one position per axis (time, height, width, ...).
  *   pkv_cross_attention        attention of ragged queries over an encoder's states in a
  *                              paged cache (no causal mask, another length).
+ *   pkv_paged_append_norm_rotary
+ *                              the append above with a norm of every query and key head in
+ *                              front of the rotation.
+ *   pkv_paged_window_attention causal attention over the paged cache, fp16 or bf16, with a
+ *                              sliding window and first tokens that stay visible.
+ *   pkv_paged_prefix_attention causal attention of requests whose first blocks are the same:
+ *                              what they share is computed once for all of them.
+ *   pkv_paged_fork             rows of the block table copied, reordered and freed.
  *
  * Conventions for every call:
  *   - Tensor pointers are DEVICE pointers owned by the caller; the library never frees
@@ -581,6 +589,172 @@ int pkv_cross_attention(const pkv_cross_attention_args* args, void* workspace,
                         size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * Paged append with norms of the heads and rotary positions
+ * ------------------------------------------------------------------------------- */
+typedef struct pkv_append_norm_args {
+  pkv_append_axes_args append;   /* as in pkv_paged_append_rotary_axes */
+  const void* query_weight;      /* [head_size], `weight_dtype`; NULL: the heads of the
+                                    queries are not normed */
+  const void* key_weight;        /* the same for the keys */
+  float epsilon;                 /* > 0 */
+  int32_t weight_dtype;          /* append.dtype or PKV_F32 */
+} pkv_append_norm_args;
+
+/* pkv_paged_append_rotary_axes with a norm in front of the rotation: every head x of a key
+ * (and, with query_out, of a query) becomes
+ *   x_i * query_weight[i] / sqrt(sum_j x_j^2 / head_size + epsilon)
+ * (key_weight for keys), which turns as there; in 32-bit arithmetic, rounded once behind the
+ * rotation. Squares are summed in 32 bits: a bf16 head whose squares sum past 3.4e38 becomes
+ * 0. What that call says of slots, positions, padding and overlaps holds here too; a query
+ * whose position has no table row is normed and not rotated. At least one weight is given.
+ * Same refusals and limits. */
+int pkv_paged_append_norm_rotary(const pkv_append_norm_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Causal paged attention with a sliding window, or behind a shared prefix
+ * ------------------------------------------------------------------------------- */
+typedef struct pkv_window_attention_args {
+  const void* query;             /* [num_tokens, num_heads * head_size], `dtype` */
+  const void* key_cache;         /* [num_blocks, block_size, kv_num_heads, head_size] */
+  const void* value_cache;
+  const int32_t* cumulative_sequence_length;  /* [batch + 1] query rows of each sequence */
+  const int32_t* past_seqlens;   /* [batch] tokens in front of the sequence's first row */
+  const int32_t* block_table;    /* [batch, max_blocks], -1 (or any id outside the pool) =
+                                    unmapped */
+  void* output;                  /* [num_tokens, num_heads * head_size], `dtype` */
+  float* lse;                    /* optional [num_tokens, num_heads] */
+  int32_t* device_status;        /* optional */
+  int64_t num_tokens;
+  int64_t batch;
+  int64_t num_heads;
+  int64_t kv_num_heads;
+  int64_t head_size;
+  int64_t block_size;
+  int64_t num_blocks;
+  int64_t max_blocks;
+  int64_t max_query_len;         /* as in pkv_cross_attention */
+  int64_t window;                /* keys that a row sees, its own included; 0: all */
+  int64_t sinks;                 /* first keys of a sequence that stay visible (no effect
+                                    without a window) */
+  int32_t dtype;                 /* PKV_F16 or PKV_BF16 */
+  float scale;                   /* softmax scale; 0 means 1/sqrt(head_size) */
+} pkv_window_attention_args;
+
+/* Host only: workspace bytes pkv_paged_window_attention needs on the current device (may be 0). */
+int pkv_paged_window_attention_workspace_size(const pkv_window_attention_args* args,
+                                              size_t* bytes);
+
+/* Causal attention over the paged cache; the new tokens' keys and values are in it already (an
+ * append call put them there). Query row i of sequence b stands at t = past_seqlens[b] + i and
+ * sees key j <= t when window is 0, when j > t - window, or when j < sinks:
+ *   s_j = scale * <q, k_j>, lse = ln sum_j e^{s_j}, output = sum_j e^{s_j - lse} v_j
+ * in the arithmetic of pkv_cross_attention. A key whose block is unmapped takes no part, and
+ * sets PKV_DEV_BAD_BLOCK if a row sees it (so do keys from max_blocks * block_size on); blocks that
+ * no row sees any more may be given back. Cache rows that no row of the sequence sees may hold
+ * anything (NaN too); a key or value that is not finite can reach all rows of its sequence.
+ * A row that sees no mapped key gets output 0 and lse -inf. Sequences whose cumulative lengths
+ * are inconsistent or exceed max_query_len, or whose past_seqlens entry is negative, get zero
+ * rows (lse -inf) and set PKV_DEV_BAD_SEQUENCE; so do rows that no sequence covers, without
+ * the flag. Equal calls give equal bits; output, lse, workspace, PKV_DEV_TIMEOUT and the sizes
+ * supported: as in pkv_cross_attention. */
+int pkv_paged_window_attention(const pkv_window_attention_args* args, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+typedef struct pkv_prefix_attention_args {
+  const void* query;             /* as in pkv_window_attention_args, down to device_status */
+  const void* key_cache;
+  const void* value_cache;
+  const int32_t* cumulative_sequence_length;
+  const int32_t* past_seqlens;
+  const int32_t* block_table;
+  const int32_t* group_offsets;  /* [num_groups + 1] group g: sequences group_offsets[g] ..
+                                    group_offsets[g + 1] - 1; ascending, within 0 .. batch */
+  const int32_t* shared_seqlens; /* [num_groups] first keys that all of a group's sequences
+                                    have in common: the same blocks in their table rows */
+  void* output;
+  float* lse;
+  int32_t* device_status;
+  int64_t num_tokens;
+  int64_t batch;
+  int64_t num_groups;
+  int64_t num_heads;
+  int64_t kv_num_heads;
+  int64_t head_size;
+  int64_t block_size;
+  int64_t num_blocks;
+  int64_t max_blocks;
+  int64_t max_query_len;
+  int32_t dtype;
+  float scale;
+} pkv_prefix_attention_args;
+
+/* Host only: workspace bytes pkv_paged_prefix_attention needs on the current device. It holds
+ * one output in 32 bits (num_tokens * num_heads * (head_size + 1) * 4 bytes) and what the
+ * kernels need. */
+int pkv_paged_prefix_attention_workspace_size(const pkv_prefix_attention_args* args,
+                                              size_t* bytes);
+
+/* What pkv_paged_window_attention computes without a window, for sequences of which some begin
+ * alike: the keys that a group shares are read through the table row of its first sequence with
+ * new tokens, once for the rows of all of them, and joined in 32 bits with what each row sees
+ * behind them. A group shares shared_seqlens[g] keys, or fewer where one of its sequences with new tokens has a
+ * shorter past. Sequences outside all groups and groups with fewer than two sequences that have
+ * new tokens share nothing, nor does a group of which one sequence is bad. A negative shared_seqlens
+ * entry is taken as 0 and sets PKV_DEV_BAD_SEQUENCE; group offsets that descend or leave 0 ..
+ * batch set it too, and then nothing is shared at all. Sequences of a group whose table entries
+ * differ where they are said to be shared are attended with those of its first. A shared block
+ * that is unmapped sets PKV_DEV_BAD_BLOCK. */
+int pkv_paged_prefix_attention(const pkv_prefix_attention_args* args, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Fork: rows of the block table copied, reordered and freed
+ * ------------------------------------------------------------------------------- */
+#define PKV_MAX_FORK_CACHES 256
+
+typedef struct pkv_fork_args {
+  const int32_t* parents;        /* [batch] row that each row becomes a copy of: itself (it
+                                    stays), another one, or negative (it is freed) */
+  const int32_t* past_seqlens;   /* [batch] tokens of each row */
+  const int32_t* block_table;    /* [batch, max_blocks] */
+  int32_t* new_past_seqlens;     /* [batch] */
+  int32_t* new_block_table;      /* [batch, max_blocks], written whole */
+  int32_t* free_blocks;          /* optional [1] blocks of the pool that no row holds now */
+  void* const* caches;           /* HOST array of num_caches device pointers: pools of
+                                    num_blocks * block_size rows (keys and values of every
+                                    layer, any type) */
+  const int64_t* cache_row_bytes;  /* HOST array: bytes of a token's row in each */
+  int32_t* device_status;        /* optional */
+  int64_t batch;
+  int64_t max_blocks;
+  int64_t num_blocks;
+  int64_t block_size;
+  int64_t num_caches;            /* 0: tables only */
+} pkv_fork_args;
+
+/* Host only: workspace bytes pkv_paged_fork needs. */
+int pkv_paged_fork_workspace_size(const pkv_fork_args* args, size_t* bytes);
+
+/* New row b takes over the n = past_seqlens[p] tokens of old row p = parents[b]: its first
+ * n / block_size entries are p's (whole blocks are shared), and where n ends inside a block
+ * one of p's copies (row p itself if it stays, else the first) keeps that block, the others
+ * get one of their own, whose first n % block_size rows are copied from it in every cache.
+ * Entries behind are -1. A block of the pool that no new row holds is free, so what freed and
+ * replaced rows alone held is given back; the r-th row that needs a block gets the r-th free
+ * one by number. A row for which there is none is freed (PKV_DEV_NO_BLOCKS), as is one whose
+ * parent is no row, or has a negative length (PKV_DEV_BAD_SEQUENCE) or one beyond max_blocks *
+ * block_size (PKV_DEV_BAD_BLOCK). A freed row has length 0 and entries of -1. An entry outside
+ * the pool is copied as it is (any but -1 sets PKV_DEV_BAD_BLOCK); where it stands for the
+ * block that would be copied, nothing is. Rows that shared a partly filled block before go on
+ * sharing it. Rows of the caches other than those copied to are not written; the result
+ * depends on the inputs alone. The outputs must not overlap the inputs. The host arrays are read during
+ * the call. Supported: cache_row_bytes and cache pointers multiples of 16, num_caches <=
+ * PKV_MAX_FORK_CACHES, the sizes of pkv_paged_schedule and rows of a cache below 2^31 / block_size
+ * bytes; otherwise PKV_ERR_UNSUPPORTED (pointers: PKV_ERR_ALIGN). */
+int pkv_paged_fork(const pkv_fork_args* args, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* ---------------------------------------------------------------------------------
  * Runtime utilities
  * ------------------------------------------------------------------------------- */
 int pkv_abi_version(void);
@@ -593,7 +767,9 @@ int64_t pkv_launch_count(void);
  * stream; pkv_profiler_query synchronises those events and returns the summed device
  * time (ms) and launch count of `kernel` ("scatter", "append", "plan", "decode",
  * "prefill", "combine", "sparse_group", "sparse_partials", "schedule", "append_axes",
- * "cross_decode", "cross_tiles", "cross_combine"). Not thread-safe. */
+ * "cross_decode", "cross_tiles", "cross_combine", "append_norm", "window_decode",
+ * "window_tiles", "window_combine", "prefix_plan", "prefix_decode", "prefix_tiles",
+ * "prefix_combine", "fork_plan", "fork_copy"). Not thread-safe. */
 void pkv_profiler_enable(int on);
 
 /* Testing hook for the give-up path of the tensor-core kernels' bounded waits (the

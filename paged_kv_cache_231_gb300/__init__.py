@@ -12,4 +12,7 @@ from .binding import (  # noqa: F401
     pkv_paged_scatter_kv, pkv_paged_schedule, rotary_pair_axis,
     pkv_profiler_enable, pkv_profiler_query, pkv_profiler_reset,
     pkv_sparse_attention_partials, pkv_sparse_attention_partials_workspace_size,
+    make_prefix_args, make_window_args, pkv_paged_append_norm_rotary, pkv_paged_fork,
+    pkv_paged_prefix_attention, pkv_paged_prefix_attention_workspace_size,
+    pkv_paged_window_attention, pkv_paged_window_attention_workspace_size,
     release_workspaces)

@@ -136,12 +136,50 @@ class CrossAttentionArgs(ctypes.Structure):
                 ("max_query_len", c_i64), ("dtype", c_i32), ("scale", c_f32)]
 
 
+class AppendNormArgs(ctypes.Structure):
+    _fields_ = [("append", AppendAxesArgs), ("query_weight", c_vp), ("key_weight", c_vp),
+                ("epsilon", c_f32), ("weight_dtype", c_i32)]
+
+
+class WindowAttentionArgs(ctypes.Structure):
+    _fields_ = [("query", c_vp), ("key_cache", c_vp), ("value_cache", c_vp),
+                ("cumulative_sequence_length", c_vp), ("past_seqlens", c_vp),
+                ("block_table", c_vp), ("output", c_vp), ("lse", c_vp),
+                ("device_status", c_vp), ("num_tokens", c_i64), ("batch", c_i64),
+                ("num_heads", c_i64), ("kv_num_heads", c_i64), ("head_size", c_i64),
+                ("block_size", c_i64), ("num_blocks", c_i64), ("max_blocks", c_i64),
+                ("max_query_len", c_i64), ("window", c_i64), ("sinks", c_i64),
+                ("dtype", c_i32), ("scale", c_f32)]
+
+
+class PrefixAttentionArgs(ctypes.Structure):
+    _fields_ = [("query", c_vp), ("key_cache", c_vp), ("value_cache", c_vp),
+                ("cumulative_sequence_length", c_vp), ("past_seqlens", c_vp),
+                ("block_table", c_vp), ("group_offsets", c_vp), ("shared_seqlens", c_vp),
+                ("output", c_vp), ("lse", c_vp), ("device_status", c_vp),
+                ("num_tokens", c_i64), ("batch", c_i64), ("num_groups", c_i64),
+                ("num_heads", c_i64), ("kv_num_heads", c_i64), ("head_size", c_i64),
+                ("block_size", c_i64), ("num_blocks", c_i64), ("max_blocks", c_i64),
+                ("max_query_len", c_i64), ("dtype", c_i32), ("scale", c_f32)]
+
+
+class ForkArgs(ctypes.Structure):
+    _fields_ = [("parents", c_vp), ("past_seqlens", c_vp), ("block_table", c_vp),
+                ("new_past_seqlens", c_vp), ("new_block_table", c_vp), ("free_blocks", c_vp),
+                ("caches", c_vp), ("cache_row_bytes", c_vp), ("device_status", c_vp),
+                ("batch", c_i64), ("max_blocks", c_i64), ("num_blocks", c_i64),
+                ("block_size", c_i64), ("num_caches", c_i64)]
+
+
 STRUCTS = {"pkv_paged_attention_args": PagedAttentionArgs, "pkv_paged_plan": PagedPlan,
            "pkv_tensor_desc": TensorDesc, "pkv_paged_shapes": PagedShapes,
            "pkv_kv_append_args": KVAppendArgs, "pkv_sparse_args": SparseArgs,
            "pkv_combine_args": CombineArgs, "pkv_schedule_args": ScheduleArgs,
            "pkv_append_axes_args": AppendAxesArgs,
-           "pkv_cross_attention_args": CrossAttentionArgs}
+           "pkv_cross_attention_args": CrossAttentionArgs,
+           "pkv_append_norm_args": AppendNormArgs,
+           "pkv_window_attention_args": WindowAttentionArgs,
+           "pkv_prefix_attention_args": PrefixAttentionArgs, "pkv_fork_args": ForkArgs}
 
 _LIB = None
 
@@ -188,6 +226,18 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                                     ctypes.POINTER(ctypes.c_size_t)]),
             ("pkv_cross_attention", [ctypes.POINTER(CrossAttentionArgs), c_vp,
                                      ctypes.c_size_t, c_vp]),
+            ("pkv_paged_append_norm_rotary", [ctypes.POINTER(AppendNormArgs), c_vp]),
+            ("pkv_paged_window_attention_workspace_size",
+             [ctypes.POINTER(WindowAttentionArgs), ctypes.POINTER(ctypes.c_size_t)]),
+            ("pkv_paged_window_attention", [ctypes.POINTER(WindowAttentionArgs), c_vp,
+                                            ctypes.c_size_t, c_vp]),
+            ("pkv_paged_prefix_attention_workspace_size",
+             [ctypes.POINTER(PrefixAttentionArgs), ctypes.POINTER(ctypes.c_size_t)]),
+            ("pkv_paged_prefix_attention", [ctypes.POINTER(PrefixAttentionArgs), c_vp,
+                                            ctypes.c_size_t, c_vp]),
+            ("pkv_paged_fork_workspace_size", [ctypes.POINTER(ForkArgs),
+                                               ctypes.POINTER(ctypes.c_size_t)]),
+            ("pkv_paged_fork", [ctypes.POINTER(ForkArgs), c_vp, ctypes.c_size_t, c_vp]),
             ("pkv_testing_wait_limit", [ctypes.c_uint32, c_i32])):
         fn = getattr(lib, name)
         fn.restype = c_i32
@@ -584,6 +634,10 @@ def pkv_combine_partials(o, m, l, segment_offsets=None, *, num_segments: int, la
 _SCHEDULE_PACK = struct.Struct("@9Q5q")
 _AXES_PACK = struct.Struct("@11Q8q4i128s")
 _CROSS_PACK = struct.Struct("@9Q9qif")
+_NORM_PACK = struct.Struct("@11Q8q4i128s2Qfi")
+_WINDOW_PACK = struct.Struct("@9Q11qif")
+_PREFIX_PACK = struct.Struct("@11Q10qif")
+_FORK_PACK = struct.Struct("@9Q5q")
 _STEP = {}   # entry points that take packed blocks
 
 
@@ -592,10 +646,15 @@ def _step_call(name: str, *args):
     if fn is None:
         lib = load_library()
         for pack, cls in ((_SCHEDULE_PACK, ScheduleArgs), (_AXES_PACK, AppendAxesArgs),
-                          (_CROSS_PACK, CrossAttentionArgs)):
+                          (_CROSS_PACK, CrossAttentionArgs), (_NORM_PACK, AppendNormArgs),
+                          (_WINDOW_PACK, WindowAttentionArgs),
+                          (_PREFIX_PACK, PrefixAttentionArgs), (_FORK_PACK, ForkArgs)):
             assert pack.size == ctypes.sizeof(cls)
+        worked = [c_vp, ctypes.c_size_t, c_vp]   # workspace, its bytes, stream
         for n, more in (("pkv_paged_schedule", [c_vp]), ("pkv_paged_append_rotary_axes", [c_vp]),
-                        ("pkv_cross_attention", [c_vp, ctypes.c_size_t, c_vp])):
+                        ("pkv_paged_append_norm_rotary", [c_vp]),
+                        ("pkv_cross_attention", worked), ("pkv_paged_window_attention", worked),
+                        ("pkv_paged_prefix_attention", worked), ("pkv_paged_fork", worked)):
             f = lib[n]   # a function object of its own
             f.restype, f.argtypes = c_i32, [ctypes.c_char_p] + more
             _STEP[n] = f
@@ -721,18 +780,11 @@ def rotary_pair_axis(sections, by_turns: bool = False):
     return axis
 
 
-def pkv_paged_append_rotary_axes(query, key, value, key_cache, value_cache, slot_mapping,
-                                 positions, *, num_heads: int, kv_num_heads: int,
-                                 cos_cache=None, sin_cache=None, rotary_dim: int = 0,
-                                 pair_axis=None, rotary_interleaved: bool = False,
-                                 query_out=None, rotate_query: bool = True,
-                                 device_status=None, stream=None):
-    """K and V rows into the paged cache (pool row slot_mapping[i], negative = padding), K
-    and Q rotated with ``positions`` [axes, num_tokens]; ``pair_axis`` names the axis of each
-    rotary pair (all axis 0 when None). float16 or bfloat16; the tables in that type or
-    float32. Packed rows when key and value are None. Returns the rotated queries
-    [num_tokens, num_heads * head_size] (made here unless ``query_out`` is given; rows of
-    padding are not written), or None without them (``rotate_query`` false, or no query)."""
+def _append_fields(query, key, value, key_cache, value_cache, slot_mapping, positions,
+                   num_heads, kv_num_heads, cos_cache, sin_cache, rotary_dim, pair_axis,
+                   rotary_interleaved, query_out, rotate_query, device_status, stream,
+                   weights=()):
+    """The fields of an append with rotary axes, the raw stream and the query output."""
     torch = _torch()
     if key_cache is None or value_cache is None or slot_mapping is None:
         _need(key_cache=key_cache, value_cache=value_cache, slot_mapping=slot_mapping)
@@ -769,17 +821,64 @@ def pkv_paged_append_rotary_axes(query, key, value, key_cache, value_cache, slot
         ("query_out", query_out, dt, (T, qh)), ("key_cache", key_cache, dt, pool),
         ("value_cache", value_cache, dt, pool), ("slot_mapping", slot_mapping, i32, (T,)),
         ("positions", positions, i32, (axes, T)), ("cos_cache", cos_cache, tdt, (rows, half)),
-        ("sin_cache", sin_cache, tdt, (rows, half)), ("device_status", device_status, i32, (1,))))
+        ("sin_cache", sin_cache, tdt, (rows, half)), ("device_status", device_status, i32, (1,)),
+        *weights))
     if rotate_query and query is not None and query_out is None:
         query_out = _made(stream, (T, qh), dt, key_cache.device)
-    _step_call("pkv_paged_append_rotary_axes",
-               _AXES_PACK.pack(_at(query), _at(key), _at(value), _at(query_out),
-                               key_cache.data_ptr(), value_cache.data_ptr(),
-                               slot_mapping.data_ptr(), _at(positions), _at(cos_cache),
-                               _at(sin_cache), _at(device_status), T, num_heads, kv_num_heads,
-                               D, BS, NB, rotary_dim, rows, axes,
-                               1 if rotary_interleaved else 0, code,
-                               PKV_F32 if tdt is f32 else code, pairs), raw)
+    return (_at(query), _at(key), _at(value), _at(query_out), key_cache.data_ptr(),
+            value_cache.data_ptr(), slot_mapping.data_ptr(), _at(positions), _at(cos_cache),
+            _at(sin_cache), _at(device_status), T, num_heads, kv_num_heads, D, BS, NB,
+            rotary_dim, rows, axes, 1 if rotary_interleaved else 0, code,
+            PKV_F32 if tdt is f32 else code, pairs), raw, query_out
+
+
+def pkv_paged_append_rotary_axes(query, key, value, key_cache, value_cache, slot_mapping,
+                                 positions, *, num_heads: int, kv_num_heads: int,
+                                 cos_cache=None, sin_cache=None, rotary_dim: int = 0,
+                                 pair_axis=None, rotary_interleaved: bool = False,
+                                 query_out=None, rotate_query: bool = True,
+                                 device_status=None, stream=None):
+    """K and V rows into the paged cache (pool row slot_mapping[i], negative = padding), K
+    and Q rotated with ``positions`` [axes, num_tokens]; ``pair_axis`` names the axis of each
+    rotary pair (all axis 0 when None). float16 or bfloat16; the tables in that type or
+    float32. Packed rows when key and value are None. Returns the rotated queries
+    [num_tokens, num_heads * head_size] (made here unless ``query_out`` is given; rows of
+    padding are not written), or None without them (``rotate_query`` false, or no query)."""
+    fields, raw, query_out = _append_fields(
+        query, key, value, key_cache, value_cache, slot_mapping, positions, num_heads,
+        kv_num_heads, cos_cache, sin_cache, rotary_dim, pair_axis, rotary_interleaved, query_out,
+        rotate_query, device_status, stream)
+    _step_call("pkv_paged_append_rotary_axes", _AXES_PACK.pack(*fields), raw)
+    return query_out
+
+
+def pkv_paged_append_norm_rotary(query, key, value, key_cache, value_cache, slot_mapping,
+                                 positions, *, num_heads: int, kv_num_heads: int,
+                                 query_weight=None, key_weight=None, epsilon: float = 1e-6,
+                                 cos_cache=None, sin_cache=None, rotary_dim: int = 0,
+                                 pair_axis=None, rotary_interleaved: bool = False,
+                                 query_out=None, rotate_query: bool = True,
+                                 device_status=None, stream=None):
+    """pkv_paged_append_rotary_axes with a norm of every head in front of the rotation:
+    x * weight / sqrt(mean(x^2) + epsilon), weights [head_size] in the caches' type or (both)
+    float32; a weight of None leaves the queries' or the keys' heads as they are. Returns the
+    normed and rotated queries, as there."""
+    torch = _torch()
+    if query_weight is None and key_weight is None:
+        raise ValueError("query_weight, key_weight: one at least is required")
+    if key_cache is None or value_cache is None or slot_mapping is None:
+        _need(key_cache=key_cache, value_cache=value_cache, slot_mapping=slot_mapping)
+    w = query_weight if query_weight is not None else key_weight
+    wdt = torch.float32 if w.dtype is torch.float32 else key_cache.dtype
+    size = (key_cache.shape[3] if key_cache.dim() == 4 else -1,)
+    fields, raw, query_out = _append_fields(
+        query, key, value, key_cache, value_cache, slot_mapping, positions, num_heads,
+        kv_num_heads, cos_cache, sin_cache, rotary_dim, pair_axis, rotary_interleaved, query_out,
+        rotate_query, device_status, stream,
+        (("query_weight", query_weight, wdt, size), ("key_weight", key_weight, wdt, size)))
+    _step_call("pkv_paged_append_norm_rotary",
+               _NORM_PACK.pack(*fields, _at(query_weight), _at(key_weight), epsilon,
+                               PKV_F32 if wdt is torch.float32 else fields[21]), raw)
     return query_out
 
 
@@ -896,6 +995,237 @@ def pkv_cross_attention(query, key_cache, value_cache, cumulative_sequence_lengt
                                 _at(device_status), *sizes, scale),
                _at(workspace), need, raw)
     return output
+
+
+def make_window_args(query, key_cache, value_cache, cumulative_sequence_length, past_seqlens,
+                     block_table, output, lse=None, *, num_heads: int, kv_num_heads: int,
+                     window: int = 0, sinks: int = 0, max_query_len: int = 0,
+                     scale: float = 0.0, device_status=None) -> WindowAttentionArgs:
+    """Fill the C argument block of pkv_paged_window_attention from tensors."""
+    return WindowAttentionArgs(
+        query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+        cumulative_sequence_length.data_ptr(), past_seqlens.data_ptr(), block_table.data_ptr(),
+        output.data_ptr(), _ptr(lse), _ptr(device_status), query.shape[0],
+        past_seqlens.shape[0], num_heads, kv_num_heads, key_cache.shape[3],
+        key_cache.shape[1], key_cache.shape[0], block_table.shape[1], max_query_len, window,
+        sinks, _dtype_code(query), scale)
+
+
+def pkv_paged_window_attention_workspace_size(args: WindowAttentionArgs) -> int:
+    n = ctypes.c_size_t(0)
+    _check("pkv_paged_window_attention_workspace_size",
+           load_library().pkv_paged_window_attention_workspace_size(ctypes.byref(args),
+                                                                    ctypes.byref(n)))
+    return n.value
+
+
+def make_prefix_args(query, key_cache, value_cache, cumulative_sequence_length, past_seqlens,
+                     block_table, group_offsets, shared_seqlens, output, lse=None, *,
+                     num_heads: int, kv_num_heads: int, max_query_len: int = 0,
+                     scale: float = 0.0, device_status=None) -> PrefixAttentionArgs:
+    """Fill the C argument block of pkv_paged_prefix_attention from tensors."""
+    return PrefixAttentionArgs(
+        query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+        cumulative_sequence_length.data_ptr(), past_seqlens.data_ptr(), block_table.data_ptr(),
+        group_offsets.data_ptr(), shared_seqlens.data_ptr(), output.data_ptr(), _ptr(lse),
+        _ptr(device_status), query.shape[0], past_seqlens.shape[0], shared_seqlens.shape[0],
+        num_heads, kv_num_heads, key_cache.shape[3], key_cache.shape[1], key_cache.shape[0],
+        block_table.shape[1], max_query_len, _dtype_code(query), scale)
+
+
+def pkv_paged_prefix_attention_workspace_size(args: PrefixAttentionArgs) -> int:
+    n = ctypes.c_size_t(0)
+    _check("pkv_paged_prefix_attention_workspace_size",
+           load_library().pkv_paged_prefix_attention_workspace_size(ctypes.byref(args),
+                                                                    ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _window_workspace(device: int, *sizes) -> int:
+    """Workspace bytes for these sizes (the fields from num_tokens on) on this device."""
+    return pkv_paged_window_attention_workspace_size(
+        WindowAttentionArgs(*([256] * 8), None, *sizes, 0.0))
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_workspace(device: int, *sizes) -> int:
+    return pkv_paged_prefix_attention_workspace_size(
+        PrefixAttentionArgs(*([256] * 10), None, *sizes, 0.0))
+
+
+def _causal_tensors(query, key_cache, value_cache, cumulative_sequence_length, past_seqlens,
+                    block_table, num_heads, kv_num_heads, output, lse, workspace, device_status,
+                    stream, more=()):
+    """What the causal calls check of their tensors alike. Returns the raw stream, the type's code,
+    and T, B, D, BS, NB, MB."""
+    torch = _torch()
+    if (query is None or key_cache is None or value_cache is None or block_table is None or
+            cumulative_sequence_length is None or past_seqlens is None):
+        _need(query=query, key_cache=key_cache, value_cache=value_cache,
+              cumulative_sequence_length=cumulative_sequence_length, past_seqlens=past_seqlens,
+              block_table=block_table)
+    dt, i32 = query.dtype, torch.int32
+    if dt is torch.float16:
+        code = PKV_F16
+    elif dt is torch.bfloat16:
+        code = PKV_BF16
+    else:
+        raise TypeError(f"query: expected float16 or bfloat16, got {dt}")
+    if key_cache.dim() != 4:
+        raise ValueError("key_cache: [num_blocks, block_size, kv_num_heads, head_size]")
+    NB, BS, _, D = key_cache.shape
+    T = query.shape[0] if query.dim() == 2 else -1
+    B = past_seqlens.shape[0] if past_seqlens.dim() == 1 else -1
+    MB = block_table.shape[1] if block_table.dim() == 2 else -1
+    hidden, pool = (T, num_heads * D), (NB, BS, kv_num_heads, D)
+    raw = _check_tensors(stream, (
+        ("query", query, dt, hidden), ("output", output, dt, hidden),
+        ("key_cache", key_cache, dt, pool), ("value_cache", value_cache, dt, pool),
+        ("past_seqlens", past_seqlens, i32, (B,)),
+        ("cumulative_sequence_length", cumulative_sequence_length, i32, (B + 1,)),
+        ("block_table", block_table, i32, (B, MB)),
+        ("lse", lse, torch.float32, (T, num_heads)),
+        ("workspace", workspace, torch.uint8, None if workspace is None else workspace.shape),
+        ("device_status", device_status, i32, (1,)), *more))
+    return raw, code, T, B, D, BS, NB, MB
+
+
+def pkv_paged_window_attention(query, key_cache, value_cache, cumulative_sequence_length,
+                               past_seqlens, block_table, *, num_heads: int, kv_num_heads: int,
+                               window: int = 0, sinks: int = 0, max_query_len: int = 0,
+                               scale: float = 0.0, output=None, lse=None, workspace=None,
+                               device_status=None, stream=None):
+    """Causal attention of ragged query rows over the paged cache that already holds their
+    keys: row i of sequence b stands at t = past_seqlens[b] + i and sees keys j <= t with
+    j > t - window or j < sinks (all of them with a window of 0). float16 or bfloat16. Returns
+    the output [num_tokens, num_heads * head_size]; ``lse`` and ``workspace`` as in
+    pkv_cross_attention."""
+    raw, code, T, B, D, BS, NB, MB = _causal_tensors(
+        query, key_cache, value_cache, cumulative_sequence_length, past_seqlens, block_table,
+        num_heads, kv_num_heads, output, lse, workspace, device_status, stream)
+    if output is None:
+        output = _made(stream, query.shape, query.dtype, query.device)
+    sizes = (T, B, num_heads, kv_num_heads, D, BS, NB, MB, max_query_len, window, sinks, code)
+    need = _window_workspace(query.get_device(), *sizes)
+    if need and (workspace is None or workspace.numel() < need):
+        workspace = _own_workspace(need, query, stream, raw)
+    _step_call("pkv_paged_window_attention",
+               _WINDOW_PACK.pack(query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                 cumulative_sequence_length.data_ptr(), past_seqlens.data_ptr(),
+                                 block_table.data_ptr(), output.data_ptr(), _at(lse),
+                                 _at(device_status), *sizes, scale),
+               _at(workspace), need, raw)
+    return output
+
+
+def pkv_paged_prefix_attention(query, key_cache, value_cache, cumulative_sequence_length,
+                               past_seqlens, block_table, group_offsets, shared_seqlens, *,
+                               num_heads: int, kv_num_heads: int, max_query_len: int = 0,
+                               scale: float = 0.0, output=None, lse=None, workspace=None,
+                               device_status=None, stream=None):
+    """pkv_paged_window_attention without a window for sequences that begin alike: group g is
+    the sequences group_offsets[g] .. group_offsets[g + 1] - 1, whose first shared_seqlens[g]
+    keys lie in the same blocks and are computed once for all their rows. The workspace holds an
+    output in 32 bits; one of more than 64 MB is not kept behind the call."""
+    torch = _torch()
+    if group_offsets is None or shared_seqlens is None:
+        _need(group_offsets=group_offsets, shared_seqlens=shared_seqlens)
+    G = shared_seqlens.shape[0] if shared_seqlens.dim() == 1 else -1
+    raw, code, T, B, D, BS, NB, MB = _causal_tensors(
+        query, key_cache, value_cache, cumulative_sequence_length, past_seqlens, block_table,
+        num_heads, kv_num_heads, output, lse, workspace, device_status, stream,
+        (("group_offsets", group_offsets, torch.int32, (G + 1,)),
+         ("shared_seqlens", shared_seqlens, torch.int32, (G,))))
+    if output is None:
+        output = _made(stream, query.shape, query.dtype, query.device)
+    sizes = (T, B, G, num_heads, kv_num_heads, D, BS, NB, MB, max_query_len, code)
+    need = _prefix_workspace(query.get_device(), *sizes)
+    if need and (workspace is None or workspace.numel() < need):
+        if need > 64 << 20:   # an output in 32 bits of many rows: not kept
+            workspace = _made(stream, need, torch.uint8, query.device, returned=False)
+        else:
+            workspace = _own_workspace(need, query, stream, raw)
+    _step_call("pkv_paged_prefix_attention",
+               _PREFIX_PACK.pack(query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                 cumulative_sequence_length.data_ptr(), past_seqlens.data_ptr(),
+                                 block_table.data_ptr(), group_offsets.data_ptr(),
+                                 shared_seqlens.data_ptr(), output.data_ptr(), _at(lse),
+                                 _at(device_status), *sizes, scale),
+               _at(workspace), need, raw)
+    return output
+
+
+def _cache_rows(caches):
+    """Checks pools [num_blocks, block_size, ...] against the first. Returns their pointers, the
+    bytes of a token's row in each, num_blocks and block_size."""
+    first = caches[0]
+    shape, dtype, device = first.shape, first.dtype, first.get_device()
+    if first.dim() < 2 or device < 0:
+        raise ValueError("caches: CUDA tensors [num_blocks, block_size, ...]")
+    pool = max(shape[0] * shape[1], 1)
+    row = first.numel() // pool * first.element_size()
+    at, rows = [], [row] * len(caches)
+    for i, t in enumerate(caches):
+        if t.shape != shape or t.dtype is not dtype:
+            if t.dim() < 2 or t.shape[:2] != shape[:2]:
+                raise ValueError(f"caches[{i}]: expected {tuple(shape[:2])} blocks and rows, got "
+                                 f"{tuple(t.shape)}")
+            rows[i] = t.numel() // pool * t.element_size()
+        if not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"caches[{i}]: must be contiguous, on device {device}")
+        at.append(t.data_ptr())
+    return at, rows, shape[0], shape[1]
+
+
+def pkv_paged_fork(parents, past_seqlens, block_table, caches=(), *, num_blocks: int = 0,
+                   block_size: int = 0, new_past_seqlens=None, new_block_table=None,
+                   free_blocks=None, workspace=None, device_status=None, stream=None):
+    """Copies, reorders and frees rows of a block table: new row b takes over what old row
+    parents[b] holds (negative: it is freed). Whole blocks are shared; of a partly filled one
+    every copy but one gets its own, whose rows are copied in each of ``caches`` (tensors
+    [num_blocks, block_size, ...] of any type: keys and values of every layer; without any,
+    ``num_blocks`` and ``block_size`` say what the table means). Returns (new_past_seqlens [batch],
+    new_block_table [batch, max_blocks], free_blocks [1]), int32; those not passed in are made
+    here."""
+    torch = _torch()
+    i32 = torch.int32
+    if parents is None or past_seqlens is None or block_table is None:
+        _need(parents=parents, past_seqlens=past_seqlens, block_table=block_table)
+    B = past_seqlens.shape[0] if past_seqlens.dim() == 1 else -1
+    MB = block_table.shape[1] if block_table.dim() == 2 else -1
+    at = rows = ()
+    if len(caches) > 0:
+        at, rows, num_blocks, block_size = _cache_rows(caches)
+    raw = _check_tensors(stream, (
+        ("parents", parents, i32, (B,)), ("past_seqlens", past_seqlens, i32, (B,)),
+        ("block_table", block_table, i32, (B, MB)),
+        ("new_past_seqlens", new_past_seqlens, i32, (B,)),
+        ("new_block_table", new_block_table, i32, (B, MB)),
+        ("free_blocks", free_blocks, i32, (1,)),
+        ("workspace", workspace, torch.uint8, None if workspace is None else workspace.shape),
+        ("device_status", device_status, i32, (1,))))
+    if at and caches[0].get_device() != block_table.get_device():
+        raise ValueError(f"caches: on device {caches[0].get_device()}, the others on "
+                         f"{block_table.get_device()}")
+
+    def made(t, n):
+        return _made(stream, n, i32, block_table.device) if t is None else t
+
+    past, table, free = made(new_past_seqlens, B), made(new_block_table, (B, MB)), \
+        made(free_blocks, 1)
+    n = len(at)
+    pointers, widths = (c_i64 * n)(*at), (c_i64 * n)(*rows)
+    need = 256 + 16 * B   # pkv_paged_fork_workspace_size
+    if workspace is None or workspace.numel() < need:
+        workspace = _own_workspace(need, block_table, stream, raw)
+    _step_call("pkv_paged_fork",
+               _FORK_PACK.pack(parents.data_ptr(), past_seqlens.data_ptr(),
+                               block_table.data_ptr(), past.data_ptr(), table.data_ptr(),
+                               free.data_ptr(), ctypes.addressof(pointers) if n else 0,
+                               ctypes.addressof(widths) if n else 0, _at(device_status), B, MB,
+                               num_blocks, block_size, n), workspace.data_ptr(), need, raw)
+    return past, table, free
 
 
 # ----------------------------------------------------------------------------- runtime

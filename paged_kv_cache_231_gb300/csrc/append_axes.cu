@@ -13,67 +13,18 @@
 // block is one token's items, or several tokens' where a token has few. Rotary dimensions that
 // are no multiple of 16 take a thread a chunk and read each partner by itself.
 // Measured (32 + 2 x 8 heads of 128): 64 tokens 3.6 us, which is latency; 32768 tokens 134 us.
-#include <cuda_bf16.h>
-
-#include "device_common.cuh"
-#include "internal.h"
-#include "step_ops.h"
+#include "append_dev.cuh"
 
 namespace pkv {
 namespace {
 
+using append::Token;
+using append::read_token;
+using append::report;
+using elem::Num;
+
 constexpr int kThreads = 256;      // of the second kernel; and what the first fills with tokens
 constexpr int kMaxThreads = 512;
-
-template <typename T>
-struct Num;
-template <>
-struct Num<__half> {
-  static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
-  static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
-  static __device__ __forceinline__ float2 to2(uint32_t x) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&x));
-  }
-  static __device__ __forceinline__ uint32_t from2(float a, float b) { return pack_half2(a, b); }
-};
-template <>
-struct Num<__nv_bfloat16> {
-  static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
-  static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
-  static __device__ __forceinline__ float2 to2(uint32_t x) {
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
-  }
-  static __device__ __forceinline__ uint32_t from2(float a, float b) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&x);
-  }
-};
-template <>
-struct Num<float> {
-  static __device__ __forceinline__ float to(float x) { return x; }
-};
-
-// What stops a token's key and value rows; reported by one thread.
-struct Token {
-  int slot;
-  bool known, fits;   // every axis in use has a table row; the slot lies in the pool
-};
-__device__ __forceinline__ Token read_token(const AxesParams& p, int t) {
-  Token k;
-  k.slot = __ldg(p.slots + t);
-  k.known = true;
-  for (int a = 0; a < p.axes; ++a)
-    if ((p.used_axes >> a) & 1u) {
-      const int x = __ldg(p.pos + (int64_t)a * p.T + t);
-      k.known = k.known && x >= 0 && x < p.P;
-    }
-  k.fits = k.slot < p.pool_rows;
-  return k;
-}
-__device__ __forceinline__ void report(const AxesParams& p, const Token& k) {
-  if (k.slot >= 0 && (!k.known || !k.fits))
-    flag_status(p.status, (k.known ? 0 : PKV_DEV_BAD_POSITION) | (k.fits ? 0 : PKV_DEV_BAD_SLOT));
-}
 
 // The two chunks of item i of a token: where they are read and written from token 0 (slot 0) on.
 template <typename T>

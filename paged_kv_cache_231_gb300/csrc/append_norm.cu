@@ -1,0 +1,310 @@
+// K and V of new tokens into the paged cache, queries and keys normed for each head and rotated
+// (pkv_paged_append_norm_rotary).
+//
+// For a head x of D elements: y_i = x_i * w_i / sqrt(sum_j x_j^2 / D + epsilon), then pair j turns
+// by the angle of table row pos[axis(j)][token], column j:
+//   lead' = lead * cos - trail * sin,   trail' = trail * cos + lead * sin
+// in fp32, rounded once. Every element is read once and written once: the operator is bound by
+// HBM, 4 * (Hq + 2 Hkv) * D bytes per token.
+//
+// D / 16 neighbouring lanes hold a head, 16 elements each: a lane has both members of its 8 pairs
+// (two 16-byte chunks rotary_dim / 2 apart, or side by side) or two chunks behind rotary_dim, so
+// the norm is log2(D / 16) shuffles and the rotation none. A block stays on its SM with one or more
+// tokens side by side; while a group of tokens is normed, turned and written, the next one's rows and table
+// entries are on their way and the slots and positions of the one behind it. Cos and sin of a group
+// are gathered once into shared memory, whatever the axes' order. Other head sizes and rotary
+// dimensions take a warp for a head, which passes the normed row on through shared memory.
+#include <type_traits>
+
+#include "append_dev.cuh"
+
+namespace pkv {
+namespace {
+
+using append::Token;
+using append::read_token;
+using append::report;
+using elem::Num;
+
+constexpr int kMaxThreads = 512;
+constexpr int kFill = 256;   // threads that tokens side by side fill
+
+__device__ __forceinline__ float weight_at(const void* w, bool f32, bool bf16, int i) {
+  return f32    ? __ldg(static_cast<const float*>(w) + i)
+         : bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i])
+                : __half2float(static_cast<const __half*>(w)[i]);
+}
+
+// tokens: tokens of a block side by side, N times as many a group; heads: heads of a token that
+// this block works on (blockIdx.y: which).
+template <typename T, typename TT, int D, bool kSide, int N>
+__global__ void __launch_bounds__(kMaxThreads)
+    append_norm_kernel(const __grid_constant__ NormParams np, int tokens, int heads) {
+  constexpr int kLanes = D / 16;
+  const AxesParams& p = np.axes;
+  // [2][N * tokens][4][R / 16] (cos, cos, sin, sin) of pairs 2 y and 2 y + 1 of item c at [y][c], so
+  // that neighbouring lanes read neighbouring words; then (slot, flags) of each token, twice
+  extern __shared__ __align__(16) float4 turn[];
+  const int half = p.R / 2, per_head = p.R / 16, group = N * tokens;
+  const int words = group * per_head * 4;
+  int2* about = reinterpret_cast<int2*>(turn + 2 * words);
+  const int items = heads * kLanes, w = threadIdx.x / items, i = threadIdx.x - w * items;
+  const int groups = (p.T + group - 1) / group;
+  const int h = blockIdx.y * heads + i / kLanes, c = i % kLanes;
+  const bool mine = w < tokens && h < p.Hq + 2 * p.Hkv;
+  const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;   // query, key, value
+  const bool turns = c < per_head && kind < 2;
+  int chunk[2];
+  chunk[0] = c >= per_head ? 2 * c : kSide ? 2 * c : c;
+  chunk[1] = c >= per_head || kSide ? 2 * c + 1 : c + per_head;
+  const int hh = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
+  const T* const src = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) + hh * D;
+  T* const dst = static_cast<T*>(kind == 0 ? p.q_out : kind == 1 ? p.kc : p.vc) + hh * D;
+  const int64_t in_row = kind == 0 ? p.q_stride : p.kv_stride;
+  const int out_row = (kind == 0 ? p.Hq : p.Hkv) * D;
+  const void* const weight = kind == 0 ? np.qw : np.kw;
+  const bool normed = kind < 2 && weight != nullptr;
+
+  const auto load = [&](int g, uint4 (&x)[N][2]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int t = g * group + n * tokens + w;
+      if (mine && g < groups && t < p.T) {
+        const uint4* row = reinterpret_cast<const uint4*>(src + (int64_t)t * in_row);
+        x[n][0] = __ldcs(row + chunk[0]);
+        x[n][1] = __ldcs(row + chunk[1]);
+      }
+    }
+  };
+  // gathering: pair j of token t0 + k of the group, one to a thread and round
+  const auto gather = [&](int g, int buf) {
+    float* const to = reinterpret_cast<float*>(turn + buf * words);
+    for (int k = threadIdx.x; k < group * half; k += blockDim.x) {
+      const int tok = k / half, j = k - tok * half, t = g * group + tok;
+      if (t >= p.T) break;
+      const int r = __ldg(p.pos + (int64_t)p.pair_axis[j] * p.T + t);
+      if (r >= 0 && r < p.P) {
+        const int64_t at = (int64_t)r * half + j;
+        float* z = to + 4 * ((tok * 4 + (j & 7) / 2) * per_head + j / 8) + (j & 1);
+        z[0] = Num<TT>::to(__ldg(static_cast<const TT*>(p.cos) + at));
+        z[2] = Num<TT>::to(__ldg(static_cast<const TT*>(p.sin) + at));
+      }
+    }
+    for (int k = threadIdx.x; k < group; k += blockDim.x) {
+      const int t = g * group + k;
+      if (t >= p.T) break;
+      const Token tk = read_token(p, t);
+      if (blockIdx.y == 0) report(p, tk);
+      about[buf * group + k] =
+          make_int2(tk.slot, (tk.known ? 1 : 0) | (tk.known && tk.fits ? 2 : 0));
+    }
+  };
+
+  int g = blockIdx.x;
+  uint4 x[N][2], ahead[N][2];
+#pragma unroll
+  for (int n = 0; n < N; ++n) x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
+  load(g, x);
+  float wt[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    wt[e] = normed && mine ? weight_at(weight, np.weight_f32, p.bf16, chunk[e / 8] * 8 + e % 8)
+                           : 1.f;
+  gather(g, 0);
+  __syncthreads();
+  for (int buf = 0; g < groups; g += gridDim.x, buf ^= 1) {
+    load(g + gridDim.x, ahead);
+    if (g + (int)gridDim.x < groups) gather(g + gridDim.x, buf ^ 1);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int tok = n * tokens + w, t = g * group + tok;
+      // the shuffles are the whole warp's; rows that are not there are not written
+      float v[16], sum = 0.f;
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[n][0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 f = Num<T>::to2(u[e]);
+        v[2 * e] = f.x;
+        v[2 * e + 1] = f.y;
+        sum += f.x * f.x;
+        sum += f.y * f.y;
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (!mine || t >= p.T) continue;
+      const int2 k = about[buf * group + tok];
+      if (k.x < 0 || (kind > 0 && !(k.y & 2))) continue;
+      uint4 out[2] = {x[n][0], x[n][1]};
+      if (kind < 2) {
+        if (normed) {
+          const float by = rsqrtf(sum * (1.f / D) + np.epsilon);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] *= by * wt[e];
+        }
+        if (turns && (k.y & 1)) {
+          const float4* cs = turn + buf * words + tok * 4 * per_head + c;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float4 a = cs[y * per_head];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int lead = kSide ? 4 * y + 2 * z : 2 * y + z;
+              const int trail = kSide ? lead + 1 : lead + 8;
+              const float co = z ? a.y : a.x, si = z ? a.w : a.z, l = v[lead], r = v[trail];
+              v[lead] = l * co - r * si;
+              v[trail] = r * co + l * si;
+            }
+          }
+        }
+        uint32_t* q = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = Num<T>::from2(v[2 * e], v[2 * e + 1]);
+      }
+      uint4* row = reinterpret_cast<uint4*>(dst + (int64_t)(kind == 0 ? t : k.x) * out_row);
+      row[chunk[0]] = out[0];
+      row[chunk[1]] = out[1];
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      x[n][0] = ahead[n][0];
+      x[n][1] = ahead[n][1];
+    }
+    __syncthreads();
+  }
+}
+
+// Any head size and rotary dimension: a warp for a head of a token.
+constexpr int kWarps = 8;
+template <typename T, typename TT>
+__global__ void __launch_bounds__(32 * kWarps)
+    append_norm_heads_kernel(const __grid_constant__ NormParams np) {
+  __shared__ float s_row[kWarps][256];
+  const AxesParams& p = np.axes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = p.Hq + 2 * p.Hkv;
+  for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < (int64_t)p.T * heads;
+       unit += (int64_t)gridDim.x * kWarps) {
+    const int t = (int)(unit / heads), h = (int)(unit - (int64_t)t * heads);
+    const Token k = read_token(p, t);
+    if (k.slot < 0) continue;
+    if (h == 0 && lane == 0) report(p, k);
+    const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;
+    if (kind > 0 && !(k.known && k.fits)) continue;
+    const int hh = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv, half = p.R / 2;
+    const T* src = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+                   (int64_t)t * (kind == 0 ? p.q_stride : p.kv_stride) + (int64_t)hh * p.D;
+    T* dst = kind == 0 ? static_cast<T*>(p.q_out) + ((int64_t)t * p.Hq + hh) * p.D
+                       : static_cast<T*>(kind == 1 ? p.kc : p.vc) +
+                             ((int64_t)k.slot * p.Hkv + hh) * p.D;
+    const bool there = lane * 8 < p.D;
+    __align__(16) T x[8];
+    float sum = 0.f;
+    if (there) {
+      *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + lane * 8);
+  #pragma unroll
+      for (int e = 0; e < 8; ++e) sum += Num<T>::to(x[e]) * Num<T>::to(x[e]);
+    }
+    if (kind < 2) {
+      const void* weight = kind == 0 ? np.qw : np.kw;
+      sum = warp_sum(sum);
+      const float by = weight ? rsqrtf(sum / (float)p.D + np.epsilon) : 1.f;
+      float* row = s_row[warp];
+      if (there)
+  #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = lane * 8 + e;
+          row[i] = Num<T>::to(x[e]) * by *
+                   (weight ? weight_at(weight, np.weight_f32, p.bf16, i) : 1.f);
+        }
+      __syncwarp();
+      if (there)
+  #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = lane * 8 + e;
+          float y = row[i];
+          if (i < p.R && k.known) {
+            const int j = p.interleaved ? i >> 1 : (i < half ? i : i - half);
+            const bool lead = p.interleaved ? (i & 1) == 0 : i < half;
+            const int other = p.interleaved ? i ^ 1 : (lead ? i + half : i - half);
+            const int64_t at = (int64_t)__ldg(p.pos + (int64_t)p.pair_axis[j] * p.T + t) * half + j;
+            const float co = Num<TT>::to(static_cast<const TT*>(p.cos)[at]);
+            const float si = Num<TT>::to(static_cast<const TT*>(p.sin)[at]);
+            y = lead ? y * co - row[other] * si : y * co + row[other] * si;
+          }
+          x[e] = Num<T>::from(y);
+        }
+    }
+    if (there) *reinterpret_cast<uint4*>(dst + lane * 8) = *reinterpret_cast<const uint4*>(x);
+    __syncwarp();   // the row is read before the next one takes its place
+  }
+}
+
+template <typename T, typename TT, int D, bool kSide>
+void launch_lanes(const NormParams& np, cudaStream_t s) {
+  const AxesParams& p = np.axes;
+  constexpr int kLanes = D / 16;
+  const int all = p.Hq + 2 * p.Hkv;
+  const int parts = (all * kLanes + kMaxThreads - 1) / kMaxThreads, heads = (all + parts - 1) / parts;
+  const int items = heads * kLanes, tokens = items * 2 <= kFill ? kFill / items : 1;
+  const int threads = (tokens * items + 31) / 32 * 32, sms = device_sms();
+  const auto run = [&](auto n, int regs) {
+    constexpr int N = decltype(n)::value;
+    const int group = N * tokens, groups = (p.T + group - 1) / group;
+    const int per_sm = 65536 / (threads * regs) > 1 ? 65536 / (threads * regs) : 1;
+    const int fit = per_sm * sms / parts > 1 ? per_sm * sms / parts : 1;
+    const dim3 grid((unsigned)(groups < fit ? groups : fit), (unsigned)parts);
+    const size_t smem = 2 * (size_t)group * (sizeof(float4) * (p.R / 4) + sizeof(int2));
+    append_norm_kernel<T, TT, D, kSide, N><<<grid, threads, smem, s>>>(np, tokens, heads);
+  };
+  if (p.T >= 4 * tokens * sms)
+    run(std::integral_constant<int, 2>(), 96);
+  else
+    run(std::integral_constant<int, 1>(), 80);
+}
+
+template <typename T, typename TT>
+void launch_typed(const NormParams& np, cudaStream_t s) {
+  const AxesParams& p = np.axes;
+  const bool lanes = p.R % 16 == 0 && (p.D == 64 || p.D == 128 || p.D == 256);
+  if (!lanes) {
+    const int64_t blocks = ((int64_t)p.T * (p.Hq + 2 * p.Hkv) + kWarps - 1) / kWarps;
+    const int64_t fit = (int64_t)64 * device_sms();   // 8 waves
+    append_norm_heads_kernel<T, TT>
+        <<<(unsigned)(blocks < fit ? blocks : fit), 32 * kWarps, 0, s>>>(np);
+    return;
+  }
+  if (p.interleaved) {
+    if (p.D == 64)
+      launch_lanes<T, TT, 64, true>(np, s);
+    else if (p.D == 128)
+      launch_lanes<T, TT, 128, true>(np, s);
+    else
+      launch_lanes<T, TT, 256, true>(np, s);
+  } else {
+    if (p.D == 64)
+      launch_lanes<T, TT, 64, false>(np, s);
+    else if (p.D == 128)
+      launch_lanes<T, TT, 128, false>(np, s);
+    else
+      launch_lanes<T, TT, 256, false>(np, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append_norm(const NormParams& p, cudaStream_t s) {
+  ProfScope ps("append_norm", s);
+  if (p.axes.bf16) {
+    if (p.axes.table_f32)
+      launch_typed<__nv_bfloat16, float>(p, s);
+    else
+      launch_typed<__nv_bfloat16, __nv_bfloat16>(p, s);
+  } else {
+    if (p.axes.table_f32)
+      launch_typed<__half, float>(p, s);
+    else
+      launch_typed<__half, __half>(p, s);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace pkv

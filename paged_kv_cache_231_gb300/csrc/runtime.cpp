@@ -334,6 +334,10 @@ size_t pkv_sizeof_struct(const char* name) {
   if (n == "pkv_schedule_args") return sizeof(pkv_schedule_args);
   if (n == "pkv_append_axes_args") return sizeof(pkv_append_axes_args);
   if (n == "pkv_cross_attention_args") return sizeof(pkv_cross_attention_args);
+  if (n == "pkv_append_norm_args") return sizeof(pkv_append_norm_args);
+  if (n == "pkv_window_attention_args") return sizeof(pkv_window_attention_args);
+  if (n == "pkv_prefix_attention_args") return sizeof(pkv_prefix_attention_args);
+  if (n == "pkv_fork_args") return sizeof(pkv_fork_args);
   return 0;
 }
 

@@ -24,6 +24,7 @@
 
 #include "device_common.cuh"
 #include "internal.h"
+#include "pool_dev.cuh"
 #include "step_ops.h"
 
 namespace pkv {
@@ -31,8 +32,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+using pool::block_sum;
+using pool::first_above;
+using pool::kThreads;
+using pool::kWarps;
 constexpr int kChunk = 128;   // table columns of a row that a warp marks as one piece
 constexpr unsigned kMaxCluster = 16;
 constexpr int kUnits = 4;     // such pieces whose loads are under way at once
@@ -72,42 +75,6 @@ __device__ __forceinline__ Row read_row(const ScheduleParams& p, int b) {
   r.held = min(blocks_for(p, r.past), p.MB);
   r.asked = r.tokens > 0 ? blocks_for(p, r.past + r.tokens) - r.held : 0;
   return r;
-}
-
-// Inclusive sum over the block's threads; *total gets the sum of all. scratch: kWarps words that
-// neither the call before nor the one behind uses.
-template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* total, T* scratch) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
-  }
-  if (lane == 31) scratch[w] = v;
-  __syncthreads();
-  T upto = scratch[lane];   // every warp sums the warps' sums for itself
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  *total = __shfl_sync(0xffffffffu, upto, kWarps - 1);
-  const T before = __shfl_sync(0xffffffffu, upto, w > 0 ? w - 1 : 0);
-  return w > 0 ? v + before : v;
-}
-
-// first index i of the ascending a[0, n) with a[i] > x (n when there is none)
-__device__ __forceinline__ int first_above(const int* a, int n, int x) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] > x)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo;
 }
 
 // Slots and positions of many tokens, kTokens to a thread from `from` on and every further

@@ -52,6 +52,37 @@ struct AxesParams {
 };
 cudaError_t launch_append_axes(const AxesParams& p, cudaStream_t s);
 
+// ---- append with norms ----------------------------------------------------------------
+struct NormParams {
+  AxesParams axes;
+  const void* qw;            // NULL: not normed
+  const void* kw;
+  float epsilon;
+  int weight_f32;
+};
+cudaError_t launch_append_norm(const NormParams& p, cudaStream_t s);
+
+// ---- fork -----------------------------------------------------------------------------
+struct ForkParams {
+  const int32_t* parents;
+  const int32_t* past;
+  const int32_t* table;
+  int32_t* new_past;
+  int32_t* new_table;
+  int32_t* free_out;         // may be NULL
+  int32_t* status;
+  int32_t* count;            // workspace: copies, and their [B] (source, destination, rows, -)
+  int4* list;
+  int B, MB, BS, NB, bs_shift;
+  int groups;                // groups of 1024 block ids
+  int caches;
+  int pieces;                // units of 16 KB that a block of the widest cache has
+  int row_words[PKV_MAX_FORK_CACHES];   // 16-byte words of a token's row
+  void* cache[PKV_MAX_FORK_CACHES];
+};
+constexpr int kForkPiece = 1024;   // words of a unit
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t s);
+
 // ---- cross attention ------------------------------------------------------------------
 struct CrossParams {
   const void* q;
@@ -69,6 +100,10 @@ struct CrossParams {
   int max_q;                 // longest sequence the call admits
   int bf16;
   float scale_log2;          // softmax scale * log2(e)
+  // causal forms: query row i of a sequence stands at past + i
+  const int32_t* past;
+  int window;                // keys that a row sees, 0: all
+  int sinks;                 // first keys that stay visible
   // plan (cross_dev.cuh)
   int few;                   // query rows of a sequence that the kernel for few rows takes
   int tile_pos;              // query positions of a tile of the kernel for many rows
@@ -94,6 +129,7 @@ struct CrossParams {
 // the workspace bytes
 size_t cross_layout(CrossParams* p, char* base);
 cudaError_t launch_cross(const CrossParams& p, cudaStream_t s);
+cudaError_t launch_window(const CrossParams& p, cudaStream_t s);
 // kernel for many rows (cross_tiles.cu)
 cudaError_t launch_cross_tiles(const CrossParams& p, cudaStream_t s);
 
