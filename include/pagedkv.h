@@ -653,9 +653,9 @@ int pkv_paged_window_attention_workspace_size(const pkv_window_attention_args* a
  * no row sees any more may be given back. Cache rows that no row of the sequence sees may hold
  * anything (NaN too); a key or value that is not finite can reach all rows of its sequence.
  * A row that sees no mapped key gets output 0 and lse -inf. Sequences whose cumulative lengths
- * are inconsistent or exceed max_query_len, or whose past_seqlens entry is negative, get zero
- * rows (lse -inf) and set PKV_DEV_BAD_SEQUENCE; so do rows that no sequence covers, without
- * the flag. Equal calls give equal bits; output, lse, workspace, PKV_DEV_TIMEOUT and the sizes
+ * are inconsistent or exceed max_query_len, or whose past_seqlens entry is negative or beyond
+ * max_blocks * block_size, get zero rows (lse -inf) and set PKV_DEV_BAD_SEQUENCE; so do rows
+ * that no sequence covers, without the flag. Equal calls give equal bits; output, lse, workspace, PKV_DEV_TIMEOUT and the sizes
  * supported: as in pkv_cross_attention. */
 int pkv_paged_window_attention(const pkv_window_attention_args* args, void* workspace,
                                size_t workspace_bytes, void* stream);

@@ -33,7 +33,8 @@ def causal_attention(q, key_cache, value_cache, cu, past, table, *, num_heads, k
     size, reach, status = np.zeros((T, Hq, D)), np.zeros((T, Hq)), 0
     for b in range(len(past)):
         lo, hi, p = int(cu[b]), int(cu[b + 1]), int(past[b])
-        if lo < 0 or hi < lo or hi > T or p < 0 or (max_query_len and hi - lo > max_query_len):
+        if (lo < 0 or hi < lo or hi > T or not 0 <= p <= MB * BS or
+                (max_query_len and hi - lo > max_query_len)):
             status |= BAD_SEQUENCE
             continue
         for i in range(lo, hi):

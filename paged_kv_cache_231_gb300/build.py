@@ -7,6 +7,7 @@ Output: ``paged_kv_cache_231_gb300/libpagedkv.so``. Objects and the ptxas report
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -21,7 +22,7 @@ LIB = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["runtime.cpp", "attention.cu", "scatter.cu", "combine.cu", "sparse.cu",
            "sparse16.cu", "static_workspace.cu", "step_runtime.cpp", "schedule.cu",
            "append_axes.cu", "cross.cu", "cross_tiles.cu", "append_norm.cu", "fork.cu",
-           "window.cu"]
+           "window.cu", "window_tiles.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -37,6 +38,13 @@ def _deps():
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC)
               if f.endswith((".h", ".cuh"))]
     return files
+
+
+def _included(path):
+    """Sources that a source is made of beside itself (a form of another one's kernels)."""
+    with open(path) as f:
+        names = re.findall(r'^#include "(\w+\.cu)"', f.read(), re.M)
+    return [os.path.join(CSRC, n) for n in names]
 
 
 def _stale(target, inputs):
@@ -62,7 +70,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         path = os.path.join(CSRC, src)
         obj = os.path.join(BUILD, src + ".o")
         objs.append(obj)
-        if force or _stale(obj, [path] + deps):
+        if force or _stale(obj, [path] + _included(path) + deps):
             cmd = [cc, "-c", path, "-o", obj] + common
             if src.endswith(".cu"):
                 cmd += ["-Xptxas", "-v"]

@@ -29,20 +29,28 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kLeastTile = 2;   // steps of a run of the other kernel, at least
 
 template <int D>
+__device__ __forceinline__ Span few_span(const CrossParams& p, const Seq& q) {
+  return span_of<few_keys(D)>(p, q, q.at, q.at + q.rows - 1);
+}
+
+template <int D>
 __device__ __forceinline__ int chunk_at(int r, int c) {   // 16-byte chunk c of row r, swizzled
   return (r * (D / 8) + (c ^ (r & 7))) * 8;
 }
 
-// Lane r < few_keys(D): element offset of key r of step s of (sequence b, kv head h), -1 past
-// the keys or where the block is unmapped.
-template <int D>
-__device__ __forceinline__ int64_t key_offset(const CrossParams& p, int b, int h, int s, int keys,
-                                              int lane, int& flags) {
+// Lane r < few_keys(D): element offset of key r of the cursor's step and kv head h, -1 past the
+// keys, where no row sees it, or where the block is unmapped.
+template <int D, Form F>
+__device__ __forceinline__ int64_t key_offset(const CrossParams& p, const Cursor& c, int h, int lane,
+                                              int& flags) {
   constexpr int K = few_keys(D);
+  int s = c.s;
+  if (F == kCausal) s = few_span<D>(p, c.q).key_step(s);
   const int j = s * K + lane;
-  if (lane >= K || j >= keys) return -1;
+  if (lane >= K || j >= c.q.keys) return -1;
+  if (F == kCausal && j < first_seen(p, c.q) && (p.window == 0 || j >= p.sinks)) return -1;
   const int col = p.bs_shift >= 0 ? j >> p.bs_shift : j / p.BS;
-  const int blk = __ldg(p.table + (int64_t)b * p.MB + col);
+  const int blk = __ldg(p.table + (int64_t)(F == kShared ? c.q.at : c.b) * p.MB + col);
   if (blk < 0 || blk >= p.NB) {
     flags |= PKV_DEV_BAD_BLOCK;
     return -1;
@@ -90,8 +98,27 @@ __device__ __forceinline__ void load_queries(const CrossParams& p, const Cursor&
   }
 }
 
+// Two neighbouring elements of an output row, the first at `at`.
+template <typename T, Form F>
+__device__ __forceinline__ void store_pair(const CrossParams& p, int64_t at, const Weights& w,
+                                           float a, float b) {
+  a *= w.own;
+  b *= w.own;
+  if constexpr (F == kCausal) {
+    if (w.other > 0.f) {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(p.prior_o + at));
+      a += w.other * x.x;
+      b += w.other * x.y;
+    }
+  }
+  if constexpr (F == kShared)
+    *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at) = make_float2(a, b);
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + at) = Num<T>::pack(a, b);
+}
+
 // End of the unit's part of a range: the output if the range lies in the run, else a piece.
-template <typename T, int D>
+template <typename T, int D, Form F>
 __device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int h, int gw,
                                       bool whole, int slot, float (&m)[2], float (&l)[2],
                                       float (&o)[D / 8][4], int lane) {
@@ -103,13 +130,12 @@ __device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int
     const int r = (lane >> 2) + 8 * x;
     if (r >= R) continue;
     if (whole) {
-      const float inv = inverse_of(l[x]);
       const int64_t row = (int64_t)(c.q.cu0 + r / p.G) * p.Hq + h * p.G + r % p.G;
-      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D) + t4;
+      const Weights w = weights_of<F>(p, row, m[x], l[x]);
 #pragma unroll
       for (int d = 0; d < D / 8; ++d)
-        out[d * 4] = Num<T>::pack(o[d][2 * x] * inv, o[d][2 * x + 1] * inv);
-      if (p.lse && t4 == 0) p.lse[row] = lse_of(m[x], l[x]);
+        store_pair<T, F>(p, row * D + d * 8 + 2 * t4, w, o[d][2 * x], o[d][2 * x + 1]);
+      if (p.lse && t4 == 0) p.lse[row] = w.lse;
     } else {
       const int64_t row = (int64_t)(2 * gw + slot) * p.few_rows + r;
 #pragma unroll
@@ -125,10 +151,11 @@ __device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int
 }
 
 // Whether row i lies in sequence b and sees a key of it.
+template <Form F>
 __device__ __forceinline__ bool holds_row(const CrossParams& p, int b, int i) {
   int f = 0;
   bool z = false;
-  const Seq few = read_seq<false>(p, b, &f, &z), many = read_seq<true>(p, b, &f, &z);
+  const Seq few = read_seq<false, F>(p, b, &f, &z), many = read_seq<true, F>(p, b, &f, &z);
   return few.ranges + many.ranges > 0 && i >= few.cu0 && i < few.cu0 + few.rows;
 }
 
@@ -137,7 +164,7 @@ __device__ __forceinline__ bool holds_row(const CrossParams& p, int b, int i) {
 // it. Where they do not (some sequence is bad), a later or an earlier one can: a row that the search
 // does not find held is looked for in all of them.
 // ordered: 1 they ascend, 0 they do not, -1 not known; then a warp looks when it has such a row.
-template <typename T, int D>
+template <typename T, int D, Form F>
 __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, int ordered) {
   for (int64_t i0 = (int64_t)unit * 32; i0 < p.T; i0 += (int64_t)units * 32) {
     const int i = (int)min(i0 + lane, (int64_t)p.T - 1);
@@ -151,7 +178,7 @@ __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, i
         hi = mid - 1;
       }
     }
-    const bool empty = b < 0 || !holds_row(p, b, i);
+    const bool empty = b < 0 || !holds_row<F>(p, b, i);
     uint32_t todo = __ballot_sync(0xffffffffu, empty && i0 + lane < p.T);
     if (todo && ordered < 0) {
       bool descends = false;
@@ -162,10 +189,12 @@ __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, i
       const int64_t row = i0 + __ffs(todo) - 1;
       bool held = false;
       for (int b0 = 0; ordered == 0 && !held && b0 < p.B; b0 += 32)
-        held = __any_sync(0xffffffffu, b0 + lane < p.B && holds_row(p, b0 + lane, (int)row));
+        held = __any_sync(0xffffffffu, b0 + lane < p.B && holds_row<F>(p, b0 + lane, (int)row));
       if (held) continue;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.Hq * D);
-      for (int c = lane; c < p.Hq * D / 8; c += 32) out[c] = make_uint4(0, 0, 0, 0);
+      if (F != kShared) {   // there nobody reads a row whose lse is -inf
+        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.Hq * D);
+        for (int c = lane; c < p.Hq * D / 8; c += 32) out[c] = make_uint4(0, 0, 0, 0);
+      }
       if (p.lse)
         for (int h = lane; h < p.Hq; h += 32) p.lse[row * p.Hq + h] = -INFINITY;
     }
@@ -232,13 +261,13 @@ struct Joined {
       }
     }
   }
-  template <typename T>
+  template <typename T, Form F>
   __device__ __forceinline__ void write(const CrossParams& p, int64_t row, int lane) const {
-    const float inv = inverse_of(L);
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + row * D + lane * V);
+    const Weights w = weights_of<F>(p, row, M, L);
 #pragma unroll
-    for (int v = 0; v < V; v += 2) out[v / 2] = Num<T>::pack(acc[v] * inv, acc[v + 1] * inv);
-    if (p.lse && lane == 0) p.lse[row] = lse_of(M, L);
+    for (int v = 0; v < V; v += 2)
+      store_pair<T, F>(p, row * D + lane * V + v, w, acc[v], acc[v + 1]);
+    if (p.lse && lane == 0) p.lse[row] = w.lse;
   }
 };
 
@@ -257,7 +286,7 @@ struct Ring {
 // kSmall: a block takes one sequence and kv head, its warps an eighth of the steps each, and joins
 // what they have in shared memory (few and short sequences: p.small). Behind these blocks are a few
 // that look for rows to be zeroed.
-template <typename T, int D, bool kSmall>
+template <typename T, int D, bool kSmall, Form F>
 __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   constexpr int NS = Ring<D>::kSteps, K = few_keys(D);
   extern __shared__ __align__(128) unsigned char smem[];
@@ -274,43 +303,43 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   if constexpr (kSmall) {
     const int work = p.B * p.Hkv;
     if ((int)blockIdx.x >= work) {
-      zero_rows<T, D>(p, gw - work * kWarps, ((int)gridDim.x - work) * kWarps, lane, -1);
+      zero_rows<T, D, F>(p, gw - work * kWarps, ((int)gridDim.x - work) * kWarps, lane, -1);
       return;
     }
     bool zero;
     cc.b = blockIdx.x / p.Hkv;
     cc.r = blockIdx.x - cc.b * p.Hkv;
-    cc.q = read_seq<false>(p, cc.b, &flags, &zero);
+    cc.q = read_seq<false, F>(p, cc.b, &flags, &zero);
     if (cc.r > 0 || warp > 0) flags = 0;   // every block of the sequence saw them
     const int share = (cc.q.steps + kWarps - 1) / kWarps;
     cc.s = warp * share;
     nst = max(0, min(share, cc.q.steps - cc.s));
   } else {
-    pl = make_plan<kThreads>(p, p.few_units / p.few_heads, s_pref, s_scratch, &flags);
+    pl = make_plan<kThreads, F>(p, p.few_units / p.few_heads, s_pref, s_scratch, &flags);
     if (blockIdx.x > 0) flags = 0;   // every block saw them
     unit = gw / p.few_heads;
     sub = gw % p.few_heads;
     const int64_t g0 = (int64_t)unit * pl.W;
     nst = g0 < pl.total ? (int)(min(pl.total, g0 + pl.W) - g0) : 0;
-    if (nst > 0) cc = locate(p, pl, s_pref, g0);
+    if (nst > 0) cc = locate<F>(p, pl, s_pref, g0);
   }
   if (nst > 0) {
     T* rk = reinterpret_cast<T*>(smem + warp * Ring<D>::kWarpBytes);
     T* rv = rk + NS * K * D;
     Cursor pc = cc;                                  // next step to copy
     uint32_t* live = s_live[warp];                   // keys of a step that take part
-    int64_t ahead = key_offset<D>(p, pc.b, pc.r * p.few_heads + sub, pc.s, pc.q.keys, lane, flags);
+    int64_t ahead = key_offset<D, F>(p, pc, pc.r * p.few_heads + sub, lane, flags);
     const auto issue = [&](int k, int buf) {
       if (k < nst) {
         copy_step<T, D>(p, ahead, rk + buf * K * D, rv + buf * K * D, lane);
         if (k + 1 < nst) {
-          if (++pc.s == pc.q.steps) next_range(p, pc);
+          if (++pc.s == pc.q.steps) next_range<F>(p, pc);
         }
       }
       const uint32_t w = __ballot_sync(0xffffffffu, ahead >= 0);
       if (lane == 0) live[buf] = w;
       if (k + 1 < nst)
-        ahead = key_offset<D>(p, pc.b, pc.r * p.few_heads + sub, pc.s, pc.q.keys, lane, flags);
+        ahead = key_offset<D, F>(p, pc, pc.r * p.few_heads + sub, lane, flags);
       cp_async_commit();
     };
     // one copy of the step's code: unrolled over the ring it did not fit the instruction cache
@@ -319,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
     uint32_t qa[D / 16][4];
     load_queries<T, D>(p, cc, cc.r * p.few_heads + sub, lane, qa);
     // while the first steps are on their way (in front of them it took 1 us of 64 tokens' 178 us)
-    if (!kSmall && lane == 0) write_record(p, pl, s_pref, unit, sub, p.few_rec + 2 * gw);
+    if (!kSmall && lane == 0) write_record<F>(p, pl, s_pref, unit, sub, p.few_rec + 2 * gw);
     __syncwarp();
     const int t4 = lane & 3;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[D / 8][4];
@@ -359,6 +388,25 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
           s[n][e] *= p.scale_log2;
           if (!all && !((w >> (n * 8 + 2 * t4 + (e & 1))) & 1u)) s[n][e] = -INFINITY;
         }
+      if constexpr (F == kCausal) {
+        // keys that some rows see and others do not; `live` has told of those that none sees
+        const int k0 = few_span<D>(p, cc.q).key_step(cc.s) * K;
+        const int last = cc.q.at + cc.q.rows - 1;
+        if (cc.q.rows > 1 && (k0 + K - 1 > cc.q.at || (p.window > 0 && k0 <= last - p.window))) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int pos = cc.q.at + ((lane >> 2) + 8 * x) / p.G;
+            const int from = p.window > 0 ? pos - p.window : -1;   // sees keys behind it
+#pragma unroll
+            for (int n = 0; n < K / 8; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = k0 + n * 8 + 2 * t4 + e;
+                if (key > pos || (key <= from && key >= p.sinks)) s[n][2 * x + e] = -INFINITY;
+              }
+          }
+        }
+      }
       // online softmax; m is raised when a score exceeds the maximum that it stands for by kRaise
       float top[2];
       bool raise = false;
@@ -417,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
       }
       const bool last = cc.s == cc.q.steps - 1;
       if (!kSmall && (last || k == nst - 1)) {
-        flush<T, D>(p, cc, cc.r * p.few_heads + sub, gw, from_start && last, first ? 0 : 1, m, l, o,
+        flush<T, D, F>(p, cc, cc.r * p.few_heads + sub, gw, from_start && last, first ? 0 : 1, m, l, o,
                     lane);
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
@@ -428,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
       }
       if (k < nst - 1) {
         if (last) {
-          next_range(p, cc);
+          next_range<F>(p, cc);
           load_queries<T, D>(p, cc, cc.r * p.few_heads + sub, lane, qa);
         } else {
           ++cc.s;
@@ -445,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
       here.few_m = here.few_o + 2 * kWarps * 16 * D;
       here.few_l = here.few_m + 2 * kWarps * 16;
       here.few_rows = 16;
-      flush<T, D>(here, cc, cc.r, warp, false, 0, m, l, o, lane);
+      flush<T, D, F>(here, cc, cc.r, warp, false, 0, m, l, o, lane);
     }
   } else if constexpr (kSmall) {
     named_barrier();
@@ -479,10 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
         for (int v = 0; v < Joined<D>::V; ++v)
           j.acc[v] += by * po[at * D + lane * Joined<D>::V + v];
       }
-      j.template write<T>(p, (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G, lane);
+      j.template write<T, F>(p, (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G, lane);
     }
   } else if (pl.zero) {
-    zero_rows<T, D>(p, gw, p.few_units, lane, pl.ordered ? 1 : 0);
+    zero_rows<T, D, F>(p, gw, p.few_units, lane, pl.ordered ? 1 : 0);
   }
   if (flags) flag_status(p.status, flags);
   // the join behind this kernel waits for it alone: it must not end before the one in front
@@ -492,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
 // Blocks 0 .. : kJoinRows rows of a tile's record each (256 / kJoinRows blocks a record). Behind
 // them a block for the record of each warp of the kernel for few rows: 8 warps share the rows that
 // fall to it, several warps a row when there are fewer.
-template <typename T, int D>
+template <typename T, int D, Form F>
 __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams p) {
   constexpr int V = D / 32, kBlocks = 256 / kJoinRows;
   __shared__ float s_o[kJoinWarps][D];
@@ -518,7 +566,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
       Joined<D> j;
       j.add(p.tile_o + first * D, p.tile_m + first, p.tile_l + first, row, a.y * 256, 512, a.x, 0,
             1, lane);
-      j.template write<T>(p, (int64_t)(a.z + pos) * p.Hq + a.w * p.G + x - by_g * p.G, lane);
+      j.template write<T, F>(p, (int64_t)(a.z + pos) * p.Hq + a.w * p.G + x - by_g * p.G, lane);
     }
     return;
   }
@@ -567,28 +615,32 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
     }
     const int by_g = (int)(r * over_g >> 16);
     if (live && part == 0)
-      j.template write<T>(p, (int64_t)(a.z + by_g) * p.Hq + a.w * p.G + r - by_g * p.G, lane);
+      j.template write<T, F>(p, (int64_t)(a.z + by_g) * p.Hq + a.w * p.G + r - by_g * p.G, lane);
   }
 }
 
-template <typename T, int D>
+constexpr const char* kNames[][2] = {{"cross_decode", "cross_combine"},
+                                     {"prefix_decode", "prefix_combine"},
+                                     {"window_decode", "window_combine"}};
+
+template <typename T, int D, Form F>
 cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
   int dev = -1;
   if (needs_configure(configured, &dev)) {
-    cudaError_t e = cudaFuncSetAttribute(cross_few_kernel<T, D, false>,
+    cudaError_t e = cudaFuncSetAttribute(cross_few_kernel<T, D, false, F>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Ring<D>::kBytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(cross_few_kernel<T, D, true>,
+      e = cudaFuncSetAttribute(cross_few_kernel<T, D, true, F>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<D>::kBytes);
     if (e != cudaSuccess) return e;
     mark_configured(configured, dev);
   }
   if (p.small) {
-    ProfScope ps("cross_decode", s);
+    ProfScope ps(kNames[F][0], s);
     const unsigned zero = (unsigned)((p.T + kThreads - 1) / kThreads);
-    cross_few_kernel<T, D, true>
+    cross_few_kernel<T, D, true, F>
         <<<(unsigned)(p.B * p.Hkv) + zero, kThreads, Ring<D>::kBytes, s>>>(p);
     return cudaGetLastError();
   }
@@ -601,35 +653,41 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   // The tiles first: the other kernel's blocks then fill the SMs as theirs end (a call without few
   // rows spends 7 us on them otherwise). They read inputs and write rows of their own.
   if (p.tile_units > 0) {
-    const cudaError_t e = launch_cross_tiles(p, s);
+    const cudaError_t e = PKV_LAUNCH(_tiles)(p, s);
     if (e != cudaSuccess) return e;
     cfg.numAttrs = 1;
   }
   {
-    ProfScope ps("cross_decode", s);
+    ProfScope ps(kNames[F][0], s);
     cfg.gridDim = dim3((unsigned)(p.few_units / kWarps));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Ring<D>::kBytes;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D, false>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D, false, F>, p);
     if (e != cudaSuccess) return e;
   }
-  ProfScope ps("cross_combine", s);
+  ProfScope ps(kNames[F][1], s);
   cfg.gridDim = dim3((unsigned)(p.few_units + 256 / kJoinRows * p.tile_units));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cross_join_kernel<T, D>, p);
+  return cudaLaunchKernelEx(&cfg, cross_join_kernel<T, D, F>, p);
 }
 
 }  // namespace
 
+#ifdef PKV_CROSS_FORM
 size_t cross_layout(CrossParams* p, char* base) {
   const int sms = device_sms();
   p->few = 16 / p->G;
   p->tile_pos = 2 * (128 / p->G);
   // no more units than the longest possible work has runs of the least length (in floating point:
   // the products may pass 64 bits)
-  const double keys = (double)p->MB * p->BS, seqs = p->T < p->B ? p->T : p->B;
+  double keys = (double)p->MB * p->BS;
+  const double seqs = p->T < p->B ? p->T : p->B;
+  if (p->window > 0) {   // what the rows of a sequence see, in steps cut at both ends and the sinks'
+    const double seen = (double)p->window + p->max_q + p->sinks + 3 * kTileKeys;
+    if (seen < keys) keys = seen;
+  }
   const double runs = seqs * p->Hkv * (keys / few_keys(p->D) + 1);
   const int ctas = runs >= (double)sms * kWarps ? sms : (int)(runs / kWarps) + 1;
   p->few_units = ctas * kWarps;
@@ -680,11 +738,14 @@ size_t cross_layout(CrossParams* p, char* base) {
   return off;
 }
 
-cudaError_t launch_cross(const CrossParams& p, cudaStream_t s) {
+#endif
+
+cudaError_t PKV_LAUNCH()(const CrossParams& p, cudaStream_t s) {
   if (p.bf16)
-    return p.D == 64 ? launch_typed<__nv_bfloat16, 64>(p, s)
-                     : launch_typed<__nv_bfloat16, 128>(p, s);
-  return p.D == 64 ? launch_typed<__half, 64>(p, s) : launch_typed<__half, 128>(p, s);
+    return p.D == 64 ? launch_typed<__nv_bfloat16, 64, PKV_FORM>(p, s)
+                     : launch_typed<__nv_bfloat16, 128, PKV_FORM>(p, s);
+  return p.D == 64 ? launch_typed<__half, 64, PKV_FORM>(p, s)
+                   : launch_typed<__half, 128, PKV_FORM>(p, s);
 }
 
 }  // namespace pkv

@@ -10,6 +10,16 @@
 // pieces in order. The unit in whose run such a range begins writes the record that the join
 // reads. Tiles that are many are dealt out whole first (cross_tiles.cu); the rest is cut.
 // Lengths live on the device, so every block makes the plan for itself from cu and klen.
+//
+// Forms. The kernels are written once and compiled for three kinds of calls:
+//   kCross   every row of a sequence sees all of its klen keys;
+//   kShared  the same for groups of sequences over the keys that these have in common; output and
+//            lse go to 32-bit arrays in the workspace;
+//   kCausal  row i stands at past + i and sees keys j <= past + i with j > past + i - window or
+//            j < sinks, or (behind a shared prefix) with j >= start; then the result of the kShared
+//            call is joined in where the row is written.
+// Steps of keys that no row of a range sees are not among its steps: those behind the `ns` steps of
+// the sinks and in front of the window are passed over (`gap` steps).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -19,6 +29,13 @@
 #include "device_common.cuh"
 #include "internal.h"
 #include "step_ops.h"
+
+// The form that a translation unit compiles (see below) and the name of its launchers.
+#ifndef PKV_FORM
+#define PKV_FORM kCross
+#define PKV_LAUNCH(suffix) launch_cross##suffix
+#define PKV_CROSS_FORM
+#endif
 
 namespace pkv {
 namespace cross {
@@ -36,6 +53,8 @@ constexpr float kLift = 7.f, kRaise = 8.f;
 // without a bound 77 us
 constexpr int kMaxPieces = 512;
 constexpr int kMaxTileUnits = 256; // blocks of the kernel for many rows
+
+enum Form { kCross, kShared, kCausal };
 
 template <typename T>
 struct Num;
@@ -68,26 +87,61 @@ struct Num<__nv_bfloat16> {
 // One sequence as a kernel of one kind sees it; ranges == 0: nothing to do here.
 struct Seq {
   int cu0, rows, keys;   // first query row, query rows, keys
-  int steps;             // steps of a range
+  int steps;             // steps of a range (kCausal, many rows: of its tiles for one kv head)
   int ranges;
+  int at;                // kCausal: position of the first row; kShared: row of the block table
+  int lo;                // kCausal: first key that takes part (in a window or not)
 };
+
+// Steps of N keys that rows at positions first .. last of a sequence go through: step j < ns is the
+// j-th of the sequence, the others the (j + gap)-th. One at least, so that every row is written.
+struct Span {
+  int ns, gap, steps;
+  __device__ __forceinline__ int key_step(int j) const { return j < ns ? j : j + gap; }
+};
+template <int N>
+__device__ __forceinline__ Span span_of(const CrossParams& p, const Seq& q, int first, int last) {
+  Span x;
+  x.ns = p.window > 0 ? (int)(((uint32_t)p.sinks + N - 1) / N) : 0;
+  const int end = min(last, q.keys - 1) / N + 1;
+  const int from = p.window > 0 ? max(q.lo, first - p.window + 1) : q.lo;
+  x.gap = min(max(from / N - x.ns, 0), end - 1);
+  x.steps = end - x.gap;
+  return x;
+}
+// of tile t of a sequence
+__device__ __forceinline__ Span tile_span(const CrossParams& p, const Seq& q, int t) {
+  const int q0 = t * p.tile_pos;
+  return span_of<kTileKeys>(p, q, q.at + q0, q.at + min(q0 + p.tile_pos, q.rows) - 1);
+}
+// first key in a window that some row of the sequence sees
+__device__ __forceinline__ int first_seen(const CrossParams& p, const Seq& q) {
+  return p.window > 0 ? max(q.lo, q.at - p.window + 1) : q.lo;
+}
 
 // kTiles: the kernel for many rows. *flags gets what is wrong with the sequence, *zero is set
 // when some of its rows see no key.
-template <bool kTiles>
+template <bool kTiles, Form F>
 __device__ __forceinline__ Seq read_seq(const CrossParams& p, int b, int* flags, bool* zero) {
   Seq s;
   s.cu0 = __ldg(p.cu + b);
   const int hi = __ldg(p.cu + b + 1);
-  s.keys = __ldg(p.klen + b);
+  s.keys = __ldg((F == kCausal ? p.past : p.klen) + b);
+  if (F == kCausal) s.lo = p.start ? __ldcg(p.start + b) : 0;
+  if (F == kShared) s.at = __ldcg(p.table_row + b);
   s.steps = s.ranges = 0;
   // Of any two numbers, so it may wrap around, and is looked at behind the other checks only.
   // (Formed behind them: 128 tokens over 1500 states 67.0 us, so 66.2 us.)
   s.rows = (int)((uint32_t)hi - (uint32_t)s.cu0);
-  if (s.cu0 < 0 || hi < s.cu0 || hi > p.T || s.rows > p.max_q || s.keys < 0) {
+  if (s.cu0 < 0 || hi < s.cu0 || hi > p.T || s.rows > p.max_q || s.keys < 0 ||
+      (F == kCausal && s.keys > p.MB * p.BS)) {
     *flags |= PKV_DEV_BAD_SEQUENCE;
     *zero = true;
     return s;
+  }
+  if (F == kCausal) {   // both below 2^30
+    s.at = s.keys;
+    s.keys += s.rows;
   }
   if (s.rows > 0 && s.keys > p.MB * p.BS) {
     *flags |= PKV_DEV_BAD_BLOCK;
@@ -96,11 +150,20 @@ __device__ __forceinline__ Seq read_seq(const CrossParams& p, int b, int* flags,
   if (s.rows > 0 && s.keys == 0) *zero = true;
   if (s.rows == 0 || s.keys == 0 || (s.rows > p.few) != kTiles) return s;
   if (kTiles) {
-    s.steps = (s.keys + kTileKeys - 1) / kTileKeys;
-    s.ranges = p.Hkv * ((s.rows + p.tile_pos - 1) / p.tile_pos);
+    const int tiles = (s.rows + p.tile_pos - 1) / p.tile_pos;
+    if (F == kCausal) {
+      for (int t = 0; t < tiles; ++t) s.steps += tile_span(p, s, t).steps;
+    } else {
+      s.steps = (s.keys + kTileKeys - 1) / kTileKeys;
+    }
+    s.ranges = p.Hkv * tiles;
   } else {
     const int n = few_keys(p.D);
-    s.steps = (s.keys + n - 1) / n;
+    if (F == kCausal)
+      s.steps = (p.D == 64 ? span_of<few_keys(64)>(p, s, s.at, s.at + s.rows - 1)
+                           : span_of<few_keys(128)>(p, s, s.at, s.at + s.rows - 1)).steps;
+    else
+      s.steps = (s.keys + n - 1) / n;
     s.ranges = p.Hkv / p.few_heads;
   }
   return s;
@@ -148,7 +211,7 @@ struct Plan {
 };
 
 // Block-wide. pref: [kEntries] steps before entry e (shared memory); scratch: [NT / 32 + 2].
-template <int NT>
+template <int NT, Form F>
 __device__ Plan make_plan(const CrossParams& p, int units, int64_t* pref, int64_t* scratch,
                           int* flags) {
   Plan pl;
@@ -163,7 +226,7 @@ __device__ Plan make_plan(const CrossParams& p, int units, int64_t* pref, int64_
     if (e < pl.entries) {
       const int b1 = min(p.B, (e + 1) * pl.group);
       for (int b = e * pl.group; b < b1; ++b) {
-        const Seq s = read_seq<false>(p, b, flags, &zero);
+        const Seq s = read_seq<false, F>(p, b, flags, &zero);
         descends |= __ldg(p.cu + b + 1) < s.cu0;
         mine += (int64_t)s.steps * s.ranges;
         longest = max(longest, s.steps);
@@ -194,6 +257,7 @@ struct Cursor {
 };
 
 // cursor at step g < total
+template <Form F>
 __device__ __forceinline__ Cursor locate(const CrossParams& p, const Plan& pl,
                                          const int64_t* pref, int64_t g) {
   int lo = 0, hi = pl.entries - 1, e = 0;
@@ -211,7 +275,7 @@ __device__ __forceinline__ Cursor locate(const CrossParams& p, const Plan& pl,
   int f = 0;
   bool z = false;
   for (c.b = e * pl.group; c.b < p.B; ++c.b) {
-    c.q = read_seq<false>(p, c.b, &f, &z);
+    c.q = read_seq<false, F>(p, c.b, &f, &z);
     const int64_t n = (int64_t)c.q.steps * c.q.ranges;
     if (at < n) break;
     at -= n;
@@ -222,6 +286,7 @@ __device__ __forceinline__ Cursor locate(const CrossParams& p, const Plan& pl,
 }
 
 // first step of the next range
+template <Form F>
 __device__ __forceinline__ void next_range(const CrossParams& p, Cursor& c) {
   c.s = 0;
   if (++c.r < c.q.ranges) return;
@@ -229,7 +294,7 @@ __device__ __forceinline__ void next_range(const CrossParams& p, Cursor& c) {
   int f = 0;
   bool z = false;
   while (++c.b < p.B) {
-    c.q = read_seq<false>(p, c.b, &f, &z);
+    c.q = read_seq<false, F>(p, c.b, &f, &z);
     if (c.q.ranges > 0) return;
   }
 }
@@ -238,12 +303,13 @@ __device__ __forceinline__ void next_range(const CrossParams& p, Cursor& c) {
 // behind the unit's run. The unit in whose run the range begins joins its pieces, and so do the
 // units that hold nothing else: unit number i of them takes the rows i, i + n, ... of n units.
 // rec[2w] = {pieces, first piece's slot, first query row, kv head}, rec[2w + 1] = {query rows, i}
+template <Form F>
 __device__ __forceinline__ void write_record(const CrossParams& p, const Plan& pl,
                                              const int64_t* pref, int64_t u, int sub, int4* rec) {
   const int64_t g0 = u * pl.W, g1 = min(pl.total, g0 + pl.W);
   int4 a = make_int4(0, 0, 0, 0), b = make_int4(0, 0, 0, 0);
   if (g0 < pl.total) {
-    const Cursor c = locate(p, pl, pref, g1 - 1);
+    const Cursor c = locate<F>(p, pl, pref, g1 - 1);
     const int64_t start = g1 - 1 - c.s, end = start + c.q.steps;
     if (end > g1) {
       const int64_t own = quotient(start, pl.W);
@@ -262,6 +328,27 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 __device__ __forceinline__ float inverse_of(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+// What a row is written with: out = o * own + prior * other, lse. Without a prior result other is 0.
+struct Weights {
+  float own, other, lse;
+};
+// m, l: maximum (log2 units) and sum of the row; kCausal joins the result of the keys that its
+// sequence shares with others, out_1 = o_1 / l_1 with lse_1 = ln(l_1 2^{m_1}):
+//   M = max(m, lse_1 log2 e), L = l 2^{m - M} + 2^{lse_1 log2 e - M}
+template <Form F>
+__device__ __forceinline__ Weights weights_of(const CrossParams& p, int64_t row, float m, float l) {
+  if constexpr (F == kCausal) {
+    if (p.prior_lse) {
+      const float before = __ldcg(p.prior_lse + row) * kLog2e, mine = l == 0.f ? -INFINITY : m;
+      const float top = fmaxf(mine, before), base = top == -INFINITY ? 0.f : top;
+      const float a = ex2(mine - base), b = ex2(before - base), all = l * a + b;
+      const float inv = inverse_of(all);
+      return {a * inv, b * inv, lse_of(top, all)};
+    }
+  }
+  return {inverse_of(l), 0.f, lse_of(m, l)};
+}
 
 }  // namespace cross
 }  // namespace pkv

@@ -80,8 +80,8 @@ struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr size_t kBytes = kEnd + 1024;
 };
 static_assert(Lay<128>::kBytes <= 232448, "shared memory over the limit");
-static_assert((3 * kEntries + kThreads + 48) * 8 <= Lay<64>::kStages * Lay<64>::kTile &&
-                  (3 * kEntries + kThreads + 48) * 8 <= Lay<128>::kStages * Lay<128>::kTile,
+static_assert((5 * kEntries + kThreads + 52) * 8 <= Lay<64>::kStages * Lay<64>::kTile &&
+                  (5 * kEntries + kThreads + 52) * 8 <= Lay<128>::kStages * Lay<128>::kTile,
               "plan fits the ring");
 
 // mbarriers
@@ -260,13 +260,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // This unit's part of a range: the tile under the cursor, steps [c.s, c.s + n).
 struct Part {
   int b, h, row0, pos, n, halves;   // first query row of the tile, its positions, steps, halves
+  int first_step, at;               // step of the range; position of the first row (kCausal)
+  Span span;                        // kCausal
   bool whole, shared;               // shared: one half of rows, both halves at work on it
   // half h works on steps first(h) + stride() * i, i < count(h)
   __device__ __forceinline__ bool active(int half) const { return shared || half < halves; }
   __device__ __forceinline__ int first(int half) const { return shared ? half : 0; }
   __device__ __forceinline__ int stride() const { return shared ? 2 : 1; }
   __device__ __forceinline__ int count(int half) const { return shared ? (n + 1 - half) / 2 : n; }
+  // first key of the i-th step of half h
+  __device__ __forceinline__ int key_of(int h, int i) const {
+    return span.key_step(first_step + first(h) + stride() * i) * kTileKeys;
+  }
 };
+// steps of the range that the cursor is in
+template <Form F>
+__device__ __forceinline__ int steps_of(const CrossParams& p, const Seq& q, int r) {
+  if constexpr (F == kCausal) return tile_span(p, q, r % (q.ranges / p.Hkv)).steps;
+  return q.steps;
+}
+template <Form F>
 __device__ __forceinline__ Part part_of(const CrossParams& p, const Cursor& c, int64_t left) {
   Part t;
   const int tiles = c.q.ranges / p.Hkv, q0 = (c.r % tiles) * p.tile_pos;
@@ -274,14 +287,22 @@ __device__ __forceinline__ Part part_of(const CrossParams& p, const Cursor& c, i
   t.h = c.r / tiles;
   t.row0 = c.q.cu0 + q0;
   t.pos = min(p.tile_pos, c.q.rows - q0);
-  t.n = (int)min((int64_t)(c.q.steps - c.s), left);
+  t.first_step = c.s;
+  t.span.ns = t.span.gap = t.at = 0;
+  t.span.steps = c.q.steps;
+  if (F == kCausal) {
+    t.at = c.q.at + q0;
+    t.span = tile_span(p, c.q, c.r % tiles);
+  }
+  t.n = (int)min((int64_t)(t.span.steps - c.s), left);
   t.halves = t.pos > p.tile_pos / 2 ? 2 : 1;
-  t.whole = c.s == 0 && t.n == c.q.steps;
+  t.whole = c.s == 0 && t.n == t.span.steps;
   t.shared = t.halves == 1 && t.n > 1;
   return t;
 }
 
 // n ranges on from the start of a range; the whole warp (32 sequences at a time)
+template <Form F>
 __device__ __forceinline__ void skip_ranges(const CrossParams& p, Cursor& c, int n) {
   const int lane = threadIdx.x & 31;
   c.s = 0;
@@ -291,7 +312,7 @@ __device__ __forceinline__ void skip_ranges(const CrossParams& p, Cursor& c, int
     bool z = false;
     const int b0 = c.b + 1;
     Seq q{};
-    if (b0 + lane < p.B) q = read_seq<true>(p, b0 + lane, &f, &z);
+    if (b0 + lane < p.B) q = read_seq<true, F>(p, b0 + lane, &f, &z);
     int upto = q.ranges;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -306,6 +327,8 @@ __device__ __forceinline__ void skip_ranges(const CrossParams& p, Cursor& c, int
     c.q.keys = __shfl_sync(0xffffffffu, q.keys, at);
     c.q.steps = __shfl_sync(0xffffffffu, q.steps, at);
     c.q.ranges = __shfl_sync(0xffffffffu, q.ranges, at);
+    if (F != kCross) c.q.at = __shfl_sync(0xffffffffu, q.at, at);
+    if (F == kCausal) c.q.lo = __shfl_sync(0xffffffffu, q.lo, at);
     c.b = b0 + at;
     if (c.b >= p.B) return;   // never: the tiles asked for exist
   }
@@ -313,20 +336,20 @@ __device__ __forceinline__ void skip_ranges(const CrossParams& p, Cursor& c, int
 
 // Walks the parts of a run; every role walks for itself. f gets the part, its cursor and its
 // number among the cut parts (-1: a whole tile).
-template <typename F>
-__device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, F f) {
+template <Form F, typename Fn>
+__device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, Fn f) {
   Cursor c = run.first;
   for (int i = run.whole; i > 0; --i) {
-    if (!f(part_of(p, c, c.q.steps), c, -1)) return;
-    if (i > 1) skip_ranges(p, c, p.tile_units);
+    if (!f(part_of<F>(p, c, INT_MAX), c, -1)) return;
+    if (i > 1) skip_ranges<F>(p, c, p.tile_units);
   }
   c = run.at;
   int64_t steps = run.steps;
   for (int i = 0; steps > 0; ++i) {
-    const Part t = part_of(p, c, steps);
+    const Part t = part_of<F>(p, c, steps);
     if (!f(t, c, i)) return;
     steps -= t.n;
-    if (steps > 0) skip_ranges(p, c, 1);
+    if (steps > 0) skip_ranges<F>(p, c, 1);
   }
 }
 
@@ -335,25 +358,34 @@ __device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, 
 // them; of the others (between one and two for each block, if there are as many) each block
 // gets a run of steps that evens out what it had before.
 // mem: [kEntries + 1] steps and tiles before an entry each, [kThreads + 1] cuts, scratch,
-// [kEntries] steps of an entry's tiles (the mean, where an entry holds several sequences).
+// [kEntries] steps of an entry's tiles (the mean, where an entry holds several sequences; kCausal,
+// whose tiles differ: those of one kv head), (kCausal) [kEntries] the entry's sequence.
+template <Form F>
 __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   int64_t *steps_at = mem, *tiles_at = steps_at + kEntries + 1, *cut = tiles_at + kEntries + 1,
           *scratch = cut + kThreads + 1;
   int* per_tile = reinterpret_cast<int*>(scratch + 32);
+  int4* about = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(per_tile + kEntries) + 15) &
+                                        ~static_cast<uintptr_t>(15));   // rows, keys, at, lo
   const int tid = threadIdx.x, units = p.tile_units;
   const int group = (p.B + kEntries - 1) / kEntries, entries = (p.B + group - 1) / group;
   int f = 0;
   bool z = false;
   int64_t total = 0, tiles = 0;
+  const auto steps_in = [&](const Seq& q) {   // of a sequence
+    return F == kCausal ? (int64_t)q.steps * (q.ranges > 0 ? p.Hkv : 0)
+                        : (int64_t)q.steps * q.ranges;
+  };
   for (int e0 = 0; e0 < entries; e0 += kThreads) {
     const int e = e0 + tid;
     int64_t s = 0, n = 0;
     if (e < entries) {
       const int b1 = min(p.B, (e + 1) * group);
       for (int b = e * group; b < b1; ++b) {
-        const Seq q = read_seq<true>(p, b, &f, &z);
-        s += (int64_t)q.steps * q.ranges;
+        const Seq q = read_seq<true, F>(p, b, &f, &z);
+        s += steps_in(q);
         n += q.ranges;
+        if (F == kCausal) about[e] = make_int4(q.rows, q.keys, q.at, q.lo);
       }
     }
     int64_t all_s, all_n;
@@ -362,7 +394,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     if (e < entries) {
       steps_at[e] = total + upto_s - s;
       tiles_at[e] = tiles + upto_n - n;
-      per_tile[e] = n > 0 ? (int)quotient(s, n) : 0;
+      per_tile[e] = n > 0 ? (int)quotient(s, F == kCausal && group == 1 ? p.Hkv : n) : 0;
     }
     total += all_s;
     tiles += all_n;
@@ -385,6 +417,17 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     }
     return e;
   };
+  // steps of tile k, which lies in entry e
+  const auto steps_at_tile = [&](int e, int64_t k) {
+    if (F != kCausal || group > 1) return per_tile[e];
+    Seq q{};
+    q.rows = about[e].x;
+    q.keys = about[e].y;
+    q.at = about[e].z;
+    q.lo = about[e].w;
+    const int tiles_h = (q.rows + p.tile_pos - 1) / p.tile_pos;
+    return tile_span(p, q, (int)(k - tiles_at[e]) % tiles_h).steps;
+  };
   // cursor at tile k, or (by_step) at step k; *before: steps before it
   const auto find = [&](int64_t k, bool by_step, int64_t* before) {
     const int64_t* at = by_step ? steps_at : tiles_at;
@@ -392,11 +435,27 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     int64_t left = k - at[e], s = steps_at[e];
     Cursor c{};
     for (c.b = e * group; c.b < p.B; ++c.b) {
-      c.q = read_seq<true>(p, c.b, &f, &z);
-      const int64_t n = by_step ? (int64_t)c.q.steps * c.q.ranges : c.q.ranges;
+      c.q = read_seq<true, F>(p, c.b, &f, &z);
+      const int64_t n = by_step ? steps_in(c.q) : c.q.ranges;
       if (left < n) break;
       left -= n;
-      s += (int64_t)c.q.steps * c.q.ranges;
+      s += steps_in(c.q);
+    }
+    if constexpr (F == kCausal) {   // c.q.steps: those of a kv head's tiles
+      const int tiles_h = max(c.q.ranges / p.Hkv, 1);
+      const int h = (int)(by_step ? quotient(left, max(c.q.steps, 1)) : left / tiles_h);
+      const int n = by_step ? (int)(left - (int64_t)h * c.q.steps) : 0;
+      const int last = by_step ? tiles_h - 1 : (int)(left - (int64_t)h * tiles_h);
+      int t = 0, upto = 0;
+      for (; t < last; ++t) {
+        const int x = tile_span(p, c.q, t).steps;
+        if (by_step && upto + x > n) break;
+        upto += x;
+      }
+      c.r = h * tiles_h + t;
+      c.s = by_step ? n - upto : 0;
+      *before = s + (int64_t)h * c.q.steps + upto + c.s;
+      return c;
     }
     c.r = by_step ? (int)quotient(left, max(c.q.steps, 1)) : (int)left;
     c.s = by_step ? (int)(left - (int64_t)c.r * c.q.steps) : 0;
@@ -407,7 +466,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   int64_t x, from = 0;
   if (whole > 0) {
     const int64_t k = whole * units;
-    if (group == 1) {
+    if (F != kCausal && group == 1) {
       const int e = entry(tiles_at, k);
       from = steps_at[e] + (k - tiles_at[e]) * per_tile[e];
     } else {
@@ -422,7 +481,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     int64_t had = i0 > 0 ? quotient(i0 * total, tiles) : 0, k = tid + i0 * units;
     for (int e = whole > 0 ? entry(tiles_at, k) : 0; k < whole * units; k += units) {
       while (tiles_at[e + 1] <= k) ++e;
-      had += per_tile[e];
+      had += steps_at_tile(e, k);
     }
     weight = whole > 0 ? max(share - had, (int64_t)1)
                        : tid < max(quotient(rest + kLeast - 1, kLeast), (int64_t)1);
@@ -439,7 +498,12 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   // much longer than an even share, the kv heads of a sequence are read in step: neighbouring
   // heads lie together in a cache row. (2 sequences of 100 queries, 16 heads of 64, 20000 to
   // 60000 keys: 80 us, cut at even shares 113 us.)
-  if (tiles <= units && entries <= 64 && p.Hkv > 1) {
+  // (kCausal: where every sequence is one tile.)
+  bool even = true;
+  if (F == kCausal)
+    for (int e = 0; e < min(entries, 65); ++e)
+      even = even && tiles_at[e + 1] - tiles_at[e] <= p.Hkv;
+  if (tiles <= units && entries <= 64 && p.Hkv > 1 && even) {
     // thread t tries pieces of at most lo + (hi - lo) * t / (kThreads - 1) steps
     const int lo = (int)max(share, (int64_t)kLeast), span = lo * 2 / 5;
     int need = 0;
@@ -484,11 +548,11 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     int4 a = make_int4(0, 0, 0, 0), b = make_int4(0, 0, 0, 0);
     if (c1 > c0) {
       const Cursor c = find(c1 - 1, true, &x);
-      const int64_t start = c1 - 1 - c.s, end = start + c.q.steps;
+      const int64_t start = c1 - 1 - c.s, end = start + steps_of<F>(p, c.q, c.r);
       if (start >= c0 && end > c1) {
         int v = u;
         while (v + 1 < units && cut[v + 1] < end) ++v;
-        const Part t = part_of(p, c, 1);
+        const Part t = part_of<F>(p, c, 1);
         a = make_int4(v - u + 1, start == c0 ? 0 : 1, t.row0, t.h);
         b.x = t.pos;
       }
@@ -511,7 +575,7 @@ __device__ __forceinline__ void load_box(void* dst, const void* map, int group, 
       : "memory");
 }
 
-template <typename T, int D>
+template <typename T, int D, Form F>
 __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char* sm,
                           int kv, const Run& run, const Wait& wait) {
   using L = Lay<D>;
@@ -590,7 +654,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       __syncwarp();
     }
   };
-  each_part(p, run, [&](const Part& t, const Cursor& c, int) {
+  each_part<F>(p, run, [&](const Part& t, const Cursor& c, int) {
     const int PT = p.tile_pos / 2;
     for (int h = 0; kv == 0 && h < (t.shared ? 2 : t.halves); ++h) {
       if (q_use[h] > 0 &&
@@ -607,23 +671,35 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
     }
     // R consecutive keys of a block to a lane (none when rows are copied one by one); the block
     // of the step ahead is on its way while a step is loaded
+    const int32_t* const table = p.table + (int64_t)(F == kShared ? c.q.at : t.b) * p.MB;
     const auto column = [&](int key) { return p.bs_shift >= 0 ? key >> p.bs_shift : key / p.BS; };
     const auto lookup = [&](int key) {
       int blk;
       asm volatile("ld.global.nc.b32 %0, [%1];\n"
                    : "=r"(blk)
-                   : "l"(p.table + (int64_t)t.b * p.MB + column(min(key, c.q.keys - 1))));
+                   : "l"(table + column(min(key, c.q.keys - 1))));
       return blk;
     };
-    int ahead = lookup(c.s * kTileKeys + lane * R);
+    // keys that some row of the sequence sees: those from `seen_from` on, and the sinks
+    const int seen_from = F == kCausal ? first_seen(p, c.q) : 0;
+    const int sinks = F == kCausal && p.window > 0 ? p.sinks : 0;
+    const auto seen_key = [&](int key) {
+      return key < c.q.keys && (F != kCausal || key >= seen_from || key < sinks);
+    };
+    const auto step_key = [&](int j) {   // first key of step j of the range
+      return (F == kCausal ? t.span.key_step(j) : j) * kTileKeys;
+    };
+    int ahead = lookup(step_key(c.s) + lane * R);
     for (int j = c.s; j < c.s + t.n; ++j, use += 2, ++issued) {
-      const int key0 = j * kTileKeys + lane * R;
-      const bool there = R > 0 && lane * R < kTileKeys && key0 < c.q.keys;
+      const int first = step_key(j), key0 = first + lane * R;
+      const bool there = R > 0 && lane * R < kTileKeys && key0 < c.q.keys &&
+                         (F != kCausal || key0 + R > seen_from || key0 < sinks);
       const bool mapped = there && ahead >= 0 && ahead < p.NB;
       const int row = ahead * p.BS + (key0 - column(key0) * p.BS);   // where mapped
       const uint32_t boxes = __ballot_sync(0xffffffffu, mapped);
-      const bool clear = R > 0 && (j + 1) * kTileKeys <= c.q.keys && boxes == every;
-      ahead = lookup(key0 + kTileKeys);
+      const bool clear = R > 0 && first + kTileKeys <= c.q.keys && boxes == every &&
+                         (F != kCausal || first >= seen_from || first + kTileKeys <= sinks);
+      ahead = lookup((F == kCausal ? step_key(j + 1) : first + kTileKeys) + lane * R);
       if (!room()) return false;
       unsigned char* dst = sm + L::kRing + to.stage * L::kTile;
       uint64_t* full = bars + kFull + to.stage;
@@ -637,18 +713,18 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       }
       if (there && !mapped) flags |= PKV_DEV_BAD_BLOCK;
       if (kv == 0) {
-        const int k0 = j * kTileKeys + 4 * lane;   // 4 keys of one block, if boxes are used
+        const int k0 = first + 4 * lane;   // 4 keys of one block, if boxes are used
         uint32_t words[4];
         if (R > 0) {
           const bool in = __shfl_sync(0xffffffffu, mapped ? 1 : 0, 4 * lane / R) != 0;
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            words[x] = __ballot_sync(0xffffffffu, in && k0 + x < c.q.keys);
+            words[x] = __ballot_sync(0xffffffffu, in && seen_key(k0 + x));
         } else {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int blk = lookup(k0 + x);
-            words[x] = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.NB && k0 + x < c.q.keys);
+            words[x] = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.NB && seen_key(k0 + x));
           }
         }
 #pragma unroll
@@ -657,18 +733,19 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       }
       {
         // key rows behind the last key may stay what they are: their scores are masked
-        const bool whole = mapped && key0 + R <= c.q.keys;
+        const bool whole = mapped && key0 + R <= c.q.keys &&
+                           (F != kCausal || key0 >= seen_from || key0 + R <= sinks);
         const uint32_t copy = __ballot_sync(0xffffffffu, kv == 0 ? mapped : whole);
         const T* src = static_cast<const T*>(kv == 0 ? p.kc : p.vc);
         bool rows = false;   // rows copied one by one
         if (R == 0) {
           rows = true;
           for (int r = 0; r < kTileKeys; ++r) {
-            const int key = j * kTileKeys + r;
+            const int key = first + r;
             int64_t at = -1;
-            if (key < c.q.keys) {
+            if (seen_key(key)) {
               const int col = p.bs_shift >= 0 ? key >> p.bs_shift : key / p.BS;
-              const int blk = __ldg(p.table + (int64_t)t.b * p.MB + col);
+              const int blk = __ldg(table + col);
               if (blk >= 0 && blk < p.NB)
                 at = (((int64_t)blk * p.BS + (key - col * p.BS)) * p.Hkv + t.h) * D;
               else
@@ -688,7 +765,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
             const int mapped_i = __shfl_sync(0xffffffffu, mapped ? 1 : 0, i);
             for (int x = lane; x < R * (D / 8); x += 32) {
               const int r = x / (D / 8), ch = x % (D / 8);
-              const bool live = mapped_i && j * kTileKeys + i * R + r < c.q.keys;
+              const bool live = mapped_i && seen_key(first + i * R + r);
               const int64_t at = live ? ((int64_t)(row_i + r) * p.Hkv + t.h) * D + ch * 8 : 0;
               const int k = i * R + r;
               cp_async_16(dst + (k >> 3) * L::kGroup + (ch >> 3) * 1024 + tc::sw128(k & 7, ch & 7),
@@ -719,7 +796,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
 }
 
 // ---------------------------------------------------------------------------- products
-template <typename T, int D>
+template <typename T, int D, Form F>
 __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, const Run& run,
                          const Wait& wait) {
   using L = Lay<D>;
@@ -742,7 +819,7 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
     if (half == 0) return n == 0 || ready(kTurn, (n - 1) & 1u);
     return ready(kTurn + 1, n & 1u);
   };
-  each_part(p, run, [&](const Part& t, const Cursor&, int) {
+  each_part<F>(p, run, [&](const Part& t, const Cursor&, int) {
     Place<L::kStages> k = next, v = next;   // K of step j is 2 j tiles on, V 2 j + 1
     next.step(2 * t.n);
     if (!t.active(half)) return true;
@@ -827,7 +904,13 @@ __device__ void mma_role(const CrossParams& p, unsigned char* sm, int half, cons
 }
 
 // ---------------------------------------------------------------------------- softmax
-template <typename T, int D>
+// Of the keys 4 i + x of a step those below n, as bit i.
+__device__ __forceinline__ uint32_t below(int n, int x) {
+  const int bits = (n + 3 - x) >> 2;
+  return bits >= 32 ? 0xffffffffu : bits <= 0 ? 0u : (1u << bits) - 1u;
+}
+
+template <typename T, int D, Form F>
 __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run& run,
                              const Wait& wait) {
   using L = Lay<D>;
@@ -847,7 +930,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     __syncwarp();
     if (lane == 0) arrive(bars + bar + half);
   };
-  each_part(p, run, [&](const Part& t, const Cursor&, int index) {
+  each_part<F>(p, run, [&](const Part& t, const Cursor&, int index) {
     uint32_t k = use + 2 * t.first(half);   // ring tile of this half's K; V is k + 1
     Place<L::kStages> tile = next;          // the next tile to be given back: K, V, K, V ...
     use += 2 * t.n;
@@ -866,6 +949,9 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     };
     float m = -INFINITY, l = 0.f;
     const int n = t.count(half);
+    // kCausal: the row's position; it sees keys behind row_from
+    const int row_at = t.at + (t.shared ? 0 : half * (p.tile_pos / 2)) + r / p.G;
+    const int row_from = p.window > 0 ? row_at - p.window : -1;
     for (int j = 0; j < n; ++j, k += apart) {
       // the loads and stores of TMEM below are the whole warp's
       if (!wait.warp(kSFull + half, s_use & 1u)) return false;
@@ -881,7 +967,17 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld32_max(s_at + x * 32, v32[x], e[x]);
       }
-      const uint4 seen = *reinterpret_cast<const uint4*>(sm + L::kSeen + (k / 2 % kMasks) * 16);
+      uint4 seen = *reinterpret_cast<const uint4*>(sm + L::kSeen + (k / 2 % kMasks) * 16);
+      if constexpr (F == kCausal) {
+        const int k0 = t.key_of(half, j);
+        if (k0 + kTileKeys - 1 > row_at || k0 <= row_from) {   // not all of the step's
+          const int upto = row_at + 1 - k0, gone = row_from + 1 - k0, kept = p.sinks - k0;
+          seen.x &= below(upto, 0) & (~below(gone, 0) | below(kept, 0));
+          seen.y &= below(upto, 1) & (~below(gone, 1) | below(kept, 1));
+          seen.z &= below(upto, 2) & (~below(gone, 2) | below(kept, 2));
+          seen.w &= below(upto, 3) & (~below(gone, 3) | below(kept, 3));
+        }
+      }
       tc::tmem_wait_ld();
       const bool masked = (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu;
       if (masked || p.scale_log2 < 0.f) {   // the maximum is another one
@@ -982,23 +1078,46 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     const int pos = half * (p.tile_pos / 2) + r / p.G;
     const bool mine = r < (p.tile_pos / 2) * p.G && pos < t.pos;
     if (t.whole) {
-      const float inv = inverse_of(l);
       const int64_t row = (int64_t)(t.row0 + pos) * p.Hq + t.h * p.G + r % p.G;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D);
+      Weights w{0.f, 0.f, 0.f};
+      if (mine) w = weights_of<F>(p, row, m, l);
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         float o[32];
         result(x, o);
         if (mine) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            out[x * 4 + y] = make_uint4(Num<T>::pack(o[y * 8] * inv, o[y * 8 + 1] * inv),
-                                        Num<T>::pack(o[y * 8 + 2] * inv, o[y * 8 + 3] * inv),
-                                        Num<T>::pack(o[y * 8 + 4] * inv, o[y * 8 + 5] * inv),
-                                        Num<T>::pack(o[y * 8 + 6] * inv, o[y * 8 + 7] * inv));
+          for (int y = 0; y < 32; ++y) o[y] *= w.own;
+          if constexpr (F == kCausal) {
+            if (w.other > 0.f) {
+              const float4* prior = reinterpret_cast<const float4*>(p.prior_o + row * D) + x * 8;
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const float4 z = __ldcg(prior + y);
+                o[4 * y] += w.other * z.x;
+                o[4 * y + 1] += w.other * z.y;
+                o[4 * y + 2] += w.other * z.z;
+                o[4 * y + 3] += w.other * z.w;
+              }
+            }
+          }
+          if constexpr (F == kShared) {
+            float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D) + x * 8;
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              out[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          } else {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D) + x * 4;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              out[y] = make_uint4(Num<T>::pack(o[y * 8], o[y * 8 + 1]),
+                                  Num<T>::pack(o[y * 8 + 2], o[y * 8 + 3]),
+                                  Num<T>::pack(o[y * 8 + 4], o[y * 8 + 5]),
+                                  Num<T>::pack(o[y * 8 + 6], o[y * 8 + 7]));
+          }
         }
       }
-      if (mine && p.lse) p.lse[row] = lse_of(m, l);
+      if (mine && p.lse) p.lse[row] = w.lse;
     } else {
       const int64_t row = (2 * (int64_t)blockIdx.x + (index == 0 ? 0 : 1)) * 256 + half * 128 + r;
       float4* out = reinterpret_cast<float4*>(p.tile_o + row * D);
@@ -1026,7 +1145,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
   });
 }
 
-template <typename T, int D>
+template <typename T, int D, Form F>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_tiles_kernel(CrossParams p, const __grid_constant__ Maps maps) {
   using L = Lay<D>;
@@ -1072,7 +1191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   // in the ring's memory before the ring is used; the other kernel reports bad sequences
-  plan_tiles(p, reinterpret_cast<int64_t*>(sm + L::kRing), run);
+  plan_tiles<F>(p, reinterpret_cast<int64_t*>(sm + L::kRing), run);
   tc::fence_async_shared();
   tc::fence_before_sync();
   __syncthreads();
@@ -1082,13 +1201,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (run->whole > 0 || run->steps > 0) {
     if (warp < kSoftmaxWarps) {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
-      softmax_role<T, D>(p, sm, *run, wait);
+      softmax_role<T, D, F>(p, sm, *run, wait);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
       if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 2)
-        mma_role<T, D>(p, sm, (warp - kSoftmaxWarps) / 2, *run, wait);
+        mma_role<T, D, F>(p, sm, (warp - kSoftmaxWarps) / 2, *run, wait);
       else
-        load_role<T, D>(p, maps, sm, warp == kSoftmaxWarps + 1 ? 0 : 1, *run, wait);
+        load_role<T, D, F>(p, maps, sm, warp == kSoftmaxWarps + 1 ? 0 : 1, *run, wait);
     }
   }
   cp_async_wait<0>();
@@ -1140,16 +1259,16 @@ bool encode_pool(CUtensorMap* m, const CrossParams& p, const void* base) {
   return encode(m, p.bf16, base, 5, dims, strides, box);
 }
 
-template <typename T, int D>
+template <typename T, int D, Form F>
 cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
   int dev = -1;
   if (needs_configure(configured, &dev)) {
     cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, cross_tiles_kernel<T, D>);
+    cudaError_t e = cudaFuncGetAttributes(&at, cross_tiles_kernel<T, D, F>);
     if (e != cudaSuccess) return e;
     if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;   // the split would not fit
-    e = cudaFuncSetAttribute(cross_tiles_kernel<T, D>,
+    e = cudaFuncSetAttribute(cross_tiles_kernel<T, D, F>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<D>::kBytes);
     if (e != cudaSuccess) return e;
     mark_configured(configured, dev);
@@ -1159,18 +1278,19 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   maps.k = maps.v = maps.q;   // not used without boxes
   if (p.box_keys > 0 && (!encode_pool(&maps.k, p, p.kc) || !encode_pool(&maps.v, p, p.vc)))
     return cudaErrorInvalidValue;
-  ProfScope ps("cross_tiles", s);
-  cross_tiles_kernel<T, D><<<p.tile_units, kThreads, Lay<D>::kBytes, s>>>(p, maps);
+  ProfScope ps(F == kCross ? "cross_tiles" : F == kShared ? "prefix_tiles" : "window_tiles", s);
+  cross_tiles_kernel<T, D, F><<<p.tile_units, kThreads, Lay<D>::kBytes, s>>>(p, maps);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cross_tiles(const CrossParams& p, cudaStream_t s) {
+cudaError_t PKV_LAUNCH(_tiles)(const CrossParams& p, cudaStream_t s) {
   if (p.bf16)
-    return p.D == 64 ? launch_typed<__nv_bfloat16, 64>(p, s)
-                     : launch_typed<__nv_bfloat16, 128>(p, s);
-  return p.D == 64 ? launch_typed<__half, 64>(p, s) : launch_typed<__half, 128>(p, s);
+    return p.D == 64 ? launch_typed<__nv_bfloat16, 64, PKV_FORM>(p, s)
+                     : launch_typed<__nv_bfloat16, 128, PKV_FORM>(p, s);
+  return p.D == 64 ? launch_typed<__half, 64, PKV_FORM>(p, s)
+                   : launch_typed<__half, 128, PKV_FORM>(p, s);
 }
 
 }  // namespace pkv

@@ -104,6 +104,12 @@ struct CrossParams {
   const int32_t* past;
   int window;                // keys that a row sees, 0: all
   int sinks;                 // first keys that stay visible
+  // behind a shared prefix (NULL without): keys of a sequence that its group computes
+  const int32_t* start;      // [B]
+  const float* prior_o;      // [T][Hq][D] what the shared keys gave, and its lse [T][Hq]
+  const float* prior_lse;
+  // the shared keys' own call: B groups; row of the block table of each
+  const int32_t* table_row;  // [B]
   // plan (cross_dev.cuh)
   int few;                   // query rows of a sequence that the kernel for few rows takes
   int tile_pos;              // query positions of a tile of the kernel for many rows
@@ -128,9 +134,12 @@ struct CrossParams {
 // fills the plan fields and the workspace pointers (from base, which may be NULL); returns
 // the workspace bytes
 size_t cross_layout(CrossParams* p, char* base);
+// the kernels of the three forms (cross_dev.cuh) and, of each, the one for many rows (*_tiles.cu)
 cudaError_t launch_cross(const CrossParams& p, cudaStream_t s);
-cudaError_t launch_window(const CrossParams& p, cudaStream_t s);
-// kernel for many rows (cross_tiles.cu)
+cudaError_t launch_shared(const CrossParams& p, cudaStream_t s);
+cudaError_t launch_causal(const CrossParams& p, cudaStream_t s);
 cudaError_t launch_cross_tiles(const CrossParams& p, cudaStream_t s);
+cudaError_t launch_shared_tiles(const CrossParams& p, cudaStream_t s);
+cudaError_t launch_causal_tiles(const CrossParams& p, cudaStream_t s);
 
 }  // namespace pkv

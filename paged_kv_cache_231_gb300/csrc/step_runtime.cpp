@@ -344,7 +344,7 @@ int pkv_paged_window_attention_workspace_size(const pkv_window_attention_args* a
   CrossParams p{};
   const int st = check_window(args, &p);
   if (st != PKV_OK) return st;
-  *bytes = 0;
+  *bytes = cross_layout(&p, nullptr);
   return PKV_OK;
 }
 
@@ -355,7 +355,10 @@ int pkv_paged_window_attention(const pkv_window_attention_args* args, void* work
   if (st != PKV_OK) return st;
   if (args->num_tokens == 0) return PKV_OK;
   if (args->output == args->query) return PKV_ERR_SHAPE;
-  return status_of(launch_window(p, static_cast<cudaStream_t>(stream)));
+  const size_t need = cross_layout(&p, static_cast<char*>(workspace));
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return PKV_ERR_WORKSPACE;
+  return status_of(launch_causal(p, static_cast<cudaStream_t>(stream)));
 }
 
 int pkv_paged_prefix_attention_workspace_size(const pkv_prefix_attention_args* args,
@@ -364,7 +367,7 @@ int pkv_paged_prefix_attention_workspace_size(const pkv_prefix_attention_args* a
   CrossParams p{};
   const int st = check_prefix(args, &p);
   if (st != PKV_OK) return st;
-  *bytes = 0;
+  *bytes = cross_layout(&p, nullptr);
   return PKV_OK;
 }
 
@@ -375,7 +378,10 @@ int pkv_paged_prefix_attention(const pkv_prefix_attention_args* args, void* work
   if (st != PKV_OK) return st;
   if (args->num_tokens == 0) return PKV_OK;
   if (args->output == args->query) return PKV_ERR_SHAPE;
-  return status_of(launch_window(p, static_cast<cudaStream_t>(stream)));
+  const size_t need = cross_layout(&p, static_cast<char*>(workspace));
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return PKV_ERR_WORKSPACE;
+  return status_of(launch_causal(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -103,9 +103,9 @@ def test_bad_sequences(nq):
     c.check(max_query_len=nq)
     out, lse, status = c.gpu(max_query_len=nq - 1)
     assert status == B.DEV_BAD_SEQUENCE and not out.any()
-    c.past[2] = 2 ** 31 - 1                                    # past + rows passes 32 bits
-    out, lse, status = c.gpu()
-    assert status == B.DEV_BAD_BLOCK
+    for past in (2 ** 31 - 1, c.table.shape[1] * c.bs + 1):
+        c.past[2] = past
+        c.check(status=B.DEV_BAD_SEQUENCE)
 
 
 @pytest.mark.parametrize("spread,scale", [(4.0, 0.0), (1.0, 0.5), (1.0, -0.25), (0.0, 0.0)])
@@ -158,8 +158,8 @@ def test_captured_and_replayed():
     c.past = [300, 0, 7]
     g.replay()
     torch.cuda.synchronize()
-    again, _, _ = c.gpu()
-    assert torch.equal(out.cpu(), again)
+    again, _, _ = c.gpu()             # one row sees cache rows of NaN now: compared bit by bit
+    assert torch.equal(out.cpu().view(torch.int16), again.view(torch.int16))
 
 
 def test_other_stream():
