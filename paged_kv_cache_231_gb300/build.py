@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["runtime.cpp", "attention.cu", "scatter.cu", "combine.cu", "sparse.cu",
            "sparse16.cu", "static_workspace.cu", "step_runtime.cpp", "schedule.cu",
            "append_axes.cu", "cross.cu", "cross_tiles.cu", "append_norm.cu", "fork.cu",
-           "window.cu", "window_tiles.cu"]
+           "window.cu", "window_tiles.cu", "prefix.cu", "prefix_tiles.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -131,6 +131,20 @@ struct CrossParams {
   float* tile_m;
   float* tile_l;
 };
+struct PrefixParams {
+  const int32_t* offsets;    // [groups + 1]
+  const int32_t* shared;     // [groups] keys that the caller says they share
+  int groups;
+  // workspace, written by the plan
+  int32_t* start;            // [B] keys that are computed for the sequence's group
+  int32_t* group_cu;         // [groups + 1] query rows
+  int32_t* group_keys;       // [groups]
+  int32_t* table_row;        // [groups]
+};
+// the parameters of both calls from those of the second (its query, cache and sizes); the bytes
+size_t prefix_layout(CrossParams* shared, CrossParams* own, PrefixParams* x, char* base);
+cudaError_t launch_prefix(const CrossParams& shared, const CrossParams& own, const PrefixParams& x,
+                          cudaStream_t s);
 // fills the plan fields and the workspace pointers (from base, which may be NULL); returns
 // the workspace bytes
 size_t cross_layout(CrossParams* p, char* base);

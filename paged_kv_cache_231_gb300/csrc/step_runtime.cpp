@@ -90,10 +90,13 @@ int check_window(const pkv_window_attention_args* a, CrossParams* p) {
   return check_attention(a, a->past_seqlens, p);
 }
 
-int check_prefix(const pkv_prefix_attention_args* a, CrossParams* p) {
+int check_prefix(const pkv_prefix_attention_args* a, CrossParams* p, PrefixParams* x) {
   if (!a) return PKV_ERR_NULL;
   if (a->num_groups < 0) return PKV_ERR_SHAPE;
-  if (a->num_groups > a->batch) return PKV_ERR_UNSUPPORTED;
+  if (a->num_groups > kMax32 / 2) return PKV_ERR_UNSUPPORTED;
+  x->groups = (int)a->num_groups;
+  x->offsets = a->group_offsets;
+  x->shared = a->shared_seqlens;
   p->past = a->past_seqlens;
   const int st = check_attention(a, a->past_seqlens, p);
   if (st != PKV_OK || a->num_tokens == 0) return st;
@@ -364,24 +367,25 @@ int pkv_paged_window_attention(const pkv_window_attention_args* args, void* work
 int pkv_paged_prefix_attention_workspace_size(const pkv_prefix_attention_args* args,
                                               size_t* bytes) {
   if (!bytes) return PKV_ERR_NULL;
-  CrossParams p{};
-  const int st = check_prefix(args, &p);
+  CrossParams p{}, shared{};
+  PrefixParams x{};
+  const int st = check_prefix(args, &p, &x);
   if (st != PKV_OK) return st;
-  *bytes = cross_layout(&p, nullptr);
+  *bytes = prefix_layout(&shared, &p, &x, nullptr);
   return PKV_OK;
 }
 
 int pkv_paged_prefix_attention(const pkv_prefix_attention_args* args, void* workspace,
                                size_t workspace_bytes, void* stream) {
-  CrossParams p{};
-  const int st = check_prefix(args, &p);
+  CrossParams p{}, shared{};
+  PrefixParams x{};
+  const int st = check_prefix(args, &p, &x);
   if (st != PKV_OK) return st;
   if (args->num_tokens == 0) return PKV_OK;
   if (args->output == args->query) return PKV_ERR_SHAPE;
-  const size_t need = cross_layout(&p, static_cast<char*>(workspace));
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
-    return PKV_ERR_WORKSPACE;
-  return status_of(launch_causal(p, static_cast<cudaStream_t>(stream)));
+  const size_t need = prefix_layout(&shared, &p, &x, static_cast<char*>(workspace));
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return PKV_ERR_WORKSPACE;
+  return status_of(launch_prefix(shared, p, x, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,136 @@
+"""GPU parity of pkv_paged_prefix_attention: the causal attention of every row over its own
+table row, whatever is said to be shared."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_231_gb300 import binding as B
+
+from .cache_util import CausalCase
+from .step_util import DEV, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def case(seed, nq, own, groups, **kw):
+    """own: tokens of each sequence behind what its group shares."""
+    past, at = [], 0
+    for n, keys in groups:
+        past += [keys + own[at + i] for i in range(n)]
+        at += n
+    past += own[at:]
+    return CausalCase(seed, nq, past, groups=groups, **kw)
+
+
+@pytest.mark.parametrize("head_size,dtype,heads,kv", [(64, "f16", 4, 2), (128, "bf16", 8, 2),
+                                                      (64, "bf16", 3, 1), (128, "f16", 4, 4)])
+@pytest.mark.parametrize("shared", [16, 64, 144, 640])
+def test_single_tokens(head_size, dtype, heads, kv, shared):
+    case(1, [1] * 7, [0, 1, 5, 40, 17, 130, 9], [(7, shared)], head_size=head_size, dtype=dtype,
+         num_heads=heads, kv_heads=kv).check(prefix=True, max_query_len=1)
+
+
+@pytest.mark.parametrize("width", [1, 2, 3, 40, 100])
+@pytest.mark.parametrize("heads", [1, 4])
+def test_widths(width, heads):
+    rng = np.random.default_rng(2)
+    case(2, [1] * width, [int(x) for x in rng.integers(0, 50, width)], [(width, 160)],
+         num_heads=heads, kv_heads=1).check(prefix=True)
+
+
+@pytest.mark.parametrize("head_size,dtype,heads,kv", [(64, "f16", 4, 2), (128, "bf16", 8, 2),
+                                                      (64, "bf16", 3, 1), (128, "f16", 4, 4)])
+@pytest.mark.parametrize("block_size", [8, 24, 32])
+def test_prompts_and_groups(head_size, dtype, heads, kv, block_size):
+    n = block_size
+    case(3, [30, 1, 0, 90, 64, 2, 7, 1, 200], [0, 3, 10, 50, 0, 200, 9, 100, 64],
+         [(3, 10 * n), (1, 4 * n), (0, 5 * n), (4, 20 * n)], head_size=head_size, dtype=dtype,
+         num_heads=heads, kv_heads=kv, block_size=block_size).check(prefix=True)
+
+
+def test_what_is_shared_is_cut():
+    # more than a sequence's past, than its table; nothing; groups that leave sequences out
+    c = case(4, [1, 4, 1, 30, 1], [0, 7, 50, 2, 1], [(3, 64), (2, 320)])
+    ref = c.oracle()
+    for shared in ([64, 320], [32, 16], [0, 0], [1, 17], [63, 319], [48, 0]):
+        c.check(prefix=True, shared=shared, reference=ref)
+    c.check(prefix=True, groups=[1, 3], shared=[64], reference=ref)
+    c.check(prefix=True, groups=[3, 5], shared=[256], reference=ref)
+    c.check(prefix=True, groups=[0], shared=[], reference=ref)
+    # a sequence of the group has a shorter past than the others share (its past ends with the
+    # last block that all three have: with 33 the key behind it would not be shared)
+    c = CausalCase(5, [1, 5, 1], [100, 32, 200], groups=[(3, 32)])
+    c.check(prefix=True, shared=[400])
+    c = CausalCase(6, [2, 2], [0, 0], groups=[(2, 0)])
+    c.check(prefix=True, shared=[50])
+
+
+def test_bad_groups():
+    c = case(7, [1, 4, 1, 30, 1], [0, 7, 50, 2, 1], [(3, 64), (2, 320)])
+    ref = c.oracle()
+    for groups, shared in (([0, 3, 6], [64, 320]), ([-1, 3, 5], [64, 320]), ([0, 3, 2], [64, 320]),
+                           ([3, 0, 5], [64, 64])):
+        c.check(prefix=True, groups=groups, shared=shared, status=B.DEV_BAD_SEQUENCE, reference=ref)
+    c.check(prefix=True, shared=[-1, 320], status=B.DEV_BAD_SEQUENCE, reference=ref)
+
+
+def test_bad_sequences():
+    for past in (-1, -2 ** 31):
+        c = case(8, [1, 4, 1, 30, 1], [0, 7, 50, 2, 1], [(3, 64), (2, 320)], pad=2)
+        c.past[1] = past
+        out, lse = c.check(prefix=True, status=B.DEV_BAD_SEQUENCE)
+        assert not out[1:5].any() and torch.isneginf(lse[-2:]).all()
+    c = case(9, [1, 4, 1, 30, 1], [0, 7, 50, 2, 1], [(3, 64), (2, 320)])
+    c.check(prefix=True, max_query_len=29, status=B.DEV_BAD_SEQUENCE)
+
+
+def test_holes():
+    c = case(10, [1, 4, 1, 40], [0, 7, 50, 2], [(4, 160)], block_size=16)
+    c.table[:, 3] = -1                       # shared by all
+    c.table[2, 11] = 10 ** 6                 # one row's own
+    c.check(prefix=True, status=B.DEV_BAD_BLOCK)
+    c = CausalCase(11, [1, 1], [64, 64], groups=[(2, 64)], block_size=16)
+    c.table[:, :4] = -1
+    c.table[1, 4] = -1                       # nothing is left for the second row
+    out, lse = c.check(prefix=True, status=B.DEV_BAD_BLOCK)
+    assert not out[1].any() and torch.isneginf(lse[1]).all()
+
+
+@pytest.mark.parametrize("scale,spread", [(0.0, 4.0), (-0.5, 1.0), (1.0, 1.0)])
+def test_scores(scale, spread):
+    case(12, [1] * 20 + [50], list(range(20)) + [9], [(21, 256)], scale=scale, spread=spread,
+         head_size=128, dtype="bf16").check(prefix=True)
+
+
+def test_many_groups():
+    rng = np.random.default_rng(13)
+    groups = [(int(n), 16 * int(k)) for n, k in zip(rng.integers(0, 6, 400),
+                                                   rng.integers(0, 6, 400))]
+    rows = sum(n for n, _ in groups)
+    case(13, [int(x) for x in rng.choice([0, 1, 1, 2, 20], rows)],
+         [int(x) for x in rng.integers(0, 40, rows)], groups, num_heads=2,
+         kv_heads=1).check(prefix=True)
+
+
+def test_equal_bits_and_graph():
+    c = case(14, [1] * 30 + [70], list(range(30)) + [200], [(31, 512)], head_size=128)
+    want, wlse, _ = c.gpu(prefix=True)
+    again, alse, _ = c.gpu(prefix=True)
+    assert torch.equal(want, again) and torch.equal(wlse, alse)
+    a = c.device() + [i32(c.groups), i32(c.shared)]
+    out = torch.zeros_like(a[0])
+    kw = dict(num_heads=c.hq, kv_num_heads=c.hkv, output=out)
+    B.pkv_paged_prefix_attention(*a, **kw)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.pkv_paged_prefix_attention(*a, **kw)
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want)
+    s = torch.cuda.Stream()
+    other = B.pkv_paged_prefix_attention(*a, num_heads=c.hq, kv_num_heads=c.hkv, stream=s)
+    s.synchronize()
+    assert torch.equal(other.cpu(), want)
