@@ -26,7 +26,7 @@ using append::read_token;
 using append::report;
 using elem::Num;
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 384;   // two blocks of 85 registers a thread to an SM
 constexpr int kFill = 256;   // threads that tokens side by side fill
 
 __device__ __forceinline__ float weight_at(const void* w, bool f32, bool bf16, int i) {
@@ -38,13 +38,14 @@ __device__ __forceinline__ float weight_at(const void* w, bool f32, bool bf16, i
 // tokens: tokens of a block side by side, N times as many a group; heads: heads of a token that
 // this block works on (blockIdx.y: which).
 template <typename T, typename TT, int D, bool kSide, int N>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, 2)
     append_norm_kernel(const __grid_constant__ NormParams np, int tokens, int heads) {
   constexpr int kLanes = D / 16;
   const AxesParams& p = np.axes;
   // [2][N * tokens][4][R / 16] (cos, cos, sin, sin) of pairs 2 y and 2 y + 1 of item c at [y][c], so
   // that neighbouring lanes read neighbouring words; then (slot, flags) of each token, twice
   extern __shared__ __align__(16) float4 turn[];
+  __shared__ __align__(16) float s_weight[2][D];   // of queries and of keys
   const int half = p.R / 2, per_head = p.R / 16, group = N * tokens;
   const int words = group * per_head * 4;
   int2* about = reinterpret_cast<int2*>(turn + 2 * words);
@@ -105,11 +106,10 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
   for (int n = 0; n < N; ++n) x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
   load(g, x);
-  float wt[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    wt[e] = normed && mine ? weight_at(weight, np.weight_f32, p.bf16, chunk[e / 8] * 8 + e % 8)
-                           : 1.f;
+  for (int e = threadIdx.x; e < 2 * D; e += blockDim.x) {
+    const void* from = e < D ? np.qw : np.kw;
+    s_weight[e / D][e % D] = from ? weight_at(from, np.weight_f32, p.bf16, e % D) : 1.f;
+  }
   gather(g, 0);
   __syncthreads();
   for (int buf = 0; g < groups; g += gridDim.x, buf ^= 1) {
@@ -139,7 +139,14 @@ __global__ void __launch_bounds__(kMaxThreads)
         if (normed) {
           const float by = rsqrtf(sum * (1.f / D) + np.epsilon);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] *= by * wt[e];
+          for (int e = 0; e < 4; ++e) {
+            const float4 w4 =
+                *reinterpret_cast<const float4*>(s_weight[kind] + chunk[e / 2] * 8 + e % 2 * 4);
+            v[4 * e] *= by * w4.x;
+            v[4 * e + 1] *= by * w4.y;
+            v[4 * e + 2] *= by * w4.z;
+            v[4 * e + 3] *= by * w4.w;
+          }
         }
         if (turns && (k.y & 1)) {
           const float4* cs = turn + buf * words + tok * 4 * per_head + c;
@@ -256,7 +263,7 @@ void launch_lanes(const NormParams& np, cudaStream_t s) {
     append_norm_kernel<T, TT, D, kSide, N><<<grid, threads, smem, s>>>(np, tokens, heads);
   };
   if (p.T >= 4 * tokens * sms)
-    run(std::integral_constant<int, 2>(), 96);
+    run(std::integral_constant<int, 2>(), 80);
   else
     run(std::integral_constant<int, 1>(), 80);
 }

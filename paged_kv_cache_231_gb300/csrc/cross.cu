@@ -30,7 +30,7 @@ constexpr int kLeastTile = 2;   // steps of a run of the other kernel, at least
 
 template <int D>
 __device__ __forceinline__ Span few_span(const CrossParams& p, const Seq& q) {
-  return span_of<few_keys(D)>(p, q, q.at, q.at + q.rows - 1);
+  return span_of<few_keys(D)>(p, q, q.at, q.at + q.rows - 1, 1);
 }
 
 template <int D>
@@ -44,9 +44,8 @@ template <int D, Form F>
 __device__ __forceinline__ int64_t key_offset(const CrossParams& p, const Cursor& c, int h, int lane,
                                               int& flags) {
   constexpr int K = few_keys(D);
-  int s = c.s;
-  if (F == kCausal) s = few_span<D>(p, c.q).key_step(s);
-  const int j = s * K + lane;
+  int j = c.s * K + lane;
+  if (F == kCausal) j = few_span<D>(p, c.q).key_at(j);
   if (lane >= K || j >= c.q.keys) return -1;
   if (F == kCausal && j < first_seen(p, c.q) && (p.window == 0 || j >= p.sinks)) return -1;
   const int col = p.bs_shift >= 0 ? j >> p.bs_shift : j / p.BS;
@@ -390,20 +389,21 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
         }
       if constexpr (F == kCausal) {
         // keys that some rows see and others do not; `live` has told of those that none sees
-        const int k0 = few_span<D>(p, cc.q).key_step(cc.s) * K;
-        const int last = cc.q.at + cc.q.rows - 1;
-        if (cc.q.rows > 1 && (k0 + K - 1 > cc.q.at || (p.window > 0 && k0 <= last - p.window))) {
+        if (cc.q.rows > 1) {
+          const int gap = few_span<D>(p, cc.q).gap, k0 = cc.s * K, at = cc.q.at - gap;
+          if (k0 + K - 1 > at || (p.window > 0 && k0 <= at + cc.q.rows - 1 - p.window)) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int pos = cc.q.at + ((lane >> 2) + 8 * x) / p.G;
-            const int from = p.window > 0 ? pos - p.window : -1;   // sees keys behind it
+            for (int x = 0; x < 2; ++x) {
+              const int pos = at + ((lane >> 2) + 8 * x) / p.G;
+              const int from = p.window > 0 ? pos - p.window : -1 - gap;   // sees keys behind it
 #pragma unroll
-            for (int n = 0; n < K / 8; ++n)
+              for (int n = 0; n < K / 8; ++n)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int key = k0 + n * 8 + 2 * t4 + e;
-                if (key > pos || (key <= from && key >= p.sinks)) s[n][2 * x + e] = -INFINITY;
-              }
+                for (int e = 0; e < 2; ++e) {
+                  const int key = k0 + n * 8 + 2 * t4 + e;
+                  if (key > pos || (key <= from && key >= p.sinks)) s[n][2 * x + e] = -INFINITY;
+                }
+            }
           }
         }
       }

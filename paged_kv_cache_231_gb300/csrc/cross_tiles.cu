@@ -268,9 +268,9 @@ struct Part {
   __device__ __forceinline__ int first(int half) const { return shared ? half : 0; }
   __device__ __forceinline__ int stride() const { return shared ? 2 : 1; }
   __device__ __forceinline__ int count(int half) const { return shared ? (n + 1 - half) / 2 : n; }
-  // first key of the i-th step of half h
+  // first key (as the span counts them) of the i-th step of half h
   __device__ __forceinline__ int key_of(int h, int i) const {
-    return span.key_step(first_step + first(h) + stride() * i) * kTileKeys;
+    return (first_step + first(h) + stride() * i) * kTileKeys;
   }
 };
 // steps of the range that the cursor is in
@@ -686,20 +686,22 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
     const auto seen_key = [&](int key) {
       return key < c.q.keys && (F != kCausal || key >= seen_from || key < sinks);
     };
-    const auto step_key = [&](int j) {   // first key of step j of the range
-      return (F == kCausal ? t.span.key_step(j) : j) * kTileKeys;
-    };
-    int ahead = lookup(step_key(c.s) + lane * R);
+    const auto key_at = [&](int v) { return F == kCausal ? t.span.key_at(v) : v; };
+    int ahead = lookup(key_at(c.s * kTileKeys + lane * R));
     for (int j = c.s; j < c.s + t.n; ++j, use += 2, ++issued) {
-      const int first = step_key(j), key0 = first + lane * R;
+      const int first = j * kTileKeys, key0 = key_at(first + lane * R);
       const bool there = R > 0 && lane * R < kTileKeys && key0 < c.q.keys &&
                          (F != kCausal || key0 + R > seen_from || key0 < sinks);
       const bool mapped = there && ahead >= 0 && ahead < p.NB;
       const int row = ahead * p.BS + (key0 - column(key0) * p.BS);   // where mapped
       const uint32_t boxes = __ballot_sync(0xffffffffu, mapped);
-      const bool clear = R > 0 && first + kTileKeys <= c.q.keys && boxes == every &&
-                         (F != kCausal || first >= seen_from || first + kTileKeys <= sinks);
-      ahead = lookup((F == kCausal ? step_key(j + 1) : first + kTileKeys) + lane * R);
+      // key rows behind the last key may stay what they are: their scores are masked
+      const bool whole = mapped && key0 + R <= c.q.keys &&
+                         (F != kCausal || key0 >= seen_from || key0 + R <= sinks);
+      const bool clear =
+          R > 0 && (F == kCausal ? __ballot_sync(0xffffffffu, whole) == every
+                                 : first + kTileKeys <= c.q.keys && boxes == every);
+      ahead = lookup(key_at(first + kTileKeys + lane * R));
       if (!room()) return false;
       unsigned char* dst = sm + L::kRing + to.stage * L::kTile;
       uint64_t* full = bars + kFull + to.stage;
@@ -713,7 +715,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
       }
       if (there && !mapped) flags |= PKV_DEV_BAD_BLOCK;
       if (kv == 0) {
-        const int k0 = first + 4 * lane;   // 4 keys of one block, if boxes are used
+        const int k0 = key_at(first + 4 * lane);   // 4 keys of one block, if boxes are used
         uint32_t words[4];
         if (R > 0) {
           const bool in = __shfl_sync(0xffffffffu, mapped ? 1 : 0, 4 * lane / R) != 0;
@@ -723,8 +725,8 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
         } else {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int blk = lookup(k0 + x);
-            words[x] = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.NB && seen_key(k0 + x));
+            const int key = key_at(first + 4 * lane + x), blk = lookup(key);
+            words[x] = __ballot_sync(0xffffffffu, blk >= 0 && blk < p.NB && seen_key(key));
           }
         }
 #pragma unroll
@@ -732,16 +734,13 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
           if (lane == x) *seen = words[x];
       }
       {
-        // key rows behind the last key may stay what they are: their scores are masked
-        const bool whole = mapped && key0 + R <= c.q.keys &&
-                           (F != kCausal || key0 >= seen_from || key0 + R <= sinks);
         const uint32_t copy = __ballot_sync(0xffffffffu, kv == 0 ? mapped : whole);
         const T* src = static_cast<const T*>(kv == 0 ? p.kc : p.vc);
         bool rows = false;   // rows copied one by one
         if (R == 0) {
           rows = true;
           for (int r = 0; r < kTileKeys; ++r) {
-            const int key = first + r;
+            const int key = key_at(first + r);
             int64_t at = -1;
             if (seen_key(key)) {
               const int col = p.bs_shift >= 0 ? key >> p.bs_shift : key / p.BS;
@@ -765,7 +764,7 @@ __device__ void load_role(const CrossParams& p, const Maps& maps, unsigned char*
             const int mapped_i = __shfl_sync(0xffffffffu, mapped ? 1 : 0, i);
             for (int x = lane; x < R * (D / 8); x += 32) {
               const int r = x / (D / 8), ch = x % (D / 8);
-              const bool live = mapped_i && seen_key(first + i * R + r);
+              const bool live = mapped_i && seen_key(key_at(first + i * R + r));
               const int64_t at = live ? ((int64_t)(row_i + r) * p.Hkv + t.h) * D + ch * 8 : 0;
               const int k = i * R + r;
               cp_async_16(dst + (k >> 3) * L::kGroup + (ch >> 3) * 1024 + tc::sw128(k & 7, ch & 7),
@@ -949,8 +948,8 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     };
     float m = -INFINITY, l = 0.f;
     const int n = t.count(half);
-    // kCausal: the row's position; it sees keys behind row_from
-    const int row_at = t.at + (t.shared ? 0 : half * (p.tile_pos / 2)) + r / p.G;
+    // kCausal: the row's position, as the span counts keys; it sees those behind row_from
+    const int row_at = t.at - t.span.gap + (t.shared ? 0 : half * (p.tile_pos / 2)) + r / p.G;
     const int row_from = p.window > 0 ? row_at - p.window : -1;
     for (int j = 0; j < n; ++j, k += apart) {
       // the loads and stores of TMEM below are the whole warp's

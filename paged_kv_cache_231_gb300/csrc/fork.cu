@@ -166,29 +166,30 @@ __global__ void __launch_bounds__(kThreads)
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    for (int r = gfree[g] + x - n; open && r < given; open &= open - 1, ++r) {
-      const int b = first_above(upto, p.B, r), from = __ldg(p.parents + b);
-      const int tokens = __ldg(p.past + from), full = column(p, tokens);
-      const int id = g * 1024 + lane * 32 + __ffs(open) - 1;
-      p.new_table[(int64_t)b * p.MB + full] = id;
-      p.list[r] = make_int4(__ldg(p.table + (int64_t)from * p.MB + full), id,
-                            tokens - full * p.BS, 0);
-    }
+    for (int r = gfree[g] + x - n; open && r < given; open &= open - 1, ++r)
+      p.list[r].y = g * 1024 + lane * 32 + __ffs(open) - 1;
   }
-  // lengths, and the entries of partly filled blocks that stay where they are
+  cluster.sync();   // every block sees the ids written above
+  // lengths, the entries of partly filled blocks, and the list
   for (int b = rank * kThreads + tid; b < p.B; b += C * kThreads) {
     int f = 0;
-    const int from = __ldg(p.parents + b);
+    const int from = __ldg(p.parents + b), upto_b = upto[b];
     int n = tokens_of(p, from, &f);
-    const bool asked = upto[b] > (b > 0 ? upto[b - 1] : 0);
-    if (asked && upto[b] > given) {
+    const bool asked = upto_b > (b > 0 ? upto[b - 1] : 0);
+    if (asked && upto_b > given) {
       flags |= PKV_DEV_NO_BLOCKS;
       n = 0;
     }
     p.new_past[b] = n;
     const int full = column(p, n);
-    if (!asked && n > full * p.BS)
-      p.new_table[(int64_t)b * p.MB + full] = __ldg(p.table + (int64_t)from * p.MB + full);
+    if (n == full * p.BS) continue;
+    int id = __ldg(p.table + (int64_t)from * p.MB + full);
+    if (asked) {
+      const int src = id;
+      id = __ldcg(&p.list[upto_b - 1].y);
+      p.list[upto_b - 1] = make_int4(src, id, n - full * p.BS, 0);
+    }
+    p.new_table[(int64_t)b * p.MB + full] = id;
   }
   if (rank == 0 && tid == 0) {
     p.count[0] = given;
