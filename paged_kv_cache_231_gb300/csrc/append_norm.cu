@@ -77,29 +77,47 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
       }
     }
   };
-  // gathering: pair j of token t0 + k of the group, one to a thread and round
-  const auto gather = [&](int g, int buf) {
-    float* const to = reinterpret_cast<float*>(turn + buf * words);
-    for (int k = threadIdx.x; k < group * half; k += blockDim.x) {
-      const int tok = k / half, j = k - tok * half, t = g * group + tok;
-      if (t >= p.T) break;
-      const int r = __ldg(p.pos + (int64_t)p.pair_axis[j] * p.T + t);
-      if (r >= 0 && r < p.P) {
-        const int64_t at = (int64_t)r * half + j;
-        float* z = to + 4 * ((tok * 4 + (j & 7) / 2) * per_head + j / 8) + (j & 1);
-        z[0] = Num<TT>::to(__ldg(static_cast<const TT*>(p.cos) + at));
-        z[2] = Num<TT>::to(__ldg(static_cast<const TT*>(p.sin) + at));
-      }
+  // Cos and sin of pair j of token k of a group, one pair to a thread and round. The table rows of
+  // a group are asked for a group before its entries are, and these a group before their use.
+  const int pairs = group * half, apart = gridDim.x;
+  const auto row_of = [&](int g, int k) {   // table row, -1: none
+    if (k >= pairs || g >= groups) return -1;
+    const int t = g * group + k / half;
+    return t < p.T ? __ldg(p.pos + (int64_t)p.pair_axis[k % half] * p.T + t) : -1;
+  };
+  const auto fetch = [&](int row, int k, float& c, float& s) {
+    if (row >= 0 && row < p.P) {
+      const int64_t at = (int64_t)row * half + k % half;
+      c = Num<TT>::to(__ldg(static_cast<const TT*>(p.cos) + at));
+      s = Num<TT>::to(__ldg(static_cast<const TT*>(p.sin) + at));
     }
+  };
+  const auto put = [&](int buf, int k, float c, float s) {
+    const int tok = k / half, j = k % half;
+    float* z = reinterpret_cast<float*>(turn + buf * words) +
+               4 * ((tok * 4 + (j & 7) / 2) * per_head + j / 8) + (j & 1);
+    z[0] = c;
+    z[2] = s;
+  };
+  const auto later = [&](int g, int buf) {   // pairs behind the first round, all at once
+    for (int k = threadIdx.x + blockDim.x; k < pairs; k += blockDim.x) {
+      float c = 0.f, s = 0.f;
+      fetch(row_of(g, k), k, c, s);
+      put(buf, k, c, s);
+    }
+  };
+  const auto token = [&](int g, int buf) {
     for (int k = threadIdx.x; k < group; k += blockDim.x) {
       const int t = g * group + k;
-      if (t >= p.T) break;
+      if (g >= groups || t >= p.T) break;
       const Token tk = read_token(p, t);
       if (blockIdx.y == 0) report(p, tk);
       about[buf * group + k] =
           make_int2(tk.slot, (tk.known ? 1 : 0) | (tk.known && tk.fits ? 2 : 0));
     }
   };
+  const int first = threadIdx.x;
+  const bool gathers = first < pairs;
 
   int g = blockIdx.x;
   uint4 x[N][2], ahead[N][2];
@@ -110,11 +128,19 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     const void* from = e < D ? np.qw : np.kw;
     s_weight[e / D][e % D] = from ? weight_at(from, np.weight_f32, p.bf16, e % D) : 1.f;
   }
-  gather(g, 0);
+  float co = 0.f, si = 0.f;
+  fetch(row_of(g, first), first, co, si);
+  int row = row_of(g + apart, first);
+  token(g, 0);
+  later(g, 0);
+  if (gathers) put(0, first, co, si);
   __syncthreads();
-  for (int buf = 0; g < groups; g += gridDim.x, buf ^= 1) {
-    load(g + gridDim.x, ahead);
-    if (g + (int)gridDim.x < groups) gather(g + gridDim.x, buf ^ 1);
+  for (int buf = 0; g < groups; g += apart, buf ^= 1) {
+    load(g + apart, ahead);
+    fetch(row, first, co, si);
+    row = row_of(g + 2 * apart, first);
+    token(g + apart, buf ^ 1);
+    later(g + apart, buf ^ 1);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int tok = n * tokens + w, t = g * group + tok;
@@ -171,6 +197,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
       row[chunk[0]] = out[0];
       row[chunk[1]] = out[1];
     }
+    if (gathers) put(buf ^ 1, first, co, si);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       x[n][0] = ahead[n][0];

@@ -87,7 +87,7 @@ struct Num<__nv_bfloat16> {
 // One sequence as a kernel of one kind sees it; ranges == 0: nothing to do here.
 struct Seq {
   int cu0, rows, keys;   // first query row, query rows, keys
-  int steps;             // steps of a range (kCausal, many rows: of its tiles for one kv head)
+  int steps;             // steps of a range (kCausal, many rows: its tiles differ, see tile_span)
   int ranges;
   int at;                // kCausal: position of the first row; kShared: row of the block table
   int lo;                // kCausal: first key that takes part (in a window or not)
@@ -157,11 +157,7 @@ __device__ __forceinline__ Seq read_seq(const CrossParams& p, int b, int* flags,
   if (s.rows == 0 || s.keys == 0 || (s.rows > p.few) != kTiles) return s;
   if (kTiles) {
     const int tiles = (s.rows + p.tile_pos - 1) / p.tile_pos;
-    if (F == kCausal) {
-      for (int t = 0; t < tiles; ++t) s.steps += tile_span(p, s, t).steps;
-    } else {
-      s.steps = (s.keys + kTileKeys - 1) / kTileKeys;
-    }
+    if (F != kCausal) s.steps = (s.keys + kTileKeys - 1) / kTileKeys;
     s.ranges = p.Hkv * tiles;
   } else {
     const int n = few_keys(p.D);

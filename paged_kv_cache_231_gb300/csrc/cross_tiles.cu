@@ -80,8 +80,9 @@ struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr size_t kBytes = kEnd + 1024;
 };
 static_assert(Lay<128>::kBytes <= 232448, "shared memory over the limit");
-static_assert((5 * kEntries + kThreads + 52) * 8 <= Lay<64>::kStages * Lay<64>::kTile &&
-                  (5 * kEntries + kThreads + 52) * 8 <= Lay<128>::kStages * Lay<128>::kTile,
+constexpr int kList = 4096;   // tiles of one kv head that a causal plan lists
+static_assert((6 * kEntries + kThreads + kList + 64) * 8 <= Lay<64>::kStages * Lay<64>::kTile &&
+                  (6 * kEntries + kThreads + kList + 64) * 8 <= Lay<128>::kStages * Lay<128>::kTile,
               "plan fits the ring");
 
 // mbarriers
@@ -185,6 +186,25 @@ __device__ __forceinline__ bool elect() {
       "}\n"
       : "=r"(yes));
   return yes != 0;
+}
+
+// 32 bytes of a row, at a 32-byte boundary: rows are apart, so 16 bytes a lane would be half sectors
+__device__ __forceinline__ void store_32(void* at, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                         uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(at), "r"(a),
+               "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+__device__ __forceinline__ void store_32(float* at, const float* v) {
+  store_32(at, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+           __float_as_uint(v[3]), __float_as_uint(v[4]), __float_as_uint(v[5]),
+           __float_as_uint(v[6]), __float_as_uint(v[7]));
+}
+__device__ __forceinline__ void load_32(const float* at, float* v) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "l"(at));
 }
 
 // 16 consecutive fp32 columns of this thread's TMEM lane
@@ -358,34 +378,110 @@ __device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, 
 // them; of the others (between one and two for each block, if there are as many) each block
 // gets a run of steps that evens out what it had before.
 // mem: [kEntries + 1] steps and tiles before an entry each, [kThreads + 1] cuts, scratch,
-// [kEntries] steps of an entry's tiles (the mean, where an entry holds several sequences; kCausal,
-// whose tiles differ: those of one kv head), (kCausal) [kEntries] the entry's sequence.
+// [kEntries] steps of an entry's tiles (the mean, where an entry holds several sequences).
+// kCausal, whose tiles differ: per_tile is the steps of a kv head's tiles; then the sequence of an
+// entry, [kEntries + 1] tiles of one kv head before it, and [kList + 1] steps before each of those
+// tiles. With more sequences than entries or more tiles the steps are summed up where they are asked
+// for. (Summed up always, the plan of 8 prompts of up to 2048 tokens took 23 400 cycles.)
 template <Form F>
 __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   int64_t *steps_at = mem, *tiles_at = steps_at + kEntries + 1, *cut = tiles_at + kEntries + 1,
           *scratch = cut + kThreads + 1;
   int* per_tile = reinterpret_cast<int*>(scratch + 32);
-  int4* about = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(per_tile + kEntries) + 15) &
-                                        ~static_cast<uintptr_t>(15));   // rows, keys, at, lo
+  int64_t* before_tile = reinterpret_cast<int64_t*>(per_tile + kEntries);   // [kList + 1]
+  constexpr int kAboutAt = (2 * (kEntries + 1) + kThreads + 1 + 32 + kEntries / 2 + kList + 2) & ~1;
+  int4* about = reinterpret_cast<int4*>(mem + kAboutAt);   // rows, keys, at, lo; 16-byte aligned
+  int *about_cu0 = reinterpret_cast<int*>(about + kEntries), *first_tile = about_cu0 + kEntries;
   const int tid = threadIdx.x, units = p.tile_units;
   const int group = (p.B + kEntries - 1) / kEntries, entries = (p.B + group - 1) / group;
   int f = 0;
   bool z = false;
   int64_t total = 0, tiles = 0;
   const auto steps_in = [&](const Seq& q) {   // of a sequence
-    return F == kCausal ? (int64_t)q.steps * (q.ranges > 0 ? p.Hkv : 0)
-                        : (int64_t)q.steps * q.ranges;
+    if constexpr (F != kCausal) return (int64_t)q.steps * q.ranges;
+    int64_t s = 0;
+    for (int t = 0; t < q.ranges / p.Hkv; ++t) s += tile_span(p, q, t).steps;
+    return s * p.Hkv;
   };
+  const auto entry_of = [&](const auto* at, int64_t k) {   // the last with at[e] <= k
+    int lo = 0, hi = entries - 1, e = 0;
+    while (lo <= hi) {
+      const int mid = (lo + hi) >> 1;
+      if (at[mid] <= k) {
+        e = mid;
+        lo = mid + 1;
+      } else {
+        hi = mid - 1;
+      }
+    }
+    return e;
+  };
+  const auto listed_seq = [&](int e) {
+    Seq q;
+    q.cu0 = about_cu0[e];
+    q.rows = about[e].x;
+    q.keys = about[e].y;
+    q.at = about[e].z;
+    q.lo = about[e].w;
+    q.ranges = (first_tile[e + 1] - first_tile[e]) * p.Hkv;
+    q.steps = 0;
+    return q;
+  };
+  bool listed = false;
+  if constexpr (F == kCausal) {
+    if (group == 1) {
+      int64_t head_tiles = 0;
+      for (int e0 = 0; e0 < entries; e0 += kThreads) {
+        const int e = e0 + tid;
+        Seq q{};
+        if (e < entries) q = read_seq<true, F>(p, e, &f, &z);
+        const int64_t n = q.ranges / p.Hkv;
+        int64_t all;
+        const int64_t upto = block_sum<kThreads>(n, &all, scratch);
+        if (e < entries) {
+          about[e] = make_int4(q.rows, q.keys, q.at, q.lo);
+          about_cu0[e] = q.cu0;
+          first_tile[e] = (int)min(head_tiles + upto - n, (int64_t)kList + 1);
+        }
+        head_tiles += all;
+      }
+      listed = head_tiles <= kList;
+      if (tid == 0) first_tile[entries] = (int)head_tiles;
+      __syncthreads();
+      if (listed) {
+        const int n = (int)head_tiles, each = (n + kThreads - 1) / kThreads;
+        for (int i = tid; i < n; i += kThreads) {
+          const int e = entry_of(first_tile, i);
+          before_tile[i + 1] = tile_span(p, listed_seq(e), i - first_tile[e]).steps;
+        }
+        __syncthreads();
+        const int i0 = min(tid * each, n), i1 = min(i0 + each, n);
+        int64_t mine = 0, all;
+        for (int i = i0; i < i1; ++i) mine += before_tile[i + 1];
+        int64_t at = block_sum<kThreads>(mine, &all, scratch) - mine;
+        for (int i = i0; i < i1; ++i) {
+          at += before_tile[i + 1];
+          before_tile[i + 1] = at;
+        }
+        if (tid == 0) before_tile[0] = 0;
+        __syncthreads();
+      }
+    }
+  }
   for (int e0 = 0; e0 < entries; e0 += kThreads) {
     const int e = e0 + tid;
     int64_t s = 0, n = 0;
     if (e < entries) {
       const int b1 = min(p.B, (e + 1) * group);
       for (int b = e * group; b < b1; ++b) {
+        if (F == kCausal && listed) {
+          s = (before_tile[first_tile[e + 1]] - before_tile[first_tile[e]]) * p.Hkv;
+          n = (first_tile[e + 1] - first_tile[e]) * p.Hkv;
+          continue;
+        }
         const Seq q = read_seq<true, F>(p, b, &f, &z);
         s += steps_in(q);
         n += q.ranges;
-        if (F == kCausal) about[e] = make_int4(q.rows, q.keys, q.at, q.lo);
       }
     }
     int64_t all_s, all_n;
@@ -404,58 +500,70 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     tiles_at[entries] = tiles;
   }
   __syncthreads();
-  const auto entry = [&](const int64_t* at, int64_t k) {   // the last with at[e] <= k
-    int lo = 0, hi = entries - 1, e = 0;
-    while (lo <= hi) {
-      const int mid = (lo + hi) >> 1;
-      if (at[mid] <= k) {
-        e = mid;
-        lo = mid + 1;
-      } else {
-        hi = mid - 1;
-      }
-    }
-    return e;
-  };
   // steps of tile k, which lies in entry e
   const auto steps_at_tile = [&](int e, int64_t k) {
     if (F != kCausal || group > 1) return per_tile[e];
-    Seq q{};
-    q.rows = about[e].x;
-    q.keys = about[e].y;
-    q.at = about[e].z;
-    q.lo = about[e].w;
-    const int tiles_h = (q.rows + p.tile_pos - 1) / p.tile_pos;
-    return tile_span(p, q, (int)(k - tiles_at[e]) % tiles_h).steps;
+    const int t = (int)(k - tiles_at[e]);
+    if (listed) {
+      const int i = first_tile[e] + t % (first_tile[e + 1] - first_tile[e]);
+      return (int)(before_tile[i + 1] - before_tile[i]);
+    }
+    const Seq q = read_seq<true, F>(p, e, &f, &z);
+    return tile_span(p, q, t % (q.ranges / p.Hkv)).steps;
   };
   // cursor at tile k, or (by_step) at step k; *before: steps before it
   const auto find = [&](int64_t k, bool by_step, int64_t* before) {
     const int64_t* at = by_step ? steps_at : tiles_at;
-    const int e = entry(at, k);
+    const int e = entry_of(at, k);
     int64_t left = k - at[e], s = steps_at[e];
     Cursor c{};
-    for (c.b = e * group; c.b < p.B; ++c.b) {
-      c.q = read_seq<true, F>(p, c.b, &f, &z);
-      const int64_t n = by_step ? steps_in(c.q) : c.q.ranges;
-      if (left < n) break;
-      left -= n;
-      s += steps_in(c.q);
-    }
-    if constexpr (F == kCausal) {   // c.q.steps: those of a kv head's tiles
+    if constexpr (F == kCausal) {
+      int64_t mine = 0;   // steps of a kv head's tiles
+      for (c.b = e * group; c.b < p.B; ++c.b) {
+        c.q = listed ? listed_seq(c.b) : read_seq<true, F>(p, c.b, &f, &z);
+        mine = listed ? per_tile[c.b] : steps_in(c.q) / p.Hkv;
+        const int64_t n = by_step ? mine * p.Hkv : c.q.ranges;
+        if (left < n) break;
+        left -= n;
+        s += mine * p.Hkv;
+      }
       const int tiles_h = max(c.q.ranges / p.Hkv, 1);
-      const int h = (int)(by_step ? quotient(left, max(c.q.steps, 1)) : left / tiles_h);
-      const int n = by_step ? (int)(left - (int64_t)h * c.q.steps) : 0;
-      const int last = by_step ? tiles_h - 1 : (int)(left - (int64_t)h * tiles_h);
-      int t = 0, upto = 0;
-      for (; t < last; ++t) {
-        const int x = tile_span(p, c.q, t).steps;
-        if (by_step && upto + x > n) break;
-        upto += x;
+      const int h = (int)(by_step ? quotient(left, max(mine, (int64_t)1)) : left / tiles_h);
+      left -= h * (by_step ? mine : tiles_h);   // steps, or tiles, of that kv head
+      int t = 0;
+      int64_t upto = 0;
+      if (listed) {
+        const int64_t* at_tile = before_tile + first_tile[c.b];
+        int hi = tiles_h;   // the last tile t with as many steps before it
+        if (by_step)
+          while (hi - t > 1) {
+            const int mid = (t + hi) >> 1;
+            if (at_tile[mid] - at_tile[0] <= left)
+              t = mid;
+            else
+              hi = mid;
+          }
+        else
+          t = (int)left;
+        upto = at_tile[t] - at_tile[0];
+      } else {
+        for (; t < (by_step ? tiles_h - 1 : (int)left); ++t) {
+          const int x = tile_span(p, c.q, t).steps;
+          if (by_step && upto + x > left) break;
+          upto += x;
+        }
       }
       c.r = h * tiles_h + t;
-      c.s = by_step ? n - upto : 0;
-      *before = s + (int64_t)h * c.q.steps + upto + c.s;
+      c.s = by_step ? (int)(left - upto) : 0;
+      *before = s + h * mine + upto + c.s;
       return c;
+    }
+    for (c.b = e * group; c.b < p.B; ++c.b) {
+      c.q = read_seq<true, F>(p, c.b, &f, &z);
+      const int64_t n = by_step ? (int64_t)c.q.steps * c.q.ranges : c.q.ranges;
+      if (left < n) break;
+      left -= n;
+      s += (int64_t)c.q.steps * c.q.ranges;
     }
     c.r = by_step ? (int)quotient(left, max(c.q.steps, 1)) : (int)left;
     c.s = by_step ? (int)(left - (int64_t)c.r * c.q.steps) : 0;
@@ -467,7 +575,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   if (whole > 0) {
     const int64_t k = whole * units;
     if (F != kCausal && group == 1) {
-      const int e = entry(tiles_at, k);
+      const int e = entry_of(tiles_at, k);
       from = steps_at[e] + (k - tiles_at[e]) * per_tile[e];
     } else {
       find(k, false, &from);
@@ -479,7 +587,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   if (tid < units) {
     const int64_t i0 = max(whole - 64, (int64_t)0);
     int64_t had = i0 > 0 ? quotient(i0 * total, tiles) : 0, k = tid + i0 * units;
-    for (int e = whole > 0 ? entry(tiles_at, k) : 0; k < whole * units; k += units) {
+    for (int e = whole > 0 ? entry_of(tiles_at, k) : 0; k < whole * units; k += units) {
       while (tiles_at[e + 1] <= k) ++e;
       had += steps_at_tile(e, k);
     }
@@ -1080,6 +1188,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
       const int64_t row = (int64_t)(t.row0 + pos) * p.Hq + t.h * p.G + r % p.G;
       Weights w{0.f, 0.f, 0.f};
       if (mine) w = weights_of<F>(p, row, m, l);
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         float o[32];
@@ -1087,47 +1196,44 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
         if (mine) {
 #pragma unroll
           for (int y = 0; y < 32; ++y) o[y] *= w.own;
-          if constexpr (F == kCausal) {
-            if (w.other > 0.f) {
-              const float4* prior = reinterpret_cast<const float4*>(p.prior_o + row * D) + x * 8;
+          if (F == kCausal && w.other > 0.f) {
+            float before[32];
 #pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const float4 z = __ldcg(prior + y);
-                o[4 * y] += w.other * z.x;
-                o[4 * y + 1] += w.other * z.y;
-                o[4 * y + 2] += w.other * z.z;
-                o[4 * y + 3] += w.other * z.w;
-              }
-            }
+            for (int y = 0; y < 32; y += 8) load_32(p.prior_o + row * D + x * 32 + y, before + y);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] += w.other * before[y];
           }
           if constexpr (F == kShared) {
-            float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * D) + x * 8;
 #pragma unroll
-            for (int y = 0; y < 8; ++y)
-              out[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            for (int y = 0; y < 32; y += 8)
+              store_32(static_cast<float*>(p.out) + row * D + x * 32 + y, o + y);
           } else {
-            uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * D) + x * 4;
+            T* out = static_cast<T*>(p.out) + row * D + x * 32;
+            uint32_t u[16];
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              out[y] = make_uint4(Num<T>::pack(o[y * 8], o[y * 8 + 1]),
-                                  Num<T>::pack(o[y * 8 + 2], o[y * 8 + 3]),
-                                  Num<T>::pack(o[y * 8 + 4], o[y * 8 + 5]),
-                                  Num<T>::pack(o[y * 8 + 6], o[y * 8 + 7]));
+            for (int y = 0; y < 16; ++y) u[y] = Num<T>::pack(o[2 * y], o[2 * y + 1]);
+            if (wide) {
+              store_32(out, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+              store_32(out + 16, u[8], u[9], u[10], u[11], u[12], u[13], u[14], u[15]);
+            } else {
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                reinterpret_cast<uint4*>(out)[y] =
+                    make_uint4(u[4 * y], u[4 * y + 1], u[4 * y + 2], u[4 * y + 3]);
+            }
           }
         }
       }
       if (mine && p.lse) p.lse[row] = w.lse;
     } else {
       const int64_t row = (2 * (int64_t)blockIdx.x + (index == 0 ? 0 : 1)) * 256 + half * 128 + r;
-      float4* out = reinterpret_cast<float4*>(p.tile_o + row * D);
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         float o[32];
         result(x, o);
         if (mine) {
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            out[x * 8 + y] = make_float4(o[y * 4], o[y * 4 + 1], o[y * 4 + 2], o[y * 4 + 3]);
+          for (int y = 0; y < 32; y += 8) store_32(p.tile_o + row * D + x * 32 + y, o + y);
         }
       }
       if (mine) {
