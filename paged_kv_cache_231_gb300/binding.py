@@ -7,6 +7,7 @@ raises. Function names match the C entry points.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -1166,15 +1167,18 @@ def _cache_rows(caches):
     pool = max(shape[0] * shape[1], 1)
     row = first.numel() // pool * first.element_size()
     at, rows = [], [row] * len(caches)
-    for i, t in enumerate(caches):
-        if t.shape != shape or t.dtype is not dtype:
+    add = at.append
+    for t in caches:
+        if (t.dtype is not dtype or t.shape != shape or t.get_device() != device or
+                not t.is_contiguous()):
+            i = len(at)
             if t.dim() < 2 or t.shape[:2] != shape[:2]:
                 raise ValueError(f"caches[{i}]: expected {tuple(shape[:2])} blocks and rows, got "
                                  f"{tuple(t.shape)}")
+            if not t.is_contiguous() or t.get_device() != device:
+                raise ValueError(f"caches[{i}]: must be contiguous, on device {device}")
             rows[i] = t.numel() // pool * t.element_size()
-        if not t.is_contiguous() or t.get_device() != device:
-            raise ValueError(f"caches[{i}]: must be contiguous, on device {device}")
-        at.append(t.data_ptr())
+        add(t.data_ptr())
     return at, rows, shape[0], shape[1]
 
 
@@ -1215,15 +1219,15 @@ def pkv_paged_fork(parents, past_seqlens, block_table, caches=(), *, num_blocks:
     past, table, free = made(new_past_seqlens, B), made(new_block_table, (B, MB)), \
         made(free_blocks, 1)
     n = len(at)
-    pointers, widths = (c_i64 * n)(*at), (c_i64 * n)(*rows)
+    pointers, widths = array.array("q", at), array.array("q", rows)
     need = 256 + 16 * B   # pkv_paged_fork_workspace_size
     if workspace is None or workspace.numel() < need:
         workspace = _own_workspace(need, block_table, stream, raw)
     _step_call("pkv_paged_fork",
                _FORK_PACK.pack(parents.data_ptr(), past_seqlens.data_ptr(),
                                block_table.data_ptr(), past.data_ptr(), table.data_ptr(),
-                               free.data_ptr(), ctypes.addressof(pointers) if n else 0,
-                               ctypes.addressof(widths) if n else 0, _at(device_status), B, MB,
+                               free.data_ptr(), pointers.buffer_info()[0] if n else 0,
+                               widths.buffer_info()[0] if n else 0, _at(device_status), B, MB,
                                num_blocks, block_size, n), workspace.data_ptr(), need, raw)
     return past, table, free
 

@@ -28,6 +28,8 @@ using elem::Num;
 
 constexpr int kMaxThreads = 384;   // two blocks of 85 registers a thread to an SM
 constexpr int kFill = 256;   // threads that tokens side by side fill
+// groups of N tokens a thread whose rows are held or on their way
+__host__ __device__ constexpr int stages_of(int n) { return n == 4 ? 2 : 4; }
 
 __device__ __forceinline__ float weight_at(const void* w, bool f32, bool bf16, int i) {
   return f32    ? __ldg(static_cast<const float*>(w) + i)
@@ -40,15 +42,18 @@ __device__ __forceinline__ float weight_at(const void* w, bool f32, bool bf16, i
 template <typename T, typename TT, int D, bool kSide, int N>
 __global__ void __launch_bounds__(kMaxThreads, 2)
     append_norm_kernel(const __grid_constant__ NormParams np, int tokens, int heads) {
-  constexpr int kLanes = D / 16;
+  constexpr int kLanes = D / 16, kStages = stages_of(N);
   const AxesParams& p = np.axes;
   // [2][N * tokens][4][R / 16] (cos, cos, sin, sin) of pairs 2 y and 2 y + 1 of item c at [y][c], so
   // that neighbouring lanes read neighbouring words; then (slot, flags) of each token, twice
+  // Behind them the ring of rows: each thread copies what it will work on itself, so nothing but
+  // its own copies is waited for; [kStages][N][2] 16 bytes of each thread.
   extern __shared__ __align__(16) float4 turn[];
   __shared__ __align__(16) float s_weight[2][D];   // of queries and of keys
   const int half = p.R / 2, per_head = p.R / 16, group = N * tokens;
   const int words = group * per_head * 4;
   int2* about = reinterpret_cast<int2*>(turn + 2 * words);
+  uint4* const ring = reinterpret_cast<uint4*>(turn + 2 * words + group) + threadIdx.x;
   const int items = heads * kLanes, w = threadIdx.x / items, i = threadIdx.x - w * items;
   const int groups = (p.T + group - 1) / group;
   const int h = blockIdx.y * heads + i / kLanes, c = i % kLanes;
@@ -66,16 +71,20 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   const void* const weight = kind == 0 ? np.qw : np.kw;
   const bool normed = kind < 2 && weight != nullptr;
 
-  const auto load = [&](int g, uint4 (&x)[N][2]) {
+  const auto slot_of = [&](int stage, int n, int y) {
+    return ring + ((stage * N + n) * 2 + y) * blockDim.x;
+  };
+  const auto load = [&](int g, int stage) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int t = g * group + n * tokens + w;
       if (mine && g < groups && t < p.T) {
         const uint4* row = reinterpret_cast<const uint4*>(src + (int64_t)t * in_row);
-        x[n][0] = __ldcs(row + chunk[0]);
-        x[n][1] = __ldcs(row + chunk[1]);
+        cp_async_16(slot_of(stage, n, 0), row + chunk[0], 16);
+        cp_async_16(slot_of(stage, n, 1), row + chunk[1], 16);
       }
     }
+    cp_async_commit();
   };
   // Cos and sin of pair j of token k of a group, one pair to a thread and round. The table rows of
   // a group are asked for a group before its entries are, and these a group before their use.
@@ -106,24 +115,20 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
       put(buf, k, c, s);
     }
   };
-  const auto token = [&](int g, int buf) {
-    for (int k = threadIdx.x; k < group; k += blockDim.x) {
-      const int t = g * group + k;
-      if (g >= groups || t >= p.T) break;
-      const Token tk = read_token(p, t);
-      if (blockIdx.y == 0) report(p, tk);
-      about[buf * group + k] =
-          make_int2(tk.slot, (tk.known ? 1 : 0) | (tk.known && tk.fits ? 2 : 0));
-    }
+  // slot and flags of this thread's token of a group, asked for a group before they are put down
+  const auto token = [&](int g) {
+    const int t = g * group + (int)threadIdx.x;
+    if ((int)threadIdx.x >= group || g >= groups || t >= p.T) return make_int2(-1, 0);
+    const Token tk = read_token(p, t);
+    if (blockIdx.y == 0) report(p, tk);
+    return make_int2(tk.slot, (tk.known ? 1 : 0) | (tk.known && tk.fits ? 2 : 0));
   };
   const int first = threadIdx.x;
   const bool gathers = first < pairs;
 
   int g = blockIdx.x;
-  uint4 x[N][2], ahead[N][2];
 #pragma unroll
-  for (int n = 0; n < N; ++n) x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
-  load(g, x);
+  for (int i = 0; i < kStages - 1; ++i) load(g + i * apart, i);
   for (int e = threadIdx.x; e < 2 * D; e += blockDim.x) {
     const void* from = e < D ? np.qw : np.kw;
     s_weight[e / D][e % D] = from ? weight_at(from, np.weight_f32, p.bf16, e % D) : 1.f;
@@ -131,22 +136,25 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   float co = 0.f, si = 0.f;
   fetch(row_of(g, first), first, co, si);
   int row = row_of(g + apart, first);
-  token(g, 0);
+  int2 tok_about = token(g);
   later(g, 0);
   if (gathers) put(0, first, co, si);
+  if (first < group) about[first] = tok_about;
   __syncthreads();
-  for (int buf = 0; g < groups; g += apart, buf ^= 1) {
-    load(g + apart, ahead);
+  for (int buf = 0, stage = 0; g < groups; g += apart, buf ^= 1, stage = (stage + 1) % kStages) {
+    cp_async_wait<kStages - 2>();
+    load(g + (kStages - 1) * apart, (stage + kStages - 1) % kStages);
     fetch(row, first, co, si);
     row = row_of(g + 2 * apart, first);
-    token(g + apart, buf ^ 1);
+    tok_about = token(g + apart);
     later(g + apart, buf ^ 1);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int tok = n * tokens + w, t = g * group + tok;
       // the shuffles are the whole warp's; rows that are not there are not written
       float v[16], sum = 0.f;
-      const uint32_t* u = reinterpret_cast<const uint32_t*>(&x[n][0]);
+      uint4 x[2] = {*slot_of(stage, n, 0), *slot_of(stage, n, 1)};
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float2 f = Num<T>::to2(u[e]);
@@ -160,7 +168,6 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
       if (!mine || t >= p.T) continue;
       const int2 k = about[buf * group + tok];
       if (k.x < 0 || (kind > 0 && !(k.y & 2))) continue;
-      uint4 out[2] = {x[n][0], x[n][1]};
       if (kind < 2) {
         if (normed) {
           const float by = rsqrtf(sum * (1.f / D) + np.epsilon);
@@ -189,20 +196,16 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
             }
           }
         }
-        uint32_t* q = reinterpret_cast<uint32_t*>(out);
+        uint32_t* q = reinterpret_cast<uint32_t*>(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = Num<T>::from2(v[2 * e], v[2 * e + 1]);
       }
       uint4* row = reinterpret_cast<uint4*>(dst + (int64_t)(kind == 0 ? t : k.x) * out_row);
-      row[chunk[0]] = out[0];
-      row[chunk[1]] = out[1];
+      row[chunk[0]] = x[0];
+      row[chunk[1]] = x[1];
     }
     if (gathers) put(buf ^ 1, first, co, si);
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      x[n][0] = ahead[n][0];
-      x[n][1] = ahead[n][1];
-    }
+    if (first < group) about[(buf ^ 1) * group + first] = tok_about;
     __syncthreads();
   }
 }
@@ -272,31 +275,53 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
 }
 
+// Of the largest block: 384 threads of 8 tokens' rows, or 128 tokens (of two heads of 64) with the
+// cos and sin of 32 pairs twice.
+constexpr int kMostShared = 150 * 1024;
+constexpr int kFewGroups = 2;   // groups of a block up to which it has two tokens a thread
+
 template <typename T, typename TT, int D, bool kSide>
-void launch_lanes(const NormParams& np, cudaStream_t s) {
+cudaError_t launch_lanes(const NormParams& np, cudaStream_t s) {
   const AxesParams& p = np.axes;
   constexpr int kLanes = D / 16;
   const int all = p.Hq + 2 * p.Hkv;
   const int parts = (all * kLanes + kMaxThreads - 1) / kMaxThreads, heads = (all + parts - 1) / parts;
   const int items = heads * kLanes, tokens = items * 2 <= kFill ? kFill / items : 1;
   const int threads = (tokens * items + 31) / 32 * 32, sms = device_sms();
-  const auto run = [&](auto n, int regs) {
-    constexpr int N = decltype(n)::value;
-    const int group = N * tokens, groups = (p.T + group - 1) / group;
-    const int per_sm = 65536 / (threads * regs) > 1 ? 65536 / (threads * regs) : 1;
-    const int fit = per_sm * sms / parts > 1 ? per_sm * sms / parts : 1;
-    const dim3 grid((unsigned)(groups < fit ? groups : fit), (unsigned)parts);
-    const size_t smem = 2 * (size_t)group * (sizeof(float4) * (p.R / 4) + sizeof(int2));
-    append_norm_kernel<T, TT, D, kSide, N><<<grid, threads, smem, s>>>(np, tokens, heads);
+  const auto shared = [&](int n) {   // turned pairs, tokens and rows
+    return (size_t)n * tokens * (2 * sizeof(float4) * (p.R / 4) + sizeof(float4)) +
+           (size_t)threads * stages_of(n) * n * 32;
   };
-  if (p.T >= 4 * tokens * sms)
-    run(std::integral_constant<int, 2>(), 80);
-  else
-    run(std::integral_constant<int, 1>(), 80);
+  const auto fit = [&](int n) {   // blocks that the SMs take at once, by 80 registers a thread
+    const int regs = 65536 / (threads * 80), smem = (int)(225 * 1024 / (shared(n) + 1024 + 8 * D));
+    const int per_sm = regs < smem ? regs : smem;
+    return per_sm * sms / parts > 1 ? per_sm * sms / parts : 1;
+  };
+  const auto run = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    static std::atomic<uint64_t> configured{0};
+    int dev = -1;
+    if (needs_configure(configured, &dev)) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(append_norm_kernel<T, TT, D, kSide, N>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+      if (e != cudaSuccess) return e;
+      mark_configured(configured, dev);
+    }
+    const int group = N * tokens, groups = (p.T + group - 1) / group, most = fit(N);
+    const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)parts);
+    append_norm_kernel<T, TT, D, kSide, N><<<grid, threads, shared(N), s>>>(np, tokens, heads);
+    return cudaGetLastError();
+  };
+  // Tokens of a thread and group: one while a wave of blocks takes all of them, four where a block
+  // goes through several groups (each ends with a barrier that waits for the slowest warp).
+  if (p.T <= (int64_t)tokens * fit(1)) return run(std::integral_constant<int, 1>());
+  if (p.T <= (int64_t)2 * tokens * fit(2) * kFewGroups) return run(std::integral_constant<int, 2>());
+  return run(std::integral_constant<int, 4>());
 }
 
 template <typename T, typename TT>
-void launch_typed(const NormParams& np, cudaStream_t s) {
+cudaError_t launch_typed(const NormParams& np, cudaStream_t s) {
   const AxesParams& p = np.axes;
   const bool lanes = p.R % 16 == 0 && (p.D == 64 || p.D == 128 || p.D == 256);
   if (!lanes) {
@@ -304,41 +329,25 @@ void launch_typed(const NormParams& np, cudaStream_t s) {
     const int64_t fit = (int64_t)64 * device_sms();   // 8 waves
     append_norm_heads_kernel<T, TT>
         <<<(unsigned)(blocks < fit ? blocks : fit), 32 * kWarps, 0, s>>>(np);
-    return;
+    return cudaGetLastError();
   }
-  if (p.interleaved) {
-    if (p.D == 64)
-      launch_lanes<T, TT, 64, true>(np, s);
-    else if (p.D == 128)
-      launch_lanes<T, TT, 128, true>(np, s);
-    else
-      launch_lanes<T, TT, 256, true>(np, s);
-  } else {
-    if (p.D == 64)
-      launch_lanes<T, TT, 64, false>(np, s);
-    else if (p.D == 128)
-      launch_lanes<T, TT, 128, false>(np, s);
-    else
-      launch_lanes<T, TT, 256, false>(np, s);
-  }
+  if (p.interleaved)
+    return p.D == 64    ? launch_lanes<T, TT, 64, true>(np, s)
+           : p.D == 128 ? launch_lanes<T, TT, 128, true>(np, s)
+                        : launch_lanes<T, TT, 256, true>(np, s);
+  return p.D == 64    ? launch_lanes<T, TT, 64, false>(np, s)
+         : p.D == 128 ? launch_lanes<T, TT, 128, false>(np, s)
+                      : launch_lanes<T, TT, 256, false>(np, s);
 }
 
 }  // namespace
 
 cudaError_t launch_append_norm(const NormParams& p, cudaStream_t s) {
   ProfScope ps("append_norm", s);
-  if (p.axes.bf16) {
-    if (p.axes.table_f32)
-      launch_typed<__nv_bfloat16, float>(p, s);
-    else
-      launch_typed<__nv_bfloat16, __nv_bfloat16>(p, s);
-  } else {
-    if (p.axes.table_f32)
-      launch_typed<__half, float>(p, s);
-    else
-      launch_typed<__half, __half>(p, s);
-  }
-  return cudaGetLastError();
+  if (p.axes.bf16)
+    return p.axes.table_f32 ? launch_typed<__nv_bfloat16, float>(p, s)
+                            : launch_typed<__nv_bfloat16, __nv_bfloat16>(p, s);
+  return p.axes.table_f32 ? launch_typed<__half, float>(p, s) : launch_typed<__half, __half>(p, s);
 }
 
 }  // namespace pkv

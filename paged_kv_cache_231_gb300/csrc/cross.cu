@@ -130,7 +130,7 @@ __device__ __forceinline__ void flush(const CrossParams& p, const Cursor& c, int
     if (r >= R) continue;
     if (whole) {
       const int64_t row = (int64_t)(c.q.cu0 + r / p.G) * p.Hq + h * p.G + r % p.G;
-      const Weights w = weights_of<F>(p, row, m[x], l[x]);
+      const Weights w = weights_of<F>(p, row, m[x], l[x], F == kCausal && c.q.lo > 0);
 #pragma unroll
       for (int d = 0; d < D / 8; ++d)
         store_pair<T, F>(p, row * D + d * 8 + 2 * t4, w, o[d][2 * x], o[d][2 * x + 1]);
@@ -190,10 +190,8 @@ __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, i
       for (int b0 = 0; ordered == 0 && !held && b0 < p.B; b0 += 32)
         held = __any_sync(0xffffffffu, b0 + lane < p.B && holds_row<F>(p, b0 + lane, (int)row));
       if (held) continue;
-      if (F != kShared) {   // there nobody reads a row whose lse is -inf
-        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.Hq * D);
-        for (int c = lane; c < p.Hq * D / 8; c += 32) out[c] = make_uint4(0, 0, 0, 0);
-      }
+      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + row * p.Hq * D);
+      for (int c = lane; c < p.Hq * D / 8; c += 32) out[c] = make_uint4(0, 0, 0, 0);
       if (p.lse)
         for (int h = lane; h < p.Hq; h += 32) p.lse[row * p.Hq + h] = -INFINITY;
     }
@@ -207,7 +205,8 @@ __device__ void zero_rows(const CrossParams& p, int unit, int units, int lane, i
 constexpr int kJoinWarps = 8;
 // pieces of a row that a warp asks for at once (8 lowered the occupancy: 64 tokens 16 us, not 12)
 constexpr int kAhead = 4;
-// rows of a tile's record that a block takes (records of many pieces: 12 us, with 64 18 us)
+// rows of a tile's record that a block takes, where one unit alone joins it (records of many pieces:
+// 12 us, with 64 18 us; of 16 pieces joined by their 15 units XXX us)
 constexpr int kJoinRows = 16;
 
 template <int D>
@@ -261,8 +260,9 @@ struct Joined {
     }
   }
   template <typename T, Form F>
-  __device__ __forceinline__ void write(const CrossParams& p, int64_t row, int lane) const {
-    const Weights w = weights_of<F>(p, row, M, L);
+  __device__ __forceinline__ void write(const CrossParams& p, int64_t row, int lane,
+                                        bool joins) const {
+    const Weights w = weights_of<F>(p, row, M, L, joins);
 #pragma unroll
     for (int v = 0; v < V; v += 2)
       store_pair<T, F>(p, row * D + lane * V + v, w, acc[v], acc[v + 1]);
@@ -282,6 +282,16 @@ struct Ring {
   static constexpr size_t kBytes = kWarps * kWarpBytes;
 };
 
+// What is wrong with the groups of a call that shares nothing (else the plan tells).
+__device__ __forceinline__ int check_groups(const CrossParams& p) {
+  bool bad = false;
+  for (int g = threadIdx.x; g < p.check_groups; g += kThreads) {
+    const int lo = __ldg(p.check_offsets + g), hi = __ldg(p.check_offsets + g + 1);
+    bad = bad || lo < 0 || hi < lo || hi > p.B || __ldg(p.check_shared + g) < 0;
+  }
+  return bad ? PKV_DEV_BAD_SEQUENCE : 0;
+}
+
 // kSmall: a block takes one sequence and kv head, its warps an eighth of the steps each, and joins
 // what they have in shared memory (few and short sequences: p.small). Behind these blocks are a few
 // that look for rows to be zeroed.
@@ -296,6 +306,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int flags = 0;
   const int gw = blockIdx.x * kWarps + warp;
+  if constexpr (F == kCausal) {
+    if (p.choice) {   // both kinds of this kernel are launched: one of them works
+      if ((__ldcg(p.choice) != 0) != kSmall) {
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        return;
+      }
+    }
+  }
   Plan pl{};
   Cursor cc{};   // step computed
   int nst = 0, unit = 0, sub = 0;
@@ -310,12 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
     cc.r = blockIdx.x - cc.b * p.Hkv;
     cc.q = read_seq<false, F>(p, cc.b, &flags, &zero);
     if (cc.r > 0 || warp > 0) flags = 0;   // every block of the sequence saw them
+    if (F == kCausal && blockIdx.x == 0) flags |= check_groups(p);
     const int share = (cc.q.steps + kWarps - 1) / kWarps;
     cc.s = warp * share;
     nst = max(0, min(share, cc.q.steps - cc.s));
   } else {
     pl = make_plan<kThreads, F>(p, p.few_units / p.few_heads, s_pref, s_scratch, &flags);
     if (blockIdx.x > 0) flags = 0;   // every block saw them
+    if (F == kCausal && blockIdx.x == 0) flags |= check_groups(p);
     unit = gw / p.few_heads;
     sub = gw % p.few_heads;
     const int64_t g0 = (int64_t)unit * pl.W;
@@ -527,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
         for (int v = 0; v < Joined<D>::V; ++v)
           j.acc[v] += by * po[at * D + lane * Joined<D>::V + v];
       }
-      j.template write<T, F>(p, (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G, lane);
+      j.template write<T, F>(p, (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G, lane,
+                             F == kCausal && cc.q.lo > 0);
     }
   } else if (pl.zero) {
     zero_rows<T, D, F>(p, gw, p.few_units, lane, pl.ordered ? 1 : 0);
@@ -537,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
-// Blocks 0 .. : kJoinRows rows of a tile's record each (256 / kJoinRows blocks a record). Behind
+// Blocks 0 .. : kBlocks for the record of each block of the kernel for many rows. Behind
 // them a block for the record of each warp of the kernel for few rows: 8 warps share the rows that
 // fall to it, several warps a row when there are fewer.
 template <typename T, int D, Form F>
@@ -546,27 +567,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
   __shared__ float s_o[kJoinWarps][D];
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  // behind the wait: what follows reads what kernels in front of this one wrote
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile_blocks = p.tile_units * kBlocks;
   const bool tile = (int)blockIdx.x < tile_blocks;
   const int unit = tile ? blockIdx.x / kBlocks : blockIdx.x - tile_blocks;
+  if (F == kShared && __ldcg(p.active) == 0) return;
+  if (F == kCausal && !tile && p.choice && __ldcg(p.choice) != 0) return;   // no pieces
   const int4* rec = (tile ? p.tile_rec : p.few_rec) + 2 * unit;
-  const int4 a = __ldcg(rec);
-  const int2 about = __ldcg(reinterpret_cast<const int2*>(rec + 1));
+  const int4 a = __ldcg(rec), about = __ldcg(rec + 1);
   const int tokens = about.x;
+  const bool joins = F == kCausal && about.z != 0;
   if (a.x <= 0) return;
   const unsigned over_g = 65536u / p.G + 1;          // x / G = x * over_g >> 16 for x < 256
-  if (tile) {
-    const int64_t first = (int64_t)unit * 512;
-    const int PT = p.tile_pos / 2, row0 = blockIdx.x % kBlocks * kJoinRows;
-    for (int i = warp; i < kJoinRows; i += kJoinWarps) {
-      const int row = row0 + i, x = row & 127, by_g = (int)(x * over_g >> 16);
+  if (tile) {   // its rows by turns to the warps of the units that hold nothing but this range
+    const int64_t first = (int64_t)(unit - about.y) * 512;
+    const int PT = p.tile_pos / 2, warps = (a.x - 1) * kBlocks * kJoinWarps;
+    int row = (about.y * kBlocks + blockIdx.x % kBlocks) * kJoinWarps + warp;
+    for (; row < 256; row += warps) {
+      const int x = row & 127, by_g = (int)(x * over_g >> 16);
       const int pos = (row >> 7) * PT + by_g;
       if (x >= PT * p.G || pos >= tokens) continue;
       Joined<D> j;
       j.add(p.tile_o + first * D, p.tile_m + first, p.tile_l + first, row, a.y * 256, 512, a.x, 0,
             1, lane);
-      j.template write<T, F>(p, (int64_t)(a.z + pos) * p.Hq + a.w * p.G + x - by_g * p.G, lane);
+      j.template write<T, F>(p, (int64_t)(a.z + pos) * p.Hq + a.w * p.G + x - by_g * p.G, lane,
+                             joins);
     }
     return;
   }
@@ -615,7 +642,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
     }
     const int by_g = (int)(r * over_g >> 16);
     if (live && part == 0)
-      j.template write<T, F>(p, (int64_t)(a.z + by_g) * p.Hq + a.w * p.G + r - by_g * p.G, lane);
+      j.template write<T, F>(p, (int64_t)(a.z + by_g) * p.Hq + a.w * p.G + r - by_g * p.G, lane,
+                             joins);
   }
 }
 
@@ -625,25 +653,6 @@ constexpr const char* kNames[][2] = {{"cross_decode", "cross_combine"},
 
 template <typename T, int D, Form F>
 cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
-  static std::atomic<uint64_t> configured{0};
-  int dev = -1;
-  if (needs_configure(configured, &dev)) {
-    cudaError_t e = cudaFuncSetAttribute(cross_few_kernel<T, D, false, F>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Ring<D>::kBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(cross_few_kernel<T, D, true, F>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<D>::kBytes);
-    if (e != cudaSuccess) return e;
-    mark_configured(configured, dev);
-  }
-  if (p.small) {
-    ProfScope ps(kNames[F][0], s);
-    const unsigned zero = (unsigned)((p.T + kThreads - 1) / kThreads);
-    cross_few_kernel<T, D, true, F>
-        <<<(unsigned)(p.B * p.Hkv) + zero, kThreads, Ring<D>::kBytes, s>>>(p);
-    return cudaGetLastError();
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -657,11 +666,34 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cfg.numAttrs = 1;
   }
-  {
-    ProfScope ps(kNames[F][0], s);
-    cfg.gridDim = dim3((unsigned)(p.few_units / kWarps));
+  if (F == kCausal && p.choice) cfg.numAttrs = 1;   // behind the kernels of the shared keys
+  if constexpr (F != kShared) {
+    static std::atomic<uint64_t> configured{0};
+    int dev = -1;
+    if (needs_configure(configured, &dev)) {
+      cudaError_t e = cudaFuncSetAttribute(cross_few_kernel<T, D, false, F>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)Ring<D>::kBytes);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(cross_few_kernel<T, D, true, F>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)Ring<D>::kBytes);
+      if (e != cudaSuccess) return e;
+      mark_configured(configured, dev);
+    }
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Ring<D>::kBytes;
+    if (p.small) {
+      ProfScope ps(kNames[F][0], s);
+      const unsigned zero = (unsigned)((p.T + kThreads - 1) / kThreads);
+      cfg.gridDim = dim3((unsigned)(p.B * p.Hkv) + zero);
+      CrossParams one = p;
+      one.few_heads = 1;
+      const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D, true, F>, one);
+      if (e != cudaSuccess || !p.choice) return e;
+    }
+    ProfScope ps(kNames[F][0], s);
+    cfg.gridDim = dim3((unsigned)(p.few_units / kWarps));
     const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D, false, F>, p);
     if (e != cudaSuccess) return e;
   }
@@ -676,9 +708,9 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
 }  // namespace
 
 #ifdef PKV_CROSS_FORM
-size_t cross_layout(CrossParams* p, char* base) {
+size_t cross_layout(CrossParams* p, char* base, bool tiles_only) {
   const int sms = device_sms();
-  p->few = 16 / p->G;
+  p->few = tiles_only ? 0 : 16 / p->G;
   p->tile_pos = 2 * (128 / p->G);
   // no more units than the longest possible work has runs of the least length (in floating point:
   // the products may pass 64 bits)
@@ -721,11 +753,10 @@ size_t cross_layout(CrossParams* p, char* base) {
   const double steps = std::ceil(std::ceil(keys / few_keys(p->D)) / kWarps);
   const double even = ranges * steps / sms;
   p->small = p->max_q <= p->few && ranges <= 4.0 * sms &&
-             waves * steps + 3.5 * (waves - 1) <= 5 + (even > 1 ? even : 1);
-  if (p->small) {
-    p->few_heads = 1;
-    return 0;
-  }
+             (p->choice != nullptr ||
+              waves * steps + 3.5 * (waves - 1) <= 5 + (even > 1 ? even : 1));
+  if (p->small && !p->choice) return 0;
+  if (tiles_only) p->few_units = 0;
   const size_t fu = (size_t)p->few_units, tu = (size_t)p->tile_units;
   p->few_rec = reinterpret_cast<int4*>(take(fu * 32));
   p->few_o = reinterpret_cast<float*>(take(2 * fu * p->few_rows * p->D * 4));

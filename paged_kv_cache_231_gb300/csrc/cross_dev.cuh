@@ -13,8 +13,8 @@
 //
 // Forms. The kernels are written once and compiled for three kinds of calls:
 //   kCross   every row of a sequence sees all of its klen keys;
-//   kShared  the same for groups of sequences over the keys that these have in common; output and
-//            lse go to 32-bit arrays in the workspace;
+//   kShared  the same for groups of sequences over the keys that these have in common, all of them
+//            as tiles; output and lse go to 32-bit arrays in the workspace;
 //   kCausal  row i stands at past + i and sees keys j <= past + i with j > past + i - window or
 //            j < sinks, or (behind a shared prefix) with j >= start; then the result of the kShared
 //            call is joined in where the row is written.
@@ -304,7 +304,8 @@ __device__ __forceinline__ void next_range(const CrossParams& p, Cursor& c) {
 // Record of warp w, which works on head `sub` of unit u: the range of its last step, if that ends
 // behind the unit's run. The unit in whose run the range begins joins its pieces, and so do the
 // units that hold nothing else: unit number i of them takes the rows i, i + n, ... of n units.
-// rec[2w] = {pieces, first piece's slot, first query row, kv head}, rec[2w + 1] = {query rows, i}
+// rec[2w] = {pieces, first piece's slot, first query row, kv head}, rec[2w + 1] = {query rows, i,
+// whether the result of shared keys is joined in}
 template <Form F>
 __device__ __forceinline__ void write_record(const CrossParams& p, const Plan& pl,
                                              const int64_t* pref, int64_t u, int sub, int4* rec) {
@@ -319,6 +320,7 @@ __device__ __forceinline__ void write_record(const CrossParams& p, const Plan& p
                     c.r * p.few_heads + sub);
       b.x = c.q.rows;
       b.y = (int)(u - own);
+      if (F == kCausal) b.z = c.q.lo > 0;
     }
   }
   rec[0] = a;
@@ -335,13 +337,15 @@ __device__ __forceinline__ float inverse_of(float l) { return l == 0.f ? 0.f : 1
 struct Weights {
   float own, other, lse;
 };
-// m, l: maximum (log2 units) and sum of the row; kCausal joins the result of the keys that its
-// sequence shares with others, out_1 = o_1 / l_1 with lse_1 = ln(l_1 2^{m_1}):
+// m, l: maximum (log2 units) and sum of the row; where `joins` (kCausal, a sequence whose first keys
+// its group computes) the result of those, out_1 with lse_1, is joined in:
 //   M = max(m, lse_1 log2 e), L = l 2^{m - M} + 2^{lse_1 log2 e - M}
 template <Form F>
-__device__ __forceinline__ Weights weights_of(const CrossParams& p, int64_t row, float m, float l) {
+__device__ __forceinline__ Weights weights_of(const CrossParams& p, int64_t row, float m, float l,
+                                              bool joins) {
   if constexpr (F == kCausal) {
-    if (p.prior_lse) {
+    if (joins) {
+      asm volatile("griddepcontrol.wait;\n" ::: "memory");   // for whoever writes it
       const float before = __ldcg(p.prior_lse + row) * kLog2e, mine = l == 0.f ? -INFINITY : m;
       const float top = fmaxf(mine, before), base = top == -INFINITY ? 0.f : top;
       const float a = ex2(mine - base), b = ex2(before - base), all = l * a + b;

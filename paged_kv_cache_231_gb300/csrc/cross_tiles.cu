@@ -652,17 +652,22 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   }
   if (tid == 32 && whole > 0) run->first = find(u, false, &x);
   if (tid == 64 && c1 > c0) run->at = find(c0, true, &x);
-  if (tid == 96) {   // the record: the range that begins in the run and ends behind it
+  // The record: the range that the run ends in, if it goes on behind it. The unit in whose run the
+  // range begins joins the pieces, and so does every further one but the last (their runs lie inside
+  // the range, or are empty): a share of the rows each.
+  if (tid == 96) {
     int4 a = make_int4(0, 0, 0, 0), b = make_int4(0, 0, 0, 0);
-    if (c1 > c0) {
-      const Cursor c = find(c1 - 1, true, &x);
-      const int64_t start = c1 - 1 - c.s, end = start + steps_of<F>(p, c.q, c.r);
-      if (start >= c0 && end > c1) {
-        int v = u;
+    const int64_t in = c1 > c0 ? c1 - 1 : c0;
+    if (in < total) {
+      const Cursor c = find(in, true, &x);
+      const int64_t start = in - c.s, end = start + steps_of<F>(p, c.q, c.r);
+      if (end > c1 && (c1 > c0 || start < c0)) {
+        int v = u, from = u;
         while (v + 1 < units && cut[v + 1] < end) ++v;
+        while (cut[from] > start) --from;
         const Part t = part_of<F>(p, c, 1);
-        a = make_int4(v - u + 1, start == c0 ? 0 : 1, t.row0, t.h);
-        b.x = t.pos;
+        a = make_int4(v - from + 1, start == cut[from] ? 0 : 1, t.row0, t.h);
+        b = make_int4(t.pos, u - from, F == kCausal && c.q.lo > 0, 0);
       }
     }
     p.tile_rec[2 * u] = a;
@@ -1037,7 +1042,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     __syncwarp();
     if (lane == 0) arrive(bars + bar + half);
   };
-  each_part<F>(p, run, [&](const Part& t, const Cursor&, int index) {
+  each_part<F>(p, run, [&](const Part& t, const Cursor& c, int index) {
     uint32_t k = use + 2 * t.first(half);   // ring tile of this half's K; V is k + 1
     Place<L::kStages> tile = next;          // the next tile to be given back: K, V, K, V ...
     use += 2 * t.n;
@@ -1187,7 +1192,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
     if (t.whole) {
       const int64_t row = (int64_t)(t.row0 + pos) * p.Hq + t.h * p.G + r % p.G;
       Weights w{0.f, 0.f, 0.f};
-      if (mine) w = weights_of<F>(p, row, m, l);
+      if (mine) w = weights_of<F>(p, row, m, l, F == kCausal && c.q.lo > 0);
       const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
@@ -1258,6 +1263,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if constexpr (F == kShared) {   // the plan may have found nothing worth sharing
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (__ldcg(p.active) == 0) return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Wait wait;
   wait.bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
@@ -1295,6 +1304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(&run->tmem, 512);
     tc::tmem_relinquish();
   }
+  if (F == kCausal && p.start)   // starts of sequences, and the result of the keys before them
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // in the ring's memory before the ring is used; the other kernel reports bad sequences
   plan_tiles<F>(p, reinterpret_cast<int64_t*>(sm + L::kRing), run);
   tc::fence_async_shared();
@@ -1384,8 +1395,17 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   if (p.box_keys > 0 && (!encode_pool(&maps.k, p, p.kc) || !encode_pool(&maps.v, p, p.vc)))
     return cudaErrorInvalidValue;
   ProfScope ps(F == kCross ? "cross_tiles" : F == kShared ? "prefix_tiles" : "window_tiles", s);
-  cross_tiles_kernel<T, D, F><<<p.tile_units, kThreads, Lay<D>::kBytes, s>>>(p, maps);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.tile_units);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Lay<D>::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = F == kShared || (F == kCausal && p.start) ? 1 : 0;   // they wait for the one in front
+  return cudaLaunchKernelEx(&cfg, cross_tiles_kernel<T, D, F>, p, maps);
 }
 
 }  // namespace

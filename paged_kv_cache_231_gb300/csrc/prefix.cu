@@ -9,6 +9,8 @@
 // takes it in where it writes a row. So a group's S keys are read once and multiplied as matrices
 // with all its rows, where every sequence for itself would read them again: 64 single tokens
 // behind 8192 keys read 1/64 of that.
+// Where that saves less than it costs (few sequences or short prefixes, which the cache holds
+// for those that read them again; prompts that fill tiles by themselves) nothing is shared.
 //
 // This file: the plan, which finds how many keys each group can share, and the launches; the
 // kShared form of cross.cu is at the end.
@@ -19,70 +21,137 @@
 namespace pkv {
 namespace {
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 
-// A block takes the groups blockIdx.x, + gridDim.x, ... and writes group_cu, shared, table_row of
-// each and `start` of its sequences (0: nothing shared).
+// What sharing saves, in nanoseconds. A sequence of few rows reads all of its keys, from the cache
+// where others read the same (64 single tokens over the same 8192 keys: 7.3 TB/s); one of many rows
+// takes half a tile's step for each 128 rows and keys. Shared, a group's rows fill tiles together,
+// and their result makes a way through memory. The kernels of the shared keys cost a call some XXX us.
+constexpr int64_t kCallCost = 30000;
+__device__ __forceinline__ int64_t few_cost(const CrossParams& p, int64_t keys) {
+  return keys * p.Hkv * p.D * 4 / 7300;
+}
+__device__ __forceinline__ int64_t tile_cost(const CrossParams& p, int sms, int rows, int keys) {
+  const int half = p.tile_pos / 2;
+  const int64_t steps = (int64_t)((rows + half - 1) / half) * ((keys + kTileKeys - 1) / kTileKeys);
+  return steps * p.Hkv * (p.D == 64 ? 600 : 1030) / sms;
+}
+
+// One block. A warp looks at a group: how many keys it can share, and what that saves. If all of
+// them together save more than the call costs, group_cu, group_keys, table_row of each group and
+// `start` of its sequences say what is shared; else nothing is.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p, PrefixParams x) {
-  __shared__ int s_past, s_live, s_first, s_bad;
-  const int tid = threadIdx.x;
+  __shared__ unsigned long long s_saved, s_steps;
+  __shared__ int s_longest;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   bool wrong = false;   // group offsets that descend or leave 0 .. B
   for (int g = tid; g < x.groups; g += kPlanThreads) {
     const int lo = __ldg(x.offsets + g), hi = __ldg(x.offsets + g + 1);
     wrong = wrong || lo < 0 || hi < lo || hi > p.B;
   }
+  if (tid == 0) {
+    s_saved = s_steps = 0;
+    s_longest = 0;
+  }
   wrong = __syncthreads_or(wrong) != 0;
-  if (wrong && blockIdx.x == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_SEQUENCE);
-  // sequences that lie in no group
-  const int from = wrong || x.groups == 0 ? p.B : __ldg(x.offsets);
-  const int to = wrong || x.groups == 0 ? p.B : __ldg(x.offsets + x.groups);
-  for (int b = blockIdx.x * kPlanThreads + tid; b < p.B; b += gridDim.x * kPlanThreads)
-    if (b < from || b >= to) x.start[b] = 0;
-  for (int g = blockIdx.x; g < x.groups; g += gridDim.x) {
+  int flags = wrong ? PKV_DEV_BAD_SEQUENCE : 0;
+  for (int g = warp; g < x.groups; g += kPlanWarps) {
     const int lo = wrong ? 0 : __ldg(x.offsets + g), hi = wrong ? 0 : __ldg(x.offsets + g + 1);
     const int asked = __ldg(x.shared + g);
-    if (tid == 0) {
-      s_past = INT32_MAX;
-      s_first = p.B;
-      s_live = s_bad = 0;
-      if (asked < 0) flag_status(p.status, PKV_DEV_BAD_SEQUENCE);
-    }
-    __syncthreads();
-    int least = INT32_MAX, first = p.B, live = 0, bad = 0;
-    for (int b = lo + tid; b < hi; b += kPlanThreads) {
+    if (asked < 0) flags |= PKV_DEV_BAD_SEQUENCE;
+    int least = INT32_MAX, first = p.B, live = 0, rows = 0;
+    bool bad = false;
+    for (int b = lo + lane; b < hi; b += 32) {
       const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), past = __ldg(p.past + b);
       if (c0 < 0 || c1 < c0 || c1 > p.T || c1 - c0 > p.max_q || past < 0 || past > p.MB * p.BS) {
-        bad = 1;
+        bad = true;
       } else if (c1 > c0) {
         least = min(least, past);
         first = min(first, b);
+        rows += c1 - c0;
         ++live;
       }
     }
     least = __reduce_min_sync(0xffffffffu, least);
     first = __reduce_min_sync(0xffffffffu, first);
     live = __reduce_add_sync(0xffffffffu, live);
-    bad = __reduce_or_sync(0xffffffffu, bad);
-    if ((tid & 31) == 0) {
-      atomicMin(&s_past, least);
-      atomicMin(&s_first, first);
-      atomicAdd(&s_live, live);
-      atomicOr(&s_bad, bad);
+    rows = __reduce_add_sync(0xffffffffu, rows);
+    bad = __any_sync(0xffffffffu, bad);
+    int keys = bad || live < 2 ? 0 : min(max(asked, 0), least);
+    int64_t saved = 0;
+    if (keys > 0) {
+      for (int b = lo + lane; b < hi; b += 32) {
+        const int n = __ldg(p.cu + b + 1) - __ldg(p.cu + b);
+        if (n > 0) saved += n > p.few ? tile_cost(p, x.sms, n, keys) : few_cost(p, keys);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) saved += __shfl_xor_sync(0xffffffffu, saved, o);
+      saved -= tile_cost(p, x.sms, rows, keys) + (int64_t)rows * p.Hq * p.D * 8 / 4000;
+      if (saved <= 0) keys = 0;
     }
-    __syncthreads();
-    const int keys = s_bad || s_live < 2 ? 0 : min(max(asked, 0), s_past);
-    for (int b = lo + tid; b < hi; b += kPlanThreads) x.start[b] = keys;
-    if (tid == 0) {
+    if (lane == 0) {
+      if (keys > 0) atomicAdd(&s_saved, (unsigned long long)saved);
       x.group_keys[g] = keys;
       x.group_cu[g] = wrong ? 0 : __ldg(p.cu + lo);
       if (g == x.groups - 1) x.group_cu[g + 1] = wrong ? 0 : __ldg(p.cu + hi);
-      x.table_row[g] = keys > 0 ? s_first : 0;
+      x.table_row[g] = keys > 0 ? first : 0;
     }
-    __syncthreads();
+  }
+  if (flags) flag_status(p.status, flags);
+  const int from = wrong || x.groups == 0 ? p.B : __ldg(x.offsets);
+  const int to = wrong || x.groups == 0 ? p.B : __ldg(x.offsets + x.groups);
+  for (int b = tid; b < p.B; b += kPlanThreads)   // sequences that lie in no group
+    if (b < from || b >= to) x.start[b] = 0;
+  __syncthreads();
+  const bool share = (int64_t)s_saved > kCallCost;
+  // of the sequences' own keys: steps of the kernel for few rows
+  const int step = few_keys(p.D);
+  int64_t steps = 0;
+  int longest = 0;
+  const auto own = [&](int b, int start) {
+    const int64_t n = (int64_t)__ldg(p.past + b) + __ldg(p.cu + b + 1) - __ldg(p.cu + b) - start;
+    const int k = (int)min(max((n + step - 1) / step, (int64_t)0), (int64_t)p.MB * p.BS);
+    steps += k;
+    longest = max(longest, k);
+  };
+  for (int g = warp; g < x.groups; g += kPlanWarps) {
+    const int lo = wrong ? 0 : __ldg(x.offsets + g), hi = wrong ? 0 : __ldg(x.offsets + g + 1);
+    const int keys = share ? __ldcg(x.group_keys + g) : 0;
+    for (int b = lo + lane; b < hi; b += 32) {
+      x.start[b] = keys;
+      own(b, keys);
+    }
+  }
+  for (int b = tid; b < p.B; b += kPlanThreads)
+    if (b < from || b >= to) own(b, 0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, o);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) {
+    atomicAdd(&s_steps, (unsigned long long)steps);
+    atomicMax(&s_longest, longest);
+  }
+  __syncthreads();
+  if (tid == 0) *x.active = share ? 1 : 0;
+  if (tid == 0 && x.choice) {   // as cross_layout does it, but with the lengths
+    const int64_t waves = ((int64_t)p.B * p.Hkv + x.sms - 1) / x.sms;
+    const int64_t even = (int64_t)s_steps * p.Hkv / (8 * x.sms);
+    *x.choice = 2 * waves * ((s_longest + 7) / 8) + 7 * (waves - 1) <= 10 + 2 * max(even, (int64_t)1);
   }
 }
 
 }  // namespace
+
+// What the rows may cost at most, one by one (see prefix_plan_kernel).
+static double most_alone(const CrossParams& p, int sms) {
+  const double keys = (double)p.MB * p.BS, seqs = p.T < p.B ? p.T : p.B;
+  double ns = seqs * keys * p.Hkv * p.D * 4 / 7300;
+  if (p.max_q > p.few)
+    ns += ((double)p.T / (p.tile_pos / 2) + seqs) * (keys / kTileKeys + 1) * p.Hkv *
+          (p.D == 64 ? 600 : 1030) / sms;
+  return ns;
+}
 
 size_t prefix_layout(CrossParams* shared, CrossParams* own, PrefixParams* x, char* base) {
   size_t off = 0;
@@ -91,11 +160,24 @@ size_t prefix_layout(CrossParams* shared, CrossParams* own, PrefixParams* x, cha
     off += (bytes + 255) / 256 * 256;
     return at;
   };
+  x->sms = device_sms();
+  own->few = 16 / own->G;
+  own->tile_pos = 2 * (128 / own->G);
+  if (x->groups == 0 || most_alone(*own, x->sms) <= kCallCost) {
+    own->check_offsets = x->offsets;
+    own->check_shared = x->shared;
+    own->check_groups = x->groups;
+    x->start = nullptr;
+    return cross_layout(own, base);
+  }
+  static const int32_t some = 0;   // sizes alone are asked for: any address
   const size_t G = (size_t)x->groups, rows = (size_t)own->T * own->Hq;
   x->start = reinterpret_cast<int32_t*>(take((size_t)own->B * 4));
   x->group_cu = reinterpret_cast<int32_t*>(take((G + 1) * 4));
   x->group_keys = reinterpret_cast<int32_t*>(take(G * 4));
   x->table_row = reinterpret_cast<int32_t*>(take(G * 4));
+  x->active = reinterpret_cast<int32_t*>(take(4));
+  x->choice = reinterpret_cast<int32_t*>(take(4));
   float* lse = reinterpret_cast<float*>(take(rows * 4));
   float* out = reinterpret_cast<float*>(take(rows * own->D * 4));
   *shared = *own;
@@ -103,35 +185,33 @@ size_t prefix_layout(CrossParams* shared, CrossParams* own, PrefixParams* x, cha
   shared->cu = x->group_cu;
   shared->klen = x->group_keys;
   shared->table_row = x->table_row;
+  shared->active = x->active;
   shared->out = out;
   shared->lse = lse;
   shared->max_q = own->T;
   own->start = x->start;
   own->prior_o = out;
   own->prior_lse = lse;
-  // one after the other, so both calls' pieces lie in the same place
-  char* const at = base ? base + off : nullptr;
-  const size_t a = G > 0 ? cross_layout(shared, at) : 0, b = cross_layout(own, at);
-  return off + (a > b ? a : b);
+  if (own->max_q <= own->few) own->choice = base ? x->choice : &some;
+  // apart: the second call's kernels begin while the first one's pieces are still joined
+  const size_t a = cross_layout(shared, base ? base + off : nullptr, true);
+  const size_t b = cross_layout(own, base ? base + off + a : nullptr);
+  if (!own->small) own->choice = nullptr;   // too many sequences for the one kernel
+  if (!own->choice) x->choice = nullptr;
+  return off + a + b;
 }
 
 cudaError_t launch_prefix(const CrossParams& shared, const CrossParams& own, const PrefixParams& x,
                           cudaStream_t s) {
+  if (!x.start) return launch_causal(own, s);
   {
     ProfScope ps("prefix_plan", s);
-    const int fit = 4 * device_sms(), most = x.groups > 1 ? x.groups : 1;
-    prefix_plan_kernel<<<most < fit ? most : fit, kPlanThreads, 0, s>>>(own, x);
+    prefix_plan_kernel<<<1, kPlanThreads, 0, s>>>(own, x);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (x.groups > 0) {
-    const cudaError_t e = launch_shared(shared, s);
-    if (e != cudaSuccess) return e;
-    return launch_causal(own, s);
-  }
-  CrossParams alone = own;   // nothing is shared: no prior results
-  alone.prior_o = alone.prior_lse = nullptr;
-  return launch_causal(alone, s);
+  const cudaError_t e = launch_shared(shared, s);
+  return e == cudaSuccess ? launch_causal(own, s) : e;
 }
 
 }  // namespace pkv

@@ -108,8 +108,13 @@ struct CrossParams {
   const int32_t* start;      // [B]
   const float* prior_o;      // [T][Hq][D] what the shared keys gave, and its lse [T][Hq]
   const float* prior_lse;
+  const int32_t* choice;     // 1: single tokens take the kernel for few and short sequences
+  const int32_t* check_offsets;   // groups that are looked at for faults alone
+  const int32_t* check_shared;
+  int check_groups;
   // the shared keys' own call: B groups; row of the block table of each
   const int32_t* table_row;  // [B]
+  const int32_t* active;     // 0: nothing is shared
   // plan (cross_dev.cuh)
   int few;                   // query rows of a sequence that the kernel for few rows takes
   int tile_pos;              // query positions of a tile of the kernel for many rows
@@ -140,14 +145,18 @@ struct PrefixParams {
   int32_t* group_cu;         // [groups + 1] query rows
   int32_t* group_keys;       // [groups]
   int32_t* table_row;        // [groups]
+  int32_t* active;           // see CrossParams
+  int32_t* choice;
+  int sms;
 };
-// the parameters of both calls from those of the second (its query, cache and sizes); the bytes
+// the parameters of both calls from those of the second (its query, cache and sizes); the bytes.
+// Without a start nothing is shared, whatever the lengths are.
 size_t prefix_layout(CrossParams* shared, CrossParams* own, PrefixParams* x, char* base);
 cudaError_t launch_prefix(const CrossParams& shared, const CrossParams& own, const PrefixParams& x,
                           cudaStream_t s);
 // fills the plan fields and the workspace pointers (from base, which may be NULL); returns
 // the workspace bytes
-size_t cross_layout(CrossParams* p, char* base);
+size_t cross_layout(CrossParams* p, char* base, bool tiles_only = false);
 // the kernels of the three forms (cross_dev.cuh) and, of each, the one for many rows (*_tiles.cu)
 cudaError_t launch_cross(const CrossParams& p, cudaStream_t s);
 cudaError_t launch_shared(const CrossParams& p, cudaStream_t s);

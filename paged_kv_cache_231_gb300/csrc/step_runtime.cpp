@@ -384,7 +384,8 @@ int pkv_paged_prefix_attention(const pkv_prefix_attention_args* args, void* work
   if (args->num_tokens == 0) return PKV_OK;
   if (args->output == args->query) return PKV_ERR_SHAPE;
   const size_t need = prefix_layout(&shared, &p, &x, static_cast<char*>(workspace));
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return PKV_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return PKV_ERR_WORKSPACE;
   return status_of(launch_prefix(shared, p, x, static_cast<cudaStream_t>(stream)));
 }
 
