@@ -268,9 +268,18 @@ def _check(call: str, status: int):
 
 
 # ----------------------------------------------------------------------------- helpers
+@functools.lru_cache(maxsize=1)
 def _torch():
     import torch
     return torch
+
+
+@functools.lru_cache(maxsize=1)
+def _device_of():
+    """The current device's number without torch.cuda's look whether CUDA is up (it is, where a
+    call has CUDA tensors), where this torch has that."""
+    torch = _torch()
+    return getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _ptr(t) -> Optional[int]:
@@ -690,20 +699,18 @@ def _check_tensors(stream, tensors) -> int:
     """tensors: (name, tensor or None, dtype, shape) each. They have to be contiguous, of that
     dtype and shape, on the current CUDA device, which is the stream's too. Returns the raw
     stream."""
-    device = None
+    device = -1
     for _, t, dtype, shape in tensors:
         if t is None:
             continue
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-            _refuse(stream, tensors)
         at = t.get_device()
-        if at != device:
-            if device is not None or at < 0:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or at != device:
+            if device >= 0 or at < 0 or not (t.dtype is dtype and t.shape == shape and
+                                             t.is_contiguous()):
                 _refuse(stream, tensors)
-            device = at
+            device = at   # the first one's
     torch = _torch()
-    if device != torch.cuda.current_device() or (stream is not None and
-                                                 stream.device_index != device):
+    if device != _device_of()() or (stream is not None and stream.device_index != device):
         _refuse(stream, tensors)
     if stream is not None:
         return stream.cuda_stream

@@ -9,11 +9,15 @@
 //
 // D / 16 neighbouring lanes hold a head, 16 elements each: a lane has both members of its 8 pairs
 // (two 16-byte chunks rotary_dim / 2 apart, or side by side) or two chunks behind rotary_dim, so
-// the norm is log2(D / 16) shuffles and the rotation none. A block stays on its SM with one or more
-// tokens side by side; while a group of tokens is normed, turned and written, the next one's rows and table
-// entries are on their way and the slots and positions of the one behind it. Cos and sin of a group
-// are gathered once into shared memory, whatever the axes' order. Other head sizes and rotary
-// dimensions take a warp for a head, which passes the normed row on through shared memory.
+// the norm is log2(D / 16) shuffles and the rotation none. Cos and sin of a group of tokens are
+// gathered once into shared memory, whatever the axes' order. Few tokens: a block for each group.
+// Many: a block stays, and while a group is normed, turned and written, the next one's rows are on
+// their way into a ring in shared memory and its table entries into registers, and so are the slots
+// and positions of the one behind it. Other head sizes and rotary dimensions take a warp for a
+// head, which passes the normed row on through shared memory.
+// Measured (32 + 2 x 8 heads of 128): 64 tokens 3.6 us, which is latency; 32768 tokens 140 us with one
+// axis and 146 us with three, 5.9 and 5.6 TB/s (87 and 83 % of measured copy bandwidth): barriers and
+// the gathering, which an append without norms (134 us) has as well, behind a longer computation.
 #include <type_traits>
 
 #include "append_dev.cuh"
@@ -28,8 +32,7 @@ using elem::Num;
 
 constexpr int kMaxThreads = 384;   // two blocks of 85 registers a thread to an SM
 constexpr int kFill = 256;   // threads that tokens side by side fill
-// groups of N tokens a thread whose rows are held or on their way
-__host__ __device__ constexpr int stages_of(int n) { return n == 4 ? 2 : 4; }
+constexpr int kStages = 2;   // groups of tokens whose rows the ring holds
 
 __device__ __forceinline__ float weight_at(const void* w, bool f32, bool bf16, int i) {
   return f32    ? __ldg(static_cast<const float*>(w) + i)
@@ -39,10 +42,12 @@ __device__ __forceinline__ float weight_at(const void* w, bool f32, bool bf16, i
 
 // tokens: tokens of a block side by side, N times as many a group; heads: heads of a token that
 // this block works on (blockIdx.y: which).
-template <typename T, typename TT, int D, bool kSide, int N>
+// kRing: the block goes on to further groups, whose rows come through a ring in shared memory; else
+// it has one.
+template <typename T, typename TT, int D, bool kSide, int N, bool kRing>
 __global__ void __launch_bounds__(kMaxThreads, 2)
     append_norm_kernel(const __grid_constant__ NormParams np, int tokens, int heads) {
-  constexpr int kLanes = D / 16, kStages = stages_of(N);
+  constexpr int kLanes = D / 16;
   const AxesParams& p = np.axes;
   // [2][N * tokens][4][R / 16] (cos, cos, sin, sin) of pairs 2 y and 2 y + 1 of item c at [y][c], so
   // that neighbouring lanes read neighbouring words; then (slot, flags) of each token, twice
@@ -74,17 +79,25 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
   const auto slot_of = [&](int stage, int n, int y) {
     return ring + ((stage * N + n) * 2 + y) * blockDim.x;
   };
+  uint4 alone[kRing ? 1 : N][2];
   const auto load = [&](int g, int stage) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int t = g * group + n * tokens + w;
       if (mine && g < groups && t < p.T) {
         const uint4* row = reinterpret_cast<const uint4*>(src + (int64_t)t * in_row);
-        cp_async_16(slot_of(stage, n, 0), row + chunk[0], 16);
-        cp_async_16(slot_of(stage, n, 1), row + chunk[1], 16);
+        if constexpr (kRing) {
+          cp_async_16(slot_of(stage, n, 0), row + chunk[0], 16);
+          cp_async_16(slot_of(stage, n, 1), row + chunk[1], 16);
+        } else {
+          alone[n][0] = __ldcs(row + chunk[0]);
+          alone[n][1] = __ldcs(row + chunk[1]);
+        }
+      } else if (!kRing) {
+        alone[n][0] = alone[n][1] = make_uint4(0, 0, 0, 0);
       }
     }
-    cp_async_commit();
+    if constexpr (kRing) cp_async_commit();
   };
   // Cos and sin of pair j of token k of a group, one pair to a thread and round. The table rows of
   // a group are asked for a group before its entries are, and these a group before their use.
@@ -128,32 +141,40 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
 
   int g = blockIdx.x;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) load(g + i * apart, i);
+  for (int i = 0; i < (kRing ? kStages - 1 : 1); ++i) load(g + i * apart, i);
   for (int e = threadIdx.x; e < 2 * D; e += blockDim.x) {
     const void* from = e < D ? np.qw : np.kw;
     s_weight[e / D][e % D] = from ? weight_at(from, np.weight_f32, p.bf16, e % D) : 1.f;
   }
   float co = 0.f, si = 0.f;
   fetch(row_of(g, first), first, co, si);
-  int row = row_of(g + apart, first);
+  int row = kRing ? row_of(g + apart, first) : -1;
   int2 tok_about = token(g);
   later(g, 0);
   if (gathers) put(0, first, co, si);
   if (first < group) about[first] = tok_about;
   __syncthreads();
   for (int buf = 0, stage = 0; g < groups; g += apart, buf ^= 1, stage = (stage + 1) % kStages) {
-    cp_async_wait<kStages - 2>();
-    load(g + (kStages - 1) * apart, (stage + kStages - 1) % kStages);
-    fetch(row, first, co, si);
-    row = row_of(g + 2 * apart, first);
-    tok_about = token(g + apart);
-    later(g + apart, buf ^ 1);
+    if constexpr (kRing) {
+      cp_async_wait<kStages - 2>();
+      load(g + (kStages - 1) * apart, (stage + kStages - 1) % kStages);
+      fetch(row, first, co, si);
+      row = row_of(g + 2 * apart, first);
+      tok_about = token(g + apart);
+      later(g + apart, buf ^ 1);
+    }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int tok = n * tokens + w, t = g * group + tok;
       // the shuffles are the whole warp's; rows that are not there are not written
       float v[16], sum = 0.f;
-      uint4 x[2] = {*slot_of(stage, n, 0), *slot_of(stage, n, 1)};
+      uint4 x[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        if constexpr (kRing)
+          x[y] = *slot_of(stage, n, y);
+        else
+          x[y] = alone[n][y];
       const uint32_t* u = reinterpret_cast<const uint32_t*>(x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -204,6 +225,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
       row[chunk[0]] = x[0];
       row[chunk[1]] = x[1];
     }
+    if (!kRing) break;
     if (gathers) put(buf ^ 1, first, co, si);
     if (first < group) about[(buf ^ 1) * group + first] = tok_about;
     __syncthreads();
@@ -278,7 +300,6 @@ __global__ void __launch_bounds__(32 * kWarps)
 // Of the largest block: 384 threads of 8 tokens' rows, or 128 tokens (of two heads of 64) with the
 // cos and sin of 32 pairs twice.
 constexpr int kMostShared = 150 * 1024;
-constexpr int kFewGroups = 2;   // groups of a block up to which it has two tokens a thread
 
 template <typename T, typename TT, int D, bool kSide>
 cudaError_t launch_lanes(const NormParams& np, cudaStream_t s) {
@@ -288,36 +309,47 @@ cudaError_t launch_lanes(const NormParams& np, cudaStream_t s) {
   const int parts = (all * kLanes + kMaxThreads - 1) / kMaxThreads, heads = (all + parts - 1) / parts;
   const int items = heads * kLanes, tokens = items * 2 <= kFill ? kFill / items : 1;
   const int threads = (tokens * items + 31) / 32 * 32, sms = device_sms();
-  const auto shared = [&](int n) {   // turned pairs, tokens and rows
+  const auto shared = [&](int n, bool ring) {   // turned pairs, tokens and rows
     return (size_t)n * tokens * (2 * sizeof(float4) * (p.R / 4) + sizeof(float4)) +
-           (size_t)threads * stages_of(n) * n * 32;
+           (ring ? (size_t)threads * kStages * n * 32 : 0);
   };
-  const auto fit = [&](int n) {   // blocks that the SMs take at once, by 80 registers a thread
-    const int regs = 65536 / (threads * 80), smem = (int)(225 * 1024 / (shared(n) + 1024 + 8 * D));
-    const int per_sm = regs < smem ? regs : smem;
-    return per_sm * sms / parts > 1 ? per_sm * sms / parts : 1;
-  };
-  const auto run = [&](auto n) {
+  const auto run = [&](auto n, auto ring) {
     constexpr int N = decltype(n)::value;
+    constexpr bool kRing = decltype(ring)::value;
     static std::atomic<uint64_t> configured{0};
     int dev = -1;
     if (needs_configure(configured, &dev)) {
       const cudaError_t e =
-          cudaFuncSetAttribute(append_norm_kernel<T, TT, D, kSide, N>,
+          cudaFuncSetAttribute(append_norm_kernel<T, TT, D, kSide, N, kRing>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
       if (e != cudaSuccess) return e;
       mark_configured(configured, dev);
     }
-    const int group = N * tokens, groups = (p.T + group - 1) / group, most = fit(N);
+    const size_t smem = shared(N, kRing);
+    const int group = N * tokens, groups = (p.T + group - 1) / group;
+    int most = groups;
+    if (kRing) {   // blocks that the SMs take at once, by 80 registers a thread
+      const int regs = 65536 / (threads * 80), by_smem = (int)(225 * 1024 / (smem + 1024 + 8 * D));
+      most = (regs < by_smem ? regs : by_smem) * sms / parts;
+      if (most < 1) most = 1;
+    }
     const dim3 grid((unsigned)(groups < most ? groups : most), (unsigned)parts);
-    append_norm_kernel<T, TT, D, kSide, N><<<grid, threads, shared(N), s>>>(np, tokens, heads);
+    append_norm_kernel<T, TT, D, kSide, N, kRing><<<grid, threads, smem, s>>>(np, tokens, heads);
     return cudaGetLastError();
   };
-  // Tokens of a thread and group: one while a wave of blocks takes all of them, four where a block
-  // goes through several groups (each ends with a barrier that waits for the slowest warp).
-  if (p.T <= (int64_t)tokens * fit(1)) return run(std::integral_constant<int, 1>());
-  if (p.T <= (int64_t)2 * tokens * fit(2) * kFewGroups) return run(std::integral_constant<int, 2>());
-  return run(std::integral_constant<int, 4>());
+  // A block for each group of tokens while one wave of blocks takes them all, with as few tokens to
+  // a thread as that needs: tokens of 384 items, with one, two, four to a thread and with the ring: 300
+  // 4.1, 4.1, 5.0 and 5.7 us, 600 6.6, 5.0, 5.1 and 5.8 us, 1200 10.9, 9.3, 7.8 and 9.2 us. Behind that
+  // blocks that stay and have the next rows on their way: 2500 22.7, 22.4, 19.9 and 18.3 us, 32768 258,
+  // 245, 192 and 140 us. Where a block holds many tokens side by side it is the gathering that takes
+  // the time, and the ring's registers and barriers cost more than they bring: 32768 tokens of 80 items
+  // 63.7, 54.6, 42.9 and 41.2 us, of 48 items 51.8, 51.2, 44.3 and 51.9 us.
+  const auto wave = [&](int n) { return (int64_t)(65536 / (threads * 80)) * n * tokens * sms / parts; };
+  if (p.T <= wave(1)) return run(std::integral_constant<int, 1>(), std::false_type());
+  if (p.T <= wave(2)) return run(std::integral_constant<int, 2>(), std::false_type());
+  if (p.T <= wave(4) || tokens > 3)
+    return run(std::integral_constant<int, 4>(), std::false_type());
+  return run(std::integral_constant<int, 4>(), std::true_type());
 }
 
 template <typename T, typename TT>

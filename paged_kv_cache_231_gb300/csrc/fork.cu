@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // Behind it: the whole table, but for the entries written above, and the copies.
 constexpr int kCopyThreads = 256;
-constexpr int kDeep = 4;                                // 16-byte words of a thread under way
+constexpr int kDeep = 8;   // 16-byte words of a thread under way
 constexpr int kPiece = kForkPiece;
 static_assert(kPiece == kCopyThreads * kDeep, "words of a unit");
 __global__ void __launch_bounds__(kCopyThreads)
@@ -222,12 +222,12 @@ __global__ void __launch_bounds__(kCopyThreads)
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const int i = piece * kPiece + k * kCopyThreads + tid;
-      if (i < n) x[k] = __ldcs(src + i);
+      if (i < n) x[k] = __ldg(src + i);   // the next copies read the same block
     }
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const int i = piece * kPiece + k * kCopyThreads + tid;
-      if (i < n) dst[i] = x[k];
+      if (i < n) __stcs(dst + i, x[k]);
     }
   }
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {

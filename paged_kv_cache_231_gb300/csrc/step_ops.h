@@ -76,11 +76,11 @@ struct ForkParams {
   int B, MB, BS, NB, bs_shift;
   int groups;                // groups of 1024 block ids
   int caches;
-  int pieces;                // units of 16 KB that a block of the widest cache has
+  int pieces;                // units of 32 KB that a block of the widest cache has
   int row_words[PKV_MAX_FORK_CACHES];   // 16-byte words of a token's row
   void* cache[PKV_MAX_FORK_CACHES];
 };
-constexpr int kForkPiece = 1024;   // words of a unit
+constexpr int kForkPiece = 2048;   // words of a unit
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t s);
 
 // ---- cross attention ------------------------------------------------------------------
