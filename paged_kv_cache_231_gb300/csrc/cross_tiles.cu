@@ -577,6 +577,11 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     if (F != kCausal && group == 1) {
       const int e = entry_of(tiles_at, k);
       from = steps_at[e] + (k - tiles_at[e]) * per_tile[e];
+    } else if (F == kCausal && listed) {
+      const int e = entry_of(tiles_at, k), left = (int)(k - tiles_at[e]);
+      const int tiles_h = first_tile[e + 1] - first_tile[e], h = left / tiles_h;
+      const int64_t* at_tile = before_tile + first_tile[e];
+      from = steps_at[e] + (int64_t)h * per_tile[e] + at_tile[left - h * tiles_h] - at_tile[0];
     } else {
       find(k, false, &from);
     }
@@ -650,16 +655,23 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
     run->whole = (int)whole;
     run->steps = c1 - c0;
   }
-  if (tid == 32 && whole > 0) run->first = find(u, false, &x);
-  if (tid == 64 && c1 > c0) run->at = find(c0, true, &x);
+  // The first whole tile, the first step and the last one, each by a thread of its own warp through
+  // one copy of the code (which all of them have to fetch: with three copies 3000 cycles more).
+  const int64_t in = c1 > c0 ? c1 - 1 : c0;
+  const bool by_step = tid != 32;
+  const int64_t k = tid == 32 ? (whole > 0 ? u : -1) : tid == 64 ? (c1 > c0 ? c0 : -1)
+                    : tid == 96 ? (in < total ? in : -1)
+                                : -1;
+  Cursor c{};
+  if (k >= 0) c = find(k, by_step, &x);
+  if (tid == 32 && k >= 0) run->first = c;
+  if (tid == 64 && k >= 0) run->at = c;
   // The record: the range that the run ends in, if it goes on behind it. The unit in whose run the
   // range begins joins the pieces, and so does every further one but the last (their runs lie inside
   // the range, or are empty): a share of the rows each.
   if (tid == 96) {
     int4 a = make_int4(0, 0, 0, 0), b = make_int4(0, 0, 0, 0);
-    const int64_t in = c1 > c0 ? c1 - 1 : c0;
-    if (in < total) {
-      const Cursor c = find(in, true, &x);
+    if (k >= 0) {
       const int64_t start = in - c.s, end = start + steps_of<F>(p, c.q, c.r);
       if (end > c1 && (c1 > c0 || start < c0)) {
         int v = u, from = u;

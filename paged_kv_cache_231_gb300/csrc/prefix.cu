@@ -134,10 +134,15 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
   }
   __syncthreads();
   if (tid == 0) *x.active = share ? 1 : 0;
-  if (tid == 0 && x.choice) {   // as cross_layout does it, but with the lengths
+  // The kernel for few and short sequences, or an even share of the steps for every warp and a join:
+  // in units of a step of 0.85 us, the longest sequence's share of a warp and 3.5 for every wave of
+  // blocks behind the first, or the even share and 15 for its plan and the join (64 tokens behind 8192
+  // shared keys and up to 64, 256, 512, 1024 of their own: 57.7, 64.4, 72.8 and 81.6 us, or 64.8, 70.6,
+  // 81.8 and 95.8 us).
+  if (tid == 0 && x.choice) {
     const int64_t waves = ((int64_t)p.B * p.Hkv + x.sms - 1) / x.sms;
     const int64_t even = (int64_t)s_steps * p.Hkv / (8 * x.sms);
-    *x.choice = 2 * waves * ((s_longest + 7) / 8) + 7 * (waves - 1) <= 10 + 2 * max(even, (int64_t)1);
+    *x.choice = 2 * ((s_longest + 7) / 8) + 7 * (waves - 1) <= 30 + 2 * even;
   }
 }
 
