@@ -93,12 +93,14 @@ typedef enum pkv_status {
                                     partial */
 #define PKV_DEV_TIMEOUT 32u      /* a bounded wait of a tensor-core kernel gave up: the
                                     outputs that CTA had not yet written (prefill tiles,
-                                    block-sparse partials, cross attention tiles) are
+                                    block-sparse partials, tiles of the cross, window and
+                                    prefix attention) are
                                     not written or not valid; it waited
                                     (bounded) for what it had issued, freed its tensor
                                     memory and returned */
 #define PKV_DEV_NO_BLOCKS 64u    /* pkv_paged_schedule: the pool has too few free blocks:
-                                    the row gets no tokens this time */
+                                    the row gets no tokens this time; pkv_paged_fork: the
+                                    row is freed */
 
 typedef enum pkv_dtype { PKV_F16 = 1, PKV_BF16 = 2, PKV_F32 = 3, PKV_I32 = 4 } pkv_dtype;
 
@@ -688,22 +690,24 @@ typedef struct pkv_prefix_attention_args {
   float scale;
 } pkv_prefix_attention_args;
 
-/* Host only: workspace bytes pkv_paged_prefix_attention needs on the current device. It holds
- * one output in 32 bits (num_tokens * num_heads * (head_size + 1) * 4 bytes) and what the
- * kernels need. */
+/* Host only: workspace bytes pkv_paged_prefix_attention needs on the current device (may be 0). It
+ * holds one output in 32 bits (num_tokens * num_heads * (head_size + 1) * 4 bytes) and what the
+ * kernels need, where these sizes may have something to share. */
 int pkv_paged_prefix_attention_workspace_size(const pkv_prefix_attention_args* args,
                                               size_t* bytes);
 
 /* What pkv_paged_window_attention computes without a window, for sequences of which some begin
  * alike: the keys that a group shares are read through the table row of its first sequence with
  * new tokens, once for the rows of all of them, and joined in 32 bits with what each row sees
- * behind them. A group shares shared_seqlens[g] keys, or fewer where one of its sequences with new tokens has a
- * shorter past. Sequences outside all groups and groups with fewer than two sequences that have
- * new tokens share nothing, nor does a group of which one sequence is bad. A negative shared_seqlens
- * entry is taken as 0 and sets PKV_DEV_BAD_SEQUENCE; group offsets that descend or leave 0 ..
- * batch set it too, and then nothing is shared at all. Sequences of a group whose table entries
- * differ where they are said to be shared are attended with those of its first. A shared block
- * that is unmapped sets PKV_DEV_BAD_BLOCK. */
+ * behind them. A group shares shared_seqlens[g] keys, or fewer where one of its sequences with new
+ * tokens has a shorter past. Sequences outside all groups and groups with fewer than two
+ * sequences that have new tokens share nothing, nor does a group of which one sequence is bad; and
+ * where sharing would save less time than its kernels take, as the lengths tell, nothing is shared
+ * (the results then differ by rounding). A negative shared_seqlens entry is taken as 0 and
+ * sets PKV_DEV_BAD_SEQUENCE; group offsets that descend or leave 0 .. batch set it too, and then
+ * nothing is shared at all. The table entries that a group is said to share have to be equal: where
+ * they are not, a sequence's output is that of its own or of the first one's. A shared block that is
+ * unmapped sets PKV_DEV_BAD_BLOCK. Equal calls give equal bits. */
 int pkv_paged_prefix_attention(const pkv_prefix_attention_args* args, void* workspace,
                                size_t workspace_bytes, void* stream);
 
@@ -773,8 +777,8 @@ int64_t pkv_launch_count(void);
 void pkv_profiler_enable(int on);
 
 /* Testing hook for the give-up path of the tensor-core kernels' bounded waits (the
- * tcgen05 prefill, the two block-sparse partial kernels and the cross attention's kernel for
- * many rows). The pages have no
+ * tcgen05 prefill, the two block-sparse partial kernels and the kernel for many rows of the
+ * cross, window and prefix attention). The pages have no
  * counterpart. max_polls replaces the default poll bound of every such wait (0 restores
  * the default); with withhold_first_copy != 0 (which needs max_polls > 0) every CTA of
  * those kernels announces its first bulk copy (the first K box of its first prefill
@@ -785,6 +789,11 @@ void pkv_profiler_enable(int on);
  * calls made after it, process-wide; not thread-safe; for tests only. Returns PKV_OK,
  * or PKV_ERR_SHAPE for withhold_first_copy without a bound. */
 int pkv_testing_wait_limit(uint32_t max_polls, int32_t withhold_first_copy);
+/* Testing hook for pkv_paged_prefix_attention: mode 1 shares whatever can be shared, 2 shares
+ * nothing, whether it saves anything or not; 0 restores the rule. The workspace size follows it.
+ * Applies to calls made after it, process-wide; for tests only. Returns PKV_OK, or PKV_ERR_SHAPE
+ * for another mode. */
+int pkv_testing_prefix_sharing(int32_t mode);
 void pkv_profiler_reset(void);
 int pkv_profiler_query(const char* kernel, double* total_ms, int64_t* launches);
 

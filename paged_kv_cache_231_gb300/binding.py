@@ -239,6 +239,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             ("pkv_paged_fork_workspace_size", [ctypes.POINTER(ForkArgs),
                                                ctypes.POINTER(ctypes.c_size_t)]),
             ("pkv_paged_fork", [ctypes.POINTER(ForkArgs), c_vp, ctypes.c_size_t, c_vp]),
+            ("pkv_testing_prefix_sharing", [c_i32]),
             ("pkv_testing_wait_limit", [ctypes.c_uint32, c_i32])):
         fn = getattr(lib, name)
         fn.restype = c_i32
@@ -272,14 +273,6 @@ def _check(call: str, status: int):
 def _torch():
     import torch
     return torch
-
-
-@functools.lru_cache(maxsize=1)
-def _device_of():
-    """The current device's number without torch.cuda's look whether CUDA is up (it is, where a
-    call has CUDA tensors), where this torch has that."""
-    torch = _torch()
-    return getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _ptr(t) -> Optional[int]:
@@ -699,7 +692,7 @@ def _check_tensors(stream, tensors) -> int:
     """tensors: (name, tensor or None, dtype, shape) each. They have to be contiguous, of that
     dtype and shape, on the current CUDA device, which is the stream's too. Returns the raw
     stream."""
-    device = -1
+    device = -2   # of no tensor; one that is not on a GPU says -1
     for _, t, dtype, shape in tensors:
         if t is None:
             continue
@@ -710,12 +703,14 @@ def _check_tensors(stream, tensors) -> int:
                 _refuse(stream, tensors)
             device = at   # the first one's
     torch = _torch()
-    if device != _device_of()() or (stream is not None and stream.device_index != device):
+    # the current device and its stream's handle without torch.cuda's look whether CUDA is up (it
+    # is) and without an object for it (a microsecond of the call), where this torch has that
+    now = getattr(torch._C, "_cuda_getDevice", None)
+    if device < 0 or device != (now() if now is not None else torch.cuda.current_device()) or (
+            stream is not None and stream.device_index != device):
         _refuse(stream, tensors)
     if stream is not None:
         return stream.cuda_stream
-    # the current stream's handle without an object for it (a microsecond of the call), where
-    # this torch has that
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
@@ -817,7 +812,8 @@ def _append_fields(query, key, value, key_cache, value_cache, slot_mapping, posi
         rows = cos_cache.shape[0] if cos_cache.dim() == 2 else -1
         if cos_cache.dtype is dt:
             tdt = dt
-        pairs = bytes(half) if pair_axis is None else bytes(list(pair_axis))
+        pairs = bytes(half) if pair_axis is None else bytes(
+            pair_axis if type(pair_axis) is list else list(pair_axis))
         if len(pairs) != half or half > MAX_ROTARY_PAIRS:
             raise ValueError(f"pair_axis: one axis for each of {half} pairs (at most "
                              f"{MAX_ROTARY_PAIRS}), got {len(pairs)}")
@@ -1267,6 +1263,13 @@ def pkv_testing_wait_limit(max_polls: int = 0, withhold_first_copy: bool = False
     up. pkv_testing_wait_limit() restores the defaults."""
     _check("pkv_testing_wait_limit",
            load_library().pkv_testing_wait_limit(int(max_polls), 1 if withhold_first_copy else 0))
+
+
+def pkv_testing_prefix_sharing(mode: int = 0):
+    """Testing hook of pkv_paged_prefix_attention: 1 shares whatever can be shared, 2 nothing, 0
+    restores the rule. For tests only."""
+    _check("pkv_testing_prefix_sharing", load_library().pkv_testing_prefix_sharing(int(mode)))
+    _prefix_workspace.cache_clear()
 
 
 def pkv_paged_attention_static_workspace(query, key, value, key_cache, value_cache,

@@ -206,7 +206,7 @@ constexpr int kJoinWarps = 8;
 // pieces of a row that a warp asks for at once (8 lowered the occupancy: 64 tokens 16 us, not 12)
 constexpr int kAhead = 4;
 // rows of a tile's record that a block takes, where one unit alone joins it (records of many pieces:
-// 12 us, with 64 18 us; of 16 pieces joined by their 15 units XXX us)
+// 12 us, with 64 18 us)
 constexpr int kJoinRows = 16;
 
 template <int D>

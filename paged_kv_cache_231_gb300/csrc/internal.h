@@ -257,6 +257,8 @@ bool sparse_tc_shape(int D, int block_size, int qhead, int page_size, int ppb,
 // whether tensor-core kernels withhold their first bulk copy
 uint32_t testing_wait_tries();
 int testing_withhold_copy();
+// testing hook of the prefix attention: 1 shares whatever can be shared, 2 nothing, 0 by the rule
+int testing_prefix_sharing();
 
 // SM count of the current device (runtime.cpp)
 int device_sms();

@@ -64,8 +64,10 @@ void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 namespace {
 std::atomic<uint32_t> g_wait_tries{0};
 std::atomic<int> g_withhold{0};
+std::atomic<int> g_sharing{0};
 }  // namespace
 uint32_t testing_wait_tries() { return g_wait_tries.load(std::memory_order_relaxed); }
+int testing_prefix_sharing() { return g_sharing.load(std::memory_order_relaxed); }
 int testing_withhold_copy() { return g_withhold.load(std::memory_order_relaxed); }
 
 // ---------------------------------------------------------------- helpers
@@ -347,6 +349,12 @@ int pkv_testing_wait_limit(uint32_t max_polls, int32_t withhold_first_copy) {
   if (withhold_first_copy && max_polls == 0) return PKV_ERR_SHAPE;
   g_wait_tries.store(max_polls, std::memory_order_relaxed);
   g_withhold.store(withhold_first_copy ? 1 : 0, std::memory_order_relaxed);
+  return PKV_OK;
+}
+
+int pkv_testing_prefix_sharing(int32_t mode) {
+  if (mode < 0 || mode > 2) return PKV_ERR_SHAPE;
+  g_sharing.store(mode, std::memory_order_relaxed);
   return PKV_OK;
 }
 

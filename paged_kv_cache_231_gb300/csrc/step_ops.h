@@ -148,6 +148,7 @@ struct PrefixParams {
   int32_t* active;           // see CrossParams
   int32_t* choice;
   int sms;
+  int always;                // testing hook: share whatever it saves
 };
 // the parameters of both calls from those of the second (its query, cache and sizes); the bytes.
 // Without a start nothing is shared, whatever the lengths are.

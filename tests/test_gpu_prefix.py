@@ -12,6 +12,14 @@ from .step_util import DEV, i32
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(params=["whatever can be", "by the rule"], autouse=True)
+def sharing(request):
+    """Small cases would hardly share anything by the rule."""
+    B.pkv_testing_prefix_sharing(1 if request.param == "whatever can be" else 0)
+    yield request.param
+    B.pkv_testing_prefix_sharing()
+
+
 def case(seed, nq, own, groups, **kw):
     """own: tokens of each sequence behind what its group shares."""
     past, at = [], 0
@@ -134,3 +142,44 @@ def test_equal_bits_and_graph():
     other = B.pkv_paged_prefix_attention(*a, num_heads=c.hq, kv_num_heads=c.hkv, stream=s)
     s.synchronize()
     assert torch.equal(other.cpu(), want)
+
+
+@pytest.mark.parametrize("nq,own,keys,heads,kv,head_size,dtype", [
+    ([1] * 64, list(range(64)), 2048, 32, 8, 128, "f16"),        # single tokens, short own keys
+    ([1] * 40, [0] * 39 + [3000], 4096, 16, 16, 64, "bf16"),     # one of them with many
+    ([4] * 40, [9] * 40, 2048, 32, 8, 128, "bf16"),              # drafts: 16 rows of a kv head
+    ([9] * 30, [5] * 30, 4096, 16, 16, 64, "f16"),               # rows of a tile's quarter
+    ([200, 150], [0, 7], 1024, 8, 2, 128, "bf16"),               # nothing to gain
+])
+def test_sizes_that_the_rule_is_about(nq, own, keys, heads, kv, head_size, dtype, sharing):
+    c = case(15, nq, own, [(len(nq), keys)], num_heads=heads, kv_heads=kv, head_size=head_size,
+             dtype=dtype, block_size=16)
+    ref = c.oracle()
+    c.check(prefix=True, max_query_len=max(nq), reference=ref)
+    c.check(prefix=True, reference=ref)            # the longest sequence is not named
+
+
+def test_shared_or_not_is_the_same_but_for_rounding():
+    c = case(16, [1] * 20 + [30], [7] * 20 + [40], [(21, 512)], head_size=128, dtype="bf16")
+    B.pkv_testing_prefix_sharing(2)
+    alone = c.gpu(prefix=True)
+    B.pkv_testing_prefix_sharing(1)
+    shared = c.gpu(prefix=True)
+    same = c.gpu()                                 # the window attention without a window
+    assert torch.equal(alone[0], same[0]) and torch.equal(alone[1], same[1])
+    assert not torch.equal(alone[0], shared[0])    # the hook does what it says
+    assert torch.allclose(alone[1], shared[1], atol=1e-5)
+
+
+def test_workspace_given_and_refused():
+    c = case(17, [1] * 6, [3] * 6, [(6, 256)])
+    a = c.device() + [i32(c.groups), i32(c.shared)]
+    want = c.gpu(prefix=True)[0]
+    out = torch.empty_like(a[0])
+    kw = dict(num_heads=c.hq, kv_num_heads=c.hkv)
+    need = B.pkv_paged_prefix_attention_workspace_size(B.make_prefix_args(*a, out, **kw))
+    ws = torch.full((max(need, 1) + 512,), 255, dtype=torch.uint8, device=DEV)
+    B.pkv_paged_prefix_attention(*a, output=out, workspace=ws, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want)
+    assert (ws[need:] == 255).all()
