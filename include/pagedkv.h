@@ -531,9 +531,8 @@ typedef struct pkv_append_axes_args {
  * copied unrotated. Two tokens of one slot leave there, in each 16 bytes, the one's or the
  * other's. query_out and the caches must not overlap the inputs or one another. head_size a
  * multiple of 8, <= 256; otherwise PKV_ERR_UNSUPPORTED.
- * pkv_paged_attention reads fp16 pools alone. A bf16 pool is read by pkv_cross_attention, which has
- * no causal mask: single tokens over their past + 1 states and encoder states, not the tokens of a
- * prompt over one another. */
+ * pkv_paged_attention reads fp16 pools alone. A bf16 pool is read by pkv_paged_window_attention
+ * and pkv_paged_prefix_attention, and by pkv_cross_attention, which has no causal mask. */
 int pkv_paged_append_rotary_axes(const pkv_append_axes_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------------

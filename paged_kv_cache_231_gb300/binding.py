@@ -942,8 +942,8 @@ def _own_workspace(need: int, like, stream, raw: int):
 
 
 def release_workspaces():
-    """Gives back the workspaces that pkv_cross_attention keeps for the calling thread (memory
-    of torch's caching allocator; calls under way finish undisturbed)."""
+    """Gives back the workspaces that the attention calls and pkv_paged_fork keep for the calling
+    thread (memory of torch's caching allocator; calls under way finish undisturbed)."""
     _OWN.__dict__.clear()
 
 

@@ -2,6 +2,10 @@
 // (pkv_cross_attention): out = softmax(scale q k^T) v over the n_b states of the row's
 // sequence, lse = ln sum e^{scale q k}. Scores are held in log2 units (scale * log2 e).
 //
+// window.cu and prefix.cu compile this file for the causal form and the keys that a group shares
+// (see cross_dev.cuh): 64 single tokens over windows of 4096 of 512 to 8192 keys, 8 kv heads of 128,
+// 133 us with the join (90 % of measured copy bandwidth).
+//
 // This file: the kernel for few query rows (sequences with at most 16 rows of a kv head:
 // single tokens, drafts), the join of pieces and the launches. cross_tiles.cu: many rows.
 //

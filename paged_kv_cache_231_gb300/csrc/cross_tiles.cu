@@ -1,4 +1,5 @@
-// Cross attention, sequences with many query rows: tiles on the 5th-generation tensor core.
+// Cross attention, sequences with many query rows: tiles on the 5th-generation tensor core; also
+// in its causal form and for the keys that a group shares (window_tiles.cu, prefix_tiles.cu).
 //
 // A range is a tile of 256 rows = two halves of 128 rows = (128 / G) query positions x G
 // heads of one kv head each, against 128 keys a step. Per step the tensor core does
@@ -26,7 +27,7 @@
 // odd ones, and half 0 joins the two (m, l, O) at the end.
 // TMEM columns: S_0 0..127 (weights over 0..63), S_1 128..255, O_0 256.., O_1 384...
 // Measured: 16 sequences of up to 2048 queries over up to 4096 states, 32 heads of 128 on 8 kv
-// heads: 460 us for 0.571 TFLOP, 1240 TFLOP/s (64 % of the measured dense rate; the tensor pipe is
+// heads: 440 us for 0.571 TFLOP, 1300 TFLOP/s (67 % of the measured dense rate; the tensor pipe is
 // active 56 % of the time): the two halves' softmaxes, each a chain of TMEM loads, exponentials and
 // TMEM stores, and the hand-offs between them and the products set the pace. Few rows and long
 // sequences (100 queries, 20000 to 60000 states, 16 heads of 64): 80 us, 4.7 TB/s.
@@ -356,9 +357,9 @@ __device__ __forceinline__ void skip_ranges(const CrossParams& p, Cursor& c, int
 
 // Walks the parts of a run; every role walks for itself. f gets the part, its cursor and its
 // number among the cut parts (-1: a whole tile). One loop for both kinds, so that a role's code is
-// there once: code that an SM has not run yet costs it a cycle for every three bytes, and a second
-// copy for the cut parts cost each block 12 000 cycles (8 prompts of up to 2048 tokens behind a window
-// of 1024: XXX us, so YYY us).
+// there once: an SM has to fetch code that it has not run yet, and a second copy for the cut parts
+// cost each block 12 000 cycles (8 prompts of up to 2048 tokens behind a window of 1024: 180 us, so
+// 167 us).
 template <Form F, typename Fn>
 __device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, Fn f) {
   int whole = run.whole, i = whole > 0 ? -1 : 0;
