@@ -1114,14 +1114,18 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
       }
       tc::tmem_wait_ld();
       const bool masked = (seen.x & seen.y & seen.z & seen.w) != 0xffffffffu;
-      if (masked || p.scale_log2 < 0.f) {   // the maximum is another one
-        const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
+      const bool turned = p.scale_log2 < 0.f;
+      if (masked || turned) {   // the maximum is another one
+        if (turned) {
+#pragma unroll
+          for (int x = 0; x < 128; ++x) v[x] = -v[x];
+        }
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
-          v[4 * x] = (seen.x >> x) & 1u ? sign * v[4 * x] : -INFINITY;
-          v[4 * x + 1] = (seen.y >> x) & 1u ? sign * v[4 * x + 1] : -INFINITY;
-          v[4 * x + 2] = (seen.z >> x) & 1u ? sign * v[4 * x + 2] : -INFINITY;
-          v[4 * x + 3] = (seen.w >> x) & 1u ? sign * v[4 * x + 3] : -INFINITY;
+          v[4 * x] = (seen.x >> x) & 1u ? v[4 * x] : -INFINITY;
+          v[4 * x + 1] = (seen.y >> x) & 1u ? v[4 * x + 1] : -INFINITY;
+          v[4 * x + 2] = (seen.z >> x) & 1u ? v[4 * x + 2] : -INFINITY;
+          v[4 * x + 3] = (seen.w >> x) & 1u ? v[4 * x + 3] : -INFINITY;
         }
 #pragma unroll
         for (int y = 0; y < 4; ++y) e[y] = fmaxf(v[2 * y], v[2 * y + 1]);
@@ -1216,7 +1220,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
       Weights w{0.f, 0.f, 0.f};
       if (mine) w = weights_of<F>(p, row, m, l, F == kCausal && c.q.lo > 0);
       const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-#pragma unroll
+#pragma unroll 1   // code that the loop above drove out of the nearest cache: fetched once, not four times
       for (int x = 0; x < D / 32; ++x) {
         float o[32];
         result(x, o);
@@ -1254,7 +1258,7 @@ __device__ void softmax_role(const CrossParams& p, unsigned char* sm, const Run&
       if (mine && p.lse) p.lse[row] = w.lse;
     } else {
       const int64_t row = (2 * (int64_t)blockIdx.x + (index == 0 ? 0 : 1)) * 256 + half * 128 + r;
-#pragma unroll
+#pragma unroll 1   // code that the loop above drove out of the nearest cache: fetched once, not four times
       for (int x = 0; x < D / 32; ++x) {
         float o[32];
         result(x, o);

@@ -108,6 +108,31 @@ def test_types_and_axes(dtype, table, weight, packed, axes, turns):
          pad=(0, 7, 60)).check()
 
 
+@pytest.mark.parametrize("tokens,heads,kv,head_size,rotary_dim,interleaved", [
+    # one, two and four tokens a thread, a block for each group or blocks that stay
+    (200, 16, 4, 256, 256, False), (500, 16, 4, 256, 256, True), (900, 16, 4, 256, 64, False),
+    (1300, 16, 4, 256, 256, False), (1500, 4, 2, 256, 64, True), (3000, 4, 2, 256, 32, False),
+    (4000, 4, 2, 256, 64, True), (5000, 1, 1, 64, 32, False), (9000, 6, 3, 128, 16, True),
+    (30000, 2, 1, 64, 16, False)])
+def test_tokens_of_a_thread(tokens, heads, kv, head_size, rotary_dim, interleaved):
+    Case(10, tokens, num_heads=heads, kv_heads=kv, head_size=head_size, rotary_dim=rotary_dim,
+         interleaved=interleaved, axes=2, pad=(1, tokens - 1)).check()
+
+
+@pytest.mark.parametrize("tokens", [40, 2000])
+def test_packed_rows_whose_queries_are_left(tokens):
+    c = Case(11, tokens, packed=True, head_size=128, rotary_dim=64, axes=1)
+    kc, vc = (x.to(DEV) for x in (c.kc, c.vc))
+    want = [x.cpu() for x in c.check()]
+    args = dict(num_heads=c.hq, kv_num_heads=c.hkv, key_weight=c.kw.to(DEV), epsilon=c.eps,
+                query_weight=c.qw.to(DEV), cos_cache=c.cos.to(DEV), sin_cache=c.sin.to(DEV),
+                rotary_dim=c.r, pair_axis=c.axis)
+    assert B.pkv_paged_append_norm_rotary(c.q.to(DEV), None, None, kc, vc, i32(c.slots),
+                                          i32(c.pos), rotate_query=False, **args) is None
+    torch.cuda.synchronize()
+    assert torch.equal(kc.cpu(), want[1]) and torch.equal(vc.cpu(), want[2])
+
+
 @pytest.mark.parametrize("weights", ["q", "k", "qk"])
 @pytest.mark.parametrize("head_size", [128, 72])
 def test_one_side_alone(weights, head_size):
