@@ -756,9 +756,18 @@ size_t cross_layout(CrossParams* p, char* base, bool tiles_only) {
   const double ranges = (double)p->B * p->Hkv, waves = std::ceil(ranges / sms);
   const double steps = std::ceil(std::ceil(keys / few_keys(p->D)) / kWarps);
   const double even = ranges * steps / sms;
+  double alone = waves * steps + 3.5 * (waves - 1);
+  // Causal calls go by a closer fit (the others keep theirs, and with it the order of their sums): what
+  // the last wave costs when it fills a part f of the SMs, and a sixth of a wave for lengths that
+  // differ. 32 tokens, 8 kv heads of 128, 100, 500, 1200 and 4000 keys: 9.8, 19.6, 33.1 and 86.0 us, by
+  // even shares 14.5, 24.1, 39.3 and 91.2 us; keys from a tenth of that on 9.1, 16.1, 22.1 and 66.5 us,
+  // by even shares 11.9, 19.7, 25.7 and 59.9 us.
+  if (p->past && ranges > sms) {
+    const double w = ranges / sms, f = w - std::floor(w), last = 1.04 - 0.5 * f;
+    alone = (std::floor(w) + (f > 0 ? (f > last ? f : last) + 0.15 : 0)) * steps + 2 * (waves - 1);
+  }
   p->small = p->max_q <= p->few && ranges <= 4.0 * sms &&
-             (p->choice != nullptr ||
-              waves * steps + 3.5 * (waves - 1) <= 5 + (even > 1 ? even : 1));
+             (p->choice != nullptr || alone <= 5 + (even > 1 ? even : 1));
   if (p->small && !p->choice) return 0;
   if (tiles_only) p->few_units = 0;
   const size_t fu = (size_t)p->few_units, tu = (size_t)p->tile_units;
