@@ -272,6 +272,19 @@ struct Joined {
       store_pair<T, F>(p, row * D + lane * V + v, w, acc[v], acc[v + 1]);
     if (p.lse && lane == 0) p.lse[row] = w.lse;
   }
+  // for the join, which knows the result of the shared keys
+  __device__ __forceinline__ void keep(const CrossParams& p, int64_t row, int lane) const {
+#pragma unroll
+    for (int v = 0; v < V; ++v) __stcg(p.apart_o + row * D + lane * V + v, acc[v]);
+    if (lane == 0) __stcg(p.apart_ml + row, make_float2(M, L));
+  }
+  __device__ __forceinline__ void take(const CrossParams& p, int64_t row, int lane) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = __ldcg(p.apart_o + row * D + lane * V + v);
+    const float2 ml = __ldcg(p.apart_ml + row);
+    M = ml.x;
+    L = ml.y;
+  }
 };
 
 // ---------------------------------------------------------------------------- few rows
@@ -310,10 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int flags = 0;
   const int gw = blockIdx.x * kWarps + warp;
+  // Beside the tiles of the shared keys the others leave their SM to the next block; one waits, so
+  // that this kernel's end is that of the tiles too.
+  const bool last_block = blockIdx.x + 1 == gridDim.x;
   if constexpr (F == kCausal) {
     if (p.choice) {   // both kinds of this kernel are launched: one of them works
       if ((__ldcg(p.choice) != 0) != kSmall) {
-        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        if (!kSmall || last_block) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         return;
       }
     }
@@ -325,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
     const int work = p.B * p.Hkv;
     if ((int)blockIdx.x >= work) {
       zero_rows<T, D, F>(p, gw - work * kWarps, ((int)gridDim.x - work) * kWarps, lane, -1);
+      if (last_block) asm volatile("griddepcontrol.wait;\n" ::: "memory");
       return;
     }
     bool zero;
@@ -551,15 +568,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossParams p) {
         for (int v = 0; v < Joined<D>::V; ++v)
           j.acc[v] += by * po[at * D + lane * Joined<D>::V + v];
       }
-      j.template write<T, F>(p, (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G, lane,
-                             F == kCausal && cc.q.lo > 0);
+      const int64_t row = (int64_t)(cc.q.cu0 + r / p.G) * p.Hq + cc.r * p.G + r % p.G;
+      if (F == kCausal && p.apart_o && cc.q.lo > 0)
+        j.keep(p, row, lane);
+      else
+        j.template write<T, F>(p, row, lane, F == kCausal && cc.q.lo > 0);
     }
   } else if (pl.zero) {
     zero_rows<T, D, F>(p, gw, p.few_units, lane, pl.ordered ? 1 : 0);
   }
   if (flags) flag_status(p.status, flags);
   // the join behind this kernel waits for it alone: it must not end before the one in front
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (!kSmall || F != kCausal || !p.apart_o)
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
 // Blocks 0 .. : kBlocks for the record of each block of the kernel for many rows. Behind
@@ -578,7 +599,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cross_join_kernel(CrossParams
   const bool tile = (int)blockIdx.x < tile_blocks;
   const int unit = tile ? blockIdx.x / kBlocks : blockIdx.x - tile_blocks;
   if (F == kShared && __ldcg(p.active) == 0) return;
-  if (F == kCausal && !tile && p.choice && __ldcg(p.choice) != 0) return;   // no pieces
+  if (F == kCausal && !tile && p.choice && __ldcg(p.choice) != 0) {   // no pieces: whole rows
+    const int per_head = p.few_rows, work = p.B * p.Hkv * per_head;   // at most 4 * 16 for an SM
+    for (int i = unit * kJoinWarps + warp; i < work; i += p.few_units * kJoinWarps) {
+      const int head = i / per_head, r = i - head * per_head, b = head / p.Hkv;
+      int flags = 0;
+      bool zero;
+      const Seq q = read_seq<false, F>(p, b, &flags, &zero);   // the other kernel reports
+      if (q.ranges == 0 || q.lo == 0 || r >= q.rows * p.G) continue;
+      const int64_t row = (int64_t)(q.cu0 + r / p.G) * p.Hq + (head - b * p.Hkv) * p.G + r % p.G;
+      Joined<D> j;
+      j.take(p, row, lane);
+      j.template write<T, F>(p, row, lane, true);
+    }
+    return;
+  }
   const int4* rec = (tile ? p.tile_rec : p.few_rec) + 2 * unit;
   const int4 a = __ldcg(rec), about = __ldcg(rec + 1);
   const int tokens = about.x;
@@ -656,7 +691,7 @@ constexpr const char* kNames[][2] = {{"cross_decode", "cross_combine"},
                                      {"window_decode", "window_combine"}};
 
 template <typename T, int D, Form F>
-cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
+cudaError_t launch_typed(const CrossParams& p, cudaStream_t s, int parts) {
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -666,7 +701,7 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
   // The tiles first: the other kernel's blocks then fill the SMs as theirs end (a call without few
   // rows spends 7 us on them otherwise). They read inputs and write rows of their own.
   if (p.tile_units > 0) {
-    const cudaError_t e = PKV_LAUNCH(_tiles)(p, s);
+    const cudaError_t e = parts & kTilesPart ? PKV_LAUNCH(_tiles)(p, s) : cudaSuccess;
     if (e != cudaSuccess) return e;
     cfg.numAttrs = 1;
   }
@@ -687,7 +722,7 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
     }
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Ring<D>::kBytes;
-    if (p.small) {
+    if (p.small && (parts & kSmallPart)) {
       ProfScope ps(kNames[F][0], s);
       const unsigned zero = (unsigned)((p.T + kThreads - 1) / kThreads);
       cfg.gridDim = dim3((unsigned)(p.B * p.Hkv) + zero);
@@ -696,11 +731,13 @@ cudaError_t launch_typed(const CrossParams& p, cudaStream_t s) {
       const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D, true, F>, one);
       if (e != cudaSuccess || !p.choice) return e;
     }
+    if (!(parts & kRestPart)) return cudaSuccess;
     ProfScope ps(kNames[F][0], s);
     cfg.gridDim = dim3((unsigned)(p.few_units / kWarps));
     const cudaError_t e = cudaLaunchKernelEx(&cfg, cross_few_kernel<T, D, false, F>, p);
     if (e != cudaSuccess) return e;
   }
+  if (!(parts & kRestPart)) return cudaSuccess;
   ProfScope ps(kNames[F][1], s);
   cfg.gridDim = dim3((unsigned)(p.few_units + 256 / kJoinRows * p.tile_units));
   cfg.blockDim = dim3(32 * kJoinWarps);
@@ -784,12 +821,12 @@ size_t cross_layout(CrossParams* p, char* base, bool tiles_only) {
 
 #endif
 
-cudaError_t PKV_LAUNCH()(const CrossParams& p, cudaStream_t s) {
+cudaError_t PKV_LAUNCH()(const CrossParams& p, cudaStream_t s, int parts) {
   if (p.bf16)
-    return p.D == 64 ? launch_typed<__nv_bfloat16, 64, PKV_FORM>(p, s)
-                     : launch_typed<__nv_bfloat16, 128, PKV_FORM>(p, s);
-  return p.D == 64 ? launch_typed<__half, 64, PKV_FORM>(p, s)
-                   : launch_typed<__half, 128, PKV_FORM>(p, s);
+    return p.D == 64 ? launch_typed<__nv_bfloat16, 64, PKV_FORM>(p, s, parts)
+                     : launch_typed<__nv_bfloat16, 128, PKV_FORM>(p, s, parts);
+  return p.D == 64 ? launch_typed<__half, 64, PKV_FORM>(p, s, parts)
+                   : launch_typed<__half, 128, PKV_FORM>(p, s, parts);
 }
 
 }  // namespace pkv

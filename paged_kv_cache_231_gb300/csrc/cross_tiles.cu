@@ -61,8 +61,9 @@ struct Run {
   uint32_t tmem;
   int whole;
   int64_t steps;
+  int units;
 };
-static_assert(sizeof(Run) <= 96, "run area");
+static_assert(sizeof(Run) <= 112, "run area");
 
 template <int D>
 struct Lay {   // byte offsets from a 1024-byte-aligned base
@@ -76,7 +77,7 @@ struct Lay {   // byte offsets from a 1024-byte-aligned base
   static constexpr uint32_t kBars = kRing + kStages * kTile;
   static constexpr uint32_t kSeen = kBars + 384;        // [kMasks] keys of a step that take part
   static constexpr uint32_t kRun = kSeen + 16 * kMasks;  // Run
-  static constexpr uint32_t kPairMl = kRun + 96;        // [128] (m, l) of half 1
+  static constexpr uint32_t kPairMl = kRun + 112;       // [128] (m, l) of half 1
   static constexpr uint32_t kEnd = kPairMl + 1024;
   static constexpr size_t kBytes = kEnd + 1024;
 };
@@ -374,7 +375,7 @@ __device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, 
       i = 0;
       continue;
     }
-    const int on = i < 0 ? p.tile_units : 1;
+    const int on = i < 0 ? run.units : 1;
     if (i >= 0) {
       steps -= t.n;
       ++i;
@@ -394,7 +395,7 @@ __device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, 
 // tiles. With more sequences than entries or more tiles the steps are summed up where they are asked
 // for. (Summed up always, the plan of 8 prompts of up to 2048 tokens took 23 400 cycles.)
 template <Form F>
-__device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
+__device__ void plan_tiles(const CrossParams& p, int units, int64_t* mem, Run* run) {
   int64_t *steps_at = mem, *tiles_at = steps_at + kEntries + 1, *cut = tiles_at + kEntries + 1,
           *scratch = cut + kThreads + 1;
   int* per_tile = reinterpret_cast<int*>(scratch + 32);
@@ -402,7 +403,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   constexpr int kAboutAt = (2 * (kEntries + 1) + kThreads + 1 + 32 + kEntries / 2 + kList + 2) & ~1;
   int4* about = reinterpret_cast<int4*>(mem + kAboutAt);   // rows, keys, at, lo; 16-byte aligned
   int *about_cu0 = reinterpret_cast<int*>(about + kEntries), *first_tile = about_cu0 + kEntries;
-  const int tid = threadIdx.x, units = p.tile_units;
+  const int tid = threadIdx.x;
   const int group = (p.B + kEntries - 1) / kEntries, entries = (p.B + group - 1) / group;
   int f = 0;
   bool z = false;
@@ -662,6 +663,7 @@ __device__ void plan_tiles(const CrossParams& p, int64_t* mem, Run* run) {
   const int u = blockIdx.x;
   const int64_t c0 = cut[u], c1 = cut[u + 1];
   if (tid == 0) {
+    run->units = units;
     run->whole = (int)whole;
     run->steps = c1 - c0;
   }
@@ -1288,10 +1290,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  int units = p.tile_units;
   if constexpr (F == kShared) {   // the plan may have found nothing worth sharing
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    // behind the wait: the kernel of the own keys may begin now, and reads what the plan wrote
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (__ldcg(p.active) == 0) return;
+    if (p.units) units = __ldcg(p.units);
+    if ((int)blockIdx.x >= units) {   // this SM is the other kernel's
+      if (threadIdx.x < 2) p.tile_rec[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
+      return;
+    }
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Wait wait;
@@ -1333,7 +1344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (F == kCausal && p.start)   // starts of sequences, and the result of the keys before them
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // in the ring's memory before the ring is used; the other kernel reports bad sequences
-  plan_tiles<F>(p, reinterpret_cast<int64_t*>(sm + L::kRing), run);
+  plan_tiles<F>(p, units, reinterpret_cast<int64_t*>(sm + L::kRing), run);
   tc::fence_async_shared();
   tc::fence_before_sync();
   __syncthreads();

@@ -29,6 +29,9 @@ constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 // and their result makes a way through memory. The kernels of the shared keys cost a call some 30 us
 // (and 10 us where they find nothing to do).
 constexpr int64_t kCallCost = 30000;
+// Of the tiles: plan, first steps, pieces. Of a block of the kernel for few and short sequences beside
+// them, and what each step of a sequence (few_keys) adds.
+constexpr int64_t kTilesFirst = 15000, kBlockFirst = 4200, kBlockStep = 200;
 __device__ __forceinline__ int64_t few_cost(const CrossParams& p, int64_t keys) {
   return keys * p.Hkv * p.D * 4 / 7300;
 }
@@ -42,7 +45,7 @@ __device__ __forceinline__ int64_t tile_cost(const CrossParams& p, int sms, int 
 // them together save more than the call costs, group_cu, group_keys, table_row of each group and
 // `start` of its sequences say what is shared; else nothing is.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p, PrefixParams x) {
-  __shared__ unsigned long long s_saved, s_steps;
+  __shared__ unsigned long long s_saved, s_steps, s_tiles, s_best;
   __shared__ int s_longest;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -52,7 +55,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
     wrong = wrong || lo < 0 || hi < lo || hi > p.B;
   }
   if (tid == 0) {
-    s_saved = s_steps = 0;
+    s_saved = s_steps = s_tiles = 0;
+    s_best = ~0ull;
     s_longest = 0;
   }
   wrong = __syncthreads_or(wrong) != 0;
@@ -88,8 +92,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) saved += __shfl_xor_sync(0xffffffffu, saved, o);
-      saved -= tile_cost(p, x.sms, rows, keys) + (int64_t)rows * p.Hq * p.D * 8 / 4000;
+      const int64_t tiles = tile_cost(p, x.sms, rows, keys);
+      saved -= tiles + (int64_t)rows * p.Hq * p.D * 8 / 4000;
       if (saved <= 0 && !x.always) keys = 0;
+      if (lane == 0 && keys > 0) atomicAdd(&s_tiles, (unsigned long long)tiles);
     }
     if (lane == 0) {
       if (keys > 0) atomicAdd(&s_saved, (unsigned long long)(x.always ? kCallCost + 1 : saved));
@@ -140,11 +146,24 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
   // blocks behind the first, or the even share and 15 for its plan and the join (64 tokens behind 8192
   // shared keys and up to 64, 256, 512, 1024 of their own: 57.7, 64.4, 72.8 and 81.6 us, or 64.8, 70.6,
   // 81.8 and 95.8 us).
-  if (tid == 0 && x.choice) {
-    const int64_t waves = ((int64_t)p.B * p.Hkv + x.sms - 1) / x.sms;
-    const int64_t even = (int64_t)s_steps * p.Hkv / (8 * x.sms);
-    *x.choice = 2 * ((s_longest + 7) / 8) + 7 * (waves - 1) <= 30 + 2 * even;
+  if (!x.choice) return;
+  const int64_t waves = ((int64_t)p.B * p.Hkv + x.sms - 1) / x.sms;
+  const int64_t even = (int64_t)s_steps * p.Hkv / (8 * x.sms);
+  const bool small = 2 * ((s_longest + 7) / 8) + 7 * (waves - 1) <= 30 + 2 * even;
+  if (tid == 0) *x.choice = small;
+  // The kernel for few and short sequences runs beside the tiles: on the SMs that these leave free
+  // and, as they end, on theirs. The tiles take `at` ns on n SMs, the other kernel's blocks `all` on
+  // one; the n for which both are done first (64 tokens behind 8192 shared keys and up to 256,
+  // 512 of their own: on 16, 48, 76, 104 and 152 SMs 77.5, 49.0, 49.0, 55.2 and 61.1 us, or 86.7, 53.7,
+  // 63.2, 64.8 and 70.4 us).
+  const int64_t all = ((int64_t)p.B * kBlockFirst + (int64_t)s_steps * kBlockStep) * p.Hkv;
+  for (int n = tid + 1; n <= x.units_most; n += kPlanThreads) {
+    const int64_t at = kTilesFirst + (int64_t)s_tiles * x.sms / n;
+    const int64_t end = max(at, (all + n * at) / x.sms);
+    atomicMin(&s_best, (unsigned long long)end << 16 | (unsigned)n);
   }
+  __syncthreads();
+  if (tid == 0) *x.units = small ? (int)(s_best & 0xffff) : x.units_most;
 }
 
 }  // namespace
@@ -186,8 +205,13 @@ size_t prefix_layout(CrossParams* shared, CrossParams* own, PrefixParams* x, cha
   x->table_row = reinterpret_cast<int32_t*>(take(G * 4));
   x->active = reinterpret_cast<int32_t*>(take(4));
   x->choice = reinterpret_cast<int32_t*>(take(4));
+  x->units = reinterpret_cast<int32_t*>(take(4));
   float* lse = reinterpret_cast<float*>(take(rows * 4));
   float* out = reinterpret_cast<float*>(take(rows * own->D * 4));
+  if (own->max_q <= own->few) {   // single tokens
+    own->apart_o = reinterpret_cast<float*>(take(rows * own->D * 4));
+    own->apart_ml = reinterpret_cast<float2*>(take(rows * 8));
+  }
   *shared = *own;
   shared->B = x->groups;
   shared->cu = x->group_cu;
@@ -205,7 +229,13 @@ size_t prefix_layout(CrossParams* shared, CrossParams* own, PrefixParams* x, cha
   const size_t a = cross_layout(shared, base ? base + off : nullptr, true);
   const size_t b = cross_layout(own, base ? base + off + a : nullptr);
   if (!own->small) own->choice = nullptr;   // too many sequences for the one kernel
-  if (!own->choice) x->choice = nullptr;
+  if (!own->choice) {
+    x->choice = nullptr;
+    own->apart_o = nullptr;
+  } else {
+    shared->units = x->units;
+  }
+  x->units_most = shared->tile_units;
   return off + a + b;
 }
 
@@ -218,8 +248,14 @@ cudaError_t launch_prefix(const CrossParams& shared, const CrossParams& own, con
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = launch_shared(shared, s);
-  return e == cudaSuccess ? launch_causal(own, s) : e;
+  if (!own.choice) {
+    const cudaError_t e = launch_shared(shared, s);
+    return e == cudaSuccess ? launch_causal(own, s) : e;
+  }
+  cudaError_t e = launch_shared(shared, s, kTilesPart);
+  if (e == cudaSuccess) e = launch_causal(own, s, kSmallPart);
+  if (e == cudaSuccess) e = launch_shared(shared, s, kRestPart);
+  return e == cudaSuccess ? launch_causal(own, s, kRestPart) : e;
 }
 
 }  // namespace pkv

@@ -109,12 +109,17 @@ struct CrossParams {
   const float* prior_o;      // [T][Hq][D] what the shared keys gave, and its lse [T][Hq]
   const float* prior_lse;
   const int32_t* choice;     // 1: single tokens take the kernel for few and short sequences
+  // Where that kernel runs beside the tiles of the shared keys, what a sequence's own keys gave:
+  // [T][Hq][D] sums and [T][Hq] (maximum in log2 units, sum of weights); the join takes both in
+  float* apart_o;
+  float2* apart_ml;
   const int32_t* check_offsets;   // groups that are looked at for faults alone
   const int32_t* check_shared;
   int check_groups;
   // the shared keys' own call: B groups; row of the block table of each
   const int32_t* table_row;  // [B]
   const int32_t* active;     // 0: nothing is shared
+  const int32_t* units;      // blocks of the tiles that work (NULL: all)
   // plan (cross_dev.cuh)
   int few;                   // query rows of a sequence that the kernel for few rows takes
   int tile_pos;              // query positions of a tile of the kernel for many rows
@@ -147,6 +152,8 @@ struct PrefixParams {
   int32_t* table_row;        // [groups]
   int32_t* active;           // see CrossParams
   int32_t* choice;
+  int32_t* units;
+  int units_most;            // blocks of the tiles
   int sms;
   int always;                // testing hook: share whatever it saves
 };
@@ -159,9 +166,11 @@ cudaError_t launch_prefix(const CrossParams& shared, const CrossParams& own, con
 // the workspace bytes
 size_t cross_layout(CrossParams* p, char* base, bool tiles_only = false);
 // the kernels of the three forms (cross_dev.cuh) and, of each, the one for many rows (*_tiles.cu)
-cudaError_t launch_cross(const CrossParams& p, cudaStream_t s);
-cudaError_t launch_shared(const CrossParams& p, cudaStream_t s);
-cudaError_t launch_causal(const CrossParams& p, cudaStream_t s);
+// parts of a call: the tiles, the kernel for few and short sequences, and what follows them
+enum { kTilesPart = 1, kSmallPart = 2, kRestPart = 4, kAllParts = 7 };
+cudaError_t launch_cross(const CrossParams& p, cudaStream_t s, int parts = kAllParts);
+cudaError_t launch_shared(const CrossParams& p, cudaStream_t s, int parts = kAllParts);
+cudaError_t launch_causal(const CrossParams& p, cudaStream_t s, int parts = kAllParts);
 cudaError_t launch_cross_tiles(const CrossParams& p, cudaStream_t s);
 cudaError_t launch_shared_tiles(const CrossParams& p, cudaStream_t s);
 cudaError_t launch_causal_tiles(const CrossParams& p, cudaStream_t s);
