@@ -690,8 +690,9 @@ typedef struct pkv_prefix_attention_args {
 } pkv_prefix_attention_args;
 
 /* Host only: workspace bytes pkv_paged_prefix_attention needs on the current device (may be 0). It
- * holds one output in 32 bits (num_tokens * num_heads * (head_size + 1) * 4 bytes) and what the
- * kernels need, where these sizes may have something to share. */
+ * holds one output in 32 bits (num_tokens * num_heads * (head_size + 1) * 4 bytes; two where every
+ * sequence has few tokens, max_query_len * num_heads / kv_num_heads <= 16) and what the kernels
+ * need, where these sizes may have something to share. */
 int pkv_paged_prefix_attention_workspace_size(const pkv_prefix_attention_args* args,
                                               size_t* bytes);
 

@@ -6,7 +6,8 @@
 // where (out_1, lse_1) comes from the shared keys, computed once for the rows of the whole group
 // (kShared: a group is a sequence of as many rows, no causal mask), and (out_2, lse_2) from a
 // row's own keys j >= S (kCausal). The first goes to 32-bit arrays in the workspace, the second
-// takes it in where it writes a row. So a group's S keys are read once and multiplied as matrices
+// takes it in where it writes a row. Single tokens with few keys of their own go beside the first:
+// both parts go to the workspace, and the join behind them writes the rows. So a group's S keys are read once and multiplied as matrices
 // with all its rows, where every sequence for itself would read them again: 64 single tokens
 // behind 8192 keys read 1/64 of that.
 // Where that saves less than it costs (few sequences or short prefixes, which the cache holds
@@ -27,8 +28,13 @@ constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 // where others read the same (64 single tokens over the same 8192 keys: 7.3 TB/s); one of many rows
 // takes half a tile's step for each 128 rows and keys. Shared, a group's rows fill tiles together,
 // and their result makes a way through memory. The kernels of the shared keys cost a call some 30 us
-// (and 10 us where they find nothing to do).
-constexpr int64_t kCallCost = 30000;
+// (and 10 us where they find nothing to do), 24 us where the kernel for few and short sequences runs
+// beside them (saved by this count, shared, alone: 32 tokens behind 1024 keys 17.7, 30.5, 28.2 us, behind
+// 2048 35.6, 32.0, 44.2 us; 64 behind 512 17.4, 34.3, 36.2 us; with 16 heads of 64 32 behind 1024 17.8, 31.6,
+// 31.6 us, 8 behind 8192 32.7, 35.8, 46.1 us).
+// Once the plan looks, finding nothing costs 12 us there, so what is saved weighs against the difference
+// (64 behind 512 keys, looked at: shared 34.3, not shared 48.8 us).
+constexpr int64_t kCallCost = 30000, kBesideCost = 24000, kLookCost = 11000;
 // Of the tiles: plan, first steps, pieces. Of a block of the kernel for few and short sequences beside
 // them, and what each step of a sequence (few_keys) adds.
 constexpr int64_t kTilesFirst = 15000, kBlockFirst = 4200, kBlockStep = 200;
@@ -49,6 +55,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
   __shared__ int s_longest;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t cost = x.choice ? kBesideCost - kLookCost : kCallCost;
   bool wrong = false;   // group offsets that descend or leave 0 .. B
   for (int g = tid; g < x.groups; g += kPlanThreads) {
     const int lo = __ldg(x.offsets + g), hi = __ldg(x.offsets + g + 1);
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
       if (lane == 0 && keys > 0) atomicAdd(&s_tiles, (unsigned long long)tiles);
     }
     if (lane == 0) {
-      if (keys > 0) atomicAdd(&s_saved, (unsigned long long)(x.always ? kCallCost + 1 : saved));
+      if (keys > 0) atomicAdd(&s_saved, (unsigned long long)(x.always ? cost + 1 : saved));
       x.group_keys[g] = keys;
       x.group_cu[g] = wrong ? 0 : __ldg(p.cu + lo);
       if (g == x.groups - 1) x.group_cu[g + 1] = wrong ? 0 : __ldg(p.cu + hi);
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
   for (int b = tid; b < p.B; b += kPlanThreads)   // sequences that lie in no group
     if (b < from || b >= to) x.start[b] = 0;
   __syncthreads();
-  const bool share = (int64_t)s_saved > kCallCost;
+  const bool share = (int64_t)s_saved > cost;
   // of the sequences' own keys: steps of the kernel for few rows
   const int step = few_keys(p.D);
   int64_t steps = 0;
@@ -144,8 +151,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
   // The kernel for few and short sequences, or an even share of the steps for every warp and a join:
   // in units of a step of 0.85 us, the longest sequence's share of a warp and 3.5 for every wave of
   // blocks behind the first, or the even share and 15 for its plan and the join (64 tokens behind 8192
-  // shared keys and up to 64, 256, 512, 1024 of their own: 57.7, 64.4, 72.8 and 81.6 us, or 64.8, 70.6,
-  // 81.8 and 95.8 us).
+  // shared keys and up to 64, 256, 512, 1024 of their own: 42.5, 47.9, 56.4 and 67.6 us, or 64.8, 70.6,
+  // 81.8 and 95.8 us; behind the tiles instead of beside them the first took 52.8, 60.5, 70.0 and 79.6 us).
   if (!x.choice) return;
   const int64_t waves = ((int64_t)p.B * p.Hkv + x.sms - 1) / x.sms;
   const int64_t even = (int64_t)s_steps * p.Hkv / (8 * x.sms);
@@ -190,7 +197,8 @@ size_t prefix_layout(CrossParams* shared, CrossParams* own, PrefixParams* x, cha
   own->tile_pos = 2 * (128 / own->G);
   const int hook = testing_prefix_sharing();
   x->always = hook == 1;
-  if (x->groups == 0 || hook == 2 || (hook == 0 && most_alone(*own, x->sms) <= kCallCost)) {
+  if (x->groups == 0 || hook == 2 || (hook == 0 && most_alone(*own, x->sms) <=
+                                               (own->max_q <= own->few ? kBesideCost : kCallCost))) {
     own->check_offsets = x->offsets;
     own->check_shared = x->shared;
     own->check_groups = x->groups;
