@@ -183,3 +183,32 @@ def test_workspace_given_and_refused():
     torch.cuda.synchronize()
     assert torch.equal(out.cpu(), want)
     assert (ws[need:] == 255).all()
+
+
+@pytest.mark.parametrize("nq", [1, 3])
+@pytest.mark.parametrize("head_size,dtype,heads,kv", [(128, "f16", 8, 2), (64, "bf16", 4, 4)])
+def test_few_tokens_beside_the_shared_keys(nq, head_size, dtype, heads, kv, sharing):
+    # groups, rows of none, empty and bad sequences, padding: each row is written by one of three
+    # kernels; the same bits eagerly, replayed and from a workspace full of something else
+    lengths, own = [nq] * 40, [int(x) for x in np.random.default_rng(18).integers(0, 90, 40)]
+    lengths[3] = lengths[17] = lengths[30] = 0
+    c = case(18, lengths, own, [(14, 512), (2, 0), (16, 1024)], head_size=head_size, dtype=dtype,
+             num_heads=heads, kv_heads=kv, pad=3)
+    c.check(prefix=True, max_query_len=nq)
+    c.past[35] = -1
+    c.check(prefix=True, max_query_len=nq, status=B.DEV_BAD_SEQUENCE)
+    a = c.device() + [i32(c.groups), i32(c.shared)]
+    kw = dict(num_heads=heads, kv_num_heads=kv, max_query_len=nq)
+    out = torch.empty_like(a[0])
+    need = B.pkv_paged_prefix_attention_workspace_size(B.make_prefix_args(*a, out, **kw))
+    ws = torch.zeros(need + 256, dtype=torch.uint8, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.pkv_paged_prefix_attention(*a, output=out, workspace=ws, **kw)
+    want = c.gpu(prefix=True, max_query_len=nq)[0]
+    for fill in (0, 255, 0x7f):
+        out.fill_(float("nan"))
+        ws.fill_(fill)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want)
