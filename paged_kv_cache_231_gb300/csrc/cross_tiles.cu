@@ -61,7 +61,7 @@ struct Run {
   uint32_t tmem;
   int whole;
   int64_t steps;
-  int units;
+  int units;   // kShared
 };
 static_assert(sizeof(Run) <= 112, "run area");
 
@@ -375,7 +375,7 @@ __device__ __forceinline__ void each_part(const CrossParams& p, const Run& run, 
       i = 0;
       continue;
     }
-    const int on = i < 0 ? run.units : 1;
+    const int on = i < 0 ? (F == kShared ? run.units : p.tile_units) : 1;
     if (i >= 0) {
       steps -= t.n;
       ++i;
@@ -663,7 +663,7 @@ __device__ void plan_tiles(const CrossParams& p, int units, int64_t* mem, Run* r
   const int u = blockIdx.x;
   const int64_t c0 = cut[u], c1 = cut[u + 1];
   if (tid == 0) {
-    run->units = units;
+    if (F == kShared) run->units = units;
     run->whole = (int)whole;
     run->steps = c1 - c0;
   }
