@@ -110,7 +110,8 @@ __device__ __forceinline__ Span span_of(const CrossParams& p, const Seq& q, int 
   x.ns = p.window > 0 ? (p.sinks + unit - 1) & -unit : 0;
   const int end = min(last + 1, q.keys);
   const int from = p.window > 0 ? max(q.lo, first - p.window + 1) : q.lo;
-  x.gap = min(max((from & -unit) - x.ns, 0), (end - 1) & -unit);
+  // where every row stands behind the last key of the table, the sinks are still among the steps
+  x.gap = max(min(from & -unit, (end - 1) & -unit) - x.ns, 0);
   x.steps = (end - x.gap + N - 1) / N;
   return x;
 }
