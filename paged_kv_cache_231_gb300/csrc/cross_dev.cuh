@@ -130,10 +130,13 @@ __device__ __forceinline__ int first_seen(const CrossParams& p, const Seq& q) {
 // when some of its rows see no key.
 template <bool kTiles, Form F>
 __device__ __forceinline__ Seq read_seq(const CrossParams& p, int b, int* flags, bool* zero) {
+  // The groups' rows and keys (kShared) are written by the plan, behind which this kernel may already
+  // have begun: the read-only path is for memory that nobody writes as long as a kernel lasts.
+  const auto at = [](const int32_t* x) { return F == kShared ? __ldcg(x) : __ldg(x); };
   Seq s;
-  s.cu0 = __ldg(p.cu + b);
-  const int hi = __ldg(p.cu + b + 1);
-  s.keys = __ldg((F == kCausal ? p.past : p.klen) + b);
+  s.cu0 = at(p.cu + b);
+  const int hi = at(p.cu + b + 1);
+  s.keys = at((F == kCausal ? p.past : p.klen) + b);
   if (F == kCausal) s.lo = p.start ? __ldcg(p.start + b) : 0;
   if (F == kShared) s.at = __ldcg(p.table_row + b);
   s.steps = s.ranges = 0;
