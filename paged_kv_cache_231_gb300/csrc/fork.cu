@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
 
   // mark them, a warp kUnits pieces of a row at a time
-  const int chunks = (p.MB + kChunk - 1) / kChunk, units = p.B * chunks;
+  const int chunks = (p.MB - 1) / kChunk + 1, units = p.B * chunks;
   const int apart = C * kWarps;
   for (int u0 = rank + C * warp; u0 < units; u0 += apart * kUnits) {
     int id[kUnits][kChunk / 32];
@@ -235,8 +235,9 @@ __global__ void __launch_bounds__(kCopyThreads)
     const int full = column(p, n), part = n > full * p.BS ? full : -1;
     const int32_t* old = p.table + (int64_t)from * p.MB;   // read where n > 0 alone
     int32_t* row = p.new_table + (int64_t)b * p.MB;
-    for (int c = tid; c < p.MB; c += kCopyThreads)
-      if (c != part) row[c] = c < full ? __ldg(old + c) : -1;
+    // unsigned: a row may end less than a block's step in front of 2^31
+    for (uint32_t c = tid; c < (uint32_t)p.MB; c += kCopyThreads)
+      if ((int)c != part) row[c] = (int)c < full ? __ldg(old + c) : -1;
   }
 }
 
@@ -279,7 +280,7 @@ cudaError_t launch_fork(const ForkParams& p, cudaStream_t s) {
   }
   // as the schedule's cluster: 16 blocks where there are many entries to mark
   const int64_t work =
-      (int64_t)p.B * ((p.MB + kChunk - 1) / kChunk) / kWarps + p.groups / kWarps;
+      (int64_t)p.B * ((p.MB - 1) / kChunk + 1) / kWarps + p.groups / kWarps;
   const bool can = dev >= 0 && dev < 64 && (wide.load() & (1ull << dev));
   {
     ProfScope ps("fork_plan", s);
