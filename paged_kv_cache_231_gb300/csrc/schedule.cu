@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) schedule_kernel(ScheduleParams p) {
   __syncthreads();
 
   // mark the held entries, a warp kUnits pieces of a row at a time
-  const int chunks = (p.MB + kChunk - 1) / kChunk, units = p.B * chunks;
+  const int chunks = (p.MB - 1) / kChunk + 1, units = p.B * chunks;
   const int apart = C * kWarps;
   for (int u0 = rank + C * warp; u0 < units; u0 += apart * kUnits) {
     int id[kUnits][kChunk / 32];
@@ -377,7 +377,7 @@ cudaError_t launch_schedule(const ScheduleParams& p, cudaStream_t s) {
   // Blocks of the cluster: 16 where many entries or tokens are to be gone through (2048 rows of
   // 600 entries and 325 000 tokens, their slots included: 52 us with 8, 33 us with 16), else 8 (64
   // rows of 520 entries: 10.6 us with 8, 13.9 us with 1; 2 rows: 6.1 us with either).
-  const int64_t work = (int64_t)p.B * ((p.MB + kChunk - 1) / kChunk) / kWarps +
+  const int64_t work = (int64_t)p.B * ((p.MB - 1) / kChunk + 1) / kWarps +
                        (int64_t)p.T / (kThreads * kTokens) + p.groups / kWarps;
   const bool can = dev >= 0 && dev < 64 && (wide.load() & (1ull << dev));
   const unsigned C = work < 64 || !can ? 8 : kMaxCluster;
