@@ -1202,6 +1202,8 @@ def pkv_paged_fork(parents, past_seqlens, block_table, caches=(), *, num_blocks:
     B = past_seqlens.shape[0] if past_seqlens.dim() == 1 else -1
     MB = block_table.shape[1] if block_table.dim() == 2 else -1
     at = rows = ()
+    if hasattr(caches, "data_ptr"):   # its blocks would be taken for caches
+        raise TypeError("caches: a list of tensors, got one tensor")
     if len(caches) > 0:
         at, rows, num_blocks, block_size = _cache_rows(caches)
     raw = _check_tensors(stream, (
