@@ -27,13 +27,15 @@ constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 // What sharing saves, in nanoseconds. A sequence of few rows reads all of its keys, from the cache
 // where others read the same (64 single tokens over the same 8192 keys: 7.3 TB/s); one of many rows
 // takes half a tile's step for each 128 rows and keys. Shared, a group's rows fill tiles together,
-// and their result makes a way through memory. The kernels of the shared keys cost a call some 30 us
-// (and 10 us where they find nothing to do), 24 us where the kernel for few and short sequences runs
-// beside them (saved by this count, shared, alone: 32 tokens behind 1024 keys 17.7, 30.5, 28.2 us, behind
-// 2048 35.6, 32.0, 44.2 us; 64 behind 512 17.4, 34.3, 36.2 us; with 16 heads of 64 32 behind 1024 17.8, 31.6,
-// 31.6 us, 8 behind 8192 32.7, 35.8, 46.1 us).
-// Once the plan looks, finding nothing costs 12 us there, so what is saved weighs against the difference
-// (64 behind 512 keys, looked at: shared 34.3, not shared 48.8 us).
+// and their result makes a way through memory. The kernels of the shared keys cost a call some 30 us,
+// 24 us where the kernel for few and short sequences runs beside them (saved by this count, shared,
+// alone: 32 tokens behind 1024 keys 17.7, 30.5, 28.2 us, behind 2048 35.6, 32.0, 44.2 us; 64 behind 512 17.4,
+// 34.3, 36.2 us; with 16 heads of 64 32 behind 1024 17.8, 31.6, 31.6 us, 8 behind 8192 32.7, 35.8, 46.1 us).
+// A call that looks and finds nothing has paid for kLookCost of that (8 to 12 us), so what is saved weighs
+// against the rest of what the path that would run costs. Saved, shared, not shared though looked at: 64
+// behind 512 keys 17.4, 34.3, 48.8 us; 32 behind 768 with 3000 keys of their own one of them (an even share
+// for every warp) 13.2, 46.1, 41.3 us; 16 drafts of 8 tokens behind 4096 19.8, 65.4, 72.9 us; 16 prompts of up
+// to 100 behind 8192 25.6, 151.5, 173.3 us.
 constexpr int64_t kCallCost = 30000, kBesideCost = 24000, kLookCost = 11000;
 // Of the tiles: plan, first steps, pieces. Of a block of the kernel for few and short sequences beside
 // them, and what each step of a sequence (few_keys) adds.
@@ -55,7 +57,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
   __shared__ int s_longest;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t cost = x.choice ? kBesideCost - kLookCost : kCallCost;
+  // the least that sharing costs: whether single tokens' own keys go beside it is known further down
+  const int64_t cost = (x.choice ? kBesideCost : kCallCost) - kLookCost;
   bool wrong = false;   // group offsets that descend or leave 0 .. B
   for (int g = tid; g < x.groups; g += kPlanThreads) {
     const int lo = __ldg(x.offsets + g), hi = __ldg(x.offsets + g + 1);
@@ -118,45 +121,55 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(CrossParams p
   for (int b = tid; b < p.B; b += kPlanThreads)   // sequences that lie in no group
     if (b < from || b >= to) x.start[b] = 0;
   __syncthreads();
-  const bool share = (int64_t)s_saved > cost;
-  // of the sequences' own keys: steps of the kernel for few rows
-  const int step = few_keys(p.D);
-  int64_t steps = 0;
-  int longest = 0;
-  const auto own = [&](int b, int start) {
-    const int64_t n = (int64_t)__ldg(p.past + b) + __ldg(p.cu + b + 1) - __ldg(p.cu + b) - start;
-    const int k = (int)min(max((n + step - 1) / step, (int64_t)0), (int64_t)p.MB * p.BS);
-    steps += k;
-    longest = max(longest, k);
-  };
-  for (int g = warp; g < x.groups; g += kPlanWarps) {
-    const int lo = wrong ? 0 : __ldg(x.offsets + g), hi = wrong ? 0 : __ldg(x.offsets + g + 1);
-    const int keys = share ? __ldcg(x.group_keys + g) : 0;
-    for (int b = lo + lane; b < hi; b += 32) {
-      x.start[b] = keys;
-      own(b, keys);
+  bool share = (int64_t)s_saved > cost, small = false;
+  const int step = few_keys(p.D), shift = 31 - __clz(step);   // a power of two
+#pragma unroll 1   // once, or once more where that turns out to save less than it costs
+  for (;;) {
+    // what is shared of each sequence, and of its own keys the steps of the kernel for few rows
+    int64_t steps = 0;
+    int longest = 0;
+    const auto own = [&](int b, int start) {
+      const int64_t n = (int64_t)__ldg(p.past + b) + __ldg(p.cu + b + 1) - __ldg(p.cu + b) - start;
+      const int k = (int)min(max((n + step - 1) >> shift, (int64_t)0), (int64_t)p.MB * p.BS);
+      steps += k;
+      longest = max(longest, k);
+    };
+    for (int g = warp; g < x.groups; g += kPlanWarps) {
+      const int lo = wrong ? 0 : __ldg(x.offsets + g), hi = wrong ? 0 : __ldg(x.offsets + g + 1);
+      const int keys = share ? __ldcg(x.group_keys + g) : 0;
+      for (int b = lo + lane; b < hi; b += 32) {
+        x.start[b] = keys;
+        own(b, keys);
+      }
     }
-  }
-  for (int b = tid; b < p.B; b += kPlanThreads)
-    if (b < from || b >= to) own(b, 0);
+    for (int b = tid; b < p.B; b += kPlanThreads)
+      if (b < from || b >= to) own(b, 0);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, o);
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  if (lane == 0) {
-    atomicAdd(&s_steps, (unsigned long long)steps);
-    atomicMax(&s_longest, longest);
+    for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, o);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+      atomicAdd(&s_steps, (unsigned long long)steps);
+      atomicMax(&s_longest, longest);
+    }
+    __syncthreads();
+    if (!x.choice) break;
+    // The kernel for few and short sequences, or an even share of the steps for every warp and a join:
+    // in units of a step of 0.85 us, the longest sequence's share of a warp and 3.5 for every wave of
+    // blocks behind the first, or the even share and 15 for its plan and the join (64 tokens behind 8192
+    // shared keys and up to 64, 256, 512, 1024 of their own: 42.5, 47.9, 56.4 and 67.6 us, or 64.8, 70.6,
+    // 81.8 and 95.8 us; behind the tiles instead of beside them the first took 52.8, 60.5, 70.0 and 79.6 us).
+    // (n <= 2 * floor(s / m), without the division of 64 bits)
+    const int waves = (p.B * p.Hkv + x.sms - 1) / x.sms;   // at most 4
+    const int64_t n = (int64_t)(s_longest + 7) / 8 * 2 + 7 * (waves - 1) - 30;
+    small = n <= 0 || (n + 1) / 2 * (8 * x.sms) <= (int64_t)s_steps * p.Hkv;
+    if (!share || small || x.always || (int64_t)s_saved > kCallCost - kLookCost) break;
+    share = false;   // these kernels would follow one another, and cost more
+    __syncthreads();
+    if (tid == 0) s_steps = s_longest = 0;
+    __syncthreads();
   }
-  __syncthreads();
   if (tid == 0) *x.active = share ? 1 : 0;
-  // The kernel for few and short sequences, or an even share of the steps for every warp and a join:
-  // in units of a step of 0.85 us, the longest sequence's share of a warp and 3.5 for every wave of
-  // blocks behind the first, or the even share and 15 for its plan and the join (64 tokens behind 8192
-  // shared keys and up to 64, 256, 512, 1024 of their own: 42.5, 47.9, 56.4 and 67.6 us, or 64.8, 70.6,
-  // 81.8 and 95.8 us; behind the tiles instead of beside them the first took 52.8, 60.5, 70.0 and 79.6 us).
   if (!x.choice) return;
-  const int64_t waves = ((int64_t)p.B * p.Hkv + x.sms - 1) / x.sms;
-  const int64_t even = (int64_t)s_steps * p.Hkv / (8 * x.sms);
-  const bool small = 2 * ((s_longest + 7) / 8) + 7 * (waves - 1) <= 30 + 2 * even;
   if (tid == 0) *x.choice = small;
   // The kernel for few and short sequences runs beside the tiles: on the SMs that these leave free
   // and, as they end, on theirs. The tiles take `at` ns on n SMs, the other kernel's blocks `all` on
