@@ -26,7 +26,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 using pool::block_sum;
-using pool::first_above;
 using pool::kThreads;
 using pool::kWarps;
 
