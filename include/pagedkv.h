@@ -608,7 +608,8 @@ typedef struct pkv_append_norm_args {
  * rotation. Squares are summed in 32 bits: a bf16 head whose squares sum past 3.4e38 becomes
  * 0. What that call says of slots, positions, padding and overlaps holds here too; a query
  * whose position has no table row is normed and not rotated. At least one weight is given.
- * Same refusals and limits. */
+ * Same refusals and limits. Heads of other sizes than 64 and 128 (256 among them) are appended for
+ * readers of the caller's own: the attention calls here take those two alone. */
 int pkv_paged_append_norm_rotary(const pkv_append_norm_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------------

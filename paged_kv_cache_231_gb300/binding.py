@@ -923,7 +923,7 @@ def _own_workspace(need: int, like, stream, raw: int):
     """A workspace for a call that brought none. Each thread keeps one for each of the last
     ``_OWN_STREAMS`` streams that it called on as the current one (an allocation costs a call
     6 us): calls of one thread on one stream run one after the other. One takes up to 61 MB on
-    a GPU of 152 SMs, as much as its largest call needed, until the thread ends, has called on
+    a GPU of 152 SMs (64 MB where prefix attentions call), as much as its largest call needed, until the thread ends, has called on
     as many other streams, or calls release_workspaces. A call that is captured gets memory of
     its graph's, one on another stream than the current one its own."""
     torch = _torch()

@@ -27,7 +27,7 @@
 // odd ones, and half 0 joins the two (m, l, O) at the end.
 // TMEM columns: S_0 0..127 (weights over 0..63), S_1 128..255, O_0 256.., O_1 384...
 // Measured: 16 sequences of up to 2048 queries over up to 4096 states, 32 heads of 128 on 8 kv
-// heads: 432 us for 0.571 TFLOP, 1320 TFLOP/s (68 % of the measured dense rate; the tensor pipe is
+// heads: 432 us for 0.571 TFLOP, 1320 TFLOP/s (70 % of 1882 measured dense; the tensor pipe is
 // active 58 % of the time): the two halves' softmaxes, each a chain of TMEM loads, exponentials and
 // TMEM stores, and the hand-offs between them and the products set the pace. Few rows and long
 // sequences (100 queries, 20000 to 60000 states, 16 heads of 64): 80 us, 4.7 TB/s.
